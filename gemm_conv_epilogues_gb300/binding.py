@@ -18,9 +18,11 @@ TF_OK, TF_ERR_INVALID_ARG, TF_ERR_UNSUPPORTED, TF_ERR_CUDA, TF_ERR_TIMEOUT = 0, 
 (TF_CONV_AUTO, TF_CONV_DIRECT, TF_CONV_TILED, TF_CONV_UMMA, TF_CONV_UMMA_PAIR, TF_CONV_UMMA_PAIR_WIDE,
  TF_CONV_UMMA_WIDE) = -1, 0, 1, 2, 3, 4, 5
 TF_LN_AUTO, TF_LN_WARP, TF_LN_CTA, TF_LN_CLUSTER = -1, 0, 1, 2
+TF_FP16, TF_BF16, TF_FP32 = 0, 1, 2
+TF_ACT_NONE, TF_ACT_SILU, TF_ACT_GELU = 0, 1, 2
 TF_DEVERR_PRODUCER_WAIT, TF_DEVERR_MMA_WAIT, TF_DEVERR_EPILOGUE_WAIT = 0x1, 0x2, 0x4
 TF_DEVERR_DRAIN_WAIT, TF_DEVERR_PROBE_WAIT, TF_DEVERR_EXCHANGE_WAIT = 0x8, 0x10, 0x20
-TF_DEVERR_PAIR_TMEM, TF_DEVERR_SMEM_ALIGN = 0x40, 0x80
+TF_DEVERR_PAIR_TMEM, TF_DEVERR_SMEM_ALIGN, TF_DEVERR_OFFSETS = 0x40, 0x80, 0x100
 
 
 class TfError(RuntimeError):
@@ -63,6 +65,16 @@ _SIGS = {
     "tf_unfused_residual_add": ([_vp, _vp, _vp, _i64, _vp], _i),
     "tf_unfused_layernorm": ([_vp, _vp, _i64, _i64, _f, _vp], _i),
     "tf_unfused_affine": ([_vp, _vp, _vp, _vp, _i64, _i64, _vp], _i),
+    "tf_layernorm_forward": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _f, _i, _vp],
+                             _i),
+    "tf_layernorm_backward_workspace_size": ([_i64, _i64, _i], _i64),
+    "tf_layernorm_backward": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i, _i,
+                               _vp, _i64, _vp], _i),
+    "tf_grouped_matmul": ([_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i, _i, _vp], _i),
+    "tf_grouped_matmul_dgrad": ([_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _i, _i, _vp], _i),
+    "tf_grouped_matmul_wgrad_workspace_size": ([_i64, _i64, _i64, _i64, _i], _i64),
+    "tf_grouped_matmul_wgrad": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _i, _vp, _i64, _vp],
+                                _i),
     "tf_set_wait_limit_ns": ([_u64], None),
     "tf_get_wait_limit_ns": ([], _u64),
     "tf_read_device_error": ([ctypes.POINTER(ctypes.c_uint32)], _i),
@@ -180,6 +192,68 @@ def tf_residual_layernorm_variant(act, res, gamma, beta, y, rows, hidden, eps, v
 
 def tf_residual_layernorm_select(hidden) -> int:
     return _lib.tf_residual_layernorm_select(int(hidden))
+
+
+def _same_device(*tensors):
+    """The library launches on the current device: an operand of another one is refused here."""
+    import torch
+    here = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if here is None:
+            here = torch.cuda.current_device()
+        if t.get_device() != here and t.is_cuda:
+            raise ValueError(f"operand on cuda:{t.get_device()} while the current device is cuda:{here}")
+
+
+def tf_layernorm_forward(x, x_stride, res, res_stride, gamma, beta, y, y_stride, sum, sum_stride, mean, rstd, rows,
+                         hidden, eps, dtype, stream=None, check=True):
+    _same_device(x, res, gamma, beta, y, sum, mean, rstd)
+    return _check(_lib.tf_layernorm_forward(_ptr(x), x_stride, _ptr(res), res_stride, _ptr(gamma), _ptr(beta), _ptr(y),
+                                            y_stride, _ptr(sum), sum_stride, _ptr(mean), _ptr(rstd), rows, hidden, eps,
+                                            dtype, _stream(stream)), "tf_layernorm_forward", check)
+
+
+def tf_layernorm_backward_workspace_size(rows, hidden, dtype) -> int:
+    return int(_lib.tf_layernorm_backward_workspace_size(rows, hidden, dtype))
+
+
+def tf_layernorm_backward(dy, dy_stride, x, x_stride, gamma, mean, rstd, dres, dres_stride, dx, dx_stride, dgamma,
+                          dbeta, rows, hidden, accumulate, dtype, workspace, workspace_bytes, stream=None, check=True):
+    _same_device(dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace)
+    return _check(_lib.tf_layernorm_backward(_ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(gamma), _ptr(mean),
+                                             _ptr(rstd), _ptr(dres), dres_stride, _ptr(dx), dx_stride, _ptr(dgamma),
+                                             _ptr(dbeta), rows, hidden, accumulate, dtype, _ptr(workspace),
+                                             workspace_bytes, _stream(stream)), "tf_layernorm_backward", check)
+
+
+def tf_grouped_matmul(x, x_stride, w, bias, offsets, y, y_stride, pre, pre_stride, rows, groups, N, K, act, dtype,
+                      stream=None, check=True):
+    _same_device(x, w, bias, offsets, y, pre)
+    return _check(_lib.tf_grouped_matmul(_ptr(x), x_stride, _ptr(w), _ptr(bias), _ptr(offsets), _ptr(y), y_stride,
+                                         _ptr(pre), pre_stride, rows, groups, N, K, act, dtype, _stream(stream)),
+                  "tf_grouped_matmul", check)
+
+
+def tf_grouped_matmul_dgrad(dy, dy_stride, w, offsets, pre, pre_stride, dx, dx_stride, rows, groups, N, K, act, dtype,
+                            stream=None, check=True):
+    _same_device(dy, w, offsets, pre, dx)
+    return _check(_lib.tf_grouped_matmul_dgrad(_ptr(dy), dy_stride, _ptr(w), _ptr(offsets), _ptr(pre), pre_stride,
+                                               _ptr(dx), dx_stride, rows, groups, N, K, act, dtype, _stream(stream)),
+                  "tf_grouped_matmul_dgrad", check)
+
+
+def tf_grouped_matmul_wgrad_workspace_size(rows, groups, N, K, dtype) -> int:
+    return int(_lib.tf_grouped_matmul_wgrad_workspace_size(rows, groups, N, K, dtype))
+
+
+def tf_grouped_matmul_wgrad(dy, dy_stride, x, x_stride, offsets, dw, dbias, rows, groups, N, K, accumulate, dtype,
+                            workspace, workspace_bytes, stream=None, check=True):
+    _same_device(dy, x, offsets, dw, dbias, workspace)
+    return _check(_lib.tf_grouped_matmul_wgrad(_ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(offsets), _ptr(dw),
+                                               _ptr(dbias), rows, groups, N, K, accumulate, dtype, _ptr(workspace),
+                                               workspace_bytes, _stream(stream)), "tf_grouped_matmul_wgrad", check)
 
 
 def tf_unfused_conv2d(x, w_ohwi, t1, shape, variant=TF_CONV_AUTO, stream=None, check=True):

@@ -88,6 +88,13 @@ typedef enum {
                            its peers' shared memory once per row (16384 < hidden <= 131072) */
 } tf_ln_variant;
 
+/* Storage types of the calls that take a `dtype`. */
+typedef enum { TF_FP16 = 0, TF_BF16 = 1, TF_FP32 = 2 } tf_dtype;
+
+/* Activations of the grouped products' epilogues: none, z*sigmoid(z), and
+ * z*Phi(z) with the normal distribution function (the erf form). */
+typedef enum { TF_ACT_NONE = 0, TF_ACT_SILU = 1, TF_ACT_GELU = 2 } tf_act;
+
 /* Human-readable name of a status code (static storage). */
 const char *tf_status_string(int status);
 
@@ -240,6 +247,106 @@ int tf_residual_layernorm_variant(const void *act, const void *res, const float 
  * negative tf_status value when no strategy takes it. */
 int tf_residual_layernorm_select(int64_t hidden);
 
+/* ---------------------------------------------------------------- layer norm, forward and backward */
+
+/* LayerNorm for training and serving, in one pass over HBM, with the residual
+ * sum and the row statistics as further outputs.
+ *   s = x + res (or x);  mean and biased variance of s per row, in fp32;
+ *   rstd = 1/sqrt(var + eps);  y = (s - mean)*rstd*gamma + beta
+ *   x, res, y, sum : dtype (TF_FP16, TF_BF16 or TF_FP32) [rows][hidden], row i
+ *                    at i*stride elements, each with a stride >= hidden of its own
+ *   gamma, beta    : fp32 [hidden];  mean, rstd : fp32 [rows]
+ * NULL leaves an operand out: res (s = x), gamma (1), beta (0), sum, mean,
+ * rstd.  `sum` receives s rounded to dtype; the statistics and y are those of
+ * the unrounded s.  Any hidden from 1 to 131072, any row stride (below 2^31)
+ * and the alignment of an element; rows whose start is not a multiple of 16
+ * bytes take a slower kernel.  rows may be 0 (nothing is read or written).
+ * Elements between `hidden` and the stride are not touched. */
+int tf_layernorm_forward(const void *x, int64_t x_stride, const void *res, int64_t res_stride, const float *gamma,
+                         const float *beta, void *y, int64_t y_stride, void *sum, int64_t sum_stride, float *mean,
+                         float *rstd, int64_t rows, int64_t hidden, float eps, int dtype, tf_stream_t stream);
+
+/* Bytes of device workspace tf_layernorm_backward needs when dgamma or dbeta
+ * is wanted (fp32 column sums of the rows each CTA takes).  Host only; depends
+ * on the current device's SM count. */
+int64_t tf_layernorm_backward_workspace_size(int64_t rows, int64_t hidden, int dtype);
+
+/* Gradients of tf_layernorm_forward.  With xh = (x - mean)*rstd, w = dy*gamma:
+ *   dx     = rstd*(w - mean_row(w) - xh*mean_row(w*xh)) + dres
+ *   dgamma = sum over rows of dy*xh;  dbeta = sum over rows of dy
+ *   dy, x, dres, dx : dtype [rows][hidden] with strides as above; x is what was
+ *                     normalised (the forward pass's `sum`, or its x)
+ *   mean, rstd      : fp32 [rows] from the forward pass;  gamma : fp32 [hidden] or NULL (1)
+ *   dgamma, dbeta   : fp32 [hidden], either may be NULL; with `accumulate` != 0 the sums
+ *                     are added to what they hold
+ * dres (may be NULL) is the gradient that reaches s past the norm, along the
+ * residual stream: dx is then the gradient of x and of res both.  All sums are
+ * fp32, in an order that depends on the sizes alone: equal calls give equal
+ * bits.  The workspace (16-byte aligned, not needed when both weight gradients
+ * are NULL) is in use until the stream reaches the end of the call; calls that
+ * may overlap need one each, captured graphs too.  TF_ERR_INVALID_ARG when it
+ * is missing or too small.  rows may be 0: dgamma and dbeta become 0, or stay
+ * as they are with `accumulate`. */
+int tf_layernorm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const float *gamma,
+                          const float *mean, const float *rstd, const void *dres, int64_t dres_stride, void *dx,
+                          int64_t dx_stride, float *dgamma, float *dbeta, int64_t rows, int64_t hidden, int accumulate,
+                          int dtype, void *workspace, int64_t workspace_bytes, tf_stream_t stream);
+
+/* ---------------------------------------------------------------- grouped products */
+
+/* Matrix products over rows sorted by group (the experts of a mixture, say),
+ * every group with weights of its own and any number of rows.
+ *   offsets : int32 [groups + 1] on the device; group e has the rows
+ *             offsets[e] .. offsets[e+1]-1 (none when equal).  Rows before
+ *             offsets[0] and from offsets[groups] on belong to no group: they
+ *             are not written.  `rows` is the number of rows of the buffers.
+ *             Offsets that fall, or lie outside [0, rows], make the call write
+ *             nothing and set TF_DEVERR_OFFSETS in the device error word.
+ *   w       : dtype [groups][N][K], contiguous
+ *   dtype   : TF_FP16 or TF_BF16 (TF_ERR_UNSUPPORTED for TF_FP32); sums are fp32
+ * groups up to 1024, N and K up to 65536, rows up to 4194304; row strides (in
+ * elements, below 2^31) of their own.  The tensor-core kernels need every row
+ * and base address to be a multiple of 16 bytes (N % 8 == 0, K % 8 == 0,
+ * strides % 8 == 0); other operands take a much slower kernel.  rows may be 0.
+ * A row's result depends on that row and its group's weights only: infinities
+ * or NaN in one group do not reach another.  Equal calls give equal bits. */
+
+/* y[m] = act(x[m] w[e]^T + bias[e]) for every row m of every group e.
+ *   x : dtype [rows][K];  bias : fp32 [groups][N] or NULL;  y : dtype [rows][N]
+ *   pre : dtype [rows][N] or NULL: the sum before the activation, rounded, for
+ *         the backward pass (y is the activation of the unrounded sum) */
+int tf_grouped_matmul(const void *x, int64_t x_stride, const void *w, const float *bias, const int32_t *offsets,
+                      void *y, int64_t y_stride, void *pre, int64_t pre_stride, int64_t rows, int64_t groups, int64_t N,
+                      int64_t K, int act, int dtype, tf_stream_t stream);
+
+/* Gradient of the product's input, with the activation of the layer below in
+ * the epilogue: dx[m] = (dy[m] w[e]) * act'(pre[m]).
+ *   dy : dtype [rows][N];  dx : dtype [rows][K]
+ *   pre : dtype [rows][K], that layer's sums before its activation; not read
+ *         (and may be NULL) with TF_ACT_NONE
+ * dx is then the gradient of those sums, which is what the layer below takes
+ * as its dy. */
+int tf_grouped_matmul_dgrad(const void *dy, int64_t dy_stride, const void *w, const int32_t *offsets, const void *pre,
+                            int64_t pre_stride, void *dx, int64_t dx_stride, int64_t rows, int64_t groups, int64_t N,
+                            int64_t K, int act, int dtype, tf_stream_t stream);
+
+/* Bytes of device workspace tf_grouped_matmul_wgrad can use (0: none).  Host
+ * only; depends on the current device's SM count. */
+int64_t tf_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t groups, int64_t N, int64_t K, int dtype);
+
+/* Gradients of the weights and the bias: dw[e] = dy_e^T x_e, dbias[e] = the
+ * sum of group e's rows of dy; 0 for a group without rows.  With `accumulate`
+ * != 0 they are added to what dw and dbias hold.
+ *   dy : dtype [rows][N];  x : dtype [rows][K]
+ *   dw : fp32 [groups][N][K], contiguous;  dbias : fp32 [groups][N] or NULL
+ * With a workspace smaller than tf_grouped_matmul_wgrad_workspace_size
+ * (including 0) it runs without one.  The workspace must be 16-byte aligned
+ * and is in use until the stream reaches the end of the call; calls that may
+ * overlap need one each, captured graphs too. */
+int tf_grouped_matmul_wgrad(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const int32_t *offsets,
+                            float *dw, float *dbias, int64_t rows, int64_t groups, int64_t N, int64_t K, int accumulate,
+                            int dtype, void *workspace, int64_t workspace_bytes, tf_stream_t stream);
+
 /* ---------------------------------------------------------------- unfused chains */
 
 /* The separate kernels that the fused calls replace, for the traffic and time
@@ -304,9 +411,13 @@ uint64_t tf_get_wait_limit_ns(void);
 #define TF_DEVERR_SMEM_ALIGN 0x80u    /* tensor-core conv: dynamic shared memory not 1024-byte
                                          aligned (the CTA did no work) */
 
+#define TF_DEVERR_OFFSETS 0x100u      /* grouped products: the row offsets fall or leave [0, rows]
+                                         (the call wrote nothing) */
+
 /* Synchronises the current device, copies the device error word of the
  * current device into *word (may be NULL), clears it, and returns TF_OK if it
- * was zero, TF_ERR_TIMEOUT if a wait gave up, TF_ERR_CUDA if the runtime
+ * was zero, TF_ERR_TIMEOUT if a bit is set (a wait gave up, or what else the bit
+ * stands for), TF_ERR_CUDA if the runtime
  * failed.  Not for use inside stream capture. */
 int tf_read_device_error(uint32_t *word);
 
