@@ -164,15 +164,6 @@ cudaError_t launch_grouped_simple(const GroupedArgs &a, int mode, cudaStream_t s
     return a.dtype == TF_BF16 ? launch_typed<__nv_bfloat16>(a, mode, err, st) : launch_typed<__half>(a, mode, err, st);
 }
 
-int64_t grouped_wgrad_workspace(int64_t, int, int64_t, int64_t, int) { return 0; }
-
-cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st)
-{
-    const cudaError_t e = launch_grouped_simple(a, mode, st);
-    if (e != cudaSuccess || mode != GROUPED_WGRAD || !a.dbias) return e;
-    return launch_grouped_bias_grad(a, st);
-}
-
 cudaError_t launch_grouped_bias_grad(const GroupedArgs &a, cudaStream_t st)
 {
     uint32_t *err = device_error_word();

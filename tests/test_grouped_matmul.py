@@ -519,4 +519,4 @@ def test_norm_and_experts_forward_and_backward(b, hidden, inner):
     # at most seven stored bf16 tensors (2^-9 each) lie on the longest path; random signs make the sum far smaller
     for got, want in ((out, outd), (dx, p["x"].grad), (dgamma, p["gamma"].grad), (dbeta, p["beta"].grad),
                       (dw1, p["w1"].grad), (dw2, p["w2"].grad), (db1, p["b1"].grad), (db2, p["b2"].grad)):
-        assert float((got.double() - want.detach()).norm() / want.norm()) <= 7 * 2.0 ** -8
+        assert float((got.double() - want.detach()).norm() / want.detach().norm()) <= 7 * 2.0 ** -8
