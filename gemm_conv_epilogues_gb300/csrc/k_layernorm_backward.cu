@@ -4,8 +4,9 @@
 //   dgamma = sum over rows of dy*xh,  dbeta = sum over rows of dy
 // One pass over HBM: dy, x (and dres) read once, dx written once.  A thread
 // keeps its columns' dgamma and dbeta in fp32 registers over all the rows its
-// CTA takes; a CTA's sums go to the workspace and a second, small kernel adds
-// them in order, so that equal calls give equal bits (no atomics).
+// group takes; the row groups of an SM form one CTA and add their sums in
+// shared memory, one set per SM goes to the workspace, and a second, small
+// kernel adds those in order, so that equal calls give equal bits (no atomics).
 #include "norm_rows.cuh"
 
 namespace tf {
@@ -13,119 +14,132 @@ namespace {
 
 using namespace norm;
 
-template <typename T, bool ALIGNED, bool CLUSTER, int NT>
-__global__ void __launch_bounds__(kMaxThreads)
+// Threads per SM, from the registers the columns take (two fp32 sums, gamma,
+// and the row in its storage type): 128 for 16 columns, 80 for 8 (96 where they
+// are element-wise).   Spilled registers cost far more than a few warps fewer: with most of the
+// SM's memory in the rings, the little L1 that is left does not hold them.
+constexpr int sm_threads(int cols, bool aligned) { return cols > 8 ? 512 : aligned ? 768 : 640; }
+
+// Columns per thread: 16, or 8 for narrow rows and for element-wise columns
+// (16 above 4096 of them).
+int cols_for(int64_t hidden, int size, bool aligned)
+{
+    if (!aligned) return hidden > 4096 ? 16 : 8;
+    if (hidden <= 256) return 8;
+    return 16;
+}
+
+// GROUP: threads per row where the columns are element-wise (a constant makes
+// them immediate offsets), 0 for 16-byte vectors.
+template <typename T, int GROUP, bool CLUSTER, int NT, int COLS>
+__global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 1)
     norm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Sources src,
                          const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
+    constexpr bool ALIGNED = GROUP == 0;
+    using C = Cols<T, ALIGNED, COLS>;
+    constexpr int PAIRS = C::PAIRS;
     pdl_begin();
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float2 red[2][kMaxThreads / 32];
+    __shared__ float2 red[2][768 / 32];
     __shared__ __align__(8) float2 slot[2][kMaxRanks];
     __shared__ __align__(8) uint64_t xbar[2];
-    const uint32_t rank = CLUSTER ? ptx::cluster_ctarank() : 0u;
-    const int gt = threadIdx.x % g.group, c0 = (int)rank * g.slice;
-    const int64_t unit = blockIdx.x / g.csize;
-    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, a.rows, unit, gridDim.x / g.csize, c0, err,
-                                                    wait_ns, xbar);
-    Exchange xch = {slot, xbar, rank, (uint32_t)g.csize, wait_ns, err, false};
+    const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0;
+    const int gsize = ALIGNED ? g.group : GROUP, gt = threadIdx.x % gsize, c0 = rank * g.slice;
+    const int unit = (int)blockIdx.x / g.csize, units = (int)gridDim.x / g.csize;
+    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, unit, units, c0, err, wait_ns,
+                                                    xbar);
+    Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
 
-    float ga[kCols], dg[kCols], db[kCols];
+    float2 ga[PAIRS], dg[PAIRS], db[PAIRS];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        const int c = col_of<T, ALIGNED>(j, gt, g.group);
-        ga[j] = a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f;
-        dg[j] = db[j] = 0.0f;
+    for (int p = 0; p < PAIRS; ++p) {
+        const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
+        ga[p] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
+                            a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
+        dg[p] = db[p] = make_float2(0.0f, 0.0f);
     }
     const float inv_h = 1.0f / (float)a.hidden;
-    Edge ed = load_edge(ring, 0, ring.first, gt, g.group), ex = load_edge(ring, 1, ring.first, gt, g.group);
-    Edge er = {0.0f, 0.0f};
-    if (NT > 2) er = load_edge(ring, 2, ring.first, gt, g.group);
+    Edge<T> ed, ex, er;
+    load_edge(ring, 0, ring.first, gt, gsize, ed);
+    load_edge(ring, 1, ring.first, gt, gsize, ex);
+    if (NT > 2) load_edge(ring, 2, ring.first, gt, gsize, er);
     // the row statistics, one row ahead
     float mean = 0.0f, rstd = 0.0f;
-    if (ring.first < a.rows) {
+    if (ring.first < ring.rows) {
         mean = __ldg(a.mean + ring.first);
         rstd = __ldg(a.rstd + ring.first);
     }
-    int it = 0;
-    for (int64_t row = ring.first; row < a.rows; row += ring.step, ++it) {
-        float d[kCols], xh[kCols];
-        Held<T, ALIGNED> dr;
-        ring.wait(it);
-        load_cols(ring, 0, it, gt, g.group, ed, d);
-        load_cols(ring, 1, it, gt, g.group, ex, xh);
-        if (NT > 2) hold_cols(ring, 2, it, gt, g.group, er, dr);
-        const int64_t next = row + ring.step;
-        ed = load_edge(ring, 0, next, gt, g.group);
-        ex = load_edge(ring, 1, next, gt, g.group);
-        if (NT > 2) er = load_edge(ring, 2, next, gt, g.group);
-        const float shift = -mean * rstd, scale = rstd;
-        if (next < a.rows) {
+    for (int row = ring.first, it = 0; row < ring.rows; row += ring.step, ++it, ring.advance()) {
+        C d, x, r;
+        ring.wait();
+        put_edge(ring, 0, row, ed);
+        put_edge(ring, 1, row, ex);
+        if (NT > 2) put_edge(ring, 2, row, er);
+        d.load(ring, 0, row, gt, gsize);
+        x.load(ring, 1, row, gt, gsize);
+        if (NT > 2) r.load(ring, 2, row, gt, gsize);
+        const int64_t next = (int64_t)row + ring.step;
+        load_edge(ring, 0, next, gt, gsize, ed);
+        load_edge(ring, 1, next, gt, gsize, ex);
+        if (NT > 2) load_edge(ring, 2, next, gt, gsize, er);
+        const float2 scale = make_float2(rstd, rstd), shift = make_float2(-mean * rstd, -mean * rstd);
+        if (next < ring.rows) {
             mean = __ldg(a.mean + next);
             rstd = __ldg(a.rstd + next);
         }
-        float c1 = 0.0f, c2 = 0.0f;
+        float2 c1 = make_float2(0.0f, 0.0f), c2 = c1;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {   // past the slice dy is zero and adds nothing
-            xh[j] = fmaf(xh[j], scale, shift);
-            dg[j] = fmaf(d[j], xh[j], dg[j]);
-            db[j] += d[j];
-            d[j] *= ga[j];
-            c1 += d[j];
-            c2 = fmaf(d[j], xh[j], c2);
+        for (int p = 0; p < PAIRS; ++p) {   // past the slice dy is zero and adds nothing
+            const float2 fd = d.get(p), xh = ffma2(x.get(p), scale, shift), w = fmul2(fd, ga[p]);
+            dg[p] = ffma2(fd, xh, dg[p]);
+            db[p] = fadd2(db[p], fd);
+            c1 = fadd2(c1, w);
+            c2 = ffma2(w, xh, c2);
         }
-        float2 c = group_sum(c1, c2, g.group, red[it & 1]);
-        if (gt == 0) {   // every thread of the group holds its columns: the stage takes a later row
-            ptx::fence_proxy_async_smem();
-            ring.issue(it + g.stages);
-        }
+        float2 c = group_sum2<!CLUSTER>(c1.x + c1.y, c2.x + c2.y, gsize, red[it & 1]);
+        if (gt == 0) ring.refill(row);   // every thread of the group holds its columns
         if constexpr (CLUSTER) {
             const float2 *pairs = xch.swap(c, it);
             c = make_float2(0.0f, 0.0f);
-            for (int r = 0; r < g.csize; ++r) {
-                c.x += pairs[r].x;
-                c.y += pairs[r].y;
+            for (int i = 0; i < g.csize; ++i) {
+                c.x += pairs[i].x;
+                c.y += pairs[i].y;
             }
         }
-        const float k1 = -c.x * inv_h * scale, k2 = -c.y * inv_h * scale;
+        const float2 k1 = make_float2(-c.x * inv_h * scale.x, -c.x * inv_h * scale.x);
+        const float2 k2 = make_float2(-c.y * inv_h * scale.x, -c.y * inv_h * scale.x);
+        float2 out[PAIRS];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) d[j] = fmaf(d[j], scale, fmaf(xh[j], k2, k1));
-        if (NT > 2) add_held(dr, d);
-        store_cols<T, ALIGNED>(reinterpret_cast<T *>(a.dx) + row * a.dx_stride + c0, width, gt, g.group, d);
+        for (int p = 0; p < PAIRS; ++p) {
+            const float2 xh = ffma2(x.get(p), scale, shift);
+            out[p] = ffma2(fmul2(d.get(p), ga[p]), scale, ffma2(xh, k2, k1));
+            if (NT > 2) out[p] = fadd2(out[p], r.get(p));
+        }
+        C::store(reinterpret_cast<T *>(a.dx) + (row * a.dx_stride + c0), width, gt, gsize, out);
     }
     if (gt == 0) ring.drain();
 
     if (a.ws) {
         // this CTA's sums: row `unit` of dgamma's and of dbeta's [units][hidden] array
-        float *wg = a.ws + unit * a.hidden + c0, *wb = wg + (int64_t)(gridDim.x / g.csize) * a.hidden;
-        if (g.group < g.threads) {   // eight warps with rows of their own: added in order in shared memory
-            float *acc = reinterpret_cast<float *>(smem);
-            for (int w = 0; w < g.threads / g.group; ++w) {
-                cta_sync();   // every warp is done with its ring, and with the previous warp's turn
-                if ((int)threadIdx.x / g.group != w) continue;
+        float *wg = a.ws + (int64_t)unit * a.hidden + c0, *wb = wg + (int64_t)units * a.hidden;
+        const int groups = g.threads / gsize;
+        float *acc = reinterpret_cast<float *>(smem);
+        for (int w = 0; w < groups; ++w) {   // the groups' sums, added in order in shared memory
+            cta_sync();   // every group is done with its ring, and with the previous group's turn
+            if ((int)threadIdx.x / gsize != w) continue;
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    const int c = col_of<T, ALIGNED>(j, gt, g.group);
-                    if (c < width) {
-                        acc[c] = w ? acc[c] + dg[j] : dg[j];
-                        acc[kWarpCols + c] = w ? acc[kWarpCols + c] + db[j] : db[j];
-                    }
+            for (int j = 0; j < COLS; ++j) {
+                const int c = C::col(j, gt, gsize);
+                if (c >= width) continue;
+                float vg = j % 2 ? dg[j / 2].y : dg[j / 2].x, vb = j % 2 ? db[j / 2].y : db[j / 2].x;
+                if (w > 0) {
+                    vg += acc[c];
+                    vb += acc[g.slice + c];
                 }
-            }
-            cta_sync();
-            for (int c = threadIdx.x; c < width; c += g.threads) {
-                wg[c] = acc[c];
-                wb[c] = acc[kWarpCols + c];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-                const int c = col_of<T, ALIGNED>(j, gt, g.group);
-                if (c < width) {
-                    wg[c] = dg[j];
-                    wb[c] = db[j];
-                }
+                (w + 1 < groups ? acc : wg)[c] = vg;
+                (w + 1 < groups ? acc + g.slice : wb)[c] = vb;
             }
         }
     }
@@ -143,14 +157,15 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
     const float *src = a.ws + (blockIdx.y ? (int64_t)parts * a.hidden : 0) + c;
     float t = 0.0f;
     if (c < a.hidden) {
-        int p = warp;
-        for (; p + 3 * kSumWarps < parts; p += 4 * kSumWarps) {
-            float v[4];
+        for (int p = warp; p < parts; p += 8 * kSumWarps) {   // eight loads in flight
+            float v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = src[(int64_t)(p + i * kSumWarps) * a.hidden];
-            t += (v[0] + v[1]) + (v[2] + v[3]);
+            for (int i = 0; i < 8; ++i) {
+                const int q = p + i * kSumWarps;
+                v[i] = q < parts ? src[(int64_t)q * a.hidden] : 0.0f;
+            }
+            t += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
         }
-        for (; p < parts; p += kSumWarps) t += src[(int64_t)p * a.hidden];
     }
     red[warp][lane] = t;
     cta_sync();
@@ -163,15 +178,22 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
     }
 }
 
-// The widest set of partial sums any alignment of the operands gives.
+Geometry geometry_for(int64_t rows, int64_t hidden, int size, bool aligned, int tensors)
+{
+    const int cols = cols_for(hidden, size, aligned);
+    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned), true, rows);
+}
+
+// The most partial sums that any alignment and number of operands gives.
 int64_t most_units(int64_t rows, int64_t hidden, int dtype)
 {
     const int size = dtype == TF_FP32 ? 4 : 2;
     int64_t most = 0;
-    for (bool aligned : {false, true}) {
-        const int64_t u = launch_units(geometry(hidden, size, aligned, 3), rows);
-        if (u > most) most = u;
-    }
+    for (int tensors : {2, 3})
+        for (bool aligned : {false, true}) {
+            const int64_t u = launch_units(geometry_for(rows, hidden, size, aligned, tensors), rows);
+            if (u > most) most = u;
+        }
     return most;
 }
 
@@ -185,13 +207,27 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
                          aligned_rows(a.x, a.x_stride, size) && aligned_rows(a.dres, a.dres_stride, size) &&
                          aligned_rows(a.dx, a.dx_stride, size);
     const Sources src = {{a.dy, a.x, a.dres}, {a.dy_stride, a.x_stride, a.dres_stride}};
-    const Geometry g = geometry(a.hidden, size, aligned, a.dres ? 3 : 2);
+    const Geometry g = geometry_for(a.rows, a.hidden, size, aligned, a.dres ? 3 : 2);
     *units = launch_units(g, a.rows);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        return g.csize > 1
-                   ? (aligned ? norm_backward_kernel<T, true, true, NT> : norm_backward_kernel<T, false, true, NT>)
-                   : (aligned ? norm_backward_kernel<T, true, false, NT> : norm_backward_kernel<T, false, false, NT>);
+        if (aligned) {
+            if (g.csize > 1) return norm_backward_kernel<T, 0, true, NT, 16>;
+            return cols_for(a.hidden, size, true) == 8 ? norm_backward_kernel<T, 0, false, NT, 8> : norm_backward_kernel<T, 0, false, NT, 16>;
+        }
+        if (cols_for(a.hidden, size, false) == 16)
+            return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16> : norm_backward_kernel<T, 512, false, NT, 16>;
+        switch (g.group) {
+        case 32: return norm_backward_kernel<T, 32, false, NT, 8>;
+        case 64: return norm_backward_kernel<T, 64, false, NT, 8>;
+        case 128: return norm_backward_kernel<T, 128, false, NT, 8>;
+        case 192: return norm_backward_kernel<T, 192, false, NT, 8>;
+        case 256: return norm_backward_kernel<T, 256, false, NT, 8>;
+        case 320: return norm_backward_kernel<T, 320, false, NT, 8>;
+        case 384: return norm_backward_kernel<T, 384, false, NT, 8>;
+        case 448: return norm_backward_kernel<T, 448, false, NT, 8>;
+        default: return norm_backward_kernel<T, 512, false, NT, 8>;
+        }
     };
     return launch_rows(a.dres ? pick(std::integral_constant<int, 3>()) : pick(std::integral_constant<int, 2>()), g,
                        *units, st, a, src, g, err, wait_limit_ns());

@@ -12,89 +12,101 @@ namespace {
 
 using namespace norm;
 
-template <typename T, bool ALIGNED, bool CLUSTER, int NT>
-__global__ void __launch_bounds__(kMaxThreads)
+// Columns per thread: 16 at 128 registers, 8 at 64 where they are element-wise.
+// Fewer registers would spill, which costs far more than more threads gain: with
+// most of the SM's memory in the rings, the little L1 left does not hold them.
+// (Element-wise rows above 4096 columns take 16, too, in CTAs of 512.)
+constexpr int cols_of(bool aligned, int64_t hidden) { return aligned || hidden > 4096 ? 16 : 8; }
+constexpr int sm_threads(int cols) { return cols == 8 ? 1024 : 512; }
+
+// GROUP: threads per row where the columns are element-wise (a constant makes
+// them immediate offsets), 0 for 16-byte vectors.  SPAN: 0 for at most 256
+// threads per row, 1 for up to 512, 2 for a cluster of such CTAs.
+template <typename T, int GROUP, int SPAN, int NT, int COLS>
+__global__ void __launch_bounds__(GROUP > 256 || SPAN > 0 ? 512 : 256,
+                                  GROUP > 256 ? (COLS == 8 ? 2 : 1) : GROUP > 0 ? 4 : SPAN > 0 ? 1 : 2)
     norm_forward_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Sources src,
                         const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
+    constexpr bool ALIGNED = GROUP == 0, CLUSTER = SPAN == 2;
+    using C = Cols<T, ALIGNED, COLS>;
+    constexpr int PAIRS = C::PAIRS;
     pdl_begin();
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float2 red[2][kMaxThreads / 32];
+    __shared__ float2 red[2][kMaxGroup / 32];
     __shared__ __align__(8) float2 slot[2][kMaxRanks];
     __shared__ __align__(8) uint64_t xbar[2];
-    const uint32_t rank = CLUSTER ? ptx::cluster_ctarank() : 0u;
-    const int gt = threadIdx.x % g.group, c0 = (int)rank * g.slice;
-    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, a.rows, blockIdx.x / g.csize,
-                                                    gridDim.x / g.csize, c0, err, wait_ns, xbar);
-    Exchange xch = {slot, xbar, rank, (uint32_t)g.csize, wait_ns, err, false};
+    const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0;
+    const int gsize = ALIGNED ? g.group : GROUP, gt = threadIdx.x % gsize, c0 = rank * g.slice;
+    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, (int)blockIdx.x / g.csize,
+                                                    (int)gridDim.x / g.csize, c0, err, wait_ns, xbar);
+    Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
 
-    float ga[kCols], be[kCols];
+    float2 ga[PAIRS], be[PAIRS];
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        const int c = col_of<T, ALIGNED>(j, gt, g.group);
-        ga[j] = a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f;
-        be[j] = a.beta && c < width ? __ldg(a.beta + c0 + c) : 0.0f;
+    for (int p = 0; p < PAIRS; ++p) {
+        const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
+        ga[p] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
+                            a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
+        be[p] = make_float2(a.beta && c < width ? __ldg(a.beta + c0 + c) : 0.0f,
+                            a.beta && d < width ? __ldg(a.beta + c0 + d) : 0.0f);
     }
-    const float inv_h = 1.0f / (float)a.hidden, inv_w = 1.0f / (float)width;
-    const int lane = threadIdx.x & 31;
-    const float n_l = CLUSTER && lane < g.csize ? (float)min(a.hidden - lane * g.slice, g.slice) : 0.0f;
-    const float inv_n_l = CLUSTER && lane < g.csize ? 1.0f / n_l : 0.0f;
+    const float inv_h = 1.0f / (float)a.hidden, inv_n = 1.0f / (float)width;
 
-    Edge ex = load_edge(ring, 0, ring.first, gt, g.group), er = {0.0f, 0.0f};
-    if (NT > 1) er = load_edge(ring, 1, ring.first, gt, g.group);
-    int it = 0;
-    for (int64_t row = ring.first; row < a.rows; row += ring.step, ++it) {
-        float s[kCols];
-        ring.wait(it);
-        load_cols(ring, 0, it, gt, g.group, ex, s);
-        if (NT > 1) {
-            float r[kCols];
-            load_cols(ring, 1, it, gt, g.group, er, r);
+    Edge<T> ex, er;
+    load_edge(ring, 0, ring.first, gt, gsize, ex);
+    if (NT > 1) load_edge(ring, 1, ring.first, gt, gsize, er);
+    for (int row = ring.first, it = 0; row < ring.rows; row += ring.step, ++it, ring.advance()) {
+        float2 s[PAIRS];
+        ring.wait();
+        put_edge(ring, 0, row, ex);
+        if (NT > 1) put_edge(ring, 1, row, er);
+        {
+            C x, r;
+            x.load(ring, 0, row, gt, gsize);
+            if (NT > 1) r.load(ring, 1, row, gt, gsize);
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) s[j] += r[j];
+            for (int p = 0; p < PAIRS; ++p) s[p] = NT > 1 ? fadd2(x.get(p), r.get(p)) : x.get(p);
         }
-        ex = load_edge(ring, 0, row + ring.step, gt, g.group);
-        if (NT > 1) er = load_edge(ring, 1, row + ring.step, gt, g.group);
-        float sum = 0.0f;
+        load_edge(ring, 0, (int64_t)row + ring.step, gt, gsize, ex);
+        if (NT > 1) load_edge(ring, 1, (int64_t)row + ring.step, gt, gsize, er);
+        float2 sum = s[0];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) sum += s[j];
-        const float total = group_sum(sum, 0.0f, g.group, red[0]).x;
-        if (gt == 0) {   // every thread of the group holds its columns: the stage takes a later row
-            ptx::fence_proxy_async_smem();
-            ring.issue(it + g.stages);
-        }
-        const float centre = total * (CLUSTER ? inv_w : inv_h);   // of the slice, in a cluster
-        float sq = 0.0f;
+        for (int p = 1; p < PAIRS; ++p) sum = fadd2(sum, s[p]);
+        const float total = group_sum<false>(sum.x + sum.y, gsize, red[0]);
+        if (gt == 0) ring.refill(row);   // every thread of the group holds its columns
+        float mean = total * (CLUSTER ? inv_n : inv_h);   // of the slice, in a cluster
+        float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-            const float d = s[j] - centre;
-            if (col_of<T, ALIGNED>(j, gt, g.group) < width) sq = fmaf(d, d, sq);
+        for (int p = 0; p < PAIRS; ++p) {
+            float2 d = fsub2(s[p], make_float2(mean, mean));
+            if (!C::inside(2 * p, gt, gsize, width)) d.x = 0.0f;
+            if (!C::inside(2 * p + 1, gt, gsize, width)) d.y = 0.0f;
+            sq = ffma2(d, d, sq);
         }
-        float m2 = group_sum(sq, 0.0f, g.group, red[1]).x, mean = centre;
+        float m2 = group_sum<false>(sq.x + sq.y, gsize, red[1]);
         if constexpr (CLUSTER) {
             // the slices' (sum, M2) pairs merged pairwise (Chan et al.): M2 = sum M2_r + sum n_r (mean_r - mean)^2,
             // lane r of every warp taking rank r's terms
+            const int lane = threadIdx.x & 31;
+            const float n_l = lane < g.csize ? (float)min(a.hidden - lane * g.slice, g.slice) : 0.0f;
             const float2 *pairs = xch.swap(make_float2(total, m2), it);
             const float2 pr = lane < g.csize ? pairs[lane] : make_float2(0.0f, 0.0f);
-            float t = pr.x;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-            mean = t * inv_h;
-            const float d = pr.x * inv_n_l - mean;
-            m2 = lane < g.csize ? fmaf(n_l * d, d, pr.y) : 0.0f;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+            mean = warp_sum(pr.x) * inv_h;
+            const float d = lane < g.csize ? pr.x / n_l - mean : 0.0f;
+            m2 = warp_sum(fmaf(n_l * d, d, pr.y));
         }
         const float rstd = rsqrtf(m2 * inv_h + a.eps);
         if (gt == 0 && rank == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
-        if (a.sum) store_cols<T, ALIGNED>(reinterpret_cast<T *>(a.sum) + row * a.sum_stride + c0, width, gt, g.group, s);
+        if (a.sum) C::store(reinterpret_cast<T *>(a.sum) + (row * a.sum_stride + c0), width, gt, gsize, s);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) s[j] = fmaf((s[j] - mean) * rstd, ga[j], be[j]);
-        store_cols<T, ALIGNED>(reinterpret_cast<T *>(a.y) + row * a.y_stride + c0, width, gt, g.group, s);
+        for (int p = 0; p < PAIRS; ++p)
+            s[p] = ffma2(fmul2(fsub2(s[p], make_float2(mean, mean)), make_float2(rstd, rstd)), ga[p], be[p]);
+        C::store(reinterpret_cast<T *>(a.y) + (row * a.y_stride + c0), width, gt, gsize, s);
     }
     if (gt == 0) ring.drain();
     if constexpr (CLUSTER) ptx::cluster_sync();   // no CTA leaves while a peer's push to it may be in flight
@@ -110,12 +122,25 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
                          aligned_rows(a.res, a.res_stride, size) && aligned_rows(a.y, a.y_stride, size) &&
                          aligned_rows(a.sum, a.sum_stride, size);
     const Sources src = {{a.x, a.res}, {a.x_stride, a.res_stride}};
-    const Geometry g = geometry(a.hidden, size, aligned, a.res ? 2 : 1);
+    const int cols = cols_of(aligned, a.hidden);
+    const Geometry g = geometry(a.hidden, size, aligned, cols, a.res ? 2 : 1, sm_threads(cols), false, a.rows);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        return g.csize > 1
-                   ? (aligned ? norm_forward_kernel<T, true, true, NT> : norm_forward_kernel<T, false, true, NT>)
-                   : (aligned ? norm_forward_kernel<T, true, false, NT> : norm_forward_kernel<T, false, false, NT>);
+        if (aligned)
+            return g.csize > 1 ? norm_forward_kernel<T, 0, 2, NT, 16>
+                   : g.group > 256 ? norm_forward_kernel<T, 0, 1, NT, 16> : norm_forward_kernel<T, 0, 0, NT, 16>;
+        if (cols == 16) return g.csize > 1 ? norm_forward_kernel<T, 512, 2, NT, 16> : norm_forward_kernel<T, 512, 1, NT, 16>;
+        switch (g.group) {
+        case 32: return norm_forward_kernel<T, 32, 0, NT, 8>;
+        case 64: return norm_forward_kernel<T, 64, 0, NT, 8>;
+        case 128: return norm_forward_kernel<T, 128, 0, NT, 8>;
+        case 192: return norm_forward_kernel<T, 192, 0, NT, 8>;
+        case 256: return norm_forward_kernel<T, 256, 0, NT, 8>;
+        case 320: return norm_forward_kernel<T, 320, 0, NT, 8>;
+        case 384: return norm_forward_kernel<T, 384, 0, NT, 8>;
+        case 448: return norm_forward_kernel<T, 448, 0, NT, 8>;
+        default: return norm_forward_kernel<T, 512, 0, NT, 8>;
+        }
     };
     return launch_rows(a.res ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>()), g,
                        launch_units(g, a.rows), st, a, src, g, err, wait_limit_ns());

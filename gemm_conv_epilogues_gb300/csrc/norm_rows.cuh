@@ -3,10 +3,12 @@
 // shared-memory stages filled by bulk copies, so several rows per SM are on
 // their way while one is reduced, and every element is read from HBM once.
 //
-// A row group (one warp for rows of at most 512 columns, else the whole CTA)
-// works on one row at a time, each thread on kCols columns of it, held in fp32
-// registers.  Rows wider than kSlice columns are cut into slices over the
-// CTAs of a cluster.
+// A row group of one or more warps works on one row at a time, each thread on
+// COLS columns of it; a CTA holds one or several groups, which meet at named
+// barriers of their own.  Rows wider than 8192 columns are cut into slices
+// over the CTAs of a cluster, one group per CTA.  (Slices of 4096, with more
+// CTAs per SM, were slower: 161 against 110 us for 8192 x 8192 bf16, forward
+// with residual; the exchange lengthens every row.)
 //
 // Alignment.  With every row start a multiple of 16 bytes (ALIGNED) a row is
 // one bulk copy and a thread's columns are 16-byte vectors.  Otherwise the
@@ -27,11 +29,8 @@
 namespace tf {
 namespace norm {
 
-constexpr int kCols = 16;                 // columns per thread
-constexpr int kWarpCols = 32 * kCols;     // rows up to this width take one warp
-constexpr int kMaxThreads = 512;
-constexpr int kSlice = kMaxThreads * kCols;   // widest slice of one CTA
-constexpr int kWarpRowThreads = 256;      // CTA of warp rows: eight rows at a time
+constexpr int kSlice = 8192;              // columns of one CTA
+constexpr int kMaxGroup = 512;
 constexpr int kMaxStages = 8;
 constexpr int kMaxTensors = 3;
 constexpr int kMaxRanks = 16;
@@ -81,10 +80,11 @@ __device__ __forceinline__ void st_stream(void *p, uint4 v)
 
 // Launch geometry, from the host.
 struct Geometry {
-    int group;          // threads per row: 32, or the CTA
+    int group;          // threads per row (and CTA of the cluster)
     int threads;        // threads per CTA
+    int per_sm;         // CTAs per SM
     int csize, slice;   // CTAs per row and columns per CTA
-    int tensors, stages, tensor_bytes;   // ring of one row group: stages x tensors x tensor_bytes
+    int stages, tensor_bytes;   // ring of one row group: stages x tensors x tensor_bytes
     int bar_off;        // mbarriers behind the rings
     int smem;
 };
@@ -102,23 +102,24 @@ struct Ring {
     unsigned char *mem;
     uint64_t *full;
     int stages, tensor_bytes, c0, width;        // width: columns of this CTA's slice, from c0 on
-    int64_t first, step, rows;                  // this group's rows: first, first + step, ...
+    int first, step, rows;                      // this group's rows: first, first + step, ...
     uint64_t wait_ns;
     uint32_t *err;
     bool failed;
-    int issued, used;
+    int stage;                                  // of the current row; counted up, not divided out: rows are short
+    uint32_t phase, pending;                    // pending: stages with a copy under way (the issuing thread's)
 
-    __device__ __forceinline__ const T *at(int i, int64_t row) const {
+    __device__ __forceinline__ const T *at(int i, int64_t row) const
+    {
         return reinterpret_cast<const T *>(src.base[i]) + (row * src.stride[i] + c0);
     }
 
-    // Copies the group's it-th row into its stage (one thread of the group).
-    __device__ __forceinline__ void issue(int it)
+    // Copies `row` into stage s (one thread of the group).
+    __device__ __forceinline__ void issue(int s, int64_t row)
     {
-        const int64_t row = first + it * step;
         if (row >= rows || failed) return;
-        unsigned char *dst = mem + (it % stages) * NT * tensor_bytes;
-        uint64_t *bar = &full[it % stages];
+        unsigned char *dst = mem + s * NT * tensor_bytes;
+        uint64_t *bar = &full[s];
         const uint32_t bytes = (uint32_t)width * (uint32_t)sizeof(T);
         if constexpr (ALIGNED) {
             ptx::mbar_arrive_expect_tx(bar, bytes * (uint32_t)NT);
@@ -140,24 +141,41 @@ struct Ring {
                                    (uint32_t)(hi - lo), bar);
             }
         }
-        issued = it + 1;
+        pending |= 1u << s;
     }
 
-    __device__ __forceinline__ void wait(int it)
+    // Waits for the current row.
+    __device__ __forceinline__ void wait()
     {
-        if (!failed && !ptx::mbar_wait(&full[it % stages], (uint32_t)(it / stages) & 1u, wait_ns)) {
+        if (!failed && !ptx::mbar_wait(&full[stage], phase, wait_ns)) {
             failed = true;
             atomicOr(err, TF_DEVERR_PRODUCER_WAIT);
         }
-        used = it + 1;
+        if (!failed) pending &= ~(1u << stage);
     }
 
-    // Copies issued but never waited for (after a time-out only) land before the CTA exits.
+    // The row `stages` after `row` takes the current stage, which every thread of the group has read (one thread).
+    __device__ __forceinline__ void refill(int row)
+    {
+        ptx::fence_proxy_async_smem();
+        issue(stage, (int64_t)row + (int64_t)stages * step);
+    }
+
+    __device__ __forceinline__ void advance()
+    {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+
+    // Copies never waited for (after a time-out only) land before the CTA exits.
     __device__ __forceinline__ void drain()
     {
-        for (int k = used; k < issued; ++k)
-            if (!ptx::mbar_wait(&full[k % stages], (uint32_t)(k / stages) & 1u, wait_ns))
-                atomicOr(err, TF_DEVERR_DRAIN_WAIT);
+        for (int s = 0; s < stages; ++s)
+            if ((pending >> s) & 1u)
+                if (!ptx::mbar_wait(&full[s], s >= stage ? phase : phase ^ 1u, wait_ns))
+                    atomicOr(err, TF_DEVERR_DRAIN_WAIT);
     }
 
     // Columns of row `it` of tensor i that lie before and behind the copied pieces.
@@ -170,153 +188,202 @@ struct Ring {
     }
 };
 
-// A thread's (at most one) column of either edge of one tensor, loaded ahead.
+// The edge elements of one tensor's row that are this thread's columns (at
+// most one of either edge), loaded a row ahead and put into the row's stage
+// before the thread reads it: a thread reads its own columns only, so no
+// barrier lies between.
+template <typename T>
 struct Edge {
-    float head, tail;
+    T head, tail;
+    int head_at, tail_at;   // columns, or -1
 };
 
 template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ Edge load_edge(const Ring<T, ALIGNED, NT> &ring, int i, int64_t row, int gt, int gsize)
+__device__ __forceinline__ void load_edge(const Ring<T, ALIGNED, NT> &ring, int i, int64_t row, int gt, int gsize,
+                                          Edge<T> &e)
 {
-    Edge e = {0.0f, 0.0f};
     if constexpr (!ALIGNED) {
+        e.head_at = e.tail_at = -1;
         if (row < ring.rows) {
             int head, tail;
             ring.edges(i, row, head, tail);
             const T *p = ring.at(i, row);
-            if (gt < head) e.head = widen(p[gt]);
-            // the tail column of this thread: the one congruent to gt modulo the group's size
-            const int t0 = ring.width - tail;
-            int c = t0 + ((gt - t0) % gsize + gsize) % gsize;
-            if (c < ring.width) e.tail = widen(p[c]);
+            if (gt < head) {
+                e.head_at = gt;
+                e.head = p[gt];
+            }
+            // the last columns, at most 15: those congruent to gt modulo the group's size
+            const int t0 = ring.width - tail, d = (gt - t0) % gsize, c = t0 + (d < 0 ? d + gsize : d);
+            if (c < ring.width) {
+                e.tail_at = c;
+                e.tail = p[c];
+            }
         }
     }
-    return e;
 }
 
-// The thread's kCols columns of tensor i of the group's it-th row, fp32; zero past the slice.
+// Tensor i of the current row `row` in its stage.
 template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ void load_cols(const Ring<T, ALIGNED, NT> &ring, int i, int it, int gt, int gsize,
-                                          const Edge &edge, float (&f)[kCols])
+__device__ __forceinline__ T *stage_row(const Ring<T, ALIGNED, NT> &ring, int i, int row)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    const unsigned char *src = ring.mem + ((it % ring.stages) * NT + i) * ring.tensor_bytes;
-    if constexpr (ALIGNED) {
-        const int nvec = ring.width / VEC;
-#pragma unroll
-        for (int k = 0; k < kCols / VEC; ++k) {
-            const int v = gt + k * gsize;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (v < nvec) u = reinterpret_cast<const uint4 *>(src)[v];
-            unpack<T>(u, f + k * VEC);
-        }
-    } else {
-        const int64_t row = ring.first + it * ring.step;
-        int head, tail;
-        ring.edges(i, row, head, tail);
-        const T *p = reinterpret_cast<const T *>(src + (reinterpret_cast<uint64_t>(ring.at(i, row)) & 15u));
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const int c = gt + k * gsize;
-            f[k] = c >= ring.width ? 0.0f : c < head ? edge.head : c >= ring.width - tail ? edge.tail : widen(p[c]);
-        }
+    unsigned char *s = ring.mem + (ring.stage * NT + i) * ring.tensor_bytes;
+    if constexpr (!ALIGNED) s += reinterpret_cast<uint64_t>(ring.at(i, row)) & 15u;
+    return reinterpret_cast<T *>(s);
+}
+
+template <typename T, bool ALIGNED, int NT>
+__device__ __forceinline__ void put_edge(const Ring<T, ALIGNED, NT> &ring, int i, int row, const Edge<T> &edge)
+{
+    if constexpr (!ALIGNED) {
+        T *p = stage_row(ring, i, row);
+        if (edge.head_at >= 0) p[edge.head_at] = edge.head;
+        if (edge.tail_at >= 0) p[edge.tail_at] = edge.tail;
     }
 }
 
-// The same columns, left in the storage type until they are needed (half the registers for 16-bit types).
-template <typename T, bool ALIGNED>
-struct Held {
-    uint4 raw[ALIGNED ? kCols * (int)sizeof(T) / 16 : 1];
-    T one[ALIGNED ? 1 : kCols];
+__device__ __forceinline__ float2 widen2(uint32_t u, __half)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+__device__ __forceinline__ float2 widen2(uint32_t u, __nv_bfloat16)
+{
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// A thread's COLS columns of one row, in the storage type; zero past the slice.
+// ALIGNED: 16-byte vectors gt, gt + gsize, ...; else elements gt, gt + gsize, ...
+// The arithmetic goes over pairs (packed fp32): the kernels are close to the
+// issue rate.
+template <typename T, bool ALIGNED, int COLS>
+struct Cols {
+    static constexpr int VEC = ALIGNED ? 16 / (int)sizeof(T) : 1;
+    static constexpr int NVEC = COLS / VEC;
+    static constexpr int PAIRS = COLS / 2;
+    uint4 v[ALIGNED ? NVEC : 1];
+    T e[ALIGNED ? 1 : COLS];
+
+    template <int NT>
+    __device__ __forceinline__ void load(const Ring<T, ALIGNED, NT> &ring, int i, int row, int gt, int gsize)
+    {
+        const T *p = stage_row(ring, i, row);
+        const int n = ring.width / VEC;
+#pragma unroll
+        for (int k = 0; k < NVEC; ++k) {
+            const int c = gt + k * gsize;
+            if constexpr (ALIGNED) v[k] = c < n ? reinterpret_cast<const uint4 *>(p)[c] : make_uint4(0, 0, 0, 0);
+            else if (c < n) e[k] = p[c];
+            else narrow(e[k], 0.0f);
+        }
+    }
+    // values 2p and 2p + 1
+    __device__ __forceinline__ float2 get(int p) const
+    {
+        if constexpr (!ALIGNED) {
+            return make_float2(widen(e[2 * p]), widen(e[2 * p + 1]));
+        } else {
+            constexpr int PER = VEC / 2;   // pairs per vector
+            const uint4 &u = v[p / PER];
+            if constexpr (sizeof(T) == 4)
+                return p % PER ? make_float2(__uint_as_float(u.z), __uint_as_float(u.w))
+                               : make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+            else
+                return widen2(p % PER == 0 ? u.x : p % PER == 1 ? u.y : p % PER == 2 ? u.z : u.w, T());
+        }
+    }
+    // column of value j within the slice
+    __device__ __forceinline__ static int col(int j, int gt, int gsize) { return (gt + j / VEC * gsize) * VEC + j % VEC; }
+
+    // whether value j lies in the slice (a vector does as a whole or not at all)
+    __device__ __forceinline__ static bool inside(int j, int gt, int gsize, int width)
+    {
+        return gt + j / VEC * gsize < width / VEC;
+    }
+
+    __device__ __forceinline__ static void store(T *dst, int width, int gt, int gsize, const float2 (&f)[PAIRS])
+    {
+        if constexpr (ALIGNED) {
+            const int n = width / VEC;
+#pragma unroll
+            for (int k = 0; k < NVEC; ++k) {
+                const int c = gt + k * gsize;
+                float w[VEC];
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) {
+                    w[2 * j] = f[k * (VEC / 2) + j].x;
+                    w[2 * j + 1] = f[k * (VEC / 2) + j].y;
+                }
+                if (c < n) st_stream(dst + c * VEC, repack<T>(w));
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p) {
+                const int c = gt + 2 * p * gsize;
+                if (c < width) narrow(dst[c], f[p].x);
+                if (c + gsize < width) narrow(dst[c + gsize], f[p].y);
+            }
+        }
+    }
 };
 
-template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ void hold_cols(const Ring<T, ALIGNED, NT> &ring, int i, int it, int gt, int gsize,
-                                          const Edge &edge, Held<T, ALIGNED> &h)
+// Barrier of one row group (a warp needs none).  NAMED: several groups of more
+// than a warp share the CTA.  A kernel with named barriers takes all 16 of
+// them, which limits the CTAs of an SM (1024-column rows in CTAs of one group:
+// 59 us instead of 34), so one-group CTAs use the CTA's own.
+template <bool NAMED>
+__device__ __forceinline__ void group_sync(int gsize)
 {
-    if constexpr (ALIGNED) {
-        constexpr int VEC = 16 / (int)sizeof(T);
-        const unsigned char *src = ring.mem + ((it % ring.stages) * NT + i) * ring.tensor_bytes;
-#pragma unroll
-        for (int k = 0; k < kCols / VEC; ++k) {
-            const int v = gt + k * gsize;
-            h.raw[k] = v < ring.width / VEC ? reinterpret_cast<const uint4 *>(src)[v] : make_uint4(0, 0, 0, 0);
-        }
+    if constexpr (NAMED) {
+        __syncwarp();
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / gsize), "r"(gsize) : "memory");
     } else {
-        float f[kCols];
-        load_cols(ring, i, it, gt, gsize, edge, f);
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) narrow(h.one[k], f[k]);   // exact: the value came from T
+        cta_sync();
     }
 }
 
-// f += the held columns.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void add_held(const Held<T, ALIGNED> &h, float (&f)[kCols])
+__device__ __forceinline__ float warp_sum(float a)
 {
-    if constexpr (ALIGNED) {
-        constexpr int VEC = 16 / (int)sizeof(T);
 #pragma unroll
-        for (int k = 0; k < kCols / VEC; ++k) {
-            float v[VEC];
-            unpack<T>(h.raw[k], v);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) f[k * VEC + j] += v[j];
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) f[k] += widen(h.one[k]);
-    }
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
 }
 
-// Column of the thread's j-th value within its slice.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ int col_of(int j, int gt, int gsize)
+// Sums over the row group, in every thread of it.  `red` (one entry per warp of
+// the CTA) is a buffer no thread of the group may still be reading: callers
+// alternate two of them, and between a read and the next write of one lies the
+// other one's barrier.
+template <bool NAMED>
+__device__ __forceinline__ float2 group_sum2(float a, float b, int gsize, float2 *red)
 {
-    constexpr int VEC = 16 / (int)sizeof(T);
-    return ALIGNED ? (gt + j / VEC * gsize) * VEC + j % VEC : gt + j * gsize;
-}
-
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store_cols(T *dst, int width, int gt, int gsize, const float (&f)[kCols])
-{
-    constexpr int VEC = 16 / (int)sizeof(T);
-    if constexpr (ALIGNED) {
-#pragma unroll
-        for (int k = 0; k < kCols / VEC; ++k) {
-            const int v = gt + k * gsize;
-            if (v * VEC < width) st_stream(dst + v * VEC, repack<T>(f + k * VEC));
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const int c = gt + k * gsize;
-            if (c < width) narrow(dst[c], f[k]);
-        }
-    }
-}
-
-// Sums of two values over the row group, in every thread of it.  `red` is a
-// buffer no thread may still be reading: callers alternate two of them, and
-// between a read and the next write of one lies the other one's barrier.
-__device__ __forceinline__ float2 group_sum(float a, float b, int gsize, float2 *red)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+    a = warp_sum(a);
+    b = warp_sum(b);
     if (gsize == 32) return make_float2(a, b);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
-    cta_sync();
-    const int lane = threadIdx.x & 31;
-    float2 t = lane < (gsize >> 5) ? red[lane] : make_float2(0.0f, 0.0f);
+    const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
+    if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
+    group_sync<NAMED>(gsize);
+    // the warps' pairs (at most 16), each half-warp adding all of them
+    const int lane = threadIdx.x & 15;
+    float2 t = lane < nw ? red[w0 + lane] : make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
         t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
         t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
     }
-    return make_float2(__shfl_sync(0xffffffffu, t.x, 0), __shfl_sync(0xffffffffu, t.y, 0));
+    return t;
+}
+
+template <bool NAMED>
+__device__ __forceinline__ float group_sum(float a, int gsize, float2 *red)
+{
+    a = warp_sum(a);
+    if (gsize == 32) return a;
+    const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
+    if ((threadIdx.x & 31) == 0) red[warp].x = a;
+    group_sync<NAMED>(gsize);
+    const int lane = threadIdx.x & 15;
+    float t = lane < nw ? red[w0 + lane].x : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return t;
 }
 
 // Exchange of one pair per CTA and row over a cluster: every CTA pushes its
@@ -359,7 +426,7 @@ __device__ __forceinline__ uint32_t cluster_nctarank()
 // initialised and the first rows on their way.
 template <typename T, bool ALIGNED, bool CLUSTER, int NT>
 __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, unsigned char *smem, const Sources &src,
-                                                           int hidden, int64_t rows, int64_t unit, int64_t units, int c0,
+                                                           int hidden, int rows, int unit, int units, int c0,
                                                            uint32_t *err, uint64_t wait_ns, uint64_t *xbar)
 {
     const int gid = threadIdx.x / g.group, ngroups = g.threads / g.group;
@@ -370,21 +437,22 @@ __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, un
                            g.tensor_bytes,
                            c0,
                            min(hidden - c0, g.slice),
-                           unit * ngroups + gid,
+                           unit + gid * units,
                            units * ngroups,
                            rows,
                            wait_ns,
                            err,
                            false,
                            0,
-                           0};
+                           0u,
+                           0u};
     const bool issuer = threadIdx.x % g.group == 0;
     if (issuer) {
         for (int s = 0; s < g.stages; ++s) ptx::mbar_init(&r.full[s], 1);
         if (CLUSTER)
             for (int p = 0; p < 2; ++p) ptx::mbar_init(&xbar[p], 1);
         ptx::mbar_init_fence();
-        for (int s = 0; s < g.stages; ++s) r.issue(s);
+        for (int s = 0; s < g.stages; ++s) r.issue(s, r.first + (int64_t)s * r.step);
     }
     if constexpr (CLUSTER) ptx::cluster_sync();   // every CTA's exchange barriers exist before the first push
     else cta_sync();
@@ -393,38 +461,51 @@ __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, un
 
 // ---------------------------------------------------------------- host side
 
-// `ctas` of `threads` threads and 128 registers each share an SM's registers
-// and its 227 KB of shared memory.
-inline Geometry geometry(int64_t hidden, int size, bool aligned, int tensors)
+// Rows of `hidden` columns, `tensors` of them streaming in, in a kernel whose
+// threads take `cols` columns and of which an SM holds `sm_threads` threads.
+// MERGED: all the row groups of an SM in one CTA (whose column sums then leave
+// the SM once).
+inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int tensors, int sm_threads, bool merged,
+                         int64_t rows)
 {
     Geometry g;
     const int vec = aligned ? 16 / size : 1;
-    int csize = (int)((hidden + kSlice - 1) / kSlice);
-    int64_t slice = ((hidden + csize - 1) / csize + vec - 1) / vec * vec;
-    csize = (int)((hidden + slice - 1) / slice);   // no CTA without columns
-    g.csize = csize;
+    const int csize = (int)((hidden + kSlice - 1) / kSlice);
+    const int64_t slice = ((hidden + csize - 1) / csize + vec - 1) / vec * vec;
+    g.csize = (int)((hidden + slice - 1) / slice);   // no CTA without columns
     g.slice = (int)slice;
-    if (hidden <= kWarpCols) {
-        g.group = 32;
-        g.threads = kWarpRowThreads;
-    } else {
-        const int64_t per = (slice + kCols - 1) / kCols;
-        int t = 64;
-        while (t < per) t *= 2;
-        g.group = g.threads = t;
-    }
-    g.tensors = tensors;
+    // element-wise groups are constants of the kernels: 32, or multiples of 64
+    const int step = aligned || slice <= 32 * cols ? 32 : 64;
+    g.group = (int)(((slice + cols - 1) / cols + step - 1) / step * step);
+    if (!aligned && cols > 8) g.group = kMaxGroup;
     g.tensor_bytes = (int)((slice * size + 15) / 16 * 16) + (aligned ? 0 : 32);
-    const int groups = g.threads / g.group;
-    const int per_sm = kMaxThreads / g.threads;
-    const int budget = 224 * 1024 / per_sm - 2048;
-    int stages = budget / (groups * tensors * g.tensor_bytes + groups * 8);
+    const int ring = tensors * g.tensor_bytes + 8;
+    // row groups per SM: as many as the registers hold, fewer where shared
+    // memory has no room for two stages of each
+    const int sm_bytes = 226 * 1024;
+    const bool one_cta = merged && g.csize == 1;
+    auto room = [&](int n) {   // of one of n groups, past a CTA's own 2 KB (static memory, and what the system keeps)
+        return one_cta ? (sm_bytes - 2048) / n : sm_bytes / n - 2048;
+    };
+    int groups = sm_threads / g.group;
+    if (groups < 1) groups = 1;
+    if (g.group > 32 && merged && groups > 15) groups = 15;   // named barriers
+    while (groups > 1 && room(groups) < 2 * ring) --groups;
+    const int64_t sms = sm_count();
+    if (one_cta) {
+        const int64_t need = (rows + sms - 1) / sms;
+        if (groups > need) groups = need < 1 ? 1 : (int)need;
+    }
+    int stages = room(groups) / ring;
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages < 1) stages = 1;
     g.stages = stages;
-    g.bar_off = groups * stages * tensors * g.tensor_bytes;
-    g.smem = g.bar_off + groups * stages * 8;
-    if (g.group == 32 && g.smem < 2 * kWarpCols * 4) g.smem = 2 * kWarpCols * 4;   // the backward pass adds its warps' sums there
+    const int in_cta = g.group == 32 && !merged ? (groups < 8 ? groups : 8) : one_cta ? groups : 1;
+    g.threads = in_cta * g.group;
+    g.per_sm = groups / in_cta;
+    g.bar_off = in_cta * stages * tensors * g.tensor_bytes;
+    g.smem = g.bar_off + in_cta * stages * 8;
+    if (merged && g.smem < 8 * g.slice) g.smem = 8 * g.slice;   // the groups' column sums are added there
     return g;
 }
 
@@ -432,9 +513,9 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int tensors)
 // at most one row group per row.
 inline int64_t launch_units(const Geometry &g, int64_t rows)
 {
-    const int groups = g.threads / g.group;
-    int64_t units = (int64_t)sm_count() * (kMaxThreads / g.threads) / g.csize;
-    const int64_t need = (rows + groups - 1) / groups;
+    const int in_cta = g.threads / g.group;
+    int64_t units = (int64_t)sm_count() * g.per_sm / g.csize;
+    const int64_t need = (rows + in_cta - 1) / in_cta;
     if (units > need) units = need;
     return units < 1 ? 1 : units;
 }
