@@ -111,6 +111,53 @@ __device__ __forceinline__ float act_slope(int act, float z)
     return 1.0f;
 }
 
+// The same on pairs (packed fp32), with the activation a constant.
+__device__ __forceinline__ float2 dup2(float a) { return make_float2(a, a); }
+
+__device__ __forceinline__ float2 normal_tail2(float2 t)
+{
+    const float2 v = ffma2(t, dup2(1.0f / (TF_GELU_TMAX * 0.5f)), dup2(-1.0f));
+    float2 acc = ffma2(dup2(TF_GELU_C7), v, dup2(TF_GELU_C6));
+    acc = ffma2(acc, v, dup2(TF_GELU_C5));
+    acc = ffma2(acc, v, dup2(TF_GELU_C4));
+    acc = ffma2(acc, v, dup2(TF_GELU_C3));
+    acc = ffma2(acc, v, dup2(TF_GELU_C2));
+    acc = ffma2(acc, v, dup2(TF_GELU_C1));
+    acc = ffma2(acc, v, dup2(TF_GELU_C0));
+    return make_float2(ex2_approx(acc.x), ex2_approx(acc.y));
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_value2(float2 z)
+{
+    if constexpr (ACT == TF_ACT_SILU) {
+        const float2 v = make_float2(max_nan(z.x, -100.0f), max_nan(z.y, -100.0f));
+        return silu_f32x2(v);
+    } else if constexpr (ACT == TF_ACT_GELU) {
+        const float2 t = make_float2(min_nan(fabsf(z.x), TF_GELU_TCLAMP), min_nan(fabsf(z.y), TF_GELU_TCLAMP));
+        const float2 r = make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
+        return ffma2(make_float2(-t.x, -t.y), normal_tail2(t), r);
+    } else {
+        return z;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float2 act_slope2(float2 z)
+{
+    if constexpr (ACT == TF_ACT_SILU) {
+        return make_float2(act_slope(TF_ACT_SILU, z.x), act_slope(TF_ACT_SILU, z.y));
+    } else if constexpr (ACT == TF_ACT_GELU) {
+        const float2 t = make_float2(min_nan(fabsf(z.x), TF_GELU_TCLAMP), min_nan(fabsf(z.y), TF_GELU_TCLAMP));
+        const float2 u = fmul2(fmul2(t, t), dup2(-0.5f * kLog2e));
+        const float2 phi = make_float2(-0.3989422804f * ex2_approx(u.x), -0.3989422804f * ex2_approx(u.y));
+        const float2 h = ffma2(t, phi, normal_tail2(t));
+        return make_float2(z.x >= 0.0f ? 1.0f - h.x : h.x, z.y >= 0.0f ? 1.0f - h.y : h.y);
+    } else {
+        return dup2(1.0f);
+    }
+}
+
 // ---------------------------------------------------------------- tile schedule
 
 // The groups' rows and the running count of their tiles, in shared memory.

@@ -113,29 +113,63 @@ __global__ void __launch_bounds__(kThreads) grouped_simple_kernel(const GroupedA
     }
 }
 
-// dbias[e][n] = sum of dy[m][n] over group e's rows.  A CTA takes 32 columns
-// of one group, 8 rows at a time, then adds its 8 partial sums in order.
-template <typename T>
+// dbias[e][n] = sum of dy[m][n] over group e's rows.  A CTA takes 64 columns of
+// one group: VEC columns per thread (8: 16-byte loads), 64/VEC threads side by
+// side, the others on rows of their own, four loads each in flight; the CTA's
+// partial sums are added in order.  Bound by HBM: dy once.
+template <typename T, int VEC>
 __global__ void __launch_bounds__(256) grouped_bias_grad_kernel(const GroupedArgs a, uint32_t *err)
 {
     pdl_begin();
-    __shared__ Schedule sch;
-    __shared__ float red[8][33];
-    make_schedule(sch, a.offsets, a.groups, a.rows, 1, 1, err);
-    if (sch.bad) return;
-    const int e = blockIdx.y, lane = threadIdx.x & 31, q = threadIdx.x >> 5;
-    const int n = blockIdx.x * 32 + lane;
-    const T *dy = reinterpret_cast<const T *>(a.dy);
-    float sum = 0.0f;
-    if (n < a.N)
-        for (int m = sch.row[e] + q; m < sch.row[e + 1]; m += 8) sum += Half2Of<T>::widen(dy[m * a.dy_stride + n]);
-    red[q][lane] = sum;
+    constexpr int ACROSS = 64 / VEC, DOWN = 256 / ACROSS;
+    __shared__ float red[DOWN][65];
+    __shared__ int bad;
+    if (threadIdx.x == 0) bad = 0;
     cta_sync();
-    if (q == 0 && n < a.N) {
-        float t = 0.0f;
+    for (int i = threadIdx.x; i <= a.groups; i += blockDim.x) {
+        const int v = a.offsets[i];
+        if (v < 0 || v > a.rows || (i > 0 && a.offsets[i - 1] > v)) bad = 1;
+    }
+    cta_sync();
+    if (bad) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(err, TF_DEVERR_OFFSETS);
+        return;
+    }
+    const int e = blockIdx.y, q = threadIdx.x / ACROSS, c = (int)threadIdx.x % ACROSS * VEC, n = blockIdx.x * 64 + c;
+    const int lo = a.offsets[e], hi = a.offsets[e + 1];
+    const T *dy = reinterpret_cast<const T *>(a.dy) + n;
+    float sum[VEC] = {};
+    if (n < a.N)   // (N is a multiple of VEC)
+        for (int m = lo + q; m < hi; m += 4 * DOWN) {
+            if constexpr (VEC == 8) {
+                uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][lane];
-        float *dst = a.dbias + (int64_t)e * a.N + n;
+                for (int i = 0; i < 4; ++i)
+                    v[i] = m + i * DOWN < hi ? __ldg(reinterpret_cast<const uint4 *>(dy + (int64_t)(m + i * DOWN) * a.dy_stride))
+                                             : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = Half2Of<T>::unpack(w[j]);
+                        sum[2 * j] += f.x;
+                        sum[2 * j + 1] += f.y;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (m + i * DOWN < hi) sum[0] += Half2Of<T>::widen(dy[(int64_t)(m + i * DOWN) * a.dy_stride]);
+            }
+        }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) red[q][c + j] = sum[j];
+    cta_sync();
+    if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < (unsigned)a.N) {
+        float t = 0.0f;
+        for (int i = 0; i < DOWN; ++i) t += red[i][threadIdx.x];
+        float *dst = a.dbias + (int64_t)e * a.N + blockIdx.x * 64 + threadIdx.x;
         *dst = a.accumulate ? *dst + t : t;
     }
 }
@@ -168,9 +202,12 @@ cudaError_t launch_grouped_bias_grad(const GroupedArgs &a, cudaStream_t st)
 {
     uint32_t *err = device_error_word();
     if (!err) return cudaErrorInitializationError;
-    const dim3 grid((unsigned)((a.N + 31) / 32), (unsigned)a.groups);
-    return a.dtype == TF_BF16 ? launch_pdl(grouped_bias_grad_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a, err)
-                              : launch_pdl(grouped_bias_grad_kernel<__half>, grid, dim3(256), 0, st, a, err);
+    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)a.groups);
+    const bool vec = a.N % 8 == 0 && a.dy_stride % 8 == 0 && (reinterpret_cast<uintptr_t>(a.dy) & 15u) == 0;
+    auto launch = [&](auto kern) { return launch_pdl(kern, grid, dim3(256), 0, st, a, err); };
+    if (a.dtype == TF_BF16)
+        return vec ? launch(grouped_bias_grad_kernel<__nv_bfloat16, 8>) : launch(grouped_bias_grad_kernel<__nv_bfloat16, 1>);
+    return vec ? launch(grouped_bias_grad_kernel<__half, 8>) : launch(grouped_bias_grad_kernel<__half, 1>);
 }
 
 }  // namespace tf

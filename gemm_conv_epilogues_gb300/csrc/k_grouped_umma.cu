@@ -25,6 +25,7 @@
 #include <string.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "grouped.cuh"
 #include "ptx_sm100.cuh"
@@ -44,16 +45,22 @@ constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kABytes = BM * BK * 2;
 constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or N-major operand
-constexpr int kDwBoxBytes = 32 * 32 * 4;          // WGRAD epilogue box per warp
-constexpr int kNumBars = 3 * kMaxStages + 5;      // full, empty, land; accumulators full x2, empty x2; drain
+constexpr int kBoxBytes = 32 * 32 * 2;            // epilogue box: 32 rows (tokens) x 32 weights rows, 16-bit
+constexpr int kEpiBytes = 2 * kBoxBytes;          // per warp two of them, or WGRAD's one of 32 x 32 fp32
+constexpr int kNumBars = 3 * kMaxStages + 5 + 2 * kEpiWarps;   // full, empty, land; accumulators full x2, empty x2;
+                                                               // drain; DGRAD: each epilogue warp's boxes
+// WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
+// round, so an accumulator's error grows with the number of MMAs it takes; a
+// longer group is cut into parts whose fp32 sums are added in memory.  Measured
+// on 16384 rows in 16 groups (up to 2300 rows each): relative error 1.4e-6 in
+// one part, against 2.9e-7 for fp32 products.
+constexpr int kMaxPartRows = 1024;
 constexpr uint32_t kTmemCols = 512;
 
 struct UmmaArgs {
     const int *offsets;
     const float *bias;
-    void *y;
-    const void *pre_in;
-    void *pre_out;
+    void *y, *pre;
     uint32_t *err;
     uint64_t wait_ns;
     int64_t y_stride, pre_stride;
@@ -61,9 +68,9 @@ struct UmmaArgs {
     int M;             // extent of the weights' side (N, or K for DGRAD)
     int red;           // reduction length of FORWARD and DGRAD
     int cols;          // WGRAD: K, the N side
-    int bn;            // widest row tile
+    int bn;            // widest row tile the shared memory holds
     int box_rows;      // rows per token box
-    int stages, stage_bytes, off_dw, off_bar, off_sched;
+    int stages, stage_bytes, off_epi, off_bar, off_sched;
     int act, bf16, accumulate;
 };
 
@@ -103,19 +110,66 @@ __device__ __forceinline__ void tma_add_3d(const void *map, const void *src, int
                  : "memory");
 }
 
+__device__ __forceinline__ void tma_store_2d(const void *map, const void *src, int c0, int c1)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0),
+                 "r"(c1), "r"(ptx::smem_u32(src))
+                 : "memory");
+}
+
+// 16 TMEM lanes x 32 columns as 8 x 8 blocks: lane l of the warp receives, for
+// column block b, row l/4 (registers 4b, 4b+1) and row l/4 + 8 (4b+2, 4b+3),
+// columns 8b + 2(l%4) and the next.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Four 8 x 8 blocks between registers and shared memory, transposed on the way:
+// a lane's two values of a block are neighbours along a column of the block in
+// memory.  Lane l gives the address of row l%8 of block l/8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // One work item.  FORWARD, DGRAD: weights rows [m0, +128*CG), tokens [t0, +tv),
-// MMA N = w.  WGRAD: dw rows [m0, +128*CG), columns [t0, +w) of group e, rows
-// `first` on; tv is the group's number of rows.
+// MMA N = w.  WGRAD: dw rows [m0, +128*CG), columns [t0, +w) of group e from its
+// rows [first, +tv) -- all of the group's, or the part-th of `parts`.
 struct Item {
-    int e, m0, t0, w, tv, first, nkb;
+    int e, m0, t0, w, tv, first, nkb, part, parts;
+};
+
+// The schedule in shared memory: rows of every group, and the running count of
+// tiles (WGRAD's are the same number for every group).
+struct Plan {
+    const int *row, *tile;
+    int bn;
 };
 
 template <int MODE, int CG>
-__device__ __forceinline__ Item item_of(const UmmaArgs &p, const int *row, const int *tile, int t)
+__device__ __forceinline__ Item item_of(const UmmaArgs &p, const Plan &s, int t)
 {
     constexpr int STEP = 16 * CG;
     Item it;
     const int mt = (p.M + BM * CG - 1) / (BM * CG);
+    it.part = 0;
+    it.parts = 1;
     if (MODE == GROUPED_WGRAD) {
         const int ct = (p.cols + kMaxBN - 1) / kMaxBN;
         it.e = t / (mt * ct);
@@ -124,22 +178,22 @@ __device__ __forceinline__ Item item_of(const UmmaArgs &p, const int *row, const
         it.t0 = r % ct * kMaxBN;
         const int left = min(kMaxBN, p.cols - it.t0);
         it.w = (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
-        it.first = row[it.e];
-        it.tv = row[it.e + 1] - it.first;
-        it.nkb = (it.tv + BK - 1) / BK;
+        it.first = s.row[it.e];
+        it.tv = s.row[it.e + 1] - it.first;
+        it.parts = max(1, (it.tv + kMaxPartRows - 1) / kMaxPartRows);
     } else {
         int lo = 0, hi = p.groups - 1;   // the last group that starts at or before tile t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tile[mid] <= t) lo = mid; else hi = mid - 1;
+            if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
         }
         it.e = lo;
-        const int r = t - tile[lo], T = row[lo + 1] - row[lo];
-        const int ntt = (T + p.bn - 1) / p.bn;
+        const int r = t - s.tile[lo], T = s.row[lo + 1] - s.row[lo];
+        const int ntt = (T + s.bn - 1) / s.bn;
         const int wt = ((T + ntt - 1) / ntt + STEP - 1) / STEP * STEP;   // equal widths, at most bn
         const int tt = r % ntt;
         it.m0 = r / ntt * (BM * CG);
-        it.first = row[lo];
+        it.first = s.row[lo];
         it.t0 = it.first + tt * wt;
         it.tv = min(wt, T - tt * wt);
         it.w = (it.tv + STEP - 1) / STEP * STEP;
@@ -148,44 +202,125 @@ __device__ __forceinline__ Item item_of(const UmmaArgs &p, const int *row, const
     return it;
 }
 
-// y (and pre) of one 32 x 32 chunk: lane = weights row n, r[j] = token j of `count`.
-template <typename T, int MODE>
-__device__ __forceinline__ void store_chunk(const UmmaArgs &p, const uint32_t (&r)[32], int count, int64_t token, int n,
-                                            bool in, float bias)
+// WGRAD: narrows an item to its part's rows; parts are whole K steps but for the last.
+__device__ __forceinline__ Item part_of(Item it, int part)
 {
-    if (!in) return;
-    T *y = reinterpret_cast<T *>(p.y) + token * p.y_stride + n;
-    if (MODE == GROUPED_FORWARD) {
-        T *z = p.pre_out ? reinterpret_cast<T *>(p.pre_out) + token * p.pre_stride + n : nullptr;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j >= count) break;
-            const float v = __uint_as_float(r[j]) + bias;
-            if (z) z[j * p.pre_stride] = Half2Of<T>::round(v);
-            y[j * p.y_stride] = Half2Of<T>::round(act_value(p.act, v));
+    const int T = it.tv, len = ((T + it.parts - 1) / it.parts + BK - 1) / BK * BK;
+    it.part = part;
+    it.first += part * len;
+    it.tv = min(len, T - part * len);
+    it.nkb = (it.tv + BK - 1) / BK;
+    return it;
+}
+
+// Calls f(item) for every (part of an) item of this CTA or pair, in order,
+// until it returns false.
+template <int MODE, int CG, typename F>
+__device__ __forceinline__ void each_item(const UmmaArgs &p, const Plan &s, int num_work, int cid, int ncl, F f)
+{
+    for (int t = cid; t < num_work; t += ncl) {
+        const Item it = item_of<MODE, CG>(p, s, t);
+        if constexpr (MODE == GROUPED_WGRAD) {
+            for (int part = 0; part < it.parts; ++part)
+                if (!f(part_of(it, part))) return;
+        } else {
+            if (!f(it)) return;
         }
+    }
+}
+
+// An epilogue warp's store of the box [32 tokens][32 weights rows] (64-byte rows,
+// 64-byte swizzle) to y or pre: one TMA store, or, where fewer than 32 tokens
+// are the group's, 16-byte stores of those rows.
+__device__ __forceinline__ void store_box(const CUtensorMap *map, void *dst, int64_t stride, const uint8_t *box, int n0,
+                                          int M, int token, int count)
+{
+    const int lane = threadIdx.x & 31;
+    if (count == 32) {
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_2d(map, box, n0, token);   // clipped at M
     } else {
-        const T *z = reinterpret_cast<const T *>(p.pre_in) + token * p.pre_stride + n;
-        T zv[32];
-        if (p.act != TF_ACT_NONE) {
+        __syncwarp();
+        const int piece = lane & 3, n = n0 + 8 * piece;
+        uint16_t *out = reinterpret_cast<uint16_t *>(dst) + token * stride + n;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (j < count) zv[j] = z[j * p.pre_stride];
+        for (int i = 0; i < 4; ++i) {
+            const int r = (lane >> 2) + 8 * i;
+            if (r < count && n < M)
+                *reinterpret_cast<uint4 *>(out + r * stride) =
+                    *reinterpret_cast<const uint4 *>(box + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16));
+        }
+    }
+    if (lane == 0) ptx::bulk_commit_group();   // (an empty group where nothing was issued)
+    __syncwarp();
+}
+
+// One 32 x 32 chunk of the accumulator, from the fragments of tmem_ld_16x256b_x4
+// (r[0..15] weights rows 0..15, r[16..31] rows 16..31): bias and activation
+// (FORWARD), or the slope at pre (DGRAD, read from the box that dx replaces).
+// seq counts the warp's boxes: two take turns.
+template <typename T, int MODE, int ACT>
+__device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const CUtensorMap *map_y, const CUtensorMap *map_pre,
+                                             const uint32_t (&r)[32], const float (&bias)[4], uint8_t *boxes, int &seq,
+                                             int n0, int token, int count)
+{
+    const int lane = threadIdx.x & 31;
+    // this lane's row of each of four blocks that lie side by side along n, tokens 8b + lane%8
+    const uint32_t sw = (uint32_t)(((lane >> 3) ^ ((lane >> 1) & 3)) * 16);   // token 8b + r: (token >> 1) & 3 = (r >> 1) & 3
+    const uint32_t off = (uint32_t)((lane & 7) * 64) + sw;
+    if constexpr (MODE == GROUPED_FORWARD) {
+        auto emit = [&](auto value, const CUtensorMap *map, void *dst, int64_t stride) {
+            uint8_t *box = boxes + (seq & 1) * kBoxBytes;
+            ++seq;
+            if (lane == 0) ptx::bulk_wait_group_read<1>();   // the store before the last has read this box
+            __syncwarp();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = (j >> 1) * 16 + 4 * b + 2 * (j & 1);
+                    const float2 v = value(fadd2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), dup2(bias[j])));
+                    w[j] = Half2Of<T>::pack(v.x, v.y);
+                }
+                stmatrix_x4_trans(ptx::smem_u32(box) + off + b * 512, w[0], w[1], w[2], w[3]);
+            }
+            store_box(map, dst, stride, box, n0, p.M, token, count);
+        };
+        if (p.pre) emit([](float2 z) { return z; }, map_pre, p.pre, p.pre_stride);
+        emit([](float2 z) { return act_value2<ACT>(z); }, map_y, p.y, p.y_stride);
+    } else {
+        uint8_t *box = boxes + (seq & 1) * kBoxBytes;
+        ++seq;
+        if (ACT == TF_ACT_NONE) {
+            if (lane == 0) ptx::bulk_wait_group_read<1>();
+            __syncwarp();
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (j >= count) break;
-            float v = __uint_as_float(r[j]);
-            if (p.act != TF_ACT_NONE) v *= act_slope(p.act, Half2Of<T>::widen(zv[j]));
-            y[j * p.y_stride] = Half2Of<T>::round(v);
+        for (int b = 0; b < 4; ++b) {
+            const uint32_t addr = ptx::smem_u32(box) + off + b * 512;
+            uint32_t z[4], w[4];
+            if (ACT != TF_ACT_NONE) ldmatrix_x4_trans(addr, z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = (j >> 1) * 16 + 4 * b + 2 * (j & 1);
+                float2 v = make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                if (ACT != TF_ACT_NONE) v = fmul2(v, act_slope2<ACT>(Half2Of<T>::unpack(z[j])));
+                w[j] = Half2Of<T>::pack(v.x, v.y);
+            }
+            __syncwarp();   // (a block's four rows are read before they are replaced)
+            stmatrix_x4_trans(addr, w[0], w[1], w[2], w[3]);
         }
+        store_box(map_y, p.y, p.y_stride, box, n0, p.M, token, count);
     }
 }
 
 template <int MODE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                        const __grid_constant__ CUtensorMap tmap_dw, const UmmaArgs p)
+                        const __grid_constant__ CUtensorMap tmap_out, const __grid_constant__ CUtensorMap tmap_pre,
+                        const __grid_constant__ UmmaArgs p)
 {
     constexpr bool PAIR = CG == 2;
     constexpr bool WG = MODE == GROUPED_WGRAD;
@@ -197,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tfull = land + kMaxStages;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *loaded = drain + 1;           // DGRAD: each epilogue warp's two boxes of pre
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(loaded + 2 * kEpiWarps);
     int *row = reinterpret_cast<int *>(smem + p.off_sched);      // [groups + 1]
     int *tile = row + p.groups + 1;                              // [groups + 1]
     int *bad = tile + p.groups + 1;
@@ -220,10 +356,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&tempty[i], CG * kEpiWarps);   // one lane per epilogue warp of either CTA
         }
         ptx::mbar_init(drain, 1);
+        if (MODE == GROUPED_DGRAD)
+            for (int i = 0; i < 2 * kEpiWarps; ++i) ptx::mbar_init(&loaded[i], 1);
         ptx::mbar_init_fence();
         ptx::prefetch_tensormap(&tmap_a);
         ptx::prefetch_tensormap(&tmap_b);
-        if (WG) ptx::prefetch_tensormap(&tmap_dw);
+        ptx::prefetch_tensormap(&tmap_out);
         *bad = 0;
     }
     if (warp == 1) {
@@ -242,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
 
     // ---- the schedule: rows of every group and the running count of tiles
+    Plan plan = {row, tile, p.bn};
+    const int mt = (p.M + BM * CG - 1) / (BM * CG);
     {
         int wrong = 0;
         for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
@@ -252,13 +392,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (wrong) *bad = 1;
         cta_sync();
         if (warp == 0 && !WG) {
-            const int mt = (p.M + BM * CG - 1) / (BM * CG);
+            // The widest row tile is chosen for the last wave: each candidate's cost is the number
+            // of tiles the busiest CTA (pair) takes times their mean width, plus a constant for a
+            // tile's overhead.  (Few groups leave 256 as it is; 1152 tiles over 76 pairs leave the
+            // 16th wave 5% full, 1280 of 7/8 the width fill 17.)
+            if (p.bn == kMaxBN && !*bad) {
+                int best = 0x7fffffff, pick = p.bn;
+                for (int bn = kMaxBN; bn >= 128; bn -= 32) {
+                    int tiles = 0, width = 0;
+                    for (int e = lane; e < p.groups; e += 32) {
+                        const int T = row[e + 1] - row[e], n = (T + bn - 1) / bn;
+                        tiles += n;
+                        width += (T + 16 * CG * n - 1) / (16 * CG) * (16 * CG);
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+                        width += __shfl_xor_sync(0xffffffffu, width, o);
+                    }
+                    if (tiles == 0) break;
+                    const int cost = (tiles * mt + ncl - 1) / ncl * (width / tiles + 24);
+                    if (cost < best) {
+                        best = cost;
+                        pick = bn;
+                    }
+                }
+                plan.bn = pick;
+            }
             int before = 0;
             for (int base = 0; base < p.groups; base += 32) {
                 const int e = base + lane;
-                int sum = 0, n = 0;
-                if (e < p.groups && !*bad) n = (row[e + 1] - row[e] + p.bn - 1) / p.bn * mt;
-                sum = n;
+                int n = 0;
+                if (e < p.groups && !*bad) n = (row[e + 1] - row[e] + plan.bn - 1) / plan.bn * mt;
+                int sum = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int up = __shfl_up_sync(0xffffffffu, sum, o);
@@ -267,12 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (e < p.groups) tile[e] = before + sum - n;
                 before += __shfl_sync(0xffffffffu, sum, 31);
             }
-            if (lane == 0) tile[p.groups] = before;
+            if (lane == 0) {
+                tile[p.groups] = before;
+                bad[1] = plan.bn;
+            }
         }
         cta_sync();
+        if (!WG) plan.bn = bad[1];
     }
-    int num_work = WG ? p.groups * ((p.M + BM * CG - 1) / (BM * CG)) * ((p.cols + kMaxBN - 1) / kMaxBN)
-                      : tile[p.groups];
+    int num_work = WG ? p.groups * mt * ((p.cols + kMaxBN - 1) / kMaxBN) : tile[p.groups];
     if (*bad) {
         num_work = 0;
         if (threadIdx.x == 0) atomicOr(p.err, TF_DEVERR_OFFSETS);
@@ -296,14 +465,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0, issued = 0, last_phase = 0;
             bool ok = true;
-            for (int t = cid; ok && t < num_work; t += ncl) {
-                const Item it = item_of<MODE, CG>(p, row, tile, t);
+            each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
                 const int mrow = it.m0 + crank * BM;
                 for (int kb = 0; kb < it.nkb; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) return ok = false;
                     uint8_t *a_dst = smem + stage * p.stage_bytes, *b_dst = a_dst + kABytes;
                     const int k0 = kb * BK;
                     // boxes of the N side this CTA loads: its half of the tile's rows (or columns)
@@ -357,7 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
-            }
+                return true;
+            });
             if (!ok) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
             // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
             for (int s = 0; s < p.stages; ++s)
@@ -371,22 +537,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = cid; ok && t < num_work; t += ncl) {
-                const Item it = item_of<MODE, CG>(p, row, tile, t);
-                if (it.nkb == 0) continue;
+            each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
+                if (it.nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
                 const int b = local & 1;
-                if (!ptx::mbar_wait<PAIR>(&tempty[b], (uint32_t)((local >> 1) & 1) ^ 1u, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
+                if (!ptx::mbar_wait<PAIR>(&tempty[b], (uint32_t)((local >> 1) & 1) ^ 1u, p.wait_ns)) return ok = false;
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(b * kMaxBN);
                 for (int kb = 0; kb < it.nkb; ++kb) {
-                    if (!ptx::mbar_wait<PAIR && WG>(&full[stage], phase, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+                    if (!ptx::mbar_wait<PAIR && WG>(&full[stage], phase, p.wait_ns)) return ok = false;
                     ptx::tc_fence_after();
                     const uint32_t a = ptx::smem_u32(smem + stage * p.stage_bytes), bb = a + kABytes;
                     // WGRAD: sixteens of rows past the group's end are left out
@@ -411,7 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
-                if (!ok) break;
                 if constexpr (PAIR) {
                     ptx::umma_commit_pair(ptx::mapa_shared(&tfull[b], 0));
                     ptx::umma_commit_pair(ptx::mapa_shared(&tfull[b], 1));
@@ -419,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::umma_commit(&tfull[b]);
                 }
                 ++local;
-            }
+                return true;
+            });
             if (!ok) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
             if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
             else ptx::umma_commit(drain);
@@ -433,14 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t land_phase = 0;
         int blocks = 0;    // K steps before this item
         bool ok = true;
-        for (int t = cid; t < num_work; t += ncl) {
-            const Item it = item_of<MODE, CG>(p, row, tile, t);
+        each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
             blocks += it.nkb;
-            if ((it.tv & 15) == 0) continue;
+            if ((it.tv & 15) == 0) return true;
             const int stage = (blocks - 1) % p.stages;
             ok = ptx::mbar_wait(&land[stage], (land_phase >> stage) & 1u, p.wait_ns);
             land_phase ^= 1u << stage;
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!__all_sync(0xffffffffu, ok)) return false;
             const int r0 = it.tv - (it.nkb - 1) * BK, r1 = (r0 + 15) & ~15;
             uint8_t *base = smem + stage * p.stage_bytes;
             const int nbox = 2 + it.w / CG / 64;   // A's two boxes, then B's
@@ -455,65 +613,105 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else ptx::mbar_arrive(&full[stage]);
             }
             __syncwarp();
-        }
+            return true;
+        });
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
     } else if (warp >= kFirstEpiWarp) {
         // ------------------------------------------------------------ epilogue
         // Warp w reads TMEM lanes 32*(w%4) .. +31 (one weights row per lane) and
         // every second 32-column chunk.
         const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
-        uint8_t *box = smem + p.off_dw + (warp - kFirstEpiWarp) * kDwBoxBytes;
-        int local = 0;
+        uint8_t *boxes = smem + p.off_epi + (warp - kFirstEpiWarp) * kEpiBytes;
+        uint64_t *in_bar = loaded + 2 * (warp - kFirstEpiWarp);
+        const bool slope = MODE == GROUPED_DGRAD && p.act != TF_ACT_NONE;
+        int local = 0, seq = 0;
+        uint32_t in_phase = 0, fetching = 0;
         bool ok = true;
-        for (int t = cid; t < num_work; t += ncl) {
-            const Item it = item_of<MODE, CG>(p, row, tile, t);
-            const int n0 = it.m0 + crank * BM + q * 32, n = n0 + lane;
-            const bool in = n < p.M;
+        each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
+            const int n0 = it.m0 + crank * BM + q * 32;
             const int b = local & 1;
-            float bias = 0.0f;
-            if (MODE == GROUPED_FORWARD && p.bias && in) bias = __ldg(p.bias + (int64_t)it.e * p.M + n);
+            const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
+            const bool mine = n0 < p.M;   // (boxes past the last weights row are neither loaded nor stored)
+            // DGRAD: the box of pre under chunk c, into the box that the seq-th result will take; the store
+            // that used it last (two boxes ago) has read it
+            auto fetch = [&](int c, int s) {
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                fetching |= 1u << (s & 1);
+                if (lane == 0) {
+                    ptx::bulk_wait_group_read<0>();
+                    ptx::mbar_arrive_expect_tx(&in_bar[s & 1], kBoxBytes);
+                    ptx::tma_load_2d(boxes + (s & 1) * kBoxBytes, &tmap_pre, &in_bar[s & 1], n0, it.t0 + c * 32);
+                }
+            };
+            if (slope && mine && h * 32 < width) fetch(h, seq);
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (MODE == GROUPED_FORWARD && p.bias) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int n = n0 + 8 * j + (lane >> 2);
+                    if (n < p.M) bias[j] = __ldg(p.bias + (int64_t)it.e * p.M + n);
+                }
+            }
             if (it.nkb > 0) {
                 const bool got = ptx::mbar_wait(&tfull[b], (uint32_t)(local >> 1) & 1u, p.wait_ns);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
+                if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
             } else if (!WG || p.accumulate) {
-                continue;   // a group without rows adds nothing
+                return true;   // a group without rows adds nothing
             }
             const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kMaxBN);
-            const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
 #pragma unroll 1
-            for (int c = h; c * 32 < width; c += kEpiWarps / 4) {
+            for (int c = h; c * 32 < width && mine; c += kEpiWarps / 4) {
                 uint32_t r[32];
-                if (!WG || it.nkb > 0) {
-                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), r);
-                    ptx::tmem_ld_wait();
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = 0u;
-                }
                 if constexpr (WG) {
-                    if (lane == 0) ptx::bulk_wait_group_read<0>();
+                    if (it.nkb > 0) {
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), r);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = 0u;
+                    }
+                    // the store before has read the box, and an earlier part's sums are in memory
+                    if (lane == 0) {
+                        if (it.part > 0) ptx::bulk_wait_group_all();
+                        else ptx::bulk_wait_group_read<0>();
+                    }
                     __syncwarp();
+                    ptx::tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)   // 128-byte swizzle: 16-byte piece j of row l lies at j ^ (l % 8)
-                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                        *reinterpret_cast<uint4 *>(boxes + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                             make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && n0 < p.M) {
+                    if (lane == 0) {
                         // clipped at the group's N rows and K columns
-                        if (p.accumulate) tma_add_3d(&tmap_dw, box, it.t0 + c * 32, n0, it.e);
-                        else tma_store_3d(&tmap_dw, box, it.t0 + c * 32, n0, it.e);
+                        if (p.accumulate || it.part > 0) tma_add_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
+                        else tma_store_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
                         ptx::bulk_commit_group();
                     }
                 } else {
-                    const int count = min(32, width - c * 32);
-                    const int64_t token = it.t0 + c * 32;
-                    if (p.bf16) store_chunk<__nv_bfloat16, MODE>(p, r, count, token, n, in, bias);
-                    else store_chunk<__half, MODE>(p, r, count, token, n, in, bias);
+                    tmem_ld_16x256b_x4(taddr + (uint32_t)(c * 32), r);
+                    tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32), r + 16);
+                    const int count = min(32, width - c * 32), token = it.t0 + c * 32;
+                    if (slope) {
+                        const int s = seq & 1;
+                        if (!ptx::mbar_wait(&in_bar[s], (in_phase >> s) & 1u, p.wait_ns)) ok = false;
+                        in_phase ^= 1u << s;
+                        fetching &= ~(1u << s);
+                        if ((c + kEpiWarps / 4) * 32 < width) fetch(c + kEpiWarps / 4, seq + 1);
+                    }
+                    ptx::tmem_ld_wait();
+                    auto finish = [&](auto act) {
+                        constexpr int ACT = decltype(act)::value;
+                        if (p.bf16)
+                            finish_chunk<__nv_bfloat16, MODE, ACT>(p, &tmap_out, &tmap_pre, r, bias, boxes, seq, n0, token, count);
+                        else
+                            finish_chunk<__half, MODE, ACT>(p, &tmap_out, &tmap_pre, r, bias, boxes, seq, n0, token, count);
+                    };
+                    if (p.act == TF_ACT_GELU) finish(std::integral_constant<int, TF_ACT_GELU>());
+                    else if (p.act == TF_ACT_SILU) finish(std::integral_constant<int, TF_ACT_SILU>());
+                    else finish(std::integral_constant<int, TF_ACT_NONE>());
                 }
             }
             if (it.nkb > 0) {
@@ -525,8 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++local;
             }
-        }
-        if (WG && lane == 0) ptx::bulk_wait_group_all();
+            return true;
+        });
+        if (lane == 0) ptx::bulk_wait_group_all();
+        for (int s = 0; s < 2; ++s)   // a box asked for and not waited for (after a time-out) lands before the CTA exits
+            if ((fetching >> s) & 1u) ptx::mbar_wait(&in_bar[s], (in_phase >> s) & 1u, p.wait_ns);
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
     }
 
@@ -560,22 +761,22 @@ EncodeTiledFn encode_tiled()
 }
 
 bool encode(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box)
+            const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint32_t ones[3] = {1, 1, 1};
     EncodeTiledFn fn = encode_tiled();
     return fn && fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, ones,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [rows][cols] matrix of 16-bit values, rows `stride` elements apart.
 bool encode_rows(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_t rows, int64_t cols, int64_t stride,
-                 int box_cols, int box_rows)
+                 int box_cols, int box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    return encode(m, type, 2, base, dims, strides, box);
+    return encode(m, type, 2, base, dims, strides, box, swizzle);
 }
 
 // [groups][N][K] weights or weights' gradients.
@@ -634,8 +835,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.offsets = a.offsets;
     p.bias = a.bias;
     p.y = a.y;
-    p.pre_in = a.pre;
-    p.pre_out = a.pre;
+    p.pre = a.pre;
     p.err = device_error_word();
     p.wait_ns = wait_limit_ns();
     if (!p.err) return cudaErrorInitializationError;
@@ -652,18 +852,19 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.bf16 = a.dtype == TF_BF16;
     p.accumulate = a.accumulate;
     p.stage_bytes = kABytes + (WG ? kMaxBN : bn) / CG * BK * 2;
-    const int fixed = (WG ? kEpiWarps * kDwBoxBytes : 0) + kNumBars * 8 + 16 + (2 * (a.groups + 1) + 1) * 4;
+    const int sched = (2 * (a.groups + 1) + 2) * 4;
+    const int fixed = kEpiWarps * kEpiBytes + kNumBars * 8 + 16 + sched;
     p.stages = (kSmemLimit - fixed) / p.stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages < 2) return cudaErrorNotSupported;
-    p.off_dw = p.stages * p.stage_bytes;
-    p.off_bar = p.off_dw + (WG ? kEpiWarps * kDwBoxBytes : 0);
+    p.off_epi = p.stages * p.stage_bytes;
+    p.off_bar = p.off_epi + kEpiWarps * kEpiBytes;
     p.off_sched = p.off_bar + kNumBars * 8 + 16;
-    const int smem = p.off_sched + (2 * (a.groups + 1) + 1) * 4;
+    const int smem = p.off_sched + sched;
 
     const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap ta, tb, td;
-    memset(&td, 0, sizeof td);
+    CUtensorMap ta, tb, td, tp;
+    memset(&tp, 0, sizeof tp);
     bool ok;
     if (MODE == GROUPED_FORWARD)
         ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, BK, BM) &&
@@ -675,6 +876,9 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
         ok = encode_rows(&ta, type, a.dy, a.rows, a.N, a.dy_stride, 64, BK) &&
              encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, 64, BK) &&
              encode_groups(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.dw, a.groups, a.N, a.K, 4, 32, 32);
+    if (!WG)   // y and pre in boxes of 32 rows x 32 weights rows
+        ok = ok && encode_rows(&td, type, a.y, a.rows, p.M, a.y_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+             (!a.pre || encode_rows(&tp, type, a.pre, a.rows, p.M, a.pre_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
     if (!ok) return cudaErrorInvalidValue;
 
     int units = 0;
@@ -699,7 +903,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG>, ta, tb, td, p));
+    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG>, ta, tb, td, tp, p));
 }
 
 template <int MODE>
@@ -721,19 +925,20 @@ int64_t grouped_wgrad_workspace(int64_t, int, int64_t, int64_t, int) { return 0;
 cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st)
 {
     // what a tensor map can address: 16-byte rows and bases
+    auto rows_ok = [](const void *p, int64_t stride) { return !p || (aligned16(p) && stride % 8 == 0); };
     const bool dims = a.N % 8 == 0 && a.K % 8 == 0 && a.rows > 0;
-    cudaError_t e;
     if (mode == GROUPED_FORWARD) {
-        const bool tma = dims && a.x_stride % 8 == 0 && aligned16(a.x) && aligned16(a.w);
+        const bool tma = dims && rows_ok(a.x, a.x_stride) && rows_ok(a.y, a.y_stride) && rows_ok(a.pre, a.pre_stride) &&
+                         aligned16(a.w);
         return tma ? launch_auto<GROUPED_FORWARD>(a, st) : launch_grouped_simple(a, mode, st);
     }
     if (mode == GROUPED_DGRAD) {
-        const bool tma = dims && a.dy_stride % 8 == 0 && aligned16(a.dy) && aligned16(a.w);
+        const bool tma = dims && rows_ok(a.dy, a.dy_stride) && rows_ok(a.y, a.y_stride) && rows_ok(a.pre, a.pre_stride) &&
+                         aligned16(a.w);
         return tma ? launch_auto<GROUPED_DGRAD>(a, st) : launch_grouped_simple(a, mode, st);
     }
-    const bool tma = dims && a.dy_stride % 8 == 0 && a.x_stride % 8 == 0 && aligned16(a.dy) && aligned16(a.x) &&
-                     aligned16(a.dw);
-    e = tma ? launch_auto<GROUPED_WGRAD>(a, st) : launch_grouped_simple(a, mode, st);
+    const bool tma = dims && rows_ok(a.dy, a.dy_stride) && rows_ok(a.x, a.x_stride) && aligned16(a.dw);
+    const cudaError_t e = tma ? launch_auto<GROUPED_WGRAD>(a, st) : launch_grouped_simple(a, mode, st);
     if (e != cudaSuccess || !a.dbias) return e;
     return launch_grouped_bias_grad(a, st);
 }
