@@ -13,11 +13,15 @@
 //
 // Persistent kernel, one CTA (CG = 1) or CTA pair (CG = 2, cta_group::2) per SM
 // (pair), work items (group, weights tile, row tile) from a schedule that every
-// CTA computes from the offsets.  Warps:
+// CTA computes from the offsets, the groups with the costliest tiles first.
+// Warps:
 //   0     TMA producer of a ring of K steps (64 deep, 128-byte swizzle)
 //   1     TMEM allocator and MMA issuer; two 256-column fp32 accumulators, so
 //         the epilogue of one tile overlaps the main loop of the next
 //   2     WGRAD: zeroes what the last K step of a group holds of other rows
+//   3     lists the CTA's coming items, 32 at a time: their searches and
+//         divisions, done by the MMA issuer between two tiles, left the tensor
+//         pipe idle for 1.3 us per tile
 //   4-11  epilogue: TMEM -> registers -> bias, activation -> y
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the
 // device error word and winds down.
@@ -39,7 +43,7 @@ constexpr int BM = 128;                 // weights rows per CTA (UMMA M, or half
 constexpr int BK = 64;                  // K step: one 128-byte swizzle row of 16-bit values
 constexpr int UMMA_K = 16;
 constexpr int kMaxBN = 256;             // widest row tile: one accumulator is 256 TMEM columns
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kSmemLimit = 227 * 1024;
@@ -47,8 +51,11 @@ constexpr int kABytes = BM * BK * 2;
 constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or N-major operand
 constexpr int kBoxBytes = 32 * 32 * 2;            // epilogue box: 32 rows (tokens) x 32 weights rows, 16-bit
 constexpr int kEpiBytes = 2 * kBoxBytes;          // per warp two of them, or WGRAD's one of 32 x 32 fp32
-constexpr int kNumBars = 3 * kMaxStages + 5 + 2 * kEpiWarps;   // full, empty, land; accumulators full x2, empty x2;
-                                                               // drain; DGRAD: each epilogue warp's boxes
+constexpr int kNumBars = 3 * kMaxStages + 9 + 2 * kEpiWarps;   // full, empty, land; accumulators full x2, empty x2;
+                                                               // drain; item lists ready x2, free x2; DGRAD:
+                                                               // each epilogue warp's boxes
+constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
+constexpr int kMaxSorted = 256;                   // groups up to this many are sorted by their tiles' cost
 // WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
 // round, so an accumulator's error grows with the number of MMAs it takes; a
 // longer group is cut into parts whose fp32 sums are added in memory.  Measured
@@ -69,24 +76,55 @@ struct UmmaArgs {
     int red;           // reduction length of FORWARD and DGRAD
     int cols;          // WGRAD: K, the N side
     int bn;            // widest row tile the shared memory holds
+    int bm;            // weights rows of a tile: 128 per CTA, or 0: chosen from {128, 64, 32} by the schedule
+    int a_box;         // weights rows (or, M-major, 64 of them) per TMA box
     int box_rows;      // rows per token box
-    int stages, stage_bytes, off_epi, off_bar, off_sched;
+    int off_epi, off_bar, off_items, off_sched;   // the operand ring comes first
     int act, bf16, accumulate;
 };
 
-// Shared-memory matrix descriptor of an M- or N-major tile written by TMA with
-// 128-byte swizzling: boxes of 64 (M or N) x 64 (K) values, each a K row of 128
-// bytes.  Eight K rows are one 1024-byte swizzle atom (stride byte offset); the
-// next 64 M or N values are a box further on (leading byte offset).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr)
+// Shared-memory matrix descriptors (128-byte swizzle), as a low word that holds
+// the address and a high word that does not change: advancing along K inside a
+// tile, or to another stage, is one 32-bit addition.
+//   K-major: rows of 64 values (128 bytes), eight of them an atom of 1024 bytes,
+//     atoms stacked densely; 16 values along K are 32 bytes.
+//   M- or N-major: boxes of 64 (M or N) x 64 (K) values, each a K row of 128
+//     bytes; eight K rows are an atom (stride byte offset 1024), the next 64 M or
+//     N values are a box further on (leading byte offset); 16 along K are 2048 bytes.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride offset, version 1, 128-byte swizzle
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, bool kmajor)
 {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)(kChunkBytes >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
+    return ((smem_addr & 0x3FFFFu) >> 4) | ((kmajor ? 1u : (uint32_t)(kChunkBytes >> 4)) << 16);
+}
+constexpr uint32_t desc_step(bool kmajor) { return (kmajor ? UMMA_K * 2 : UMMA_K * 128) >> 4; }
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t low)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
     return d;
+}
+
+// One lane of the (converged) warp.  The roles that issue copies and MMAs run
+// their loops with the whole warp and let one lane issue: in code that a single
+// lane runs the compiler cannot keep what these instructions take in uniform
+// registers, and a K step then takes its issuer ~600 cycles (the tensor cores
+// 512 for the widest tile).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Arrives once on the mbarrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void commit_both(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     ptx::smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor, bool b_nmajor)
@@ -148,18 +186,19 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-// One work item.  FORWARD, DGRAD: weights rows [m0, +128*CG), tokens [t0, +tv),
-// MMA N = w.  WGRAD: dw rows [m0, +128*CG), columns [t0, +w) of group e from its
-// rows [first, +tv) -- all of the group's, or the part-th of `parts`.
-struct Item {
-    int e, m0, t0, w, tv, first, nkb, part, parts;
+// One work item.  FORWARD, DGRAD: weights rows [m0, +bm), tokens [t0, +tv), MMA
+// N = w.  WGRAD: dw rows [m0, +128*CG), columns [t0, +w) of group e from its rows
+// [first, +tv), in `parts` parts of `len` rows (the last one shorter).
+struct alignas(16) Item {
+    int e, m0, t0, w, tv, first, len, parts;
 };
+static_assert(sizeof(Item) == 32, "two 16-byte loads");
 
-// The schedule in shared memory: rows of every group, and the running count of
-// tiles (WGRAD's are the same number for every group).
+// The schedule in shared memory: rows of every group, the groups in order of
+// falling cost, and the running count of tiles in that order.
 struct Plan {
-    const int *row, *tile;
-    int bn;
+    const int *row, *tile, *order;
+    int bn, bm, mt;   // row tile, weights tile per CTA (pair), weights tiles
 };
 
 template <int MODE, int CG>
@@ -167,66 +206,78 @@ __device__ __forceinline__ Item item_of(const UmmaArgs &p, const Plan &s, int t)
 {
     constexpr int STEP = 16 * CG;
     Item it;
-    const int mt = (p.M + BM * CG - 1) / (BM * CG);
-    it.part = 0;
-    it.parts = 1;
     if (MODE == GROUPED_WGRAD) {
-        const int ct = (p.cols + kMaxBN - 1) / kMaxBN;
-        it.e = t / (mt * ct);
-        const int r = t - it.e * (mt * ct);
-        it.m0 = r / ct * (BM * CG);
+        const int ct = (p.cols + kMaxBN - 1) / kMaxBN, pos = t / (s.mt * ct), r = t - pos * (s.mt * ct);
+        it.e = s.order[pos];
+        it.m0 = r / ct * s.bm;
         it.t0 = r % ct * kMaxBN;
         const int left = min(kMaxBN, p.cols - it.t0);
         it.w = (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
         it.first = s.row[it.e];
         it.tv = s.row[it.e + 1] - it.first;
         it.parts = max(1, (it.tv + kMaxPartRows - 1) / kMaxPartRows);
+        it.len = ((it.tv + it.parts - 1) / it.parts + BK - 1) / BK * BK;
     } else {
         int lo = 0, hi = p.groups - 1;   // the last group that starts at or before tile t
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        it.e = lo;
-        const int r = t - s.tile[lo], T = s.row[lo + 1] - s.row[lo];
+        it.e = s.order[lo];
+        const int r = t - s.tile[lo], T = s.row[it.e + 1] - s.row[it.e];
         const int ntt = (T + s.bn - 1) / s.bn;
         const int wt = ((T + ntt - 1) / ntt + STEP - 1) / STEP * STEP;   // equal widths, at most bn
         const int tt = r % ntt;
-        it.m0 = r / ntt * (BM * CG);
-        it.first = s.row[lo];
+        it.m0 = r / ntt * s.bm;
+        it.first = s.row[it.e];
         it.t0 = it.first + tt * wt;
         it.tv = min(wt, T - tt * wt);
         it.w = (it.tv + STEP - 1) / STEP * STEP;
-        it.nkb = (p.red + BK - 1) / BK;
+        it.parts = 1;
+        it.len = 0;
     }
     return it;
 }
 
-// WGRAD: narrows an item to its part's rows; parts are whole K steps but for the last.
-__device__ __forceinline__ Item part_of(Item it, int part)
-{
-    const int T = it.tv, len = ((T + it.parts - 1) / it.parts + BK - 1) / BK * BK;
-    it.part = part;
-    it.first += part * len;
-    it.tv = min(len, T - part * len);
-    it.nkb = (it.tv + BK - 1) / BK;
-    return it;
-}
+// The item lists: list i of 32 lies in half i % 2 of the table.
+struct Items {
+    Item *table;
+    uint64_t *ready, *free;
+    uint64_t wait_ns;
+    int cid, ncl, num_work;
+};
 
-// Calls f(item) for every (part of an) item of this CTA or pair, in order,
-// until it returns false.
-template <int MODE, int CG, typename F>
-__device__ __forceinline__ void each_item(const UmmaArgs &p, const Plan &s, int num_work, int cid, int ncl, F f)
+// Calls f(item, part, first row, rows, K steps) for every part of every item of
+// this CTA or pair, in order, until it returns false; false where a list never
+// came.  All lanes of a warp call together.
+template <int MODE, typename F>
+__device__ __forceinline__ bool each_item(const UmmaArgs &p, const Items &s, F f)
 {
-    for (int t = cid; t < num_work; t += ncl) {
-        const Item it = item_of<MODE, CG>(p, s, t);
+    int i = 0;
+    for (int t = s.cid; t < s.num_work; t += s.ncl, ++i) {
+        const int half = (i >> 5) & 1;
+        if ((i & 31) == 0) {
+            const bool ok = ptx::mbar_wait(&s.ready[half], (uint32_t)(i >> 6) & 1u, s.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+        }
+        const int4 *src = reinterpret_cast<const int4 *>(&s.table[i & 63]);
+        const int4 a = src[0], b = src[1];
+        const Item it = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         if constexpr (MODE == GROUPED_WGRAD) {
-            for (int part = 0; part < it.parts; ++part)
-                if (!f(part_of(it, part))) return;
+            // parts are whole K steps but for the last
+            for (int part = 0, done = 0; part < it.parts; ++part, done += it.len) {
+                const int rows = min(it.len, it.tv - done);
+                if (!f(it, part, it.first + done, rows, (rows + BK - 1) / BK)) return true;
+            }
         } else {
-            if (!f(it)) return;
+            if (!f(it, 0, it.first, it.tv, (p.red + BK - 1) / BK)) return true;
+        }
+        if ((i & 31) == 31) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&s.free[half]);
         }
     }
+    return true;
 }
 
 // An epilogue warp's store of the box [32 tokens][32 weights rows] (64-byte rows,
@@ -316,6 +367,15 @@ __device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const CUtensorMa
     }
 }
 
+// Sums a tile is kept in: an MMA of few columns that adds to the sum of the one
+// before it waits for it (~150 cycles each, 44 of 50 us of a 16-row product), so
+// the four of a K step get a sum each.
+template <int MODE, int CG>
+__device__ __forceinline__ int sums_of(int w)
+{
+    return MODE != GROUPED_WGRAD && CG == 1 && w <= 64 ? 4 : 1;
+}
+
 template <int MODE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -332,30 +392,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tfull = land + kMaxStages;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint64_t *loaded = drain + 1;           // DGRAD: each epilogue warp's two boxes of pre
+    uint64_t *ready = drain + 1, *freed = ready + 2;
+    uint64_t *loaded = freed + 2;           // DGRAD: each epilogue warp's two boxes of pre
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(loaded + 2 * kEpiWarps);
     int *row = reinterpret_cast<int *>(smem + p.off_sched);      // [groups + 1]
     int *tile = row + p.groups + 1;                              // [groups + 1]
-    int *bad = tile + p.groups + 1;
+    int *order = tile + p.groups + 1;                            // [groups]
+    int *bad = order + p.groups;                                 // then the chosen bn and bm
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = PAIR ? (int)ptx::cluster_ctarank() : 0;
     const int cid = (int)blockIdx.x / CG, ncl = (int)gridDim.x / CG;
     const bool leader = crank == 0;
 
+    if (threadIdx.x < kMaxStages) {
+        // WGRAD: one arrival per CTA, from the producers' side (which arrives CG times for a whole
+        // K step) or from the CTAs' zeroing warps (a ragged one)
+        ptx::mbar_init(&full[threadIdx.x], WG ? CG : 1);
+        ptx::mbar_init(&empty[threadIdx.x], 1);
+        ptx::mbar_init(&land[threadIdx.x], 1);
+        ptx::mbar_init_fence();
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            // WGRAD: one arrival per CTA, from the producers' side (which arrives CG times for a whole
-            // K step) or from the CTAs' zeroing warps (a ragged one)
-            ptx::mbar_init(&full[s], WG ? CG : 1);
-            ptx::mbar_init(&empty[s], 1);
-            ptx::mbar_init(&land[s], 1);
-        }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&tfull[i], 1);
             ptx::mbar_init(&tempty[i], CG * kEpiWarps);   // one lane per epilogue warp of either CTA
         }
         ptx::mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&ready[i], 1);
+            // the producer, the MMA issuer (of the first CTA), WGRAD's zeroing warp, the epilogue warps
+            ptx::mbar_init(&freed[i], 1 + (leader ? 1 : 0) + (WG ? 1 : 0) + kEpiWarps);
+        }
         if (MODE == GROUPED_DGRAD)
             for (int i = 0; i < 2 * kEpiWarps; ++i) ptx::mbar_init(&loaded[i], 1);
         ptx::mbar_init_fence();
@@ -379,10 +447,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     cta_sync();
     ptx::tc_fence_after();
 
-    // ---- the schedule: rows of every group and the running count of tiles
-    Plan plan = {row, tile, p.bn};
-    const int mt = (p.M + BM * CG - 1) / (BM * CG);
+    // ---- the schedule
+    Plan plan = {row, tile, order, p.bn, BM * CG, 0};
     {
+        constexpr int STEP = 16 * CG;
         int wrong = 0;
         for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
             const int v = p.offsets[i];
@@ -391,19 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (wrong) *bad = 1;
         cta_sync();
-        if (warp == 0 && !WG) {
-            // The widest row tile is chosen for the last wave: each candidate's cost is the number
-            // of tiles the busiest CTA (pair) takes times their mean width, plus a constant for a
-            // tile's overhead.  (Few groups leave 256 as it is; 1152 tiles over 76 pairs leave the
-            // 16th wave 5% full, 1280 of 7/8 the width fill 17.)
-            if (p.bn == kMaxBN && !*bad) {
-                int best = 0x7fffffff, pick = p.bn;
-                for (int bn = kMaxBN; bn >= 128; bn -= 32) {
+        const bool void_call = *bad != 0;
+        if (warp == 0) {
+            // Tile sizes for the last wave: a candidate's cost is the number of tiles the busiest
+            // CTA (pair) takes times a tile's own, with a constant for its overhead.
+            int pick_n = p.bn, pick_m = BM * CG;
+            if (!WG && !void_call) {
+                int best = 0x7fffffff;
+                for (int bn = p.bn; bn >= (p.bn == kMaxBN ? 128 : p.bn); bn -= 32) {
                     int tiles = 0, width = 0;
                     for (int e = lane; e < p.groups; e += 32) {
                         const int T = row[e + 1] - row[e], n = (T + bn - 1) / bn;
                         tiles += n;
-                        width += (T + 16 * CG * n - 1) / (16 * CG) * (16 * CG);
+                        width += (T + STEP * n - 1) / STEP * STEP;
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) {
@@ -411,37 +479,67 @@ __global__ void __launch_bounds__(kThreads, 1)
                         width += __shfl_xor_sync(0xffffffffu, width, o);
                     }
                     if (tiles == 0) break;
-                    const int cost = (tiles * mt + ncl - 1) / ncl * (width / tiles + 24);
-                    if (cost < best) {
-                        best = cost;
-                        pick = bn;
+                    // narrower weights tiles only where a tile is paced by its weights' way from HBM (an
+                    // SM's share of it brings a K step of 52 rows in the ~290 cycles that one takes to issue)
+                    for (int bm = BM * CG; bm >= (p.bm ? BM * CG : p.a_box); bm >>= 1) {
+                        const int waves = (tiles * ((p.M + bm - 1) / bm) + ncl - 1) / ncl;
+                        const int cost = p.bm ? waves * (width / tiles + 24) : waves * max(bm, 52);
+                        if (cost < best) {
+                            best = cost;
+                            pick_n = bn;
+                            pick_m = bm;
+                        }
                     }
                 }
-                plan.bn = pick;
             }
+            if (lane == 0) {
+                bad[1] = pick_n;
+                bad[2] = pick_m;
+            }
+        }
+        cta_sync();
+        plan.bn = bad[1];
+        plan.bm = bad[2];
+        plan.mt = (p.M + plan.bm - 1) / plan.bm;
+        // the groups by falling cost: their tiles' width, or (WGRAD) their rows
+        for (int e = threadIdx.x; e < p.groups; e += kThreads) {
+            const int T = row[e + 1] - row[e], n = (T + plan.bn - 1) / plan.bn;
+            tile[e] = WG || T <= 0 ? T : (T + n - 1) / n;
+        }
+        cta_sync();
+        for (int e = threadIdx.x; e < p.groups; e += kThreads) {
+            int rank = e;
+            if (p.groups <= kMaxSorted) {
+                const int c = tile[e];
+                rank = 0;
+                for (int i = 0; i < p.groups; ++i) rank += tile[i] > c || (tile[i] == c && i < e);
+            }
+            order[rank] = e;
+        }
+        cta_sync();
+        if (warp == 0 && !WG) {
             int before = 0;
             for (int base = 0; base < p.groups; base += 32) {
-                const int e = base + lane;
+                const int pos = base + lane;
                 int n = 0;
-                if (e < p.groups && !*bad) n = (row[e + 1] - row[e] + plan.bn - 1) / plan.bn * mt;
+                if (pos < p.groups && !void_call) {
+                    const int e = order[pos];
+                    n = (row[e + 1] - row[e] + plan.bn - 1) / plan.bn * plan.mt;
+                }
                 int sum = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int up = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += up;
                 }
-                if (e < p.groups) tile[e] = before + sum - n;
+                if (pos < p.groups) tile[pos] = before + sum - n;
                 before += __shfl_sync(0xffffffffu, sum, 31);
             }
-            if (lane == 0) {
-                tile[p.groups] = before;
-                bad[1] = plan.bn;
-            }
+            if (lane == 0) tile[p.groups] = before;
         }
         cta_sync();
-        if (!WG) plan.bn = bad[1];
     }
-    int num_work = WG ? p.groups * mt * ((p.cols + kMaxBN - 1) / kMaxBN) : tile[p.groups];
+    int num_work = WG ? p.groups * plan.mt * ((p.cols + kMaxBN - 1) / kMaxBN) : tile[p.groups];
     if (*bad) {
         num_work = 0;
         if (threadIdx.x == 0) atomicOr(p.err, TF_DEVERR_OFFSETS);
@@ -459,23 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
+    // the ring: a stage's B tile follows as many rows of A as the tile has (an MMA of 128 rows then reads
+    // past them, into B and the next stage: rows that are not stored)
+    const int a_bytes = plan.bm / CG * BK * 2, stage_bytes = a_bytes + (WG ? kMaxBN : p.bn) / CG * BK * 2;
+    const int stages = min(kMaxStages, p.off_epi / stage_bytes);
+    const Items items = {reinterpret_cast<Item *>(smem + p.off_items), ready, freed, p.wait_ns, cid, ncl, num_work};
     if (warp == 0) {
         // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, last_phase = 0;
-            bool ok = true;
-            each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
-                const int mrow = it.m0 + crank * BM;
-                for (int kb = 0; kb < it.nkb; ++kb) {
-                    if (!ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) return ok = false;
-                    uint8_t *a_dst = smem + stage * p.stage_bytes, *b_dst = a_dst + kABytes;
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_phase = 0;
+        bool ok = true;
+        const bool issuer = elect_one();
+        ok &= each_item<MODE>(p, items, [&](const Item &it, int, int first, int rows, int nkb) {
+            const int mrow = it.m0 + crank * BM;
+            const int abox = plan.bm / CG / p.a_box;   // boxes of the weights' side
+            // boxes of the N side this CTA loads: its half of the tile's rows (or columns)
+            const int half = it.w / CG;
+            const int nbox = WG ? half / 64 : (half + p.box_rows - 1) / p.box_rows;
+            const uint32_t own = (uint32_t)a_bytes + (uint32_t)(nbox * (WG ? kChunkBytes : p.box_rows * BK * 2));
+            for (int kb = 0; kb < nkb; ++kb) {
+                const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) return ok = false;
+                if (issuer) {
+                    uint8_t *a_dst = smem + stage * stage_bytes, *b_dst = a_dst + a_bytes;
                     const int k0 = kb * BK;
-                    // boxes of the N side this CTA loads: its half of the tile's rows (or columns)
-                    const int half = it.w / CG;
-                    const int nbox = WG ? half / 64 : (half + p.box_rows - 1) / p.box_rows;
-                    const uint32_t own = kABytes + (uint32_t)(nbox * (WG ? kChunkBytes : p.box_rows * BK * 2));
-                    const bool ragged = WG && kb == it.nkb - 1 && (it.tv & 15) != 0;
+                    const bool ragged = WG && kb == nkb - 1 && (rows & 15) != 0;
                     uint64_t *bar = ragged ? &land[stage] : &full[stage];
                     if (ragged) {
                         ptx::mbar_arrive_expect_tx(bar, own);
@@ -484,29 +590,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (WG && PAIR) ptx::mbar_arrive(bar);
                     }
                     const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, ragged ? (uint32_t)crank : 0u) : 0u;
-                    if constexpr (MODE == GROUPED_FORWARD) {
-                        // a box that would start past the last weights row starts on it: its rows are never stored
-                        const int n = min(mrow, p.M - 1);
-                        if constexpr (PAIR) ptx::tma_load_3d_pair(a_dst, &tmap_a, bar_cl, k0, n, it.e);
-                        else ptx::tma_load_3d(a_dst, &tmap_a, bar, k0, n, it.e);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                    for (int i = 0; i < abox; ++i) {
+                        uint8_t *dst = a_dst + i * p.a_box * (BK * 2);
+                        if constexpr (MODE == GROUPED_FORWARD) {
+                            // a box that would start past the last weights row starts on it: its rows are never stored
+                            const int n = min(mrow + i * p.a_box, p.M - 1);
+                            if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, k0, n, it.e);
+                            else ptx::tma_load_3d(dst, &tmap_a, bar, k0, n, it.e);
+                        } else {
                             const int c = min(mrow + 64 * i, (p.M - 1) & ~7);   // 16-byte aligned, inside the tensor
                             if constexpr (MODE == GROUPED_DGRAD) {
-                                if constexpr (PAIR) ptx::tma_load_3d_pair(a_dst + i * kChunkBytes, &tmap_a, bar_cl, c, k0, it.e);
-                                else ptx::tma_load_3d(a_dst + i * kChunkBytes, &tmap_a, bar, c, k0, it.e);
+                                if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, c, k0, it.e);
+                                else ptx::tma_load_3d(dst, &tmap_a, bar, c, k0, it.e);
                             } else {
-                                if constexpr (PAIR) ptx::tma_load_2d_pair(a_dst + i * kChunkBytes, &tmap_a, bar_cl, c, it.first + k0);
-                                else ptx::tma_load_2d(a_dst + i * kChunkBytes, &tmap_a, bar, c, it.first + k0);
+                                if constexpr (PAIR) ptx::tma_load_2d_pair(dst, &tmap_a, bar_cl, c, first + k0);
+                                else ptx::tma_load_2d(dst, &tmap_a, bar, c, first + k0);
                             }
                         }
                     }
                     for (int i = 0; i < nbox; ++i) {
                         if constexpr (WG) {
                             const int c = min(it.t0 + crank * half + 64 * i, (p.cols - 1) & ~7);
-                            if constexpr (PAIR) ptx::tma_load_2d_pair(b_dst + i * kChunkBytes, &tmap_b, bar_cl, c, it.first + k0);
-                            else ptx::tma_load_2d(b_dst + i * kChunkBytes, &tmap_b, bar, c, it.first + k0);
+                            if constexpr (PAIR) ptx::tma_load_2d_pair(b_dst + i * kChunkBytes, &tmap_b, bar_cl, c, first + k0);
+                            else ptx::tma_load_2d(b_dst + i * kChunkBytes, &tmap_b, bar, c, first + k0);
                         } else {
                             // rows past the group are other groups' (or zero): their columns of D are never stored
                             const int m = min(it.t0 + crank * half + i * p.box_rows, p.rows - 1);
@@ -515,74 +621,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else ptx::tma_load_2d(dst, &tmap_b, bar, k0, m);
                         }
                     }
-                    issued |= 1u << stage;
-                    last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == p.stages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
                 }
-                return true;
-            });
-            if (!ok) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
-            // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
-            for (int s = 0; s < p.stages; ++s)
-                if (leader && ((issued >> s) & 1u))
-                    if (!ptx::mbar_wait<PAIR>(&full[s], (last_phase >> s) & 1u, p.wait_ns))
-                        atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
-        }
+                __syncwarp();
+                issued |= 1u << stage;
+                last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            return true;
+        });
+        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
+        // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
+        for (int s = 0; s < stages; ++s)
+            if (leader && ((issued >> s) & 1u))
+                if (!ptx::mbar_wait<PAIR>(&full[s], (last_phase >> s) & 1u, p.wait_ns) && lane == 0)
+                    atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && leader) {
+        if (leader) {
             int stage = 0, local = 0;
             uint32_t phase = 0;
             bool ok = true;
-            each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
-                if (it.nkb == 0) return true;
+            const bool issuer = elect_one();
+            constexpr uint32_t a_step = desc_step(!A_MMAJOR), b_step = desc_step(!WG);
+            const uint32_t a_low = desc_low(ptx::smem_u32(smem), !A_MMAJOR);
+            const uint32_t b_low = desc_low(ptx::smem_u32(smem) + (uint32_t)a_bytes, !WG);
+            auto mma = [](uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+                if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a), desc_of(b), id, acc);
+                else ptx::umma_bf16(d, desc_of(a), desc_of(b), id, acc);
+            };
+            ok &= each_item<MODE>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
+                if (nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
+                const uint32_t apart = sums_of<MODE, CG>(it.w) > 1 ? 64u : 0u;
                 const int b = local & 1;
-                if (!ptx::mbar_wait<PAIR>(&tempty[b], (uint32_t)((local >> 1) & 1) ^ 1u, p.wait_ns)) return ok = false;
+                bool got = ptx::mbar_wait<PAIR>(&tempty[b], (uint32_t)((local >> 1) & 1) ^ 1u, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(b * kMaxBN);
-                for (int kb = 0; kb < it.nkb; ++kb) {
-                    if (!ptx::mbar_wait<PAIR && WG>(&full[stage], phase, p.wait_ns)) return ok = false;
+                uint32_t acc = 0;   // the first K step begins its sums
+                for (int kb = 0; kb < nkb; ++kb) {
+                    got = ptx::mbar_wait<PAIR && WG>(&full[stage], phase, p.wait_ns);
+                    if (!__all_sync(0xffffffffu, got)) return ok = false;
                     ptx::tc_fence_after();
-                    const uint32_t a = ptx::smem_u32(smem + stage * p.stage_bytes), bb = a + kABytes;
+                    const uint32_t a = a_low + (uint32_t)stage * (uint32_t)(stage_bytes >> 4);
+                    const uint32_t bb = b_low + (uint32_t)stage * (uint32_t)(stage_bytes >> 4);
                     // WGRAD: sixteens of rows past the group's end are left out
-                    const int steps = WG ? min(BK / UMMA_K, (it.tv - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
-                    for (int k = 0; k < steps; ++k) {
-                        const uint64_t ad = A_MMAJOR ? sw128_mnmajor_desc(a + k * UMMA_K * 128)
-                                                     : ptx::sw128_kmajor_desc(a + k * UMMA_K * 2);
-                        const uint64_t bd = WG ? sw128_mnmajor_desc(bb + k * UMMA_K * 128)
-                                               : ptx::sw128_kmajor_desc(bb + k * UMMA_K * 2);
-                        const uint32_t acc = (kb > 0 || k > 0) ? 1u : 0u;
-                        if constexpr (PAIR) ptx::umma_bf16_pair(d_tmem, ad, bd, id, acc);
-                        else ptx::umma_bf16(d_tmem, ad, bd, id, acc);
+                    const int steps = WG ? min(BK / UMMA_K, (rows - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
+                    if (issuer) {
+                        mma(d_tmem, a, bb, id, acc);
+                        const uint32_t acc1 = apart ? acc : 1u;
+                        if (!WG || steps > 1) mma(d_tmem + apart, a + a_step, bb + b_step, id, acc1);
+                        if (!WG || steps > 2) mma(d_tmem + 2 * apart, a + 2 * a_step, bb + 2 * b_step, id, acc1);
+                        if (!WG || steps > 3) mma(d_tmem + 3 * apart, a + 3 * a_step, bb + 3 * b_step, id, acc1);
+                        if constexpr (PAIR) commit_both(&empty[stage]);
+                        else ptx::umma_commit(&empty[stage]);
+                        if (kb == nkb - 1) {
+                            if constexpr (PAIR) commit_both(&tfull[b]);
+                            else ptx::umma_commit(&tfull[b]);
+                        }
                     }
-                    if constexpr (PAIR) {
-                        ptx::umma_commit_pair(ptx::mapa_shared(&empty[stage], 0));
-                        ptx::umma_commit_pair(ptx::mapa_shared(&empty[stage], 1));
-                    } else {
-                        ptx::umma_commit(&empty[stage]);
-                    }
-                    if (++stage == p.stages) {
+                    __syncwarp();
+                    acc = 1u;
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
-                }
-                if constexpr (PAIR) {
-                    ptx::umma_commit_pair(ptx::mapa_shared(&tfull[b], 0));
-                    ptx::umma_commit_pair(ptx::mapa_shared(&tfull[b], 1));
-                } else {
-                    ptx::umma_commit(&tfull[b]);
                 }
                 ++local;
                 return true;
             });
-            if (!ok) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
-            if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
-            else ptx::umma_commit(drain);
-            if (!ptx::mbar_wait(drain, 0, p.wait_ns)) atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
+            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+            if (issuer) {   // (the lane that issued the MMAs)
+                if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
+                else ptx::umma_commit(drain);
+            }
+            __syncwarp();
+            if (!ptx::mbar_wait(drain, 0, p.wait_ns) && lane == 0) atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
         }
     } else if (WG && warp == 2) {
         // ------------------------------------------------------------ zeroing warp
@@ -592,15 +709,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t land_phase = 0;
         int blocks = 0;    // K steps before this item
         bool ok = true;
-        each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
-            blocks += it.nkb;
-            if ((it.tv & 15) == 0) return true;
-            const int stage = (blocks - 1) % p.stages;
+        ok &= each_item<MODE>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
+            blocks += nkb;
+            if ((rows & 15) == 0) return true;
+            const int stage = (blocks - 1) % stages;
             ok = ptx::mbar_wait(&land[stage], (land_phase >> stage) & 1u, p.wait_ns);
             land_phase ^= 1u << stage;
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            const int r0 = it.tv - (it.nkb - 1) * BK, r1 = (r0 + 15) & ~15;
-            uint8_t *base = smem + stage * p.stage_bytes;
+            if (!__all_sync(0xffffffffu, ok)) return ok = false;
+            const int r0 = rows - (nkb - 1) * BK, r1 = (r0 + 15) & ~15;
+            uint8_t *base = smem + stage * stage_bytes;
             const int nbox = 2 + it.w / CG / 64;   // A's two boxes, then B's
             for (int i = lane; i < nbox * (r1 - r0) * 8; i += 32) {
                 const int box = i / ((r1 - r0) * 8), j = i - box * ((r1 - r0) * 8);
@@ -616,6 +733,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         });
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ item lists
+        bool ok = true;
+        for (int k = 0; ok && cid + k * 32 * ncl < num_work; ++k) {
+            const int half = k & 1, t = cid + (k * 32 + lane) * ncl;
+            if (k >= 2) ok = ptx::mbar_wait(&freed[half], (uint32_t)((k >> 1) - 1) & 1u, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                ok = false;
+                break;
+            }
+            if (t < num_work) items.table[half * 32 + lane] = item_of<MODE, CG>(p, plan, t);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ready[half]);
+        }
+        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
     } else if (warp >= kFirstEpiWarp) {
         // ------------------------------------------------------------ epilogue
         // Warp w reads TMEM lanes 32*(w%4) .. +31 (one weights row per lane) and
@@ -627,11 +759,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int local = 0, seq = 0;
         uint32_t in_phase = 0, fetching = 0;
         bool ok = true;
-        each_item<MODE, CG>(p, plan, num_work, cid, ncl, [&](const Item &it) {
+        ok &= each_item<MODE>(p, items, [&](const Item &it, int part, int, int, int nkb) {
             const int n0 = it.m0 + crank * BM + q * 32;
             const int b = local & 1;
             const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
-            const bool mine = n0 < p.M;   // (boxes past the last weights row are neither loaded nor stored)
+            const bool mine = q * 32 < plan.bm && n0 < p.M;   // (boxes past the last weights row are neither loaded nor stored)
             // DGRAD: the box of pre under chunk c, into the box that the seq-th result will take; the store
             // that used it last (two boxes ago) has read it
             auto fetch = [&](int c, int s) {
@@ -653,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (n < p.M) bias[j] = __ldg(p.bias + (int64_t)it.e * p.M + n);
                 }
             }
-            if (it.nkb > 0) {
+            if (nkb > 0) {
                 const bool got = ptx::mbar_wait(&tfull[b], (uint32_t)(local >> 1) & 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
@@ -665,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = h; c * 32 < width && mine; c += kEpiWarps / 4) {
                 uint32_t r[32];
                 if constexpr (WG) {
-                    if (it.nkb > 0) {
+                    if (nkb > 0) {
                         ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), r);
                     } else {
 #pragma unroll
@@ -673,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // the store before has read the box, and an earlier part's sums are in memory
                     if (lane == 0) {
-                        if (it.part > 0) ptx::bulk_wait_group_all();
+                        if (part > 0) ptx::bulk_wait_group_all();
                         else ptx::bulk_wait_group_read<0>();
                     }
                     __syncwarp();
@@ -686,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         // clipped at the group's N rows and K columns
-                        if (p.accumulate || it.part > 0) tma_add_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
+                        if (p.accumulate || part > 0) tma_add_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
                         else tma_store_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
                         ptx::bulk_commit_group();
                     }
@@ -702,6 +834,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if ((c + kEpiWarps / 4) * 32 < width) fetch(c + kEpiWarps / 4, seq + 1);
                     }
                     ptx::tmem_ld_wait();
+                    for (int s = 1; s < sums_of<MODE, CG>(it.w); ++s) {   // the sums of the other sixteens of every K step
+                        uint32_t u[32];
+                        tmem_ld_16x256b_x4(taddr + (uint32_t)(c * 32 + 64 * s), u);
+                        tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32 + 64 * s), u + 16);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(u[j]));
+                    }
                     auto finish = [&](auto act) {
                         constexpr int ACT = decltype(act)::value;
                         if (p.bf16)
@@ -714,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     else finish(std::integral_constant<int, TF_ACT_NONE>());
                 }
             }
-            if (it.nkb > 0) {
+            if (nkb > 0) {
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -848,17 +988,20 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.cols = a.K;
     p.bn = bn;
     p.box_rows = bn / CG < 64 ? bn / CG : 64;
+    // few rows per group (CG = 1): weights tiles of 128, 64 or (K-major) 32 rows, as boxes of that least size
+    const bool small = CG == 1 && !WG && bn <= 64;
+    p.bm = small ? 0 : BM * CG;
+    p.a_box = MODE == GROUPED_FORWARD ? (small ? 32 : BM) : 64;
     p.act = a.act;
     p.bf16 = a.dtype == TF_BF16;
     p.accumulate = a.accumulate;
-    p.stage_bytes = kABytes + (WG ? kMaxBN : bn) / CG * BK * 2;
-    const int sched = (2 * (a.groups + 1) + 2) * 4;
-    const int fixed = kEpiWarps * kEpiBytes + kNumBars * 8 + 16 + sched;
-    p.stages = (kSmemLimit - fixed) / p.stage_bytes;
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
-    if (p.stages < 2) return cudaErrorNotSupported;
-    p.off_epi = p.stages * p.stage_bytes;
-    p.off_bar = p.off_epi + kEpiWarps * kEpiBytes;
+    const int sched = (3 * (a.groups + 1) + 2) * 4;
+    const int fixed = kEpiWarps * kEpiBytes + kItemBytes + kNumBars * 8 + 16 + sched;
+    const int ring = (kSmemLimit - fixed) / 1024 * 1024;
+    if (ring < 2 * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
+    p.off_epi = ring;
+    p.off_items = p.off_epi + kEpiWarps * kEpiBytes;
+    p.off_bar = p.off_items + kItemBytes;
     p.off_sched = p.off_bar + kNumBars * 8 + 16;
     const int smem = p.off_sched + sched;
 
@@ -867,7 +1010,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     memset(&tp, 0, sizeof tp);
     bool ok;
     if (MODE == GROUPED_FORWARD)
-        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, BK, BM) &&
+        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, BK, p.a_box) &&
              encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, BK, p.box_rows);
     else if (MODE == GROUPED_DGRAD)
         ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, 64, BK) &&
@@ -884,7 +1027,8 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     int units = 0;
     cudaError_t e = resident<MODE, CG>(&units);
     if (e != cudaSuccess) return e;
-    const int64_t mt = (p.M + BM * CG - 1) / (BM * CG);
+    const int bm = p.bm ? p.bm : p.a_box;   // (the narrowest tile gives the most work items)
+    const int64_t mt = (p.M + bm - 1) / bm;
     const int64_t most = WG ? (int64_t)a.groups * mt * ((a.K + kMaxBN - 1) / kMaxBN)
                             : ((int64_t)a.rows / bn + a.groups) * mt;
     if (most >= (int64_t)1 << 31) return cudaErrorNotSupported;
