@@ -26,7 +26,6 @@
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the
 // device error word and winds down.
 #include <cuda.h>
-#include <string.h>
 
 #include <mutex>
 #include <type_traits>
@@ -49,13 +48,15 @@ constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kABytes = BM * BK * 2;
 constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or N-major operand
-constexpr int kBoxBytes = 32 * 32 * 2;            // epilogue box: 32 rows (tokens) x 32 weights rows, 16-bit
-constexpr int kEpiBytes = 2 * kBoxBytes;          // per warp two of them, or WGRAD's one of 32 x 32 fp32
-constexpr int kNumBars = 3 * kMaxStages + 9 + 2 * kEpiWarps;   // full, empty, land; accumulators full x2, empty x2;
-                                                               // drain; item lists ready x2, free x2; DGRAD:
-                                                               // each epilogue warp's boxes
+constexpr int kNumBars = 3 * kMaxStages + 9;      // full, empty, land; accumulators full x2, empty x2; drain;
+                                                  // item lists ready x2, free x2
 constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
 constexpr int kMaxSorted = 256;                   // groups up to this many are sorted by their tiles' cost
+// An epilogue warp's box: 32 tokens x 32 weights rows of 16 bits, or WGRAD's 32 x
+// 32 fp32.  It turns the accumulator's columns into rows for 16-byte stores by
+// the threads.  (TMA stores of the same boxes cost the main loop 20 us of 160:
+// the TMA engine is busy with its loads 90% of the time.)
+constexpr int box_bytes(bool wgrad) { return wgrad ? 4096 : 2048; }
 // WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
 // round, so an accumulator's error grows with the number of MMAs it takes; a
 // longer group is cut into parts whose fp32 sums are added in memory.  Measured
@@ -67,7 +68,7 @@ constexpr uint32_t kTmemCols = 512;
 struct UmmaArgs {
     const int *offsets;
     const float *bias;
-    void *y, *pre;
+    void *y, *pre;     // WGRAD: y is dw
     uint32_t *err;
     uint64_t wait_ns;
     int64_t y_stride, pre_stride;
@@ -134,25 +135,9 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_store_3d(const void *map, const void *src, int c0, int c1, int c2)
+__device__ __forceinline__ void red_add_f32x4(float *p, uint4 v)
 {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(c0),
-                 "r"(c1), "r"(c2), "r"(ptx::smem_u32(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_add_3d(const void *map, const void *src, int c0, int c1, int c2)
-{
-    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                 "r"(c0), "r"(c1), "r"(c2), "r"(ptx::smem_u32(src))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_store_2d(const void *map, const void *src, int c0, int c1)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(c0),
-                 "r"(c1), "r"(ptx::smem_u32(src))
-                 : "memory");
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // 16 TMEM lanes x 32 columns as 8 x 8 blocks: lane l of the warp receives, for
@@ -280,90 +265,92 @@ __device__ __forceinline__ bool each_item(const UmmaArgs &p, const Items &s, F f
     return true;
 }
 
-// An epilogue warp's store of the box [32 tokens][32 weights rows] (64-byte rows,
-// 64-byte swizzle) to y or pre: one TMA store, or, where fewer than 32 tokens
-// are the group's, 16-byte stores of those rows.
-__device__ __forceinline__ void store_box(const CUtensorMap *map, void *dst, int64_t stride, const uint8_t *box, int n0,
-                                          int M, int token, int count)
+// The box [32 tokens][32 weights rows] (64-byte rows, the 16-byte pieces swizzled
+// over pairs of rows, so that neither side meets a bank twice) to `count` rows of
+// y or pre: four lanes per row.
+__device__ __forceinline__ void store_box(void *dst, int64_t stride, const uint8_t *box, int n0, int M, int token, int count)
 {
-    const int lane = threadIdx.x & 31;
-    if (count == 32) {
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tma_store_2d(map, box, n0, token);   // clipped at M
-    } else {
-        __syncwarp();
-        const int piece = lane & 3, n = n0 + 8 * piece;
-        uint16_t *out = reinterpret_cast<uint16_t *>(dst) + token * stride + n;
+    const int lane = threadIdx.x & 31, piece = lane & 3, n = n0 + 8 * piece;
+    uint16_t *out = reinterpret_cast<uint16_t *>(dst) + token * stride + n;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (lane >> 2) + 8 * i;
-            if (r < count && n < M)
-                *reinterpret_cast<uint4 *>(out + r * stride) =
-                    *reinterpret_cast<const uint4 *>(box + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16));
-        }
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        if (r < count && n < M)
+            *reinterpret_cast<uint4 *>(out + r * stride) =
+                *reinterpret_cast<const uint4 *>(box + r * 64 + ((piece ^ ((r >> 1) & 3)) * 16));
     }
-    if (lane == 0) ptx::bulk_commit_group();   // (an empty group where nothing was issued)
-    __syncwarp();
+}
+
+// The rows of pre under a chunk, in the registers of the lanes that put them into the box.
+__device__ __forceinline__ void load_pre(uint4 (&v)[4], const void *src, int64_t stride, int n0, int M, int token, int count)
+{
+    const int lane = threadIdx.x & 31, n = n0 + 8 * (lane & 3);
+    const uint16_t *in = reinterpret_cast<const uint16_t *>(src) + token * stride + n;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (lane >> 2) + 8 * i;
+        v[i] = r < count && n < M ? __ldg(reinterpret_cast<const uint4 *>(in + r * stride)) : make_uint4(0, 0, 0, 0);
+    }
 }
 
 // One 32 x 32 chunk of the accumulator, from the fragments of tmem_ld_16x256b_x4
 // (r[0..15] weights rows 0..15, r[16..31] rows 16..31): bias and activation
-// (FORWARD), or the slope at pre (DGRAD, read from the box that dx replaces).
-// seq counts the warp's boxes: two take turns.
+// (FORWARD), or the slope at pre (DGRAD; its rows are in `pre`).
 template <typename T, int MODE, int ACT>
-__device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const CUtensorMap *map_y, const CUtensorMap *map_pre,
-                                             const uint32_t (&r)[32], const float (&bias)[4], uint8_t *boxes, int &seq,
-                                             int n0, int token, int count)
+__device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const uint32_t (&r)[32], const float (&bias)[4],
+                                             const uint4 (&pre)[4], uint8_t *box, int n0, int token, int count)
 {
     const int lane = threadIdx.x & 31;
     // this lane's row of each of four blocks that lie side by side along n, tokens 8b + lane%8
-    const uint32_t sw = (uint32_t)(((lane >> 3) ^ ((lane >> 1) & 3)) * 16);   // token 8b + r: (token >> 1) & 3 = (r >> 1) & 3
-    const uint32_t off = (uint32_t)((lane & 7) * 64) + sw;
+    const uint32_t at = ptx::smem_u32(box) + (uint32_t)((lane & 7) * 64 + ((lane >> 3) ^ ((lane >> 1) & 3)) * 16);
+    // block b's fragments: weights rows 8j + lane/4, j = 0..3
+    auto pair = [&](int b, int j) {
+        const int k = (j >> 1) * 16 + 4 * b + 2 * (j & 1);
+        return make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+    };
     if constexpr (MODE == GROUPED_FORWARD) {
-        auto emit = [&](auto value, const CUtensorMap *map, void *dst, int64_t stride) {
-            uint8_t *box = boxes + (seq & 1) * kBoxBytes;
-            ++seq;
-            if (lane == 0) ptx::bulk_wait_group_read<1>();   // the store before the last has read this box
-            __syncwarp();
+        auto emit = [&](auto value, void *dst, int64_t stride) {
+            __syncwarp();   // the box has been read
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 uint32_t w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int k = (j >> 1) * 16 + 4 * b + 2 * (j & 1);
-                    const float2 v = value(fadd2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), dup2(bias[j])));
+                    const float2 v = value(fadd2(pair(b, j), dup2(bias[j])));
                     w[j] = Half2Of<T>::pack(v.x, v.y);
                 }
-                stmatrix_x4_trans(ptx::smem_u32(box) + off + b * 512, w[0], w[1], w[2], w[3]);
+                stmatrix_x4_trans(at + b * 512, w[0], w[1], w[2], w[3]);
             }
-            store_box(map, dst, stride, box, n0, p.M, token, count);
+            __syncwarp();
+            store_box(dst, stride, box, n0, p.M, token, count);
         };
-        if (p.pre) emit([](float2 z) { return z; }, map_pre, p.pre, p.pre_stride);
-        emit([](float2 z) { return act_value2<ACT>(z); }, map_y, p.y, p.y_stride);
+        if (p.pre) emit([](float2 z) { return z; }, p.pre, p.pre_stride);
+        emit([](float2 z) { return act_value2<ACT>(z); }, p.y, p.y_stride);
     } else {
-        uint8_t *box = boxes + (seq & 1) * kBoxBytes;
-        ++seq;
-        if (ACT == TF_ACT_NONE) {
-            if (lane == 0) ptx::bulk_wait_group_read<1>();
+        __syncwarp();
+        if (ACT != TF_ACT_NONE) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int q = (lane >> 2) + 8 * i;
+                *reinterpret_cast<uint4 *>(box + q * 64 + (((lane & 3) ^ ((q >> 1) & 3)) * 16)) = pre[i];
+            }
             __syncwarp();
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const uint32_t addr = ptx::smem_u32(box) + off + b * 512;
             uint32_t z[4], w[4];
-            if (ACT != TF_ACT_NONE) ldmatrix_x4_trans(addr, z);
+            if (ACT != TF_ACT_NONE) ldmatrix_x4_trans(at + b * 512, z);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int k = (j >> 1) * 16 + 4 * b + 2 * (j & 1);
-                float2 v = make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+                float2 v = pair(b, j);
                 if (ACT != TF_ACT_NONE) v = fmul2(v, act_slope2<ACT>(Half2Of<T>::unpack(z[j])));
                 w[j] = Half2Of<T>::pack(v.x, v.y);
             }
             __syncwarp();   // (a block's four rows are read before they are replaced)
-            stmatrix_x4_trans(addr, w[0], w[1], w[2], w[3]);
+            stmatrix_x4_trans(at + b * 512, w[0], w[1], w[2], w[3]);
         }
-        store_box(map_y, p.y, p.y_stride, box, n0, p.M, token, count);
+        __syncwarp();
+        store_box(p.y, p.y_stride, box, n0, p.M, token, count);
     }
 }
 
@@ -379,7 +366,6 @@ __device__ __forceinline__ int sums_of(int w)
 template <int MODE, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                        const __grid_constant__ CUtensorMap tmap_out, const __grid_constant__ CUtensorMap tmap_pre,
                         const __grid_constant__ UmmaArgs p)
 {
     constexpr bool PAIR = CG == 2;
@@ -393,8 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint64_t *ready = drain + 1, *freed = ready + 2;
-    uint64_t *loaded = freed + 2;           // DGRAD: each epilogue warp's two boxes of pre
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(loaded + 2 * kEpiWarps);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(freed + 2);
     int *row = reinterpret_cast<int *>(smem + p.off_sched);      // [groups + 1]
     int *tile = row + p.groups + 1;                              // [groups + 1]
     int *order = tile + p.groups + 1;                            // [groups]
@@ -424,12 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the producer, the MMA issuer (of the first CTA), WGRAD's zeroing warp, the epilogue warps
             ptx::mbar_init(&freed[i], 1 + (leader ? 1 : 0) + (WG ? 1 : 0) + kEpiWarps);
         }
-        if (MODE == GROUPED_DGRAD)
-            for (int i = 0; i < 2 * kEpiWarps; ++i) ptx::mbar_init(&loaded[i], 1);
         ptx::mbar_init_fence();
         ptx::prefetch_tensormap(&tmap_a);
         ptx::prefetch_tensormap(&tmap_b);
-        ptx::prefetch_tensormap(&tmap_out);
         *bad = 0;
     }
     if (warp == 1) {
@@ -753,30 +735,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Warp w reads TMEM lanes 32*(w%4) .. +31 (one weights row per lane) and
         // every second 32-column chunk.
         const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
-        uint8_t *boxes = smem + p.off_epi + (warp - kFirstEpiWarp) * kEpiBytes;
-        uint64_t *in_bar = loaded + 2 * (warp - kFirstEpiWarp);
+        uint8_t *box = smem + p.off_epi + (warp - kFirstEpiWarp) * box_bytes(WG);
         const bool slope = MODE == GROUPED_DGRAD && p.act != TF_ACT_NONE;
-        int local = 0, seq = 0;
-        uint32_t in_phase = 0, fetching = 0;
+        int local = 0;
         bool ok = true;
         ok &= each_item<MODE>(p, items, [&](const Item &it, int part, int, int, int nkb) {
             const int n0 = it.m0 + crank * BM + q * 32;
             const int b = local & 1;
             const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
-            const bool mine = q * 32 < plan.bm && n0 < p.M;   // (boxes past the last weights row are neither loaded nor stored)
-            // DGRAD: the box of pre under chunk c, into the box that the seq-th result will take; the store
-            // that used it last (two boxes ago) has read it
-            auto fetch = [&](int c, int s) {
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                fetching |= 1u << (s & 1);
-                if (lane == 0) {
-                    ptx::bulk_wait_group_read<0>();
-                    ptx::mbar_arrive_expect_tx(&in_bar[s & 1], kBoxBytes);
-                    ptx::tma_load_2d(boxes + (s & 1) * kBoxBytes, &tmap_pre, &in_bar[s & 1], n0, it.t0 + c * 32);
-                }
-            };
-            if (slope && mine && h * 32 < width) fetch(h, seq);
+            const bool mine = q * 32 < plan.bm && n0 < p.M;
             float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (MODE == GROUPED_FORWARD && p.bias) {
 #pragma unroll
@@ -785,6 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (n < p.M) bias[j] = __ldg(p.bias + (int64_t)it.e * p.M + n);
                 }
             }
+            uint4 pre[4] = {};
+            if (slope && mine && h * 32 < width)
+                load_pre(pre, p.pre, p.pre_stride, n0, p.M, it.t0 + h * 32, min(32, width - h * 32));
             if (nkb > 0) {
                 const bool got = ptx::mbar_wait(&tfull[b], (uint32_t)(local >> 1) & 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
@@ -799,40 +769,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (WG) {
                     if (nkb > 0) {
                         ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), r);
+                        ptx::tmem_ld_wait();
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0u;
                     }
-                    // the store before has read the box, and an earlier part's sums are in memory
-                    if (lane == 0) {
-                        if (part > 0) ptx::bulk_wait_group_all();
-                        else ptx::bulk_wait_group_read<0>();
-                    }
-                    __syncwarp();
-                    ptx::tmem_ld_wait();
+                    __syncwarp();   // the box has been read
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)   // 128-byte swizzle: 16-byte piece j of row l lies at j ^ (l % 8)
-                        *reinterpret_cast<uint4 *>(boxes + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                    for (int j = 0; j < 8; ++j)   // 16-byte piece j of row l lies at j ^ (l % 8)
+                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) =
                             make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        // clipped at the group's N rows and K columns
-                        if (p.accumulate || part > 0) tma_add_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
-                        else tma_store_3d(&tmap_out, boxes, it.t0 + c * 32, n0, it.e);
-                        ptx::bulk_commit_group();
+                    const int piece = lane & 7, col = it.t0 + c * 32 + 4 * piece;
+                    float *out = reinterpret_cast<float *>(p.y) + ((int64_t)it.e * p.M + n0) * p.cols + col;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int l = (lane >> 3) + 4 * i;
+                        if (n0 + l < p.M && col < p.cols) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(box + l * 128 + ((piece ^ (l & 7)) * 16));
+                            // one thread alone writes an element, part after part: the order of its additions is fixed
+                            if (p.accumulate || part > 0) red_add_f32x4(out + (int64_t)l * p.cols, v);
+                            else *reinterpret_cast<uint4 *>(out + (int64_t)l * p.cols) = v;
+                        }
                     }
                 } else {
                     tmem_ld_16x256b_x4(taddr + (uint32_t)(c * 32), r);
                     tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32), r + 16);
-                    const int count = min(32, width - c * 32), token = it.t0 + c * 32;
-                    if (slope) {
-                        const int s = seq & 1;
-                        if (!ptx::mbar_wait(&in_bar[s], (in_phase >> s) & 1u, p.wait_ns)) ok = false;
-                        in_phase ^= 1u << s;
-                        fetching &= ~(1u << s);
-                        if ((c + kEpiWarps / 4) * 32 < width) fetch(c + kEpiWarps / 4, seq + 1);
-                    }
+                    const int count = min(32, width - c * 32), token = it.t0 + c * 32, next = c + kEpiWarps / 4;
                     ptx::tmem_ld_wait();
                     for (int s = 1; s < sums_of<MODE, CG>(it.w); ++s) {   // the sums of the other sixteens of every K step
                         uint32_t u[32];
@@ -842,12 +805,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(u[j]));
                     }
+                    uint4 cur[4] = {pre[0], pre[1], pre[2], pre[3]};
+                    if (slope && next * 32 < width)
+                        load_pre(pre, p.pre, p.pre_stride, n0, p.M, it.t0 + next * 32, min(32, width - next * 32));
                     auto finish = [&](auto act) {
                         constexpr int ACT = decltype(act)::value;
-                        if (p.bf16)
-                            finish_chunk<__nv_bfloat16, MODE, ACT>(p, &tmap_out, &tmap_pre, r, bias, boxes, seq, n0, token, count);
-                        else
-                            finish_chunk<__half, MODE, ACT>(p, &tmap_out, &tmap_pre, r, bias, boxes, seq, n0, token, count);
+                        if (p.bf16) finish_chunk<__nv_bfloat16, MODE, ACT>(p, r, bias, cur, box, n0, token, count);
+                        else finish_chunk<__half, MODE, ACT>(p, r, bias, cur, box, n0, token, count);
                     };
                     if (p.act == TF_ACT_GELU) finish(std::integral_constant<int, TF_ACT_GELU>());
                     else if (p.act == TF_ACT_SILU) finish(std::integral_constant<int, TF_ACT_SILU>());
@@ -865,9 +829,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return true;
         });
-        if (lane == 0) ptx::bulk_wait_group_all();
-        for (int s = 0; s < 2; ++s)   // a box asked for and not waited for (after a time-out) lands before the CTA exits
-            if ((fetching >> s) & 1u) ptx::mbar_wait(&in_bar[s], (in_phase >> s) & 1u, p.wait_ns);
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
     }
 
@@ -901,30 +862,30 @@ EncodeTiledFn encode_tiled()
 }
 
 bool encode(CUtensorMap *m, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+            const cuuint64_t *strides, const cuuint32_t *box)
 {
     const cuuint32_t ones[3] = {1, 1, 1};
     EncodeTiledFn fn = encode_tiled();
     return fn && fn(m, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, ones,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // [rows][cols] matrix of 16-bit values, rows `stride` elements apart.
 bool encode_rows(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_t rows, int64_t cols, int64_t stride,
-                 int box_cols, int box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B)
+                 int box_cols, int box_rows)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)stride * 2};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
-    return encode(m, type, 2, base, dims, strides, box, swizzle);
+    return encode(m, type, 2, base, dims, strides, box);
 }
 
-// [groups][N][K] weights or weights' gradients.
+// [groups][N][K] weights.
 bool encode_groups(CUtensorMap *m, CUtensorMapDataType type, const void *base, int64_t groups, int64_t N, int64_t K,
-                   int size, int box_cols, int box_rows)
+                   int box_cols, int box_rows)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)N, (cuuint64_t)groups};
-    const cuuint64_t strides[2] = {(cuuint64_t)K * size, (cuuint64_t)N * K * size};
+    const cuuint64_t strides[2] = {(cuuint64_t)K * 2, (cuuint64_t)N * K * 2};
     const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
     return encode(m, type, 3, base, dims, strides, box);
 }
@@ -974,7 +935,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     UmmaArgs p = {};
     p.offsets = a.offsets;
     p.bias = a.bias;
-    p.y = a.y;
+    p.y = WG ? a.dw : a.y;
     p.pre = a.pre;
     p.err = device_error_word();
     p.wait_ns = wait_limit_ns();
@@ -996,32 +957,27 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.bf16 = a.dtype == TF_BF16;
     p.accumulate = a.accumulate;
     const int sched = (3 * (a.groups + 1) + 2) * 4;
-    const int fixed = kEpiWarps * kEpiBytes + kItemBytes + kNumBars * 8 + 16 + sched;
+    const int fixed = kEpiWarps * box_bytes(WG) + kItemBytes + kNumBars * 8 + 16 + sched;
     const int ring = (kSmemLimit - fixed) / 1024 * 1024;
     if (ring < 2 * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
     p.off_epi = ring;
-    p.off_items = p.off_epi + kEpiWarps * kEpiBytes;
+    p.off_items = p.off_epi + kEpiWarps * box_bytes(WG);
     p.off_bar = p.off_items + kItemBytes;
     p.off_sched = p.off_bar + kNumBars * 8 + 16;
     const int smem = p.off_sched + sched;
 
     const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap ta, tb, td, tp;
-    memset(&tp, 0, sizeof tp);
+    CUtensorMap ta, tb;
     bool ok;
     if (MODE == GROUPED_FORWARD)
-        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, BK, p.a_box) &&
+        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, BK, p.a_box) &&
              encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, BK, p.box_rows);
     else if (MODE == GROUPED_DGRAD)
-        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 2, 64, BK) &&
+        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 64, BK) &&
              encode_rows(&tb, type, a.dy, a.rows, a.N, a.dy_stride, BK, p.box_rows);
     else
         ok = encode_rows(&ta, type, a.dy, a.rows, a.N, a.dy_stride, 64, BK) &&
-             encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, 64, BK) &&
-             encode_groups(&td, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.dw, a.groups, a.N, a.K, 4, 32, 32);
-    if (!WG)   // y and pre in boxes of 32 rows x 32 weights rows
-        ok = ok && encode_rows(&td, type, a.y, a.rows, p.M, a.y_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
-             (!a.pre || encode_rows(&tp, type, a.pre, a.rows, p.M, a.pre_stride, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B));
+             encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, 64, BK);
     if (!ok) return cudaErrorInvalidValue;
 
     int units = 0;
@@ -1047,7 +1003,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG>, ta, tb, td, tp, p));
+    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG>, ta, tb, p));
 }
 
 template <int MODE>
