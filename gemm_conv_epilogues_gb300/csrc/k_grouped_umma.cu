@@ -54,8 +54,7 @@ constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
 constexpr int kMaxSorted = 256;                   // groups up to this many are sorted by their tiles' cost
 // An epilogue warp's box: 32 tokens x 32 weights rows of 16 bits, or WGRAD's 32 x
 // 32 fp32.  It turns the accumulator's columns into rows for 16-byte stores by
-// the threads.  (TMA stores of the same boxes cost the main loop 20 us of 160:
-// the TMA engine is busy with its loads 90% of the time.)
+// the threads (TMA stores of the same boxes measured the same).
 constexpr int box_bytes(bool wgrad) { return wgrad ? 4096 : 2048; }
 // WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
 // round, so an accumulator's error grows with the number of MMAs it takes; a
@@ -235,7 +234,7 @@ struct Items {
 // Calls f(item, part, first row, rows, K steps) for every part of every item of
 // this CTA or pair, in order, until it returns false; false where a list never
 // came.  All lanes of a warp call together.
-template <int MODE, typename F>
+template <int MODE, int KSUB, typename F>
 __device__ __forceinline__ bool each_item(const UmmaArgs &p, const Items &s, F f)
 {
     int i = 0;
@@ -255,7 +254,7 @@ __device__ __forceinline__ bool each_item(const UmmaArgs &p, const Items &s, F f
                 if (!f(it, part, it.first + done, rows, (rows + BK - 1) / BK)) return true;
             }
         } else {
-            if (!f(it, 0, it.first, it.tv, (p.red + BK - 1) / BK)) return true;
+            if (!f(it, 0, it.first, it.tv, (p.red + BK * KSUB - 1) / (BK * KSUB))) return true;
         }
         if ((i & 31) == 31) {
             __syncwarp();
@@ -363,7 +362,9 @@ __device__ __forceinline__ int sums_of(int w)
     return MODE != GROUPED_WGRAD && CG == 1 && w <= 64 ? 4 : 1;
 }
 
-template <int MODE, int CG>
+// KSUB: K blocks of 64 per stage.  Handing a stage over takes its issuers ~300
+// cycles, so small tiles take four; pairs two.
+template <int MODE, int CG, int KSUB>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                         const __grid_constant__ UmmaArgs p)
@@ -461,11 +462,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         width += __shfl_xor_sync(0xffffffffu, width, o);
                     }
                     if (tiles == 0) break;
-                    // narrower weights tiles only where a tile is paced by its weights' way from HBM (an
-                    // SM's share of it brings a K step of 52 rows in the ~290 cycles that one takes to issue)
+                    // narrower weights tiles only where a tile is paced by its weights' way from HBM
                     for (int bm = BM * CG; bm >= (p.bm ? BM * CG : p.a_box); bm >>= 1) {
                         const int waves = (tiles * ((p.M + bm - 1) / bm) + ncl - 1) / ncl;
-                        const int cost = p.bm ? waves * (width / tiles + 24) : waves * max(bm, 52);
+                        const int cost = p.bm ? waves * (width / tiles + 24) : waves * (bm + 8);
                         if (cost < best) {
                             best = cost;
                             pick_n = bn;
@@ -539,9 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    // the ring: a stage's B tile follows as many rows of A as the tile has (an MMA of 128 rows then reads
-    // past them, into B and the next stage: rows that are not stored)
-    const int a_bytes = plan.bm / CG * BK * 2, stage_bytes = a_bytes + (WG ? kMaxBN : p.bn) / CG * BK * 2;
+    // the ring: stages of `ksub` K blocks; a block's B tile follows as many rows of A as the tile has (an MMA
+    // of 128 rows then reads past them, into B and what follows: rows that are not stored)
+    const int a_bytes = plan.bm / CG * BK * 2, sub_bytes = a_bytes + (WG ? kMaxBN : p.bn) / CG * BK * 2;
+    const int stage_bytes = sub_bytes * KSUB;
     const int stages = min(kMaxStages, p.off_epi / stage_bytes);
     const Items items = {reinterpret_cast<Item *>(smem + p.off_items), ready, freed, p.wait_ns, cid, ncl, num_work};
     if (warp == 0) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 0, issued = 0, last_phase = 0;
         bool ok = true;
         const bool issuer = elect_one();
-        ok &= each_item<MODE>(p, items, [&](const Item &it, int, int first, int rows, int nkb) {
+        ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int, int first, int rows, int nkb) {
             const int mrow = it.m0 + crank * BM;
             const int abox = plan.bm / CG / p.a_box;   // boxes of the weights' side
             // boxes of the N side this CTA loads: its half of the tile's rows (or columns)
@@ -561,46 +562,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 if (issuer) {
-                    uint8_t *a_dst = smem + stage * stage_bytes, *b_dst = a_dst + a_bytes;
-                    const int k0 = kb * BK;
                     const bool ragged = WG && kb == nkb - 1 && (rows & 15) != 0;
                     uint64_t *bar = ragged ? &land[stage] : &full[stage];
+                    // K blocks of this stage (no box starts past the end of K)
+                    const int subs = KSUB == 1 ? 1 : min(KSUB, (p.red + BK - 1) / BK - kb * KSUB);
                     if (ragged) {
                         ptx::mbar_arrive_expect_tx(bar, own);
                     } else if (leader) {
-                        ptx::mbar_arrive_expect_tx(bar, CG * own);
+                        ptx::mbar_arrive_expect_tx(bar, CG * own * (uint32_t)subs);
                         if (WG && PAIR) ptx::mbar_arrive(bar);
                     }
                     const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, ragged ? (uint32_t)crank : 0u) : 0u;
-                    for (int i = 0; i < abox; ++i) {
-                        uint8_t *dst = a_dst + i * p.a_box * (BK * 2);
-                        if constexpr (MODE == GROUPED_FORWARD) {
-                            // a box that would start past the last weights row starts on it: its rows are never stored
-                            const int n = min(mrow + i * p.a_box, p.M - 1);
-                            if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, k0, n, it.e);
-                            else ptx::tma_load_3d(dst, &tmap_a, bar, k0, n, it.e);
-                        } else {
-                            const int c = min(mrow + 64 * i, (p.M - 1) & ~7);   // 16-byte aligned, inside the tensor
-                            if constexpr (MODE == GROUPED_DGRAD) {
-                                if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, c, k0, it.e);
-                                else ptx::tma_load_3d(dst, &tmap_a, bar, c, k0, it.e);
+                    for (int sub = 0; sub < subs; ++sub) {
+                        uint8_t *a_dst = smem + stage * stage_bytes + sub * sub_bytes, *b_dst = a_dst + a_bytes;
+                        const int k0 = (kb * KSUB + sub) * BK;
+                        for (int i = 0; i < abox; ++i) {
+                            uint8_t *dst = a_dst + i * p.a_box * (BK * 2);
+                            if constexpr (MODE == GROUPED_FORWARD) {
+                                // a box that would start past the last weights row starts on it: its rows are never stored
+                                const int n = min(mrow + i * p.a_box, p.M - 1);
+                                if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, k0, n, it.e);
+                                else ptx::tma_load_3d(dst, &tmap_a, bar, k0, n, it.e);
                             } else {
-                                if constexpr (PAIR) ptx::tma_load_2d_pair(dst, &tmap_a, bar_cl, c, first + k0);
-                                else ptx::tma_load_2d(dst, &tmap_a, bar, c, first + k0);
+                                const int c = min(mrow + 64 * i, (p.M - 1) & ~7);   // 16-byte aligned, inside the tensor
+                                if constexpr (MODE == GROUPED_DGRAD) {
+                                    if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, c, k0, it.e);
+                                    else ptx::tma_load_3d(dst, &tmap_a, bar, c, k0, it.e);
+                                } else {
+                                    if constexpr (PAIR) ptx::tma_load_2d_pair(dst, &tmap_a, bar_cl, c, first + k0);
+                                    else ptx::tma_load_2d(dst, &tmap_a, bar, c, first + k0);
+                                }
                             }
                         }
-                    }
-                    for (int i = 0; i < nbox; ++i) {
-                        if constexpr (WG) {
-                            const int c = min(it.t0 + crank * half + 64 * i, (p.cols - 1) & ~7);
-                            if constexpr (PAIR) ptx::tma_load_2d_pair(b_dst + i * kChunkBytes, &tmap_b, bar_cl, c, first + k0);
-                            else ptx::tma_load_2d(b_dst + i * kChunkBytes, &tmap_b, bar, c, first + k0);
-                        } else {
-                            // rows past the group are other groups' (or zero): their columns of D are never stored
-                            const int m = min(it.t0 + crank * half + i * p.box_rows, p.rows - 1);
-                            uint8_t *dst = b_dst + i * p.box_rows * (BK * 2);
-                            if constexpr (PAIR) ptx::tma_load_2d_pair(dst, &tmap_b, bar_cl, k0, m);
-                            else ptx::tma_load_2d(dst, &tmap_b, bar, k0, m);
+                        for (int i = 0; i < nbox; ++i) {
+                            if constexpr (WG) {
+                                const int c = min(it.t0 + crank * half + 64 * i, (p.cols - 1) & ~7);
+                                if constexpr (PAIR) ptx::tma_load_2d_pair(b_dst + i * kChunkBytes, &tmap_b, bar_cl, c, first + k0);
+                                else ptx::tma_load_2d(b_dst + i * kChunkBytes, &tmap_b, bar, c, first + k0);
+                            } else {
+                                // rows past the group are other groups' (or zero): their columns of D are never stored
+                                const int m = min(it.t0 + crank * half + i * p.box_rows, p.rows - 1);
+                                uint8_t *dst = b_dst + i * p.box_rows * (BK * 2);
+                                if constexpr (PAIR) ptx::tma_load_2d_pair(dst, &tmap_b, bar_cl, k0, m);
+                                else ptx::tma_load_2d(dst, &tmap_b, bar, k0, m);
+                            }
                         }
                     }
                 }
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a), desc_of(b), id, acc);
                 else ptx::umma_bf16(d, desc_of(a), desc_of(b), id, acc);
             };
-            ok &= each_item<MODE>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
+            ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
                 if (nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
                 const uint32_t apart = sums_of<MODE, CG>(it.w) > 1 ? 64u : 0u;
@@ -652,12 +657,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t bb = b_low + (uint32_t)stage * (uint32_t)(stage_bytes >> 4);
                     // WGRAD: sixteens of rows past the group's end are left out
                     const int steps = WG ? min(BK / UMMA_K, (rows - kb * BK + UMMA_K - 1) / UMMA_K) : BK / UMMA_K;
+                    const int subs = KSUB == 1 ? 1 : min(KSUB, (p.red + BK - 1) / BK - kb * KSUB);
                     if (issuer) {
                         mma(d_tmem, a, bb, id, acc);
                         const uint32_t acc1 = apart ? acc : 1u;
                         if (!WG || steps > 1) mma(d_tmem + apart, a + a_step, bb + b_step, id, acc1);
                         if (!WG || steps > 2) mma(d_tmem + 2 * apart, a + 2 * a_step, bb + 2 * b_step, id, acc1);
                         if (!WG || steps > 3) mma(d_tmem + 3 * apart, a + 3 * a_step, bb + 3 * b_step, id, acc1);
+#pragma unroll
+                        for (int sub = 1; sub < KSUB; ++sub) {
+                            if (sub >= subs) break;
+                            const uint32_t as = a + (uint32_t)sub * (uint32_t)(sub_bytes >> 4), bs = bb + (uint32_t)sub * (uint32_t)(sub_bytes >> 4);
+                            mma(d_tmem, as, bs, id, 1u);
+                            mma(d_tmem + apart, as + a_step, bs + b_step, id, 1u);
+                            mma(d_tmem + 2 * apart, as + 2 * a_step, bs + 2 * b_step, id, 1u);
+                            mma(d_tmem + 3 * apart, as + 3 * a_step, bs + 3 * b_step, id, 1u);
+                        }
                         if constexpr (PAIR) commit_both(&empty[stage]);
                         else ptx::umma_commit(&empty[stage]);
                         if (kb == nkb - 1) {
@@ -691,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t land_phase = 0;
         int blocks = 0;    // K steps before this item
         bool ok = true;
-        ok &= each_item<MODE>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
+        ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
             blocks += nkb;
             if ((rows & 15) == 0) return true;
             const int stage = (blocks - 1) % stages;
@@ -739,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool slope = MODE == GROUPED_DGRAD && p.act != TF_ACT_NONE;
         int local = 0;
         bool ok = true;
-        ok &= each_item<MODE>(p, items, [&](const Item &it, int part, int, int, int nkb) {
+        ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int part, int, int, int nkb) {
             const int n0 = it.m0 + crank * BM + q * 32;
             const int b = local & 1;
             const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
@@ -892,7 +907,7 @@ bool encode_groups(CUtensorMap *m, CUtensorMapDataType type, const void *base, i
 
 // CTAs (or pairs) that can be resident at once, by device; the kernel's
 // shared-memory limit is raised on the way.
-template <int MODE, int CG>
+template <int MODE, int CG, int KSUB>
 cudaError_t resident(int *units)
 {
     static std::mutex mu;
@@ -902,7 +917,7 @@ cudaError_t resident(int *units)
     if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!known[d]) {
-        auto kern = grouped_umma_kernel<MODE, CG>;
+        auto kern = grouped_umma_kernel<MODE, CG, KSUB>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
         if (e != cudaSuccess) return e;
         int n = sm_count();
@@ -928,7 +943,7 @@ cudaError_t resident(int *units)
     return cudaSuccess;
 }
 
-template <int MODE, int CG>
+template <int MODE, int CG, int KSUB>
 cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
 {
     constexpr bool WG = MODE == GROUPED_WGRAD;
@@ -949,8 +964,8 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.cols = a.K;
     p.bn = bn;
     p.box_rows = bn / CG < 64 ? bn / CG : 64;
-    // few rows per group (CG = 1): weights tiles of 128, 64 or (K-major) 32 rows, as boxes of that least size
-    const bool small = CG == 1 && !WG && bn <= 64;
+    // few rows per group: weights tiles of 128, 64 or (K-major) 32 rows, as boxes of that least size
+    const bool small = KSUB == 4;
     p.bm = small ? 0 : BM * CG;
     p.a_box = MODE == GROUPED_FORWARD ? (small ? 32 : BM) : 64;
     p.act = a.act;
@@ -959,7 +974,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     const int sched = (3 * (a.groups + 1) + 2) * 4;
     const int fixed = kEpiWarps * box_bytes(WG) + kItemBytes + kNumBars * 8 + 16 + sched;
     const int ring = (kSmemLimit - fixed) / 1024 * 1024;
-    if (ring < 2 * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
+    if (ring < 2 * KSUB * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
     p.off_epi = ring;
     p.off_items = p.off_epi + kEpiWarps * box_bytes(WG);
     p.off_bar = p.off_items + kItemBytes;
@@ -981,7 +996,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     if (!ok) return cudaErrorInvalidValue;
 
     int units = 0;
-    cudaError_t e = resident<MODE, CG>(&units);
+    cudaError_t e = resident<MODE, CG, KSUB>(&units);
     if (e != cudaSuccess) return e;
     const int bm = p.bm ? p.bm : p.a_box;   // (the narrowest tile gives the most work items)
     const int64_t mt = (p.M + bm - 1) / bm;
@@ -1003,7 +1018,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = CG == 2 ? 2 : 1;
-    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG>, ta, tb, p));
+    return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG, KSUB>, ta, tb, p));
 }
 
 template <int MODE>
@@ -1011,9 +1026,13 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
 {
     const int64_t M = MODE == GROUPED_DGRAD ? a.K : a.N;
     const int64_t avg = a.rows / a.groups;   // rows per group, as far as the host knows
-    if (MODE == GROUPED_WGRAD) return M > BM && a.K > 128 ? launch_mode<MODE, 2>(a, kMaxBN, st) : launch_mode<MODE, 1>(a, kMaxBN, st);
-    if (M > BM && avg > 128) return launch_mode<MODE, 2>(a, kMaxBN, st);
-    return launch_mode<MODE, 1>(a, avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256, st);
+    if constexpr (MODE == GROUPED_WGRAD) {
+        return M > BM && a.K > 128 ? launch_mode<MODE, 2, 1>(a, kMaxBN, st) : launch_mode<MODE, 1, 1>(a, kMaxBN, st);
+    } else {
+        if (M > BM && avg > 128) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
+        if (avg <= 64) return launch_mode<MODE, 1, 4>(a, avg <= 16 ? 16 : avg <= 32 ? 32 : 64, st);
+        return launch_mode<MODE, 1, 1>(a, avg <= 128 ? 128 : 256, st);
+    }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
