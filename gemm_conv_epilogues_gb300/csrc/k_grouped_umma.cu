@@ -23,6 +23,8 @@
 //         divisions, done by the MMA issuer between two tiles, left the tensor
 //         pipe idle for 1.3 us per tile
 //   4-11  epilogue: TMEM -> registers -> bias, activation -> y
+//   12-15 WGRAD: the bias gradient, from dy itself, beside the products (a kernel
+//         of its own cost 38 us of 230: it reads dy once more)
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the
 // device error word and winds down.
 #include <cuda.h>
@@ -44,7 +46,8 @@ constexpr int UMMA_K = 16;
 constexpr int kMaxBN = 256;             // widest row tile: one accumulator is 256 TMEM columns
 constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
-constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+constexpr int kBiasWarps = 4;           // WGRAD: warps that sum dy's columns for the bias gradient
+constexpr int threads_of(int mode) { return 32 * (kFirstEpiWarp + kEpiWarps + (mode == GROUPED_WGRAD ? kBiasWarps : 0)); }
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kABytes = BM * BK * 2;
 constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or N-major operand
@@ -52,15 +55,16 @@ constexpr int kNumBars = 3 * kMaxStages + 9;      // full, empty, land; accumula
                                                   // item lists ready x2, free x2
 constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
 constexpr int kMaxSorted = 256;                   // groups up to this many are sorted by their tiles' cost
-// An epilogue warp's box: 32 tokens x 32 weights rows of 16 bits, or WGRAD's 32 x
-// 32 fp32.  It turns the accumulator's columns into rows for 16-byte stores by
-// the threads (TMA stores of the same boxes measured the same).
-constexpr int box_bytes(bool wgrad) { return wgrad ? 4096 : 2048; }
+// An epilogue warp's box, 32 tokens x 32 weights rows of 16 bits: it turns the
+// accumulator's columns into rows for 16-byte stores by the threads (TMA stores
+// of the same boxes measured the same).
+constexpr int kBoxBytes = 32 * 32 * 2;
 // WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
-// round, so an accumulator's error grows with the number of MMAs it takes; a
-// longer group is cut into parts whose fp32 sums are added in memory.  Measured
-// on 16384 rows in 16 groups (up to 2300 rows each): relative error 1.4e-6 in
-// one part, against 2.9e-7 for fp32 products.
+// round, so an accumulator's error grows with the number of MMAs it takes
+// (relative error 1.4e-6 for groups of up to 2459 rows, against 2.9e-7 for fp32
+// products).  A longer group is accumulated in parts; their running sum stays
+// in the tile's other accumulator, added by the epilogue's threads.  (Adding the
+// parts in memory took 316 us for groups of 1025 rows, 208 for 1023.)
 constexpr int kMaxPartRows = 1024;
 constexpr uint32_t kTmemCols = 512;
 
@@ -81,6 +85,9 @@ struct UmmaArgs {
     int box_rows;      // rows per token box
     int off_epi, off_bar, off_items, off_sched;   // the operand ring comes first
     int act, bf16, accumulate;
+    const void *dy;    // WGRAD: for the bias gradient
+    float *dbias;
+    int64_t dy_stride;
 };
 
 // Shared-memory matrix descriptors (128-byte swizzle), as a low word that holds
@@ -134,10 +141,16 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-__device__ __forceinline__ void red_add_f32x4(float *p, uint4 v)
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t *r)
 {
-    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16 TMEM lanes x 32 columns as 8 x 8 blocks: lane l of the warp receives, for
 // column block b, row l/4 (registers 4b, 4b+1) and row l/4 + 8 (4b+2, 4b+3),
@@ -353,6 +366,53 @@ __device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const uint32_t (
     }
 }
 
+// dbias[e][n] = sum of dy[m][n] over group e's rows, without the pipeline: a warp
+// takes 64 columns of a group (16 where that leaves warps without work), 16
+// bytes per lane, eight loads in flight, fp32 sums, the lanes' rows added in a
+// fixed order.
+template <typename T>
+__device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int warp)
+{
+    const int lane = threadIdx.x & 31, warps = (int)gridDim.x * kBiasWarps;
+    const int across = p.groups * ((p.M + 63) / 64) >= warps ? 8 : 2, down = 32 / across;
+    const int piece = lane % across, r0 = lane / across, chunks = (p.M + 8 * across - 1) / (8 * across);
+    for (int u = (int)blockIdx.x * kBiasWarps + warp; u < p.groups * chunks; u += warps) {
+        const int e = s.order[u / chunks], n = (u % chunks * across + piece) * 8;
+        const int lo = s.row[e], hi = s.row[e + 1];
+        const uint16_t *src = reinterpret_cast<const uint16_t *>(p.dy) + n;
+        float2 sum[4] = {};
+        for (int m = lo + r0; m < hi && n < p.M; m += 8 * down) {
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = m + i * down < hi ? __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(m + i * down) * p.dy_stride))
+                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum[0] = fadd2(sum[0], Half2Of<T>::unpack(v[i].x));
+                sum[1] = fadd2(sum[1], Half2Of<T>::unpack(v[i].y));
+                sum[2] = fadd2(sum[2], Half2Of<T>::unpack(v[i].z));
+                sum[3] = fadd2(sum[3], Half2Of<T>::unpack(v[i].w));
+            }
+        }
+        __syncwarp();
+        for (int o = across; o < 32; o <<= 1)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum[j].x += __shfl_xor_sync(0xffffffffu, sum[j].x, o);
+                sum[j].y += __shfl_xor_sync(0xffffffffu, sum[j].y, o);
+            }
+        if (r0 == 0 && n < p.M) {
+            float *out = p.dbias + (int64_t)e * p.M + n;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                out[2 * j] = p.accumulate ? out[2 * j] + sum[j].x : sum[j].x;
+                out[2 * j + 1] = p.accumulate ? out[2 * j + 1] + sum[j].y : sum[j].y;
+            }
+        }
+    }
+}
+
 // Sums a tile is kept in: an MMA of few columns that adds to the sum of the one
 // before it waits for it (~150 cycles each, 44 of 50 us of a 16-row product), so
 // the four of a K step get a sum each.
@@ -365,7 +425,7 @@ __device__ __forceinline__ int sums_of(int w)
 // KSUB: K blocks of 64 per stage.  Handing a stage over takes its issuers ~300
 // cycles, so small tiles take four; pairs two.
 template <int MODE, int CG, int KSUB>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_of(MODE), 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                         const __grid_constant__ UmmaArgs p)
 {
@@ -435,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
         constexpr int STEP = 16 * CG;
         int wrong = 0;
-        for (int i = threadIdx.x; i <= p.groups; i += kThreads) {
+        for (int i = threadIdx.x; i <= p.groups; i += (int)blockDim.x) {
             const int v = p.offsets[i];
             row[i] = v;
             wrong |= v < 0 || v > p.rows || (i > 0 && p.offsets[i - 1] > v);
@@ -484,12 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         plan.bm = bad[2];
         plan.mt = (p.M + plan.bm - 1) / plan.bm;
         // the groups by falling cost: their tiles' width, or (WGRAD) their rows
-        for (int e = threadIdx.x; e < p.groups; e += kThreads) {
+        for (int e = threadIdx.x; e < p.groups; e += (int)blockDim.x) {
             const int T = row[e + 1] - row[e], n = (T + plan.bn - 1) / plan.bn;
             tile[e] = WG || T <= 0 ? T : (T + n - 1) / n;
         }
         cta_sync();
-        for (int e = threadIdx.x; e < p.groups; e += kThreads) {
+        for (int e = threadIdx.x; e < p.groups; e += (int)blockDim.x) {
             int rank = e;
             if (p.groups <= kMaxSorted) {
                 const int c = tile[e];
@@ -628,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (leader) {
-            int stage = 0, local = 0;
-            uint32_t phase = 0;
+            int stage = 0, b = 0;
+            uint32_t phase = 0, taken = 0;   // taken: parity of the uses of either accumulator
             bool ok = true;
             const bool issuer = elect_one();
             constexpr uint32_t a_step = desc_step(!A_MMAJOR), b_step = desc_step(!WG);
@@ -639,12 +699,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a), desc_of(b), id, acc);
                 else ptx::umma_bf16(d, desc_of(a), desc_of(b), id, acc);
             };
-            ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int, int, int rows, int nkb) {
+            ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int part, int, int rows, int nkb) {
                 if (nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
                 const uint32_t apart = sums_of<MODE, CG>(it.w) > 1 ? 64u : 0u;
-                const int b = local & 1;
-                bool got = ptx::mbar_wait<PAIR>(&tempty[b], (uint32_t)((local >> 1) & 1) ^ 1u, p.wait_ns);
+                bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(b * kMaxBN);
@@ -687,7 +746,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1u;
                     }
                 }
-                ++local;
+                taken ^= 1u << b;
+                if (part == it.parts - 1) {
+                    // a tile of several parts took the other accumulator too, for their sum; the epilogue releases
+                    // both.  (Its use of it lies between this warp's waits for the second part and for the next
+                    // tile, so no phase of that barrier is passed over unseen.)
+                    if (it.parts > 1) taken ^= 1u << (b ^ 1);
+                    b ^= 1;
+                }
                 return true;
             });
             if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
@@ -745,18 +811,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) ptx::mbar_arrive(&ready[half]);
         }
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
-    } else if (warp >= kFirstEpiWarp) {
+    } else if (warp >= kFirstEpiWarp && warp < kFirstEpiWarp + kEpiWarps) {
         // ------------------------------------------------------------ epilogue
         // Warp w reads TMEM lanes 32*(w%4) .. +31 (one weights row per lane) and
         // every second 32-column chunk.
         const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
-        uint8_t *box = smem + p.off_epi + (warp - kFirstEpiWarp) * box_bytes(WG);
+        uint8_t *box = smem + p.off_epi + (warp - kFirstEpiWarp) * kBoxBytes;
         const bool slope = MODE == GROUPED_DGRAD && p.act != TF_ACT_NONE;
-        int local = 0;
+        int b = 0;
+        uint32_t seen = 0;   // parity of the results of either accumulator
         bool ok = true;
         ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int part, int, int, int nkb) {
             const int n0 = it.m0 + crank * BM + q * 32;
-            const int b = local & 1;
             const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
             const bool mine = q * 32 < plan.bm && n0 < p.M;
             float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -771,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (slope && mine && h * 32 < width)
                 load_pre(pre, p.pre, p.pre_stride, n0, p.M, it.t0 + h * 32, min(32, width - h * 32));
             if (nkb > 0) {
-                const bool got = ptx::mbar_wait(&tfull[b], (uint32_t)(local >> 1) & 1u, p.wait_ns);
+                const bool got = ptx::mbar_wait(&tfull[b], (seen >> b) & 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
             } else if (!WG || p.accumulate) {
@@ -783,28 +849,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t r[32];
                 if constexpr (WG) {
                     if (nkb > 0) {
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c * 32), r);
+                        tmem_ld_16x256b_x4(taddr + (uint32_t)(c * 32), r);
+                        tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32), r + 16);
                         ptx::tmem_ld_wait();
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0u;
                     }
-                    __syncwarp();   // the box has been read
+                    const uint32_t saddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((b ^ 1) * kMaxBN + c * 32);
+                    if (part > 0) {   // plus the parts before
+                        uint32_t u[32];
+                        tmem_ld_16x256b_x4(saddr, u);
+                        tmem_ld_16x256b_x4(saddr + (16u << 16), u + 16);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)   // 16-byte piece j of row l lies at j ^ (l % 8)
-                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    __syncwarp();
-                    const int piece = lane & 7, col = it.t0 + c * 32 + 4 * piece;
-                    float *out = reinterpret_cast<float *>(p.y) + ((int64_t)it.e * p.M + n0) * p.cols + col;
+                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(u[j]));
+                    }
+                    if (part < it.parts - 1) {
+                        tmem_st_16x256b_x4(saddr, r);
+                        tmem_st_16x256b_x4(saddr + (16u << 16), r + 16);
+                        tmem_st_wait();
+                        continue;
+                    }
+                    // rows l/4 + 8j of the 32, columns 8k + 2(l%4) and the next: 32-byte pieces of eight rows at a time
+                    const int col = it.t0 + c * 32 + 2 * (lane & 3);
+                    float *out = reinterpret_cast<float *>(p.y) + ((int64_t)it.e * p.M + n0 + (lane >> 2)) * p.cols + col;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int l = (lane >> 3) + 4 * i;
-                        if (n0 + l < p.M && col < p.cols) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(box + l * 128 + ((piece ^ (l & 7)) * 16));
-                            // one thread alone writes an element, part after part: the order of its additions is fixed
-                            if (p.accumulate || part > 0) red_add_f32x4(out + (int64_t)l * p.cols, v);
-                            else *reinterpret_cast<uint4 *>(out + (int64_t)l * p.cols) = v;
+                    for (int j = 0; j < 4; ++j) {
+                        if (n0 + 8 * j + (lane >> 2) >= p.M) continue;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = (j >> 1) * 16 + 4 * k + 2 * (j & 1);
+                            float2 *dst = reinterpret_cast<float2 *>(out + (int64_t)(8 * j) * p.cols + 8 * k);
+                            if (col + 8 * k >= p.cols) continue;
+                            float2 v = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                            if (p.accumulate) v = fadd2(v, *dst);
+                            *dst = v;
                         }
                     }
                 } else {
@@ -834,17 +914,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (nkb > 0) {
+                const bool last = part == it.parts - 1;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[b], 0));
-                    else ptx::mbar_arrive(&tempty[b]);
+                    auto release = [&](int i) {
+                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[i], 0));
+                        else ptx::mbar_arrive(&tempty[i]);
+                    };
+                    release(b);
+                    if (last && it.parts > 1) release(b ^ 1);
                 }
-                ++local;
+                seen ^= 1u << b;
+                if (last) b ^= 1;
             }
             return true;
         });
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
+    } else if (WG && warp >= kFirstEpiWarp + kEpiWarps && p.dbias && num_work > 0) {
+        // ------------------------------------------------------------ bias gradient
+        if (p.bf16) bias_grad<__nv_bfloat16>(p, plan, warp - kFirstEpiWarp - kEpiWarps);
+        else bias_grad<__half>(p, plan, warp - kFirstEpiWarp - kEpiWarps);
     }
 
     ptx::tc_fence_before();
@@ -929,7 +1019,7 @@ cudaError_t resident(int *units)
             attr[0].val.clusterDim.z = 1;
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(n / 2 * 2));
-            cfg.blockDim = dim3(kThreads);
+            cfg.blockDim = dim3(threads_of(MODE));
             cfg.dynamicSmemBytes = kSmemLimit;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
@@ -971,12 +1061,15 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.act = a.act;
     p.bf16 = a.dtype == TF_BF16;
     p.accumulate = a.accumulate;
+    p.dy = a.dy;
+    p.dy_stride = a.dy_stride;
+    p.dbias = a.dbias;
     const int sched = (3 * (a.groups + 1) + 2) * 4;
-    const int fixed = kEpiWarps * box_bytes(WG) + kItemBytes + kNumBars * 8 + 16 + sched;
+    const int fixed = (WG ? 0 : kEpiWarps * kBoxBytes) + kItemBytes + kNumBars * 8 + 16 + sched;
     const int ring = (kSmemLimit - fixed) / 1024 * 1024;
     if (ring < 2 * KSUB * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
     p.off_epi = ring;
-    p.off_items = p.off_epi + kEpiWarps * box_bytes(WG);
+    p.off_items = p.off_epi + (WG ? 0 : kEpiWarps * kBoxBytes);
     p.off_bar = p.off_items + kItemBytes;
     p.off_sched = p.off_bar + kNumBars * 8 + 16;
     const int smem = p.off_sched + sched;
@@ -1013,7 +1106,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * CG));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_of(MODE));
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -1057,9 +1150,9 @@ cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st)
         return tma ? launch_auto<GROUPED_DGRAD>(a, st) : launch_grouped_simple(a, mode, st);
     }
     const bool tma = dims && rows_ok(a.dy, a.dy_stride) && rows_ok(a.x, a.x_stride) && aligned16(a.dw);
-    const cudaError_t e = tma ? launch_auto<GROUPED_WGRAD>(a, st) : launch_grouped_simple(a, mode, st);
-    if (e != cudaSuccess || !a.dbias) return e;
-    return launch_grouped_bias_grad(a, st);
+    if (tma) return launch_auto<GROUPED_WGRAD>(a, st);
+    const cudaError_t e = launch_grouped_simple(a, mode, st);
+    return e != cudaSuccess || !a.dbias ? e : launch_grouped_bias_grad(a, st);
 }
 
 }  // namespace tf
