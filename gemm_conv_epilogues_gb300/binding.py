@@ -109,6 +109,9 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the same handle without a Stream object (3 us)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -194,25 +197,30 @@ def tf_residual_layernorm_select(hidden) -> int:
     return _lib.tf_residual_layernorm_select(int(hidden))
 
 
-def _same_device(*tensors):
-    """The library launches on the current device: an operand of another one is refused here."""
+def _ptrs(*tensors):
+    """Device addresses (see _ptr).  The library launches on the current device: an operand of
+    another one is refused here."""
     import torch
-    here = None
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    out = []
     for t in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        if here is None:
-            here = torch.cuda.current_device()
-        if t.get_device() != here and t.is_cuda:
+        if t is None or type(t) is int:
+            out.append(t)
+        elif t.get_device() == here:
+            out.append(t.data_ptr())
+        elif t.is_cuda:
             raise ValueError(f"operand on cuda:{t.get_device()} while the current device is cuda:{here}")
+        else:
+            raise TypeError("tf_* entry points take device tensors")
+    return out
 
 
 def tf_layernorm_forward(x, x_stride, res, res_stride, gamma, beta, y, y_stride, sum, sum_stride, mean, rstd, rows,
                          hidden, eps, dtype, stream=None, check=True):
-    _same_device(x, res, gamma, beta, y, sum, mean, rstd)
-    return _check(_lib.tf_layernorm_forward(_ptr(x), x_stride, _ptr(res), res_stride, _ptr(gamma), _ptr(beta), _ptr(y),
-                                            y_stride, _ptr(sum), sum_stride, _ptr(mean), _ptr(rstd), rows, hidden, eps,
-                                            dtype, _stream(stream)), "tf_layernorm_forward", check)
+    x, res, gamma, beta, y, sum, mean, rstd = _ptrs(x, res, gamma, beta, y, sum, mean, rstd)
+    return _check(_lib.tf_layernorm_forward(x, x_stride, res, res_stride, gamma, beta, y, y_stride, sum, sum_stride,
+                                            mean, rstd, rows, hidden, eps, dtype, _stream(stream)),
+                  "tf_layernorm_forward", check)
 
 
 def tf_layernorm_backward_workspace_size(rows, hidden, dtype) -> int:
@@ -221,27 +229,25 @@ def tf_layernorm_backward_workspace_size(rows, hidden, dtype) -> int:
 
 def tf_layernorm_backward(dy, dy_stride, x, x_stride, gamma, mean, rstd, dres, dres_stride, dx, dx_stride, dgamma,
                           dbeta, rows, hidden, accumulate, dtype, workspace, workspace_bytes, stream=None, check=True):
-    _same_device(dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace)
-    return _check(_lib.tf_layernorm_backward(_ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(gamma), _ptr(mean),
-                                             _ptr(rstd), _ptr(dres), dres_stride, _ptr(dx), dx_stride, _ptr(dgamma),
-                                             _ptr(dbeta), rows, hidden, accumulate, dtype, _ptr(workspace),
+    dy, x, gamma, mean, rstd, dres, dx, dgamma, dbeta, workspace = _ptrs(dy, x, gamma, mean, rstd, dres, dx, dgamma,
+                                                                         dbeta, workspace)
+    return _check(_lib.tf_layernorm_backward(dy, dy_stride, x, x_stride, gamma, mean, rstd, dres, dres_stride, dx,
+                                             dx_stride, dgamma, dbeta, rows, hidden, accumulate, dtype, workspace,
                                              workspace_bytes, _stream(stream)), "tf_layernorm_backward", check)
 
 
 def tf_grouped_matmul(x, x_stride, w, bias, offsets, y, y_stride, pre, pre_stride, rows, groups, N, K, act, dtype,
                       stream=None, check=True):
-    _same_device(x, w, bias, offsets, y, pre)
-    return _check(_lib.tf_grouped_matmul(_ptr(x), x_stride, _ptr(w), _ptr(bias), _ptr(offsets), _ptr(y), y_stride,
-                                         _ptr(pre), pre_stride, rows, groups, N, K, act, dtype, _stream(stream)),
-                  "tf_grouped_matmul", check)
+    x, w, bias, offsets, y, pre = _ptrs(x, w, bias, offsets, y, pre)
+    return _check(_lib.tf_grouped_matmul(x, x_stride, w, bias, offsets, y, y_stride, pre, pre_stride, rows, groups, N,
+                                         K, act, dtype, _stream(stream)), "tf_grouped_matmul", check)
 
 
 def tf_grouped_matmul_dgrad(dy, dy_stride, w, offsets, pre, pre_stride, dx, dx_stride, rows, groups, N, K, act, dtype,
                             stream=None, check=True):
-    _same_device(dy, w, offsets, pre, dx)
-    return _check(_lib.tf_grouped_matmul_dgrad(_ptr(dy), dy_stride, _ptr(w), _ptr(offsets), _ptr(pre), pre_stride,
-                                               _ptr(dx), dx_stride, rows, groups, N, K, act, dtype, _stream(stream)),
-                  "tf_grouped_matmul_dgrad", check)
+    dy, w, offsets, pre, dx = _ptrs(dy, w, offsets, pre, dx)
+    return _check(_lib.tf_grouped_matmul_dgrad(dy, dy_stride, w, offsets, pre, pre_stride, dx, dx_stride, rows, groups,
+                                               N, K, act, dtype, _stream(stream)), "tf_grouped_matmul_dgrad", check)
 
 
 def tf_grouped_matmul_wgrad_workspace_size(rows, groups, N, K, dtype) -> int:
@@ -250,10 +256,10 @@ def tf_grouped_matmul_wgrad_workspace_size(rows, groups, N, K, dtype) -> int:
 
 def tf_grouped_matmul_wgrad(dy, dy_stride, x, x_stride, offsets, dw, dbias, rows, groups, N, K, accumulate, dtype,
                             workspace, workspace_bytes, stream=None, check=True):
-    _same_device(dy, x, offsets, dw, dbias, workspace)
-    return _check(_lib.tf_grouped_matmul_wgrad(_ptr(dy), dy_stride, _ptr(x), x_stride, _ptr(offsets), _ptr(dw),
-                                               _ptr(dbias), rows, groups, N, K, accumulate, dtype, _ptr(workspace),
-                                               workspace_bytes, _stream(stream)), "tf_grouped_matmul_wgrad", check)
+    dy, x, offsets, dw, dbias, workspace = _ptrs(dy, x, offsets, dw, dbias, workspace)
+    return _check(_lib.tf_grouped_matmul_wgrad(dy, dy_stride, x, x_stride, offsets, dw, dbias, rows, groups, N, K,
+                                               accumulate, dtype, workspace, workspace_bytes, _stream(stream)),
+                  "tf_grouped_matmul_wgrad", check)
 
 
 def tf_unfused_conv2d(x, w_ohwi, t1, shape, variant=TF_CONV_AUTO, stream=None, check=True):

@@ -15,30 +15,39 @@ namespace {
 using namespace norm;
 
 // Threads per SM, from the registers the columns take (two fp32 sums, gamma,
-// and the row in its storage type): 128 for 16 columns, 80 for 8 (96 where they
-// are element-wise).   Spilled registers cost far more than a few warps fewer: with most of the
-// SM's memory in the rings, the little L1 that is left does not hold them.
-constexpr int sm_threads(int cols, bool aligned) { return cols > 8 ? 512 : aligned ? 768 : 640; }
+// and the row in its storage type): 128 registers for 16 columns and 24 (gamma
+// in shared memory), 80 for 8 (96 where they are element-wise, but
+// for the widest groups).  Spilled registers cost far more than a few warps
+// fewer: with most of the SM's memory in the rings, the little L1 that is left
+// does not hold them.
+constexpr int sm_threads(int cols, bool aligned, int group)
+{
+    return cols > 8 ? 512 : aligned || group > 640 ? 768 : 640;
+}
 
-// Columns per thread: 16, or 8 for narrow rows and for element-wise columns
-// (16 above 4096 of them).
+// Columns per thread: 16, or 8 for narrow rows and for element-wise columns (16
+// above 6144 of them); 24 for 16-bit rows that then take one warp, whose sums
+// need no barrier (50001 x 640 fp16 without the weights' gradients: 52 us, 58
+// with two warps of 16; 32 columns for rows of 1024 were slower, 48 against 30).
 int cols_for(int64_t hidden, int size, bool aligned)
 {
-    if (!aligned) return hidden > 4096 ? 16 : 8;
+    if (!aligned) return hidden > 6144 ? 16 : 8;
     if (hidden <= 256) return 8;
+    if (size == 2 && hidden > 512 && hidden <= 768) return 24;
     return 16;
 }
 
 // GROUP: threads per row where the columns are element-wise (a constant makes
 // them immediate offsets), 0 for 16-byte vectors.
 template <typename T, int GROUP, bool CLUSTER, int NT, int COLS>
-__global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 1)
+__global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0, GROUP), 1)
     norm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Sources src,
                          const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
     constexpr bool ALIGNED = GROUP == 0;
     using C = Cols<T, ALIGNED, COLS>;
     constexpr int PAIRS = C::PAIRS;
+    constexpr bool HELD = COLS <= 16;   // gamma in registers
     pdl_begin();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 red[2][768 / 32];
@@ -52,14 +61,28 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 
     Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
 
-    float2 ga[PAIRS], dg[PAIRS], db[PAIRS];
+    float2 ga[HELD ? PAIRS : 1], dg[PAIRS], db[PAIRS];
+    float *gs = reinterpret_cast<float *>(smem + g.gamma_off);
+    if (!HELD) {
+        for (int c = threadIdx.x; c < width; c += (int)blockDim.x) gs[c] = a.gamma ? __ldg(a.gamma + c0 + c) : 1.0f;
+        cta_sync();
+    }
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) {
         const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
-        ga[p] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
-                            a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
+        if (HELD)
+            ga[HELD ? p : 0] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
+                                           a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
         dg[p] = db[p] = make_float2(0.0f, 0.0f);
     }
+    // (read anew for either use: held, the compiler would keep it in registers)
+    auto gamma2 = [&](int p) {
+        if (HELD) return ga[HELD ? p : 0];
+        float2 v = make_float2(1.0f, 1.0f);
+        if (C::inside(2 * p, gt, gsize, width))
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(ptx::smem_u32(gs + C::col(2 * p, gt, gsize))));
+        return v;
+    };
     const float inv_h = 1.0f / (float)a.hidden;
     Edge<T> ed, ex, er;
     load_edge(ring, 0, ring.first, gt, gsize, ed);
@@ -92,7 +115,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 
         float2 c1 = make_float2(0.0f, 0.0f), c2 = c1;
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {   // past the slice dy is zero and adds nothing
-            const float2 fd = d.get(p), xh = ffma2(x.get(p), scale, shift), w = fmul2(fd, ga[p]);
+            const float2 fd = d.get(p), xh = ffma2(x.get(p), scale, shift), w = fmul2(fd, gamma2(p));
             dg[p] = ffma2(fd, xh, dg[p]);
             db[p] = fadd2(db[p], fd);
             c1 = fadd2(c1, w);
@@ -114,7 +137,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
             const float2 xh = ffma2(x.get(p), scale, shift);
-            out[p] = ffma2(fmul2(d.get(p), ga[p]), scale, ffma2(xh, k2, k1));
+            out[p] = ffma2(fmul2(d.get(p), gamma2(p)), scale, ffma2(xh, k2, k1));
             if (NT > 2) out[p] = fadd2(out[p], r.get(p));
         }
         C::store(reinterpret_cast<T *>(a.dx) + (row * a.dx_stride + c0), width, gt, gsize, out);
@@ -125,21 +148,33 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0), 
         // this CTA's sums: row `unit` of dgamma's and of dbeta's [units][hidden] array
         float *wg = a.ws + (int64_t)unit * a.hidden + c0, *wb = wg + (int64_t)units * a.hidden;
         const int groups = g.threads / gsize;
-        float *acc = reinterpret_cast<float *>(smem);
+        float *acc = reinterpret_cast<float *>(smem) + gt;   // [2*COLS][gsize]: thread gt of every group has the same columns
         for (int w = 0; w < groups; ++w) {   // the groups' sums, added in order in shared memory
             cta_sync();   // every group is done with its ring, and with the previous group's turn
             if ((int)threadIdx.x / gsize != w) continue;
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) {
-                const int c = C::col(j, gt, gsize);
-                if (c >= width) continue;
-                float vg = j % 2 ? dg[j / 2].y : dg[j / 2].x, vb = j % 2 ? db[j / 2].y : db[j / 2].x;
+            for (int p = 0; p < PAIRS; ++p) {
+                float *at = acc + 4 * p * gsize;
                 if (w > 0) {
-                    vg += acc[c];
-                    vb += acc[g.slice + c];
+                    dg[p] = fadd2(dg[p], make_float2(at[0], at[gsize]));
+                    db[p] = fadd2(db[p], make_float2(at[2 * gsize], at[3 * gsize]));
                 }
-                (w + 1 < groups ? acc : wg)[c] = vg;
-                (w + 1 < groups ? acc + g.slice : wb)[c] = vb;
+                if (w + 1 < groups) {
+                    at[0] = dg[p].x;
+                    at[gsize] = dg[p].y;
+                    at[2 * gsize] = db[p].x;
+                    at[3 * gsize] = db[p].y;
+                } else {
+                    const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
+                    if (c < width) {
+                        wg[c] = dg[p].x;
+                        wb[c] = db[p].x;
+                    }
+                    if (d < width) {
+                        wg[d] = dg[p].y;
+                        wb[d] = db[p].y;
+                    }
+                }
             }
         }
     }
@@ -181,7 +216,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
 Geometry geometry_for(int64_t rows, int64_t hidden, int size, bool aligned, int tensors)
 {
     const int cols = cols_for(hidden, size, aligned);
-    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned), true, rows);
+    const int group = (int)(hidden + cols - 1) / cols;   // (rounded up by geometry())
+    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group), true, rows, cols > 16);
 }
 
 // The most partial sums that any alignment and number of operands gives.
@@ -213,7 +249,11 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
         constexpr int NT = decltype(nt)::value;
         if (aligned) {
             if (g.csize > 1) return norm_backward_kernel<T, 0, true, NT, 16>;
-            return cols_for(a.hidden, size, true) == 8 ? norm_backward_kernel<T, 0, false, NT, 8> : norm_backward_kernel<T, 0, false, NT, 16>;
+            switch (cols_for(a.hidden, size, true)) {
+            case 8: return norm_backward_kernel<T, 0, false, NT, 8>;
+            case 24: return norm_backward_kernel<T, 0, false, NT, size == 2 ? 24 : 16>;
+            default: return norm_backward_kernel<T, 0, false, NT, 16>;
+            }
         }
         if (cols_for(a.hidden, size, false) == 16)
             return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16> : norm_backward_kernel<T, 512, false, NT, 16>;
@@ -226,7 +266,9 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
         case 320: return norm_backward_kernel<T, 320, false, NT, 8>;
         case 384: return norm_backward_kernel<T, 384, false, NT, 8>;
         case 448: return norm_backward_kernel<T, 448, false, NT, 8>;
-        default: return norm_backward_kernel<T, 512, false, NT, 8>;
+        case 512: return norm_backward_kernel<T, 512, false, NT, 8>;
+        case 640: return norm_backward_kernel<T, 640, false, NT, 8>;
+        default: return norm_backward_kernel<T, 768, false, NT, 8>;
         }
     };
     return launch_rows(a.dres ? pick(std::integral_constant<int, 3>()) : pick(std::integral_constant<int, 2>()), g,

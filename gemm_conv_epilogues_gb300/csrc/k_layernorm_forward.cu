@@ -15,16 +15,20 @@ using namespace norm;
 // Columns per thread: 16 at 128 registers, 8 at 64 where they are element-wise.
 // Fewer registers would spill, which costs far more than more threads gain: with
 // most of the SM's memory in the rings, the little L1 left does not hold them.
-// (Element-wise rows above 4096 columns take 16, too, in CTAs of 512.)
-constexpr int cols_of(bool aligned, int64_t hidden) { return aligned || hidden > 4096 ? 16 : 8; }
+// (Element-wise rows of several CTAs take 16, too, in CTAs of 512.)
+constexpr int cols_of(bool aligned, int64_t hidden) { return aligned || hidden > kSlice ? 16 : 8; }
 constexpr int sm_threads(int cols) { return cols == 8 ? 1024 : 512; }
 
 // GROUP: threads per row where the columns are element-wise (a constant makes
 // them immediate offsets), 0 for 16-byte vectors.  SPAN: 0 for at most 256
 // threads per row, 1 for up to 512, 2 for a cluster of such CTAs.
 template <typename T, int GROUP, int SPAN, int NT, int COLS>
-__global__ void __launch_bounds__(GROUP > 256 || SPAN > 0 ? 512 : 256,
-                                  GROUP > 256 ? (COLS == 8 ? 2 : 1) : GROUP > 0 ? 4 : SPAN > 0 ? 1 : 2)
+__global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ? 512 : 256,
+                                  GROUP > 512   ? 1
+                                  : GROUP > 256 ? (COLS == 8 ? 2 : 1)
+                                  : GROUP > 0   ? 4
+                                  : SPAN > 0    ? 1
+                                                : 2)
     norm_forward_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Sources src,
                         const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
@@ -129,7 +133,7 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
         if (aligned)
             return g.csize > 1 ? norm_forward_kernel<T, 0, 2, NT, 16>
                    : g.group > 256 ? norm_forward_kernel<T, 0, 1, NT, 16> : norm_forward_kernel<T, 0, 0, NT, 16>;
-        if (cols == 16) return g.csize > 1 ? norm_forward_kernel<T, 512, 2, NT, 16> : norm_forward_kernel<T, 512, 1, NT, 16>;
+        if (g.csize > 1) return norm_forward_kernel<T, 512, 2, NT, 16>;
         switch (g.group) {
         case 32: return norm_forward_kernel<T, 32, 0, NT, 8>;
         case 64: return norm_forward_kernel<T, 64, 0, NT, 8>;
@@ -139,7 +143,11 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
         case 320: return norm_forward_kernel<T, 320, 0, NT, 8>;
         case 384: return norm_forward_kernel<T, 384, 0, NT, 8>;
         case 448: return norm_forward_kernel<T, 448, 0, NT, 8>;
-        default: return norm_forward_kernel<T, 512, 0, NT, 8>;
+        case 512: return norm_forward_kernel<T, 512, 0, NT, 8>;
+        case 640: return norm_forward_kernel<T, 640, 0, NT, 8>;
+        case 768: return norm_forward_kernel<T, 768, 0, NT, 8>;
+        case 896: return norm_forward_kernel<T, 896, 0, NT, 8>;
+        default: return norm_forward_kernel<T, 1024, 0, NT, 8>;
         }
     };
     return launch_rows(a.res ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>()), g,

@@ -30,7 +30,8 @@ namespace tf {
 namespace norm {
 
 constexpr int kSlice = 8192;              // columns of one CTA
-constexpr int kMaxGroup = 512;
+constexpr int kMaxGroup = 1024;
+constexpr int kClusterGroup = 512;
 constexpr int kMaxStages = 8;
 constexpr int kMaxTensors = 3;
 constexpr int kMaxRanks = 16;
@@ -86,6 +87,7 @@ struct Geometry {
     int csize, slice;   // CTAs per row and columns per CTA
     int stages, tensor_bytes;   // ring of one row group: stages x tensors x tensor_bytes
     int bar_off;        // mbarriers behind the rings
+    int gamma_off;      // gamma behind those, where the kernel keeps it there
     int smem;
 };
 
@@ -360,9 +362,13 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, int gsize, float2
     const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
     if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
     group_sync<NAMED>(gsize);
-    // the warps' pairs (at most 16), each half-warp adding all of them
-    const int lane = threadIdx.x & 15;
+    // the warps' pairs, all of them added in every lane (up to 16 by each half-warp)
+    const int lane = nw > 16 ? threadIdx.x & 31 : threadIdx.x & 15;
     float2 t = lane < nw ? red[w0 + lane] : make_float2(0.0f, 0.0f);
+    if (nw > 16) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, 16);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, 16);
+    }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
         t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
@@ -379,8 +385,9 @@ __device__ __forceinline__ float group_sum(float a, int gsize, float2 *red)
     const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
     if ((threadIdx.x & 31) == 0) red[warp].x = a;
     group_sync<NAMED>(gsize);
-    const int lane = threadIdx.x & 15;
+    const int lane = nw > 16 ? threadIdx.x & 31 : threadIdx.x & 15;
     float t = lane < nw ? red[w0 + lane].x : 0.0f;
+    if (nw > 16) t += __shfl_xor_sync(0xffffffffu, t, 16);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     return t;
@@ -466,7 +473,7 @@ __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, un
 // MERGED: all the row groups of an SM in one CTA (whose column sums then leave
 // the SM once).
 inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int tensors, int sm_threads, bool merged,
-                         int64_t rows)
+                         int64_t rows, bool gamma_in_smem = false)
 {
     Geometry g;
     const int vec = aligned ? 16 / size : 1;
@@ -474,15 +481,15 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     const int64_t slice = ((hidden + csize - 1) / csize + vec - 1) / vec * vec;
     g.csize = (int)((hidden + slice - 1) / slice);   // no CTA without columns
     g.slice = (int)slice;
-    // element-wise groups are constants of the kernels: 32, or multiples of 64
-    const int step = aligned || slice <= 32 * cols ? 32 : 64;
+    // element-wise groups are constants of the kernels: 32, multiples of 64, above 512 of 128
+    const int step = aligned || slice <= 32 * cols ? 32 : slice <= 512 * cols ? 64 : 128;
     g.group = (int)(((slice + cols - 1) / cols + step - 1) / step * step);
-    if (!aligned && cols > 8) g.group = kMaxGroup;
+    if (!aligned && cols > 8) g.group = kClusterGroup;
     g.tensor_bytes = (int)((slice * size + 15) / 16 * 16) + (aligned ? 0 : 32);
     const int ring = tensors * g.tensor_bytes + 8;
     // row groups per SM: as many as the registers hold, fewer where shared
     // memory has no room for two stages of each
-    const int sm_bytes = 226 * 1024;
+    const int sm_bytes = 226 * 1024 - (gamma_in_smem ? (int)slice * 4 : 0);
     const bool one_cta = merged && g.csize == 1;
     auto room = [&](int n) {   // of one of n groups, past a CTA's own 2 KB (static memory, and what the system keeps)
         return one_cta ? (sm_bytes - 2048) / n : sm_bytes / n - 2048;
@@ -504,8 +511,9 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     g.threads = in_cta * g.group;
     g.per_sm = groups / in_cta;
     g.bar_off = in_cta * stages * tensors * g.tensor_bytes;
-    g.smem = g.bar_off + in_cta * stages * 8;
-    if (merged && g.smem < 8 * g.slice) g.smem = 8 * g.slice;   // the groups' column sums are added there
+    g.gamma_off = (g.bar_off + in_cta * stages * 8 + 15) / 16 * 16;
+    g.smem = gamma_in_smem ? g.gamma_off + (int)slice * 4 : g.bar_off + in_cta * stages * 8;
+    if (merged && g.smem < 8 * cols * g.group) g.smem = 8 * cols * g.group;   // the groups' column sums are added there
     return g;
 }
 
