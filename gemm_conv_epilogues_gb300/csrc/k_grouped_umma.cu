@@ -62,9 +62,10 @@ constexpr int kBoxBytes = 32 * 32 * 2;
 // WGRAD: rows per accumulation.  The tensor cores truncate where fp32 additions
 // round, so an accumulator's error grows with the number of MMAs it takes
 // (relative error 1.4e-6 for groups of up to 2459 rows, against 2.9e-7 for fp32
-// products).  A longer group is accumulated in parts; their running sum stays
-// in the tile's other accumulator, added by the epilogue's threads.  (Adding the
-// parts in memory took 316 us for groups of 1025 rows, 208 for 1023.)
+// products).  A longer group is accumulated in parts: the first in one of the
+// two accumulators, the second in the other, and the epilogue's threads add
+// them; for a third part they leave the sum in the first.  (Adding the parts in
+// memory took 316 us for groups of 1025 rows, 208 for 1023.)
 constexpr int kMaxPartRows = 1024;
 constexpr uint32_t kTmemCols = 512;
 
@@ -703,10 +704,11 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 if (nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
                 const uint32_t apart = sums_of<MODE, CG>(it.w) > 1 ? 64u : 0u;
-                bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
+                const int c = WG && part > 0 ? b ^ 1 : b;   // the accumulator
+                bool got = ptx::mbar_wait<PAIR>(&tempty[c], ((taken >> c) & 1u) ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(b * kMaxBN);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(c * kMaxBN);
                 uint32_t acc = 0;   // the first K step begins its sums
                 for (int kb = 0; kb < nkb; ++kb) {
                     got = ptx::mbar_wait<PAIR && WG>(&full[stage], phase, p.wait_ns);
@@ -735,8 +737,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                         if constexpr (PAIR) commit_both(&empty[stage]);
                         else ptx::umma_commit(&empty[stage]);
                         if (kb == nkb - 1) {
-                            if constexpr (PAIR) commit_both(&tfull[b]);
-                            else ptx::umma_commit(&tfull[b]);
+                            if constexpr (PAIR) commit_both(&tfull[c]);
+                            else ptx::umma_commit(&tfull[c]);
                         }
                     }
                     __syncwarp();
@@ -746,14 +748,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                         phase ^= 1u;
                     }
                 }
-                taken ^= 1u << b;
-                if (part == it.parts - 1) {
-                    // a tile of several parts took the other accumulator too, for their sum; the epilogue releases
-                    // both.  (Its use of it lies between this warp's waits for the second part and for the next
-                    // tile, so no phase of that barrier is passed over unseen.)
-                    if (it.parts > 1) taken ^= 1u << (b ^ 1);
-                    b ^= 1;
-                }
+                taken ^= 1u << c;
+                if (part == it.parts - 1) b ^= 1;
                 return true;
             });
             if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
@@ -836,14 +832,20 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             uint4 pre[4] = {};
             if (slope && mine && h * 32 < width)
                 load_pre(pre, p.pre, p.pre_stride, n0, p.M, it.t0 + h * 32, min(32, width - h * 32));
+            const bool last = part == it.parts - 1;
+            if (WG && part == 0 && !last) {   // a part to come completes after this one: wait for that
+                seen ^= 1u << b;
+                return true;
+            }
+            const int acc = WG && part > 0 ? b ^ 1 : b;   // the accumulator of this part
             if (nkb > 0) {
-                const bool got = ptx::mbar_wait(&tfull[b], (seen >> b) & 1u, p.wait_ns);
+                const bool got = ptx::mbar_wait(&tfull[acc], (seen >> acc) & 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
                 ptx::tc_fence_after();
             } else if (!WG || p.accumulate) {
                 return true;   // a group without rows adds nothing
             }
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kMaxBN);
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kMaxBN);
 #pragma unroll 1
             for (int c = h; c * 32 < width && mine; c += kEpiWarps / 4) {
                 uint32_t r[32];
@@ -856,7 +858,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = 0u;
                     }
-                    const uint32_t saddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((b ^ 1) * kMaxBN + c * 32);
+                    const uint32_t saddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * kMaxBN + c * 32);
                     if (part > 0) {   // plus the parts before
                         uint32_t u[32];
                         tmem_ld_16x256b_x4(saddr, u);
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(u[j]));
                     }
-                    if (part < it.parts - 1) {
+                    if (!last) {
                         tmem_st_16x256b_x4(saddr, r);
                         tmem_st_16x256b_x4(saddr + (16u << 16), r + 16);
                         tmem_st_wait();
@@ -914,7 +916,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 }
             }
             if (nkb > 0) {
-                const bool last = part == it.parts - 1;
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -922,10 +923,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                         if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[i], 0));
                         else ptx::mbar_arrive(&tempty[i]);
                     };
-                    release(b);
-                    if (last && it.parts > 1) release(b ^ 1);
+                    release(acc);
+                    if (last && part > 0) release(b);
                 }
-                seen ^= 1u << b;
+                seen ^= 1u << acc;
                 if (last) b ^= 1;
             }
             return true;
