@@ -76,7 +76,8 @@ struct UmmaArgs {
     uint32_t *err;
     uint64_t wait_ns;
     int64_t y_stride, pre_stride;
-    int groups, rows;
+    int groups, rows;  // groups: with WGRAD's splits, real groups x splits
+    int splits;
     int M;             // extent of the weights' side (N, or K for DGRAD)
     int red;           // reduction length of FORWARD and DGRAD
     int cols;          // WGRAD: K, the N side
@@ -445,7 +446,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     int *row = reinterpret_cast<int *>(smem + p.off_sched);      // [groups + 1]
     int *tile = row + p.groups + 1;                              // [groups + 1]
     int *order = tile + p.groups + 1;                            // [groups]
-    int *bad = order + p.groups;                                 // then the chosen bn and bm
+    int *bad = order + p.groups;                                 // then the chosen bn and bm, and:
+    volatile int *dead = bad + 3;                                // a role has given up
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = PAIR ? (int)ptx::cluster_ctarank() : 0;
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         ptx::prefetch_tensormap(&tmap_a);
         ptx::prefetch_tensormap(&tmap_b);
         *bad = 0;
+        *dead = 0;
     }
     if (warp == 1) {
         if constexpr (PAIR) {
@@ -496,10 +499,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     {
         constexpr int STEP = 16 * CG;
         int wrong = 0;
-        for (int i = threadIdx.x; i <= p.groups; i += (int)blockDim.x) {
+        const int real = WG ? p.groups / p.splits : p.groups;
+        for (int i = threadIdx.x; i <= real; i += (int)blockDim.x) {
             const int v = p.offsets[i];
-            row[i] = v;
             wrong |= v < 0 || v > p.rows || (i > 0 && p.offsets[i - 1] > v);
+            if (WG && p.splits > 1 && i < real) {   // a group's rows in `splits` runs of whole K steps, the last ones maybe empty
+                const int T = max(0, p.offsets[i + 1] - v), len = ((T + p.splits - 1) / p.splits + BK - 1) / BK * BK;
+                for (int s = 0; s < p.splits; ++s) row[i * p.splits + s] = v + min(T, s * len);
+            } else {
+                row[WG ? i * p.splits : i] = v;
+            }
         }
         if (wrong) *bad = 1;
         cta_sync();
@@ -605,6 +614,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     const int a_bytes = plan.bm / CG * BK * 2, sub_bytes = a_bytes + (WG ? kMaxBN : p.bn) / CG * BK * 2;
     const int stage_bytes = sub_bytes * KSUB;
     const int stages = min(kMaxStages, p.off_epi / stage_bytes);
+    auto give_up = [&](uint32_t why) {
+        *dead = 1;
+        atomicOr(p.err, why);
+    };
     const Items items = {reinterpret_cast<Item *>(smem + p.off_items), ready, freed, p.wait_ns, cid, ncl, num_work};
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -680,7 +693,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             }
             return true;
         });
-        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
+        if (!ok && lane == 0) give_up(TF_DEVERR_PRODUCER_WAIT);
         // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
         for (int s = 0; s < stages; ++s)
             if (leader && ((issued >> s) & 1u))
@@ -752,7 +765,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                 if (part == it.parts - 1) b ^= 1;
                 return true;
             });
-            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+            if (!ok && lane == 0) give_up(TF_DEVERR_MMA_WAIT);
             if (issuer) {   // (the lane that issued the MMAs)
                 if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
                 else ptx::umma_commit(drain);
@@ -791,13 +804,16 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             __syncwarp();
             return true;
         });
-        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+        if (!ok && lane == 0) give_up(TF_DEVERR_MMA_WAIT);
     } else if (warp == 3) {
         // ------------------------------------------------------------ item lists
         bool ok = true;
         for (int k = 0; ok && cid + k * 32 * ncl < num_work; ++k) {
             const int half = k & 1, t = cid + (k * 32 + lane) * ncl;
-            if (k >= 2) ok = ptx::mbar_wait(&freed[half], (uint32_t)((k >> 1) - 1) & 1u, p.wait_ns);
+            // the list before the last is used up after up to 64 items, each of which may take a while
+            if (k >= 2)
+                for (int tries = 0; !(ok = ptx::mbar_wait(&freed[half], (uint32_t)((k >> 1) - 1) & 1u, p.wait_ns)); ++tries)
+                    if (tries == 64 || *dead) break;
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -931,7 +947,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             }
             return true;
         });
-        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
+        if (!ok && lane == 0) give_up(TF_DEVERR_EPILOGUE_WAIT);
     } else if (WG && warp >= kFirstEpiWarp + kEpiWarps && p.dbias && num_work > 0) {
         // ------------------------------------------------------------ bias gradient
         if (p.bf16) bias_grad<__nv_bfloat16>(p, plan, warp - kFirstEpiWarp - kEpiWarps);
@@ -1035,20 +1051,21 @@ cudaError_t resident(int *units)
 }
 
 template <int MODE, int CG, int KSUB>
-cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
+cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int splits = 1)
 {
     constexpr bool WG = MODE == GROUPED_WGRAD;
     UmmaArgs p = {};
     p.offsets = a.offsets;
     p.bias = a.bias;
-    p.y = WG ? a.dw : a.y;
+    p.y = WG ? (splits > 1 ? a.ws : a.dw) : a.y;   // with splits, partial sums
     p.pre = a.pre;
     p.err = device_error_word();
     p.wait_ns = wait_limit_ns();
     if (!p.err) return cudaErrorInitializationError;
     p.y_stride = a.y_stride;
     p.pre_stride = a.pre_stride;
-    p.groups = a.groups;
+    p.groups = a.groups * splits;
+    p.splits = splits;
     p.rows = a.rows;
     p.M = MODE == GROUPED_DGRAD ? a.K : a.N;
     p.red = MODE == GROUPED_DGRAD ? a.N : a.K;
@@ -1061,11 +1078,11 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     p.a_box = MODE == GROUPED_FORWARD ? (small ? 32 : BM) : 64;
     p.act = a.act;
     p.bf16 = a.dtype == TF_BF16;
-    p.accumulate = a.accumulate;
+    p.accumulate = splits > 1 ? 0 : a.accumulate;
     p.dy = a.dy;
     p.dy_stride = a.dy_stride;
-    p.dbias = a.dbias;
-    const int sched = (3 * (a.groups + 1) + 2) * 4;
+    p.dbias = splits > 1 && a.dbias ? a.ws + (int64_t)p.groups * a.N * a.K : a.dbias;
+    const int sched = (3 * (p.groups + 1) + 4) * 4;
     const int fixed = (WG ? 0 : kEpiWarps * kBoxBytes) + kItemBytes + kNumBars * 8 + 16 + sched;
     const int ring = (kSmemLimit - fixed) / 1024 * 1024;
     if (ring < 2 * KSUB * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
@@ -1094,7 +1111,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int bm = p.bm ? p.bm : p.a_box;   // (the narrowest tile gives the most work items)
     const int64_t mt = (p.M + bm - 1) / bm;
-    const int64_t most = WG ? (int64_t)a.groups * mt * ((a.K + kMaxBN - 1) / kMaxBN)
+    const int64_t most = WG ? (int64_t)p.groups * mt * ((a.K + kMaxBN - 1) / kMaxBN)
                             : ((int64_t)a.rows / bn + a.groups) * mt;
     if (most >= (int64_t)1 << 31) return cudaErrorNotSupported;
     if (units > most) units = (int)most;
@@ -1115,13 +1132,68 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st)
     return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG, KSUB>, ta, tb, p));
 }
 
+// WGRAD with fewer tiles than CTAs (pairs) and long groups: every group's rows in
+// `splits` runs, whose products a second kernel adds.  At least 256 rows per
+// run on average, as far as the host knows.
+int wgrad_splits(int64_t rows, int groups, int64_t N, int64_t K)
+{
+    const bool pair = N > BM && K > 128;
+    const int64_t tiles = (int64_t)groups * ((N + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM)) * ((K + kMaxBN - 1) / kMaxBN);
+    int64_t s = sm_count() / (pair ? 2 : 1) / tiles;
+    if (s > rows / groups / 256) s = rows / groups / 256;
+    if (s > kGroupedMaxGroups / groups) s = kGroupedMaxGroups / groups;
+    return s < 2 ? 1 : (int)s;
+}
+
+// dw's partial sums [groups*splits][N][K], then dbias's [groups*splits][N].
+int64_t split_bytes(int splits, int groups, int64_t N, int64_t K)
+{
+    return splits < 2 ? 0 : (int64_t)splits * groups * N * (K + 1) * 4;
+}
+
+// dst[e][i] (+)= the sum over s of src[e*splits + s][i], in order; 4 values per thread.
+__global__ void __launch_bounds__(256) split_sum_kernel(float *dw, float *dbias, const float *ws, int splits, int groups,
+                                                        int64_t NK, int64_t N, int accumulate)
+{
+    pdl_begin();
+    const int64_t step = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    auto add = [&](float *dst, const float *src, int64_t n) {   // n values per group, a multiple of 4
+        for (int64_t i = first; i < groups * n / 4; i += step) {
+            const int64_t e = 4 * i / n, at = 4 * i - e * n;
+            float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int s = 0; s < splits; ++s) {
+                const float4 v = *reinterpret_cast<const float4 *>(src + (e * splits + s) * n + at);
+                t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+            }
+            float *out = dst + 4 * i;   // (dbias need not be 16-byte aligned)
+            out[0] = accumulate ? out[0] + t.x : t.x;
+            out[1] = accumulate ? out[1] + t.y : t.y;
+            out[2] = accumulate ? out[2] + t.z : t.z;
+            out[3] = accumulate ? out[3] + t.w : t.w;
+        }
+    };
+    add(dw, ws, NK);
+    if (dbias) add(dbias, ws + (int64_t)groups * splits * NK, N);
+}
+
+cudaError_t launch_sum(const GroupedArgs &a, int splits, cudaStream_t st)
+{
+    const int64_t NK = (int64_t)a.N * a.K, blocks = (a.groups * NK / 4 + 255) / 256, most = 8 * (int64_t)sm_count();
+    return launch_pdl(split_sum_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st, a.dw, a.dbias,
+                      static_cast<const float *>(a.ws), splits, a.groups, NK, (int64_t)a.N, a.accumulate);
+}
+
 template <int MODE>
 cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
 {
     const int64_t M = MODE == GROUPED_DGRAD ? a.K : a.N;
     const int64_t avg = a.rows / a.groups;   // rows per group, as far as the host knows
     if constexpr (MODE == GROUPED_WGRAD) {
-        return M > BM && a.K > 128 ? launch_mode<MODE, 2, 1>(a, kMaxBN, st) : launch_mode<MODE, 1, 1>(a, kMaxBN, st);
+        const bool pair = M > BM && a.K > 128;
+        int splits = wgrad_splits(a.rows, a.groups, a.N, a.K);
+        if (a.ws_bytes < split_bytes(splits, a.groups, a.N, a.K)) splits = 1;
+        const cudaError_t e = pair ? launch_mode<MODE, 2, 1>(a, kMaxBN, st, splits) : launch_mode<MODE, 1, 1>(a, kMaxBN, st, splits);
+        return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);
     } else {
         if (M > BM && avg > 128) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
         if (avg <= 64) return launch_mode<MODE, 1, 4>(a, avg <= 16 ? 16 : avg <= 32 ? 32 : 64, st);
@@ -1133,7 +1205,11 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 }  // namespace
 
-int64_t grouped_wgrad_workspace(int64_t, int, int64_t, int64_t, int) { return 0; }
+int64_t grouped_wgrad_workspace(int64_t rows, int groups, int64_t N, int64_t K, int)
+{
+    if (N % 8 != 0 || K % 8 != 0) return 0;
+    return split_bytes(wgrad_splits(rows, groups, N, K), groups, N, K);
+}
 
 cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st)
 {

@@ -358,7 +358,10 @@ __device__ __forceinline__ float2 group_sum2(float a, float b, int gsize, float2
 {
     a = warp_sum(a);
     b = warp_sum(b);
-    if (gsize == 32) return make_float2(a, b);
+    if (gsize == 32) {
+        __syncwarp();   // the lanes' reads of the stage come before its refill
+        return make_float2(a, b);
+    }
     const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
     if ((threadIdx.x & 31) == 0) red[warp] = make_float2(a, b);
     group_sync<NAMED>(gsize);
@@ -381,7 +384,10 @@ template <bool NAMED>
 __device__ __forceinline__ float group_sum(float a, int gsize, float2 *red)
 {
     a = warp_sum(a);
-    if (gsize == 32) return a;
+    if (gsize == 32) {
+        __syncwarp();
+        return a;
+    }
     const int warp = threadIdx.x >> 5, nw = gsize >> 5, w0 = warp / nw * nw;
     if ((threadIdx.x & 31) == 0) red[warp].x = a;
     group_sync<NAMED>(gsize);

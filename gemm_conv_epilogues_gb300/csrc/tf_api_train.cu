@@ -30,7 +30,7 @@ extern "C" {
 
 namespace {
 
-constexpr int64_t kMaxRows = 0x7fffffff - 1;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;   // 32-bit row counters, with room for a step past the end
 
 size_t element_size(int dtype) { return dtype == TF_FP32 ? 4 : 2; }
 bool bad_dtype(int dtype) { return dtype < TF_FP16 || dtype > TF_FP32; }

@@ -258,7 +258,7 @@ int tf_residual_layernorm_select(int64_t hidden);
  *   gamma, beta    : fp32 [hidden];  mean, rstd : fp32 [rows]
  * NULL leaves an operand out: res (s = x), gamma (1), beta (0), sum, mean,
  * rstd.  `sum` receives s rounded to dtype; the statistics and y are those of
- * the unrounded s.  Any hidden from 1 to 131072, any row stride (below 2^31)
+ * the unrounded s.  Any hidden from 1 to 131072, up to 2^30 rows, any row stride (below 2^31)
  * and the alignment of an element; rows whose start is not a multiple of 16
  * bytes take a slower kernel.  rows may be 0 (nothing is read or written).
  * Elements between `hidden` and the stride are not touched. */
@@ -339,8 +339,9 @@ int64_t tf_grouped_matmul_wgrad_workspace_size(int64_t rows, int64_t groups, int
  * != 0 they are added to what dw and dbias hold.
  *   dy : dtype [rows][N];  x : dtype [rows][K]
  *   dw : fp32 [groups][N][K], contiguous;  dbias : fp32 [groups][N] or NULL
- * With a workspace smaller than tf_grouped_matmul_wgrad_workspace_size
- * (including 0) it runs without one.  The workspace must be 16-byte aligned
+ * Few and long groups with small products are cut along their rows over the
+ * workspace, whose partial sums a second kernel adds; with a workspace smaller
+ * than tf_grouped_matmul_wgrad_workspace_size (including 0) they are not.  The workspace must be 16-byte aligned
  * and is in use until the stream reaches the end of the call; calls that may
  * overlap need one each, captured graphs too. */
 int tf_grouped_matmul_wgrad(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const int32_t *offsets,

@@ -451,6 +451,97 @@ def test_captured_and_replayed(b, counts, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("G,N,K", [(512, 1024, 72), (900, 304, 520), (1024, 8, 264)])
+def test_many_groups_and_tiles(b, G, N, K):
+    """More work items per CTA than its lists hold at once, more groups than are sorted; every group checked."""
+    counts = [(5 * i + 3) % 7 for i in range(G)]
+    off, rows, dev = _layout(counts)
+    x, dy = _rand(rows, K, "bf16"), _rand(rows, N, "bf16", seed=1)
+    w = _rand(G * N, K, "bf16", scale=K ** -0.5, seed=2).view(G, N, K)
+    y, _ = _run_forward(b, x, w, None, dev, "bf16", "none", False)
+    dx = torch.full((rows, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    b.tf_grouped_matmul_dgrad(dy, N, w, dev, None, 0, dx, K, rows, G, N, K, 0, b.TF_BF16)
+    dw, db = torch.empty(G, N, K, device="cuda"), torch.empty(G, N, device="cuda")
+    b.tf_grouped_matmul_wgrad(dy, N, x, K, dev, dw, db, rows, G, N, K, 0, b.TF_BF16, None, 0)
+    for e in range(G):
+        r = slice(off[e], off[e + 1])
+        xd, dyd, wd = x[r].double(), dy[r].double(), w[e].double()
+        want, mag = xd @ wd.t(), xd.abs() @ wd.abs().t()
+        _within(y[r], want, 2.0 ** -8 * want.abs() + 2 * ref.product_error(K, mag), f"y[{e}]")
+        want, mag = dyd @ wd, dyd.abs() @ wd.abs()
+        _within(dx[r], want, 2.0 ** -8 * want.abs() + 2 * ref.product_error(N, mag), f"dx[{e}]")
+        _within(dw[e], dyd.t() @ xd, ref.product_error(counts[e], dyd.abs().t() @ xd.abs()) + 1e-37, f"dw[{e}]")
+        _within(db[e], dyd.sum(0), 2 * counts[e] * U * dyd.abs().sum(0) + 1e-37, f"dbias[{e}]")
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits(b):
+    """Rows 2^30 elements apart, and weights of more than 2^31 elements."""
+    N, K, stride, rows = 72, 64, (1 << 30) + 8, 6
+    big = torch.empty((rows - 1) * stride + K, dtype=torch.bfloat16, device="cuda")
+    x = big.as_strided((rows, K), (stride, 1))
+    x.copy_(_rand(rows, K, "bf16"))
+    w = _rand(2 * N, K, "bf16", seed=1).view(2, N, K)
+    off, _, dev = _layout([2, 4])
+    y, _ = _run_forward(b, x, w, None, dev, "bf16", "none", False)
+    again, _ = _run_forward(b, x.contiguous(), w, None, dev, "bf16", "none", False)
+    assert torch.equal(y, again)
+    dy = _rand(rows, N, "bf16", seed=2)
+    dx = big.as_strided((rows, K), (stride, 1), 0)
+    near = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    b.tf_grouped_matmul_dgrad(dy, N, w, dev, None, 0, near, K, rows, 2, N, K, 0, b.TF_BF16)
+    b.tf_grouped_matmul_dgrad(dy, N, w, dev, None, 0, dx, stride, rows, 2, N, K, 0, b.TF_BF16)
+    assert torch.equal(dx, near)
+    del big, x, dx
+    torch.cuda.empty_cache()
+    G, n = 5, 24576
+    w = torch.empty(G, n, n, dtype=torch.bfloat16, device="cuda").normal_(std=n ** -0.5)   # 3.0e9 elements
+    x = _rand(20, n, "bf16", seed=3)
+    off, rows, dev = _layout([4, 0, 5, 1, 10])
+    y, _ = _run_forward(b, x, w, None, dev, "bf16", "none", False)
+    for e in (0, 3, 4):
+        cols = torch.tensor([0, 1, 127, 128, n // 2, n - 2, n - 1], device="cuda")
+        xd, wd = x[off[e]:off[e + 1]].double(), w[e, cols].double()
+        want = xd @ wd.t()
+        _within(y[off[e]:off[e + 1]][:, cols], want, 2.0 ** -8 * want.abs() + 2 * ref.product_error(n, xd.abs() @ wd.abs().t()), f"y[{e}]")
+
+
+@pytest.mark.gpu
+def test_first_call_captured(b, tmp_path):
+    """A process whose first calls of the library are captured."""
+    import subprocess
+    import sys
+    script = tmp_path / "first.py"
+    script.write_text("""
+import torch
+from gemm_conv_epilogues_gb300 import binding as b
+x = torch.randn(64, 128, device="cuda").bfloat16()
+w = torch.randn(2, 256, 128, device="cuda").bfloat16()
+off = torch.tensor([0, 40, 64], dtype=torch.int32, device="cuda")
+y, s = (torch.zeros(64, c, dtype=torch.bfloat16, device="cuda") for c in (256, 128))
+dw, m, r = torch.zeros(2, 256, 128, device="cuda"), torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def step():
+    b.tf_layernorm_forward(x, 128, None, 0, None, None, s, 128, None, 0, m, r, 64, 128, 1e-5, b.TF_BF16)
+    b.tf_grouped_matmul(s, 128, w, None, off, y, 256, None, 0, 64, 2, 256, 128, b.TF_ACT_SILU, b.TF_BF16)
+    b.tf_grouped_matmul_wgrad(y, 256, s, 128, off, dw, None, 64, 2, 256, 128, 0, b.TF_BF16, None, 0)
+with torch.cuda.graph(g):
+    step()
+g.replay()
+got = [t.clone() for t in (s, y, dw)]
+step()
+assert all(torch.equal(a, c) for a, c in zip(got, (s, y, dw))) and y.float().abs().sum() > 0
+assert b.tf_read_device_error() == (0, 0)
+""")
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, str(script)], capture_output=True, text=True, timeout=120,
+                       env=dict(os.environ, PYTHONPATH=root), cwd=root)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once(b):
     """Calls of different shapes overlapping on two streams give the bits of calls one after the other."""
     jobs = []

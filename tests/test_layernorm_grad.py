@@ -259,6 +259,29 @@ def test_backward_one_weight_gradient(b):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("hidden", [64, 1000, 2048, 9000])
+@pytest.mark.parametrize("name", ["bf16", "fp32"])
+def test_offsets_past_32_bits(b, name, hidden):
+    """Rows 2^30 elements apart give the bits of the same rows side by side."""
+    rows, stride = 5, (1 << 30) + 8
+    d = _inputs(rows, hidden, name, 0)
+    big = torch.empty((rows - 1) * stride + hidden, dtype=TYPES[name], device="cuda")
+    far = big.as_strided((rows, hidden), (stride, 1))
+    far.copy_(d["x"])
+    y, s, mean, rstd = _forward(b, d, name)
+    dx, dg, db = _backward(b, d, name, mean, rstd)
+    near = dict(d)
+    d["x"] = far
+    y2, s2, mean2, rstd2 = _forward(b, d, name)
+    dx2, dg2, db2 = _backward(b, d, name, mean, rstd)
+    for a, c in ((y, y2), (s, s2), (mean, mean2), (rstd, rstd2), (dx, dx2), (dg, dg2), (db, db2)):
+        assert torch.equal(a, c)
+    b.tf_layernorm_forward(near["x"], hidden, near["res"], hidden, d["gamma"], d["beta"], far, stride, None, 0, None,
+                           None, rows, hidden, EPS, CODES[name])
+    assert torch.equal(far, y)
+
+
+@pytest.mark.gpu
 def test_no_rows(b):
     z = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
     f = torch.empty(0, device="cuda")
