@@ -13,15 +13,13 @@
 //
 // Persistent kernel, one CTA (CG = 1) or CTA pair (CG = 2, cta_group::2) per SM
 // (pair), work items (group, weights tile, row tile) from a schedule that every
-// CTA computes from the offsets, the groups with the costliest tiles first.
-// Warps:
+// CTA computes from the offsets.  Warps:
 //   0     TMA producer of a ring of K steps (64 deep, 128-byte swizzle)
 //   1     TMEM allocator and MMA issuer; two 256-column fp32 accumulators, so
 //         the epilogue of one tile overlaps the main loop of the next
 //   2     WGRAD: zeroes what the last K step of a group holds of other rows
-//   3     lists the CTA's coming items, 32 at a time: their searches and
-//         divisions, done by the MMA issuer between two tiles, left the tensor
-//         pipe idle for 1.3 us per tile
+//   3     lists the CTA's coming items, 32 at a time, so that the issuing warps
+//         do not stop for their searches and divisions
 //   4-11  epilogue: TMEM -> registers -> bias, activation -> y
 //   12-15 WGRAD: the bias gradient, from dy itself, beside the products (a kernel
 //         of its own cost 38 us of 230: it reads dy once more)
@@ -54,7 +52,6 @@ constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or
 constexpr int kNumBars = 3 * kMaxStages + 9;      // full, empty, land; accumulators full x2, empty x2; drain;
                                                   // item lists ready x2, free x2
 constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
-constexpr int kMaxSorted = 256;                   // groups up to this many are sorted by their tiles' cost
 // An epilogue warp's box, 32 tokens x 32 weights rows of 16 bits: it turns the
 // accumulator's columns into rows for 16-byte stores by the threads (TMA stores
 // of the same boxes measured the same).
@@ -82,8 +79,6 @@ struct UmmaArgs {
     int red;           // reduction length of FORWARD and DGRAD
     int cols;          // WGRAD: K, the N side
     int bn;            // widest row tile the shared memory holds
-    int bm;            // weights rows of a tile: 128 per CTA, or 0: chosen from {128, 64, 32} by the schedule
-    int a_box;         // weights rows (or, M-major, 64 of them) per TMA box
     int box_rows;      // rows per token box
     int off_epi, off_bar, off_items, off_sched;   // the operand ring comes first
     int act, bf16, accumulate;
@@ -185,7 +180,7 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "memory");
 }
 
-// One work item.  FORWARD, DGRAD: weights rows [m0, +bm), tokens [t0, +tv), MMA
+// One work item.  FORWARD, DGRAD: weights rows [m0, +128*CG), tokens [t0, +tv), MMA
 // N = w.  WGRAD: dw rows [m0, +128*CG), columns [t0, +w) of group e from its rows
 // [first, +tv), in `parts` parts of `len` rows (the last one shorter).
 struct alignas(16) Item {
@@ -193,11 +188,11 @@ struct alignas(16) Item {
 };
 static_assert(sizeof(Item) == 32, "two 16-byte loads");
 
-// The schedule in shared memory: rows of every group, the groups in order of
-// falling cost, and the running count of tiles in that order.
+// The schedule in shared memory: the rows of every group and the running count
+// of their tiles.
 struct Plan {
-    const int *row, *tile, *order;
-    int bn, bm, mt;   // row tile, weights tile per CTA (pair), weights tiles
+    const int *row, *tile;
+    int mt;   // weights tiles
 };
 
 template <int MODE, int CG>
@@ -207,8 +202,8 @@ __device__ __forceinline__ Item item_of(const UmmaArgs &p, const Plan &s, int t)
     Item it;
     if (MODE == GROUPED_WGRAD) {
         const int ct = (p.cols + kMaxBN - 1) / kMaxBN, pos = t / (s.mt * ct), r = t - pos * (s.mt * ct);
-        it.e = s.order[pos];
-        it.m0 = r / ct * s.bm;
+        it.e = pos;
+        it.m0 = r / ct * (BM * CG);
         it.t0 = r % ct * kMaxBN;
         const int left = min(kMaxBN, p.cols - it.t0);
         it.w = (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
@@ -222,13 +217,13 @@ __device__ __forceinline__ Item item_of(const UmmaArgs &p, const Plan &s, int t)
             const int mid = (lo + hi + 1) >> 1;
             if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
         }
-        it.e = s.order[lo];
-        const int r = t - s.tile[lo], T = s.row[it.e + 1] - s.row[it.e];
-        const int ntt = (T + s.bn - 1) / s.bn;
+        it.e = lo;
+        const int r = t - s.tile[lo], T = s.row[lo + 1] - s.row[lo];
+        const int ntt = (T + p.bn - 1) / p.bn;
         const int wt = ((T + ntt - 1) / ntt + STEP - 1) / STEP * STEP;   // equal widths, at most bn
         const int tt = r % ntt;
-        it.m0 = r / ntt * s.bm;
-        it.first = s.row[it.e];
+        it.m0 = r / ntt * (BM * CG);
+        it.first = s.row[lo];
         it.t0 = it.first + tt * wt;
         it.tv = min(wt, T - tt * wt);
         it.w = (it.tv + STEP - 1) / STEP * STEP;
@@ -379,7 +374,7 @@ __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int 
     const int across = p.groups * ((p.M + 63) / 64) >= warps ? 8 : 2, down = 32 / across;
     const int piece = lane % across, r0 = lane / across, chunks = (p.M + 8 * across - 1) / (8 * across);
     for (int u = (int)blockIdx.x * kBiasWarps + warp; u < p.groups * chunks; u += warps) {
-        const int e = s.order[u / chunks], n = (u % chunks * across + piece) * 8;
+        const int e = u / chunks, n = (u % chunks * across + piece) * 8;
         const int lo = s.row[e], hi = s.row[e + 1];
         const uint16_t *src = reinterpret_cast<const uint16_t *>(p.dy) + n;
         float2 sum[4] = {};
@@ -415,15 +410,6 @@ __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int 
     }
 }
 
-// Sums a tile is kept in: an MMA of few columns that adds to the sum of the one
-// before it waits for it (~150 cycles each, 44 of 50 us of a 16-row product), so
-// the four of a K step get a sum each.
-template <int MODE, int CG>
-__device__ __forceinline__ int sums_of(int w)
-{
-    return MODE != GROUPED_WGRAD && CG == 1 && w <= 64 ? 4 : 1;
-}
-
 // KSUB: K blocks of 64 per stage.  Handing a stage over takes its issuers ~300
 // cycles, so small tiles take four; pairs two.
 template <int MODE, int CG, int KSUB>
@@ -445,9 +431,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(freed + 2);
     int *row = reinterpret_cast<int *>(smem + p.off_sched);      // [groups + 1]
     int *tile = row + p.groups + 1;                              // [groups + 1]
-    int *order = tile + p.groups + 1;                            // [groups]
-    int *bad = order + p.groups;                                 // then the chosen bn and bm, and:
-    volatile int *dead = bad + 3;                                // a role has given up
+    int *bad = tile + p.groups + 1;                              // the offsets are invalid
+    volatile int *dead = bad + 1;                                // a role has given up
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = PAIR ? (int)ptx::cluster_ctarank() : 0;
@@ -495,9 +480,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
     ptx::tc_fence_after();
 
     // ---- the schedule
-    Plan plan = {row, tile, order, p.bn, BM * CG, 0};
+    const Plan plan = {row, tile, (p.M + BM * CG - 1) / (BM * CG)};
     {
-        constexpr int STEP = 16 * CG;
         int wrong = 0;
         const int real = WG ? p.groups / p.splits : p.groups;
         for (int i = threadIdx.x; i <= real; i += (int)blockDim.x) {
@@ -512,79 +496,19 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         }
         if (wrong) *bad = 1;
         cta_sync();
-        const bool void_call = *bad != 0;
-        if (warp == 0) {
-            // Tile sizes for the last wave: a candidate's cost is the number of tiles the busiest
-            // CTA (pair) takes times a tile's own, with a constant for its overhead.
-            int pick_n = p.bn, pick_m = BM * CG;
-            if (!WG && !void_call) {
-                int best = 0x7fffffff;
-                for (int bn = p.bn; bn >= (p.bn == kMaxBN ? 128 : p.bn); bn -= 32) {
-                    int tiles = 0, width = 0;
-                    for (int e = lane; e < p.groups; e += 32) {
-                        const int T = row[e + 1] - row[e], n = (T + bn - 1) / bn;
-                        tiles += n;
-                        width += (T + STEP * n - 1) / STEP * STEP;
-                    }
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
-                        width += __shfl_xor_sync(0xffffffffu, width, o);
-                    }
-                    if (tiles == 0) break;
-                    // narrower weights tiles only where a tile is paced by its weights' way from HBM
-                    for (int bm = BM * CG; bm >= (p.bm ? BM * CG : p.a_box); bm >>= 1) {
-                        const int waves = (tiles * ((p.M + bm - 1) / bm) + ncl - 1) / ncl;
-                        const int cost = p.bm ? waves * (width / tiles + 24) : waves * (bm + 8);
-                        if (cost < best) {
-                            best = cost;
-                            pick_n = bn;
-                            pick_m = bm;
-                        }
-                    }
-                }
-            }
-            if (lane == 0) {
-                bad[1] = pick_n;
-                bad[2] = pick_m;
-            }
-        }
-        cta_sync();
-        plan.bn = bad[1];
-        plan.bm = bad[2];
-        plan.mt = (p.M + plan.bm - 1) / plan.bm;
-        // the groups by falling cost: their tiles' width, or (WGRAD) their rows
-        for (int e = threadIdx.x; e < p.groups; e += (int)blockDim.x) {
-            const int T = row[e + 1] - row[e], n = (T + plan.bn - 1) / plan.bn;
-            tile[e] = WG || T <= 0 ? T : (T + n - 1) / n;
-        }
-        cta_sync();
-        for (int e = threadIdx.x; e < p.groups; e += (int)blockDim.x) {
-            int rank = e;
-            if (p.groups <= kMaxSorted) {
-                const int c = tile[e];
-                rank = 0;
-                for (int i = 0; i < p.groups; ++i) rank += tile[i] > c || (tile[i] == c && i < e);
-            }
-            order[rank] = e;
-        }
-        cta_sync();
         if (warp == 0 && !WG) {
             int before = 0;
             for (int base = 0; base < p.groups; base += 32) {
-                const int pos = base + lane;
-                int n = 0;
-                if (pos < p.groups && !void_call) {
-                    const int e = order[pos];
-                    n = (row[e + 1] - row[e] + plan.bn - 1) / plan.bn * plan.mt;
-                }
-                int sum = n;
+                const int e = base + lane;
+                int sum = 0, n = 0;
+                if (e < p.groups && !*bad) n = (row[e + 1] - row[e] + p.bn - 1) / p.bn * plan.mt;
+                sum = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int up = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += up;
                 }
-                if (pos < p.groups) tile[pos] = before + sum - n;
+                if (e < p.groups) tile[e] = before + sum - n;
                 before += __shfl_sync(0xffffffffu, sum, 31);
             }
             if (lane == 0) tile[p.groups] = before;
@@ -609,10 +533,8 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         }
     }
 
-    // the ring: stages of `ksub` K blocks; a block's B tile follows as many rows of A as the tile has (an MMA
-    // of 128 rows then reads past them, into B and what follows: rows that are not stored)
-    const int a_bytes = plan.bm / CG * BK * 2, sub_bytes = a_bytes + (WG ? kMaxBN : p.bn) / CG * BK * 2;
-    const int stage_bytes = sub_bytes * KSUB;
+    // the ring: stages of KSUB K blocks, each A's tile and then B's
+    const int sub_bytes = kABytes + (WG ? kMaxBN : p.bn) / CG * BK * 2, stage_bytes = sub_bytes * KSUB;
     const int stages = min(kMaxStages, p.off_epi / stage_bytes);
     auto give_up = [&](uint32_t why) {
         *dead = 1;
@@ -627,11 +549,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         const bool issuer = elect_one();
         ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int, int first, int rows, int nkb) {
             const int mrow = it.m0 + crank * BM;
-            const int abox = plan.bm / CG / p.a_box;   // boxes of the weights' side
             // boxes of the N side this CTA loads: its half of the tile's rows (or columns)
             const int half = it.w / CG;
             const int nbox = WG ? half / 64 : (half + p.box_rows - 1) / p.box_rows;
-            const uint32_t own = (uint32_t)a_bytes + (uint32_t)(nbox * (WG ? kChunkBytes : p.box_rows * BK * 2));
+            const uint32_t own = kABytes + (uint32_t)(nbox * (WG ? kChunkBytes : p.box_rows * BK * 2));
             for (int kb = 0; kb < nkb; ++kb) {
                 const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
@@ -648,16 +569,17 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     }
                     const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, ragged ? (uint32_t)crank : 0u) : 0u;
                     for (int sub = 0; sub < subs; ++sub) {
-                        uint8_t *a_dst = smem + stage * stage_bytes + sub * sub_bytes, *b_dst = a_dst + a_bytes;
+                        uint8_t *a_dst = smem + stage * stage_bytes + sub * sub_bytes, *b_dst = a_dst + kABytes;
                         const int k0 = (kb * KSUB + sub) * BK;
-                        for (int i = 0; i < abox; ++i) {
-                            uint8_t *dst = a_dst + i * p.a_box * (BK * 2);
-                            if constexpr (MODE == GROUPED_FORWARD) {
-                                // a box that would start past the last weights row starts on it: its rows are never stored
-                                const int n = min(mrow + i * p.a_box, p.M - 1);
-                                if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, k0, n, it.e);
-                                else ptx::tma_load_3d(dst, &tmap_a, bar, k0, n, it.e);
-                            } else {
+                        if constexpr (MODE == GROUPED_FORWARD) {
+                            // a box that would start past the last weights row starts on it: its rows are never stored
+                            const int n = min(mrow, p.M - 1);
+                            if constexpr (PAIR) ptx::tma_load_3d_pair(a_dst, &tmap_a, bar_cl, k0, n, it.e);
+                            else ptx::tma_load_3d(a_dst, &tmap_a, bar, k0, n, it.e);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                uint8_t *dst = a_dst + i * kChunkBytes;
                                 const int c = min(mrow + 64 * i, (p.M - 1) & ~7);   // 16-byte aligned, inside the tensor
                                 if constexpr (MODE == GROUPED_DGRAD) {
                                     if constexpr (PAIR) ptx::tma_load_3d_pair(dst, &tmap_a, bar_cl, c, k0, it.e);
@@ -708,7 +630,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             const bool issuer = elect_one();
             constexpr uint32_t a_step = desc_step(!A_MMAJOR), b_step = desc_step(!WG);
             const uint32_t a_low = desc_low(ptx::smem_u32(smem), !A_MMAJOR);
-            const uint32_t b_low = desc_low(ptx::smem_u32(smem) + (uint32_t)a_bytes, !WG);
+            const uint32_t b_low = desc_low(ptx::smem_u32(smem) + kABytes, !WG);
             auto mma = [](uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
                 if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a), desc_of(b), id, acc);
                 else ptx::umma_bf16(d, desc_of(a), desc_of(b), id, acc);
@@ -716,7 +638,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
             ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int part, int, int rows, int nkb) {
                 if (nkb == 0) return true;
                 const uint32_t id = idesc(BM * CG, it.w, p.bf16 != 0, A_MMAJOR, WG);
-                const uint32_t apart = sums_of<MODE, CG>(it.w) > 1 ? 64u : 0u;
                 const int c = WG && part > 0 ? b ^ 1 : b;   // the accumulator
                 bool got = ptx::mbar_wait<PAIR>(&tempty[c], ((taken >> c) & 1u) ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) return ok = false;
@@ -734,18 +655,15 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     const int subs = KSUB == 1 ? 1 : min(KSUB, (p.red + BK - 1) / BK - kb * KSUB);
                     if (issuer) {
                         mma(d_tmem, a, bb, id, acc);
-                        const uint32_t acc1 = apart ? acc : 1u;
-                        if (!WG || steps > 1) mma(d_tmem + apart, a + a_step, bb + b_step, id, acc1);
-                        if (!WG || steps > 2) mma(d_tmem + 2 * apart, a + 2 * a_step, bb + 2 * b_step, id, acc1);
-                        if (!WG || steps > 3) mma(d_tmem + 3 * apart, a + 3 * a_step, bb + 3 * b_step, id, acc1);
+                        if (!WG || steps > 1) mma(d_tmem, a + a_step, bb + b_step, id, 1u);
+                        if (!WG || steps > 2) mma(d_tmem, a + 2 * a_step, bb + 2 * b_step, id, 1u);
+                        if (!WG || steps > 3) mma(d_tmem, a + 3 * a_step, bb + 3 * b_step, id, 1u);
 #pragma unroll
                         for (int sub = 1; sub < KSUB; ++sub) {
                             if (sub >= subs) break;
                             const uint32_t as = a + (uint32_t)sub * (uint32_t)(sub_bytes >> 4), bs = bb + (uint32_t)sub * (uint32_t)(sub_bytes >> 4);
-                            mma(d_tmem, as, bs, id, 1u);
-                            mma(d_tmem + apart, as + a_step, bs + b_step, id, 1u);
-                            mma(d_tmem + 2 * apart, as + 2 * a_step, bs + 2 * b_step, id, 1u);
-                            mma(d_tmem + 3 * apart, as + 3 * a_step, bs + 3 * b_step, id, 1u);
+#pragma unroll
+                            for (int k = 0; k < BK / UMMA_K; ++k) mma(d_tmem, as + k * a_step, bs + k * b_step, id, 1u);
                         }
                         if constexpr (PAIR) commit_both(&empty[stage]);
                         else ptx::umma_commit(&empty[stage]);
@@ -836,7 +754,7 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
         ok &= each_item<MODE, KSUB>(p, items, [&](const Item &it, int part, int, int, int nkb) {
             const int n0 = it.m0 + crank * BM + q * 32;
             const int width = WG ? min(kMaxBN, p.cols - it.t0) : it.tv;
-            const bool mine = q * 32 < plan.bm && n0 < p.M;
+            const bool mine = n0 < p.M;
             float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (MODE == GROUPED_FORWARD && p.bias) {
 #pragma unroll
@@ -910,14 +828,6 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
                     tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32), r + 16);
                     const int count = min(32, width - c * 32), token = it.t0 + c * 32, next = c + kEpiWarps / 4;
                     ptx::tmem_ld_wait();
-                    for (int s = 1; s < sums_of<MODE, CG>(it.w); ++s) {   // the sums of the other sixteens of every K step
-                        uint32_t u[32];
-                        tmem_ld_16x256b_x4(taddr + (uint32_t)(c * 32 + 64 * s), u);
-                        tmem_ld_16x256b_x4(taddr + (16u << 16) + (uint32_t)(c * 32 + 64 * s), u + 16);
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(u[j]));
-                    }
                     uint4 cur[4] = {pre[0], pre[1], pre[2], pre[3]};
                     if (slope && next * 32 < width)
                         load_pre(pre, p.pre, p.pre_stride, n0, p.M, it.t0 + next * 32, min(32, width - next * 32));
@@ -1072,17 +982,13 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     p.cols = a.K;
     p.bn = bn;
     p.box_rows = bn / CG < 64 ? bn / CG : 64;
-    // few rows per group: weights tiles of 128, 64 or (K-major) 32 rows, as boxes of that least size
-    const bool small = KSUB == 4;
-    p.bm = small ? 0 : BM * CG;
-    p.a_box = MODE == GROUPED_FORWARD ? (small ? 32 : BM) : 64;
     p.act = a.act;
     p.bf16 = a.dtype == TF_BF16;
     p.accumulate = splits > 1 ? 0 : a.accumulate;
     p.dy = a.dy;
     p.dy_stride = a.dy_stride;
     p.dbias = splits > 1 && a.dbias ? a.ws + (int64_t)p.groups * a.N * a.K : a.dbias;
-    const int sched = (3 * (p.groups + 1) + 4) * 4;
+    const int sched = (2 * (p.groups + 1) + 2) * 4;
     const int fixed = (WG ? 0 : kEpiWarps * kBoxBytes) + kItemBytes + kNumBars * 8 + 16 + sched;
     const int ring = (kSmemLimit - fixed) / 1024 * 1024;
     if (ring < 2 * KSUB * (kABytes + (WG ? kMaxBN : bn) / CG * BK * 2)) return cudaErrorNotSupported;
@@ -1096,7 +1002,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     CUtensorMap ta, tb;
     bool ok;
     if (MODE == GROUPED_FORWARD)
-        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, BK, p.a_box) &&
+        ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, BK, BM) &&
              encode_rows(&tb, type, a.x, a.rows, a.K, a.x_stride, BK, p.box_rows);
     else if (MODE == GROUPED_DGRAD)
         ok = encode_groups(&ta, type, a.w, a.groups, a.N, a.K, 64, BK) &&
@@ -1109,8 +1015,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     int units = 0;
     cudaError_t e = resident<MODE, CG, KSUB>(&units);
     if (e != cudaSuccess) return e;
-    const int bm = p.bm ? p.bm : p.a_box;   // (the narrowest tile gives the most work items)
-    const int64_t mt = (p.M + bm - 1) / bm;
+    const int64_t mt = (p.M + BM * CG - 1) / (BM * CG);
     const int64_t most = WG ? (int64_t)p.groups * mt * ((a.K + kMaxBN - 1) / kMaxBN)
                             : ((int64_t)a.rows / bn + a.groups) * mt;
     if (most >= (int64_t)1 << 31) return cudaErrorNotSupported;
@@ -1196,8 +1101,8 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
         return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);
     } else {
         if (M > BM && avg > 128) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
-        if (avg <= 64) return launch_mode<MODE, 1, 4>(a, avg <= 16 ? 16 : avg <= 32 ? 32 : 64, st);
-        return launch_mode<MODE, 1, 1>(a, avg <= 128 ? 128 : 256, st);
+        if (avg <= 128) return launch_mode<MODE, 1, 2>(a, avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128, st);
+        return launch_mode<MODE, 1, 1>(a, kMaxBN, st);
     }
 }
 
