@@ -62,25 +62,26 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0, G
     const int width = ring.width;
 
     float2 ga[HELD ? PAIRS : 1], dg[PAIRS], db[PAIRS];
-    float *gs = reinterpret_cast<float *>(smem + g.gamma_off);
+    // [PAIRS][gsize] pairs: the lanes' reads of one lie side by side
+    float2 *gs = reinterpret_cast<float2 *>(smem + g.gamma_off);
+    auto gamma_of = [&](int c) { return a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f; };
     if (!HELD) {
-        for (int c = threadIdx.x; c < width; c += (int)blockDim.x) gs[c] = a.gamma ? __ldg(a.gamma + c0 + c) : 1.0f;
+        for (int i = threadIdx.x; i < PAIRS * gsize; i += (int)blockDim.x) {
+            const int p = i / gsize, l = i % gsize;
+            gs[i] = make_float2(gamma_of(C::col(2 * p, l, gsize)), gamma_of(C::col(2 * p + 1, l, gsize)));
+        }
         cta_sync();
     }
 #pragma unroll
     for (int p = 0; p < PAIRS; ++p) {
-        const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
-        if (HELD)
-            ga[HELD ? p : 0] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
-                                           a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
+        if (HELD) ga[HELD ? p : 0] = make_float2(gamma_of(C::col(2 * p, gt, gsize)), gamma_of(C::col(2 * p + 1, gt, gsize)));
         dg[p] = db[p] = make_float2(0.0f, 0.0f);
     }
     // (read anew for either use: held, the compiler would keep it in registers)
     auto gamma2 = [&](int p) {
         if (HELD) return ga[HELD ? p : 0];
-        float2 v = make_float2(1.0f, 1.0f);
-        if (C::inside(2 * p, gt, gsize, width))
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(ptx::smem_u32(gs + C::col(2 * p, gt, gsize))));
+        float2 v;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(ptx::smem_u32(gs + p * gsize + gt)));
         return v;
     };
     const float inv_h = 1.0f / (float)a.hidden;
@@ -147,33 +148,44 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0, G
     if (a.ws) {
         // this CTA's sums: row `unit` of dgamma's and of dbeta's [units][hidden] array
         float *wg = a.ws + (int64_t)unit * a.hidden + c0, *wb = wg + (int64_t)units * a.hidden;
-        const int groups = g.threads / gsize;
-        float *acc = reinterpret_cast<float *>(smem) + gt;   // [2*COLS][gsize]: thread gt of every group has the same columns
-        for (int w = 0; w < groups; ++w) {   // the groups' sums, added in order in shared memory
-            cta_sync();   // every group is done with its ring, and with the previous group's turn
-            if ((int)threadIdx.x / gsize != w) continue;
+        // the groups' sums, added as a tree in shared memory (16 groups one after the other took 5 us): thread
+        // gt of every group has the same columns, [2*COLS][gsize] per group
+        const int gid = (int)threadIdx.x / gsize;
+        cta_sync();   // every group is done with its ring
+        for (int n = g.threads / gsize; n > 1;) {
+            const int half = (n + 1) / 2;
+            float *at = reinterpret_cast<float *>(smem) + (gid < half ? gid : gid - half) * (2 * COLS * gsize) + gt;
+            if (gid >= half && gid < n) {
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) {
+                    at[4 * p * gsize] = dg[p].x;
+                    at[(4 * p + 1) * gsize] = dg[p].y;
+                    at[(4 * p + 2) * gsize] = db[p].x;
+                    at[(4 * p + 3) * gsize] = db[p].y;
+                }
+            }
+            cta_sync();
+            if (gid < n - half) {
+#pragma unroll
+                for (int p = 0; p < PAIRS; ++p) {
+                    dg[p] = fadd2(dg[p], make_float2(at[4 * p * gsize], at[(4 * p + 1) * gsize]));
+                    db[p] = fadd2(db[p], make_float2(at[(4 * p + 2) * gsize], at[(4 * p + 3) * gsize]));
+                }
+            }
+            cta_sync();
+            n = half;
+        }
+        if (gid == 0) {
 #pragma unroll
             for (int p = 0; p < PAIRS; ++p) {
-                float *at = acc + 4 * p * gsize;
-                if (w > 0) {
-                    dg[p] = fadd2(dg[p], make_float2(at[0], at[gsize]));
-                    db[p] = fadd2(db[p], make_float2(at[2 * gsize], at[3 * gsize]));
+                const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
+                if (c < width) {
+                    wg[c] = dg[p].x;
+                    wb[c] = db[p].x;
                 }
-                if (w + 1 < groups) {
-                    at[0] = dg[p].x;
-                    at[gsize] = dg[p].y;
-                    at[2 * gsize] = db[p].x;
-                    at[3 * gsize] = db[p].y;
-                } else {
-                    const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
-                    if (c < width) {
-                        wg[c] = dg[p].x;
-                        wb[c] = db[p].x;
-                    }
-                    if (d < width) {
-                        wg[d] = dg[p].y;
-                        wb[d] = db[p].y;
-                    }
+                if (d < width) {
+                    wg[d] = dg[p].y;
+                    wb[d] = db[p].y;
                 }
             }
         }

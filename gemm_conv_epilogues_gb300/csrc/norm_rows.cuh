@@ -495,7 +495,7 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     const int ring = tensors * g.tensor_bytes + 8;
     // row groups per SM: as many as the registers hold, fewer where shared
     // memory has no room for two stages of each
-    const int sm_bytes = 226 * 1024 - (gamma_in_smem ? (int)slice * 4 : 0);
+    const int gamma = gamma_in_smem ? cols * g.group * 4 : 0, sm_bytes = 226 * 1024 - gamma;
     const bool one_cta = merged && g.csize == 1;
     auto room = [&](int n) {   // of one of n groups, past a CTA's own 2 KB (static memory, and what the system keeps)
         return one_cta ? (sm_bytes - 2048) / n : sm_bytes / n - 2048;
@@ -518,8 +518,9 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     g.per_sm = groups / in_cta;
     g.bar_off = in_cta * stages * tensors * g.tensor_bytes;
     g.gamma_off = (g.bar_off + in_cta * stages * 8 + 15) / 16 * 16;
-    g.smem = gamma_in_smem ? g.gamma_off + (int)slice * 4 : g.bar_off + in_cta * stages * 8;
-    if (merged && g.smem < 8 * cols * g.group) g.smem = 8 * cols * g.group;   // the groups' column sums are added there
+    g.smem = g.gamma_off + gamma;
+    // half the groups' column sums at a time lie there to be added
+    if (merged && g.smem < in_cta / 2 * 8 * cols * g.group) g.smem = in_cta / 2 * 8 * cols * g.group;
     return g;
 }
 
