@@ -229,7 +229,7 @@ Geometry geometry_for(int64_t rows, int64_t hidden, int size, bool aligned, int 
 {
     const int cols = cols_for(hidden, size, aligned);
     const int group = (int)(hidden + cols - 1) / cols;   // (rounded up by geometry())
-    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group), true, rows, cols > 16);
+    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group), true, rows, cols > 16 ? 1 : 0);
 }
 
 // The most partial sums that any alignment and number of operands gives.

@@ -12,11 +12,18 @@ namespace {
 
 using namespace norm;
 
-// Columns per thread: 16 at 128 registers, 8 at 64 where they are element-wise.
-// Fewer registers would spill, which costs far more than more threads gain: with
-// most of the SM's memory in the rings, the little L1 left does not hold them.
-// (Element-wise rows of several CTAs take 16, too, in CTAs of 512.)
-constexpr int cols_of(bool aligned, int64_t hidden) { return aligned || hidden > kSlice ? 16 : 8; }
+// Columns per thread: 16 at 128 registers; 8 at 64 for narrow rows and where they
+// are element-wise; 24 for 16-bit rows that then take one warp, with gamma and
+// beta in shared memory.  Fewer registers would spill, which costs far more than
+// more threads gain: with most of the SM's memory in the rings, the little L1
+// left does not hold them.  (Element-wise rows of several CTAs take 16, too, in
+// CTAs of 512.)
+int cols_of(bool aligned, int size, int64_t hidden)
+{
+    if (!aligned) return hidden > kSlice ? 16 : 8;
+    if (hidden <= 256) return 8;
+    return size == 2 && hidden > 512 && hidden <= 768 ? 24 : 16;
+}
 constexpr int sm_threads(int cols) { return cols == 8 ? 1024 : 512; }
 
 // GROUP: threads per row where the columns are element-wise (a constant makes
@@ -28,6 +35,7 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
                                   : GROUP > 256 ? (COLS == 8 ? 2 : 1)
                                   : GROUP > 0   ? 4
                                   : SPAN > 0    ? 1
+                                  : COLS == 8   ? 4
                                                 : 2)
     norm_forward_kernel(const __grid_constant__ NormArgs a, const __grid_constant__ Sources src,
                         const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
@@ -35,6 +43,7 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
     constexpr bool ALIGNED = GROUP == 0, CLUSTER = SPAN == 2;
     using C = Cols<T, ALIGNED, COLS>;
     constexpr int PAIRS = C::PAIRS;
+    constexpr bool HELD = COLS <= 16;   // gamma and beta in registers
     pdl_begin();
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float2 red[2][kMaxGroup / 32];
@@ -47,14 +56,25 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
     Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
 
-    float2 ga[PAIRS], be[PAIRS];
+    float2 ga[HELD ? PAIRS : 1], be[HELD ? PAIRS : 1];
+    // [PAIRS][gsize] pairs: the lanes' reads of one lie side by side
+    float2 *gs = reinterpret_cast<float2 *>(smem + g.gamma_off), *bs = gs + PAIRS * gsize;
+    auto pair_of = [&](const float *v, int p, int l, float none) {
+        const int c = C::col(2 * p, l, gsize), d = C::col(2 * p + 1, l, gsize);
+        return make_float2(v && c < width ? __ldg(v + c0 + c) : none, v && d < width ? __ldg(v + c0 + d) : none);
+    };
+    if (HELD) {
 #pragma unroll
-    for (int p = 0; p < PAIRS; ++p) {
-        const int c = C::col(2 * p, gt, gsize), d = C::col(2 * p + 1, gt, gsize);
-        ga[p] = make_float2(a.gamma && c < width ? __ldg(a.gamma + c0 + c) : 1.0f,
-                            a.gamma && d < width ? __ldg(a.gamma + c0 + d) : 1.0f);
-        be[p] = make_float2(a.beta && c < width ? __ldg(a.beta + c0 + c) : 0.0f,
-                            a.beta && d < width ? __ldg(a.beta + c0 + d) : 0.0f);
+        for (int p = 0; p < PAIRS; ++p) {
+            ga[HELD ? p : 0] = pair_of(a.gamma, p, gt, 1.0f);
+            be[HELD ? p : 0] = pair_of(a.beta, p, gt, 0.0f);
+        }
+    } else {
+        for (int i = threadIdx.x; i < PAIRS * gsize; i += (int)blockDim.x) {
+            gs[i] = pair_of(a.gamma, i / gsize, i % gsize, 1.0f);
+            bs[i] = pair_of(a.beta, i / gsize, i % gsize, 0.0f);
+        }
+        cta_sync();
     }
     const float inv_h = 1.0f / (float)a.hidden, inv_n = 1.0f / (float)width;
 
@@ -109,7 +129,8 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
         if (a.sum) C::store(reinterpret_cast<T *>(a.sum) + (row * a.sum_stride + c0), width, gt, gsize, s);
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p)
-            s[p] = ffma2(fmul2(fsub2(s[p], make_float2(mean, mean)), make_float2(rstd, rstd)), ga[p], be[p]);
+            s[p] = ffma2(fmul2(fsub2(s[p], make_float2(mean, mean)), make_float2(rstd, rstd)), HELD ? ga[HELD ? p : 0] : gs[p * gsize + gt],
+                         HELD ? be[HELD ? p : 0] : bs[p * gsize + gt]);
         C::store(reinterpret_cast<T *>(a.y) + (row * a.y_stride + c0), width, gt, gsize, s);
     }
     if (gt == 0) ring.drain();
@@ -126,13 +147,17 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
                          aligned_rows(a.res, a.res_stride, size) && aligned_rows(a.y, a.y_stride, size) &&
                          aligned_rows(a.sum, a.sum_stride, size);
     const Sources src = {{a.x, a.res}, {a.x_stride, a.res_stride}};
-    const int cols = cols_of(aligned, a.hidden);
-    const Geometry g = geometry(a.hidden, size, aligned, cols, a.res ? 2 : 1, sm_threads(cols), false, a.rows);
+    const int cols = cols_of(aligned, size, a.hidden);
+    const Geometry g = geometry(a.hidden, size, aligned, cols, a.res ? 2 : 1, sm_threads(cols), false, a.rows,
+                                cols > 16 ? 2 : 0);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
-        if (aligned)
-            return g.csize > 1 ? norm_forward_kernel<T, 0, 2, NT, 16>
-                   : g.group > 256 ? norm_forward_kernel<T, 0, 1, NT, 16> : norm_forward_kernel<T, 0, 0, NT, 16>;
+        if (aligned) {
+            if (g.csize > 1) return norm_forward_kernel<T, 0, 2, NT, 16>;
+            if (cols == 8) return norm_forward_kernel<T, 0, 0, NT, 8>;
+            if (cols == 24) return norm_forward_kernel<T, 0, 0, NT, size == 2 ? 24 : 16>;
+            return g.group > 256 ? norm_forward_kernel<T, 0, 1, NT, 16> : norm_forward_kernel<T, 0, 0, NT, 16>;
+        }
         if (g.csize > 1) return norm_forward_kernel<T, 512, 2, NT, 16>;
         switch (g.group) {
         case 32: return norm_forward_kernel<T, 32, 0, NT, 8>;

@@ -87,7 +87,7 @@ struct Geometry {
     int csize, slice;   // CTAs per row and columns per CTA
     int stages, tensor_bytes;   // ring of one row group: stages x tensors x tensor_bytes
     int bar_off;        // mbarriers behind the rings
-    int gamma_off;      // gamma behind those, where the kernel keeps it there
+    int gamma_off;      // parameter tables behind those, where the kernel keeps them there
     int smem;
 };
 
@@ -479,7 +479,7 @@ __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, un
 // MERGED: all the row groups of an SM in one CTA (whose column sums then leave
 // the SM once).
 inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int tensors, int sm_threads, bool merged,
-                         int64_t rows, bool gamma_in_smem = false)
+                         int64_t rows, int tables = 0)
 {
     Geometry g;
     const int vec = aligned ? 16 / size : 1;
@@ -495,10 +495,11 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     const int ring = tensors * g.tensor_bytes + 8;
     // row groups per SM: as many as the registers hold, fewer where shared
     // memory has no room for two stages of each
-    const int gamma = gamma_in_smem ? cols * g.group * 4 : 0, sm_bytes = 226 * 1024 - gamma;
     const bool one_cta = merged && g.csize == 1;
+    // `tables` of the kernel's parameters (gamma, beta) per CTA
+    const int sm_bytes = 226 * 1024, table_bytes = tables * cols * g.group * 4;
     auto room = [&](int n) {   // of one of n groups, past a CTA's own 2 KB (static memory, and what the system keeps)
-        return one_cta ? (sm_bytes - 2048) / n : sm_bytes / n - 2048;
+        return one_cta ? (sm_bytes - 2048 - table_bytes) / n : sm_bytes / n - 2048 - table_bytes;
     };
     int groups = sm_threads / g.group;
     if (groups < 1) groups = 1;
@@ -518,7 +519,7 @@ inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int t
     g.per_sm = groups / in_cta;
     g.bar_off = in_cta * stages * tensors * g.tensor_bytes;
     g.gamma_off = (g.bar_off + in_cta * stages * 8 + 15) / 16 * 16;
-    g.smem = g.gamma_off + gamma;
+    g.smem = g.gamma_off + table_bytes;
     // half the groups' column sums at a time lie there to be added
     if (merged && g.smem < in_cta / 2 * 8 * cols * g.group) g.smem = in_cta / 2 * 8 * cols * g.group;
     return g;
