@@ -7,6 +7,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ptx_sm100.cuh"
 #include "train_internal.h"
 
 namespace tf {
@@ -218,6 +219,55 @@ __device__ __forceinline__ int group_of_tile(const Schedule &s, int groups, int 
         if (s.tile[mid] <= t) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// ---------------------------------------------------------------- tensor-core operands
+
+constexpr int BK = 64;                      // K step: one 128-byte swizzle row of 16-bit values
+constexpr int UMMA_K = 16;
+constexpr int kChunkBytes = 64 * BK * 2;    // one 64 x 64 box of an M- or N-major operand
+
+// Shared-memory matrix descriptors (128-byte swizzle), as a low word that holds
+// the address and a high word that does not change: advancing along K inside a
+// tile, or to another stage, is one 32-bit addition.
+//   K-major: rows of 64 values (128 bytes), eight of them an atom of 1024 bytes,
+//     atoms stacked densely; 16 values along K are 32 bytes.
+//   M- or N-major: boxes of 64 (M or N) x 64 (K) values, each a K row of 128
+//     bytes; eight K rows are an atom (stride byte offset 1024), the next 64 M or
+//     N values are a box further on (leading byte offset); 16 along K are 2048 bytes.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride offset, version 1, 128-byte swizzle
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, bool kmajor)
+{
+    return ((smem_addr & 0x3FFFFu) >> 4) | ((kmajor ? 1u : (uint32_t)(kChunkBytes >> 4)) << 16);
+}
+constexpr uint32_t desc_step(bool kmajor) { return (kmajor ? UMMA_K * 2 : UMMA_K * 128) >> 4; }
+
+__device__ __forceinline__ uint64_t desc_of(uint32_t low)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
+    return d;
+}
+
+// kind::f16 with fp32 accumulators; operands K-major unless said otherwise.
+__device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor, bool b_nmajor)
+{
+    const uint32_t fmt = bf16 ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mmajor ? 1u : 0u) << 15) | ((b_nmajor ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// One lane of the (converged) warp.  The roles that issue copies and MMAs run
+// their loops with the whole warp and let one lane issue: in code that a single
+// lane runs the compiler cannot keep what these instructions take in uniform
+// registers, and a K step then takes its issuer ~600 cycles (the tensor cores
+// 512 for the widest tile).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 }  // namespace grouped

@@ -39,8 +39,6 @@ namespace {
 using namespace grouped;
 
 constexpr int BM = 128;                 // weights rows per CTA (UMMA M, or half of the pair's 256)
-constexpr int BK = 64;                  // K step: one 128-byte swizzle row of 16-bit values
-constexpr int UMMA_K = 16;
 constexpr int kMaxBN = 256;             // widest row tile: one accumulator is 256 TMEM columns
 constexpr int kMaxStages = 24;
 constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
@@ -48,7 +46,6 @@ constexpr int kBiasWarps = 4;           // WGRAD: warps that sum dy's columns fo
 constexpr int threads_of(int mode) { return 32 * (kFirstEpiWarp + kEpiWarps + (mode == GROUPED_WGRAD ? kBiasWarps : 0)); }
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kABytes = BM * BK * 2;
-constexpr int kChunkBytes = 64 * BK * 2;          // one 64 x 64 box of an M- or N-major operand
 constexpr int kNumBars = 3 * kMaxStages + 9;      // full, empty, land; accumulators full x2, empty x2; drain;
                                                   // item lists ready x2, free x2
 constexpr int kItemBytes = 64 * 32;               // two lists of 32 items
@@ -87,41 +84,6 @@ struct UmmaArgs {
     int64_t dy_stride;
 };
 
-// Shared-memory matrix descriptors (128-byte swizzle), as a low word that holds
-// the address and a high word that does not change: advancing along K inside a
-// tile, or to another stage, is one 32-bit addition.
-//   K-major: rows of 64 values (128 bytes), eight of them an atom of 1024 bytes,
-//     atoms stacked densely; 16 values along K are 32 bytes.
-//   M- or N-major: boxes of 64 (M or N) x 64 (K) values, each a K row of 128
-//     bytes; eight K rows are an atom (stride byte offset 1024), the next 64 M or
-//     N values are a box further on (leading byte offset); 16 along K are 2048 bytes.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride offset, version 1, 128-byte swizzle
-
-__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, bool kmajor)
-{
-    return ((smem_addr & 0x3FFFFu) >> 4) | ((kmajor ? 1u : (uint32_t)(kChunkBytes >> 4)) << 16);
-}
-constexpr uint32_t desc_step(bool kmajor) { return (kmajor ? UMMA_K * 2 : UMMA_K * 128) >> 4; }
-
-__device__ __forceinline__ uint64_t desc_of(uint32_t low)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kDescHigh));
-    return d;
-}
-
-// One lane of the (converged) warp.  The roles that issue copies and MMAs run
-// their loops with the whole warp and let one lane issue: in code that a single
-// lane runs the compiler cannot keep what these instructions take in uniform
-// registers, and a K step then takes its issuer ~600 cycles (the tensor cores
-// 512 for the widest tile).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
 // Arrives once on the mbarrier at this offset in both CTAs of the pair.
 __device__ __forceinline__ void commit_both(uint64_t *bar)
 {
@@ -129,13 +91,6 @@ __device__ __forceinline__ void commit_both(uint64_t *bar)
                      ptx::smem_u32(bar)),
                  "h"((uint16_t)3)
                  : "memory");
-}
-
-__device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor, bool b_nmajor)
-{
-    const uint32_t fmt = bf16 ? 1u : 0u;
-    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mmajor ? 1u : 0u) << 15) | ((b_nmajor ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t *r)
@@ -1100,9 +1055,10 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
         const cudaError_t e = pair ? launch_mode<MODE, 2, 1>(a, kMaxBN, st, splits) : launch_mode<MODE, 1, 1>(a, kMaxBN, st, splits);
         return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);
     } else {
-        if (M > BM && avg > 128) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
-        if (avg <= 128) return launch_mode<MODE, 1, 2>(a, avg <= 16 ? 16 : avg <= 32 ? 32 : avg <= 64 ? 64 : 128, st);
-        return launch_mode<MODE, 1, 1>(a, kMaxBN, st);
+        // A group's tiles of `bn` rows each, half a tile more on average for the ragged end.
+        auto one_wave = [&](int bn) { return (M + BM - 1) / BM * (a.rows / bn + (a.groups + 1) / 2) <= sm_count(); };
+        if (M > BM && avg > 96 && !one_wave(128)) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
+        return launch_mode<MODE, 1, 2>(a, avg <= 48 || one_wave(64) ? 64 : 128, st);
     }
 }
 
@@ -1124,16 +1080,16 @@ cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st)
     if (mode == GROUPED_FORWARD) {
         const bool tma = dims && rows_ok(a.x, a.x_stride) && rows_ok(a.y, a.y_stride) && rows_ok(a.pre, a.pre_stride) &&
                          aligned16(a.w);
-        return tma ? launch_auto<GROUPED_FORWARD>(a, st) : launch_grouped_simple(a, mode, st);
+        return tma ? launch_auto<GROUPED_FORWARD>(a, st) : launch_grouped_unaligned(a, mode, st);
     }
     if (mode == GROUPED_DGRAD) {
         const bool tma = dims && rows_ok(a.dy, a.dy_stride) && rows_ok(a.y, a.y_stride) && rows_ok(a.pre, a.pre_stride) &&
                          aligned16(a.w);
-        return tma ? launch_auto<GROUPED_DGRAD>(a, st) : launch_grouped_simple(a, mode, st);
+        return tma ? launch_auto<GROUPED_DGRAD>(a, st) : launch_grouped_unaligned(a, mode, st);
     }
     const bool tma = dims && rows_ok(a.dy, a.dy_stride) && rows_ok(a.x, a.x_stride) && aligned16(a.dw);
     if (tma) return launch_auto<GROUPED_WGRAD>(a, st);
-    const cudaError_t e = launch_grouped_simple(a, mode, st);
+    const cudaError_t e = launch_grouped_unaligned(a, mode, st);
     return e != cudaSuccess || !a.dbias ? e : launch_grouped_bias_grad(a, st);
 }
 

@@ -16,31 +16,41 @@ using namespace norm;
 
 // Threads per SM, from the registers the columns take (two fp32 sums, gamma,
 // and the row in its storage type): 128 registers for 16 columns and 24 (gamma
-// in shared memory), 80 for 8 (96 where they are element-wise, but
-// for the widest groups).  Spilled registers cost far more than a few warps
-// fewer: with most of the SM's memory in the rings, the little L1 that is left
-// does not hold them.
-constexpr int sm_threads(int cols, bool aligned, int group)
+// in shared memory), 80 for 8; where those are element-wise 96, with dres 128,
+// but for the widest groups.  Spilled registers cost far more than a few warps
+// fewer, since with most of the SM's memory in the rings the little L1 that is
+// left does not hold them (8000 x 3501 fp32 with dres: FIG1).
+constexpr int sm_threads(int cols, bool aligned, int group, int tensors)
 {
-    return cols > 8 ? 512 : aligned || group > 640 ? 768 : 640;
+    if (cols > 8) return 512;
+    if (aligned || group > 640) return 768;
+    return tensors < 3 || group > 512 ? 640 : 512;
+}
+
+// ... and of a CTA with element-wise columns, which has whole groups only.
+constexpr int cta_threads(int cols, int group, int tensors)
+{
+    const int n = sm_threads(cols, group == 0, group, tensors);
+    return group == 0 || group > n ? n : n / group * group;
 }
 
 // Columns per thread: 16, or 8 for narrow rows and for element-wise columns (16
 // above 6144 of them); 24 for 16-bit rows that then take one warp, whose sums
-// need no barrier (50001 x 640 fp16 without the weights' gradients: 52 us, 58
+// need no barrier (50001 x 640 fp16 without the weights' gradients: 39 us, FIG2
 // with two warps of 16; 32 columns for rows of 1024 were slower, 48 against 30).
-int cols_for(int64_t hidden, int size, bool aligned)
+// With dres 24 do not fit the registers (122 us, FIG3).
+int cols_for(int64_t hidden, int size, bool aligned, int tensors)
 {
     if (!aligned) return hidden > 6144 ? 16 : 8;
     if (hidden <= 256) return 8;
-    if (size == 2 && hidden > 512 && hidden <= 768) return 24;
+    if (size == 2 && hidden > 512 && hidden <= 768 && tensors < 3) return 24;
     return 16;
 }
 
 // GROUP: threads per row where the columns are element-wise (a constant makes
 // them immediate offsets), 0 for 16-byte vectors.
 template <typename T, int GROUP, bool CLUSTER, int NT, int COLS>
-__global__ void __launch_bounds__(CLUSTER ? 512 : sm_threads(COLS, GROUP == 0, GROUP), 1)
+__global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 1)
     norm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Sources src,
                          const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
@@ -227,9 +237,9 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
 
 Geometry geometry_for(int64_t rows, int64_t hidden, int size, bool aligned, int tensors)
 {
-    const int cols = cols_for(hidden, size, aligned);
+    const int cols = cols_for(hidden, size, aligned, tensors);
     const int group = (int)(hidden + cols - 1) / cols;   // (rounded up by geometry())
-    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group), true, rows, cols > 16 ? 1 : 0);
+    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group, tensors), true, rows, cols > 16 ? 1 : 0);
 }
 
 // The most partial sums that any alignment and number of operands gives.
@@ -261,13 +271,13 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
         constexpr int NT = decltype(nt)::value;
         if (aligned) {
             if (g.csize > 1) return norm_backward_kernel<T, 0, true, NT, 16>;
-            switch (cols_for(a.hidden, size, true)) {
+            switch (cols_for(a.hidden, size, true, NT)) {
             case 8: return norm_backward_kernel<T, 0, false, NT, 8>;
-            case 24: return norm_backward_kernel<T, 0, false, NT, size == 2 ? 24 : 16>;
+            case 24: return norm_backward_kernel<T, 0, false, NT, size == 2 && NT < 3 ? 24 : 16>;
             default: return norm_backward_kernel<T, 0, false, NT, 16>;
             }
         }
-        if (cols_for(a.hidden, size, false) == 16)
+        if (cols_for(a.hidden, size, false, NT) == 16)
             return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16> : norm_backward_kernel<T, 512, false, NT, 16>;
         switch (g.group) {
         case 32: return norm_backward_kernel<T, 32, false, NT, 8>;

@@ -42,7 +42,7 @@ struct GroupedArgs {
 };
 // 32-bit tile counts and row indices (rows + one tile stay below 2^31)
 constexpr int64_t kGroupedMaxGroups = 1024, kGroupedMaxWidth = 65536, kGroupedMaxRows = (int64_t)1 << 22;
-cudaError_t launch_grouped_simple(const GroupedArgs &a, int mode, cudaStream_t st);
+cudaError_t launch_grouped_unaligned(const GroupedArgs &a, int mode, cudaStream_t st);
 cudaError_t launch_grouped_bias_grad(const GroupedArgs &a, cudaStream_t st);
 cudaError_t launch_grouped(const GroupedArgs &a, int mode, cudaStream_t st);
 int64_t grouped_wgrad_workspace(int64_t rows, int groups, int64_t N, int64_t K, int dtype);

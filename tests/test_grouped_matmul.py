@@ -276,6 +276,55 @@ def test_more_tiles_than_a_wave(b):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("name", ["fp16", "bf16"])
+def test_many_row_tiles(b, name, act):
+    """Groups of many rows and enough tiles for the widest ones, in rows of a wider buffer."""
+    counts = [300, 1, 777, 0, 513, 1200]
+    _check_forward(b, counts, 1288, 136, name, act, True, True, 8, 5, 9)
+    _check_dgrad(b, counts, 136, 1288, name, act, 8, 5, 9)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(130, 70), (75, 131), (1145, 76), (257, 129)])
+@pytest.mark.parametrize("counts", [[2500, 0, 311], [300, 1, 77, 0, 513]], ids=str)
+def test_unaligned_rows(b, counts, N, K):
+    """Rows of 2- and 4-byte alignment, over several tiles and reduction steps in either direction."""
+    for name, pad in (("fp16", 0), ("bf16", 1)):
+        _check_forward(b, counts, N, K, name, "silu", True, True, pad, 3, 2)
+        _check_dgrad(b, counts, N, K, name, "gelu", pad, 3, 2)
+        _check_wgrad(b, counts, N, K, name, pad=pad, before=3, after=2)
+    _check_wgrad(b, counts, N, K, "bf16", accumulate=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_unaligned_bases(b, shift):
+    """Whole 16-byte rows whose buffers start 2, 4 or 8 bytes past a 16-byte boundary."""
+    counts, N, K = [70, 0, 200], 136, 72
+    off, rows, dev = _layout(counts)
+    whole = {"x": _rand(rows, K, "bf16"), "w": _rand(3 * N, K, "bf16", scale=0.1, seed=1).view(3, N, K),
+             "dy": _rand(rows, N, "bf16", seed=2)}
+
+    def run(t):
+        y, _ = _run_forward(b, t["x"], t["w"], None, dev, "bf16", "none", False)
+        dx = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+        b.tf_grouped_matmul_dgrad(t["dy"], N, t["w"], dev, None, 0, dx, K, rows, 3, N, K, 0, b.TF_BF16)
+        dw = torch.empty(3, N, K, device="cuda")
+        b.tf_grouped_matmul_wgrad(t["dy"], N, t["x"], K, dev, dw, None, rows, 3, N, K, 0, b.TF_BF16, None, 0)
+        return y, dx, dw
+
+    want = run(whole)
+    for key in whole:
+        t = dict(whole)
+        buf = torch.full((t[key].numel() + shift,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        t[key] = buf[shift:].view(t[key].shape).copy_(t[key])
+        for got, same, red in zip(run(t), want, (K, N, 200)):
+            # the sums' order may differ: both are good to `red` steps of 2^-24 of sums of magnitudes below 9 * red
+            assert (got.double() - same.double()).abs().max() <= 2 * red * U * 9 * red + 2.0 ** -7 * same.abs().max()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("counts,N,K", [([2, 40, 0, 7, 90], 256, 320), ([1, 3, 0, 2, 5], 256, 320),
                                         ([2, 40, 0, 7, 90], 100, 60)])
 def test_groups_do_not_reach_each_other(b, counts, N, K):
