@@ -1058,7 +1058,7 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
         // A group's tiles of `bn` rows each, half a tile more on average for the ragged end.
         auto one_wave = [&](int bn) { return (M + BM - 1) / BM * (a.rows / bn + (a.groups + 1) / 2) <= sm_count(); };
         if (M > BM && avg > 96 && !one_wave(128)) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
-        return launch_mode<MODE, 1, 2>(a, avg <= 48 || one_wave(64) ? 64 : 128, st);
+        return launch_mode<MODE, 1, 2>(a, avg <= 8 ? 16 : avg <= 48 || one_wave(64) ? 64 : 128, st);
     }
 }
 

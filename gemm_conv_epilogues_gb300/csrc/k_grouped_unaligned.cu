@@ -6,15 +6,20 @@
 // Tensor cores all the same, with operands that threads bring: eight warps load
 // 128-byte pieces of rows, two values per lane (a 4-byte load where the operand
 // allows it, else two of 2 bytes), and put them into the swizzled tiles that
-// the MMAs read; a ninth warp issues the MMAs.  Values outside a row, a group
+// the MMAs read; the first of them issues those, one K step behind.  Values outside a row, a group
 // or the reduction become zeros on the way, so nothing there is read or counts.
 // The side of the output that is contiguous in memory is the MMA's M side (n,
 // k, and for WGRAD k too): a TMEM lane holds one value of every output row, and
 // a warp's stores lie side by side.
 //
 // 128 x 128 tiles, two CTAs per SM, so that one loads while the other stores.
-// Bound by the loads' way through the L1 (a K step of both operands is 256
-// pieces, the MMAs on it take 128 cycles).
+// Bound by the loads' way through the L1: a K step of both operands is 256
+// pieces, the MMAs on it take 128 cycles.  16384 rows, 16 groups, bf16: forward
+// 401 us for 2047 x 1001, 242 us (278 TFLOP/s) for 2046 x 1002, whose rows are
+// whole words; the same product on the CUDA cores took over 4 ms.  All of a K
+// step's loads are under way at once; joining the values of a word as they come
+// took 1343 and 306 us.  A ninth warp for the MMAs (96 registers instead of
+// 128): 526 and 226 us.
 #include <mutex>
 
 #include "grouped.cuh"
@@ -24,7 +29,7 @@ namespace {
 
 using namespace grouped;
 
-constexpr int TILE = 128, kStages = 3, kLoadWarps = 8, kThreads = 32 * (kLoadWarps + 1);
+constexpr int TILE = 128, kStages = 3, kLoadWarps = 8, kThreads = 32 * kLoadWarps;
 constexpr int kOperandBytes = TILE * BK * 2, kStageBytes = 2 * kOperandBytes;
 constexpr int kSmemBytes = kStages * kStageBytes + 1024;   // (the ring starts on a multiple of 1024)
 constexpr int kPerWarp = TILE / kLoadWarps;                // pieces of one operand per warp and K step
@@ -35,38 +40,55 @@ struct Source {
     const uint16_t *src;
     int64_t ld;
     int rows, cols;
-    bool pairs;   // two neighbouring values are one 4-byte load
 };
 
 // A warp's pieces of the K step at k0: piece i = warp + 8j is row i of a K-major
 // tile, values k0..k0+63, or row k0 + i%64 of an M- or N-major one, values
-// 64*(i/64) and on.  Lane l holds the values 2l and 2l+1.
+// 64*(i/64) and on.  Lane l holds the values 2l and 2l+1, as one word or as two.
+struct Pieces {
+    uint32_t lo[kPerWarp], hi[kPerWarp];
+};
+
 template <bool KMAJOR>
-__device__ __forceinline__ void load_pieces(uint32_t (&v)[kPerWarp], const Source &s, int k0, int warp, int lane)
+__device__ __forceinline__ void load_pieces(Pieces &v, const Source &s, int k0, int warp, int lane)
 {
+    const int r0 = KMAJOR ? warp : k0 + warp, c0 = (KMAJOR ? k0 : 0) + 2 * lane;
+    const uint16_t *p = s.src + r0 * s.ld + c0;
+    auto at = [&](int j, int &r, int &c) {
+        const int dr = 8 * (KMAJOR ? j : j & 7), dc = KMAJOR ? 0 : 64 * (j >> 3);
+        r = r0 + dr;
+        c = c0 + dc;
+        return p + dr * s.ld + dc;
+    };
+    // The same for all of the warp's pieces (rows 8 apart).  One loop for each way, so that its loads are all under way at once.
+    const bool words = (reinterpret_cast<uintptr_t>(p) & 3u) == 0 &&
+                       (s.cols % 2 == 0 || (KMAJOR ? k0 + 64 : TILE) <= s.cols);
+    int r, c;
+    if (words) {
 #pragma unroll
-    for (int j = 0; j < kPerWarp; ++j) {
-        const int r = KMAJOR ? warp + 8 * j : k0 + warp + 8 * (j & 7);
-        const int c = (KMAJOR ? k0 : 64 * (j >> 3)) + 2 * lane;
-        const uint16_t *p = s.src + r * s.ld + c;
-        const bool lo = r < s.rows && c < s.cols, hi = r < s.rows && c + 1 < s.cols;
-        if (s.pairs && hi) {
-            v[j] = __ldg(reinterpret_cast<const uint32_t *>(p));
-        } else {
-            const uint32_t a = lo ? __ldg(p) : 0u, b = hi ? __ldg(p + 1) : 0u;
-            v[j] = a | b << 16;
+        for (int j = 0; j < kPerWarp; ++j) {
+            const uint16_t *q = at(j, r, c);
+            v.lo[j] = r < s.rows && c < s.cols ? __ldg(reinterpret_cast<const uint32_t *>(q)) : 0u;
+            v.hi[j] = 0;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerWarp; ++j) {
+            const uint16_t *q = at(j, r, c);
+            v.lo[j] = r < s.rows && c < s.cols ? __ldg(q) : 0u;
+            v.hi[j] = r < s.rows && c + 1 < s.cols ? __ldg(q + 1) : 0u;
         }
     }
 }
 
 // Pieces warp + 8j, j < count, into the tile: 128-byte rows, 16-byte columns
 // swizzled by the row's number modulo 8 (which is the warp's).
-__device__ __forceinline__ void store_pieces(const uint32_t (&v)[kPerWarp], uint32_t tile, int count, int warp, int lane)
+__device__ __forceinline__ void store_pieces(const Pieces &v, uint32_t tile, int count, int warp, int lane)
 {
     const uint32_t at = tile + (uint32_t)(warp * 128 + (((lane >> 2) ^ warp) << 4) + (lane & 3) * 4);
 #pragma unroll
     for (int j = 0; j < kPerWarp; ++j)
-        if (j < count) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * 1024), "r"(v[j]) : "memory");
+        if (j < count) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + j * 1024), "r"(v.lo[j] | v.hi[j] << 16) : "memory");
 }
 
 template <typename T, int MODE>
@@ -90,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_unaligned_kernel(const Gr
         ptx::mbar_init_fence();
         dead = 0;
     }
-    if (warp == kLoadWarps) {
+    if (warp == 0) {
         ptx::tmem_alloc(&tmem_slot, TILE);
         ptx::tmem_relinquish();
     }
@@ -112,7 +134,6 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_unaligned_kernel(const Gr
         }
         return ok;
     };
-    auto paired = [](const void *p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0 && ld % 2 == 0; };
 
     int stage = 0;
     uint32_t phase = 0, done_phase = 0;
@@ -144,65 +165,63 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_unaligned_kernel(const Gr
             if (WG) {
                 const int first = sch.row[e] + part * len;
                 red = min(len, sch.row[e + 1] - first);
-                A = {reinterpret_cast<const uint16_t *>(a.x) + first * a.x_stride + m0, a.x_stride, red, M - m0,
-                     paired(a.x, a.x_stride)};
-                B = {reinterpret_cast<const uint16_t *>(a.dy) + first * a.dy_stride + n0, a.dy_stride, red, cols,
-                     paired(a.dy, a.dy_stride)};
+                A = {reinterpret_cast<const uint16_t *>(a.x) + first * a.x_stride + m0, a.x_stride, red, M - m0};
+                B = {reinterpret_cast<const uint16_t *>(a.dy) + first * a.dy_stride + n0, a.dy_stride, red, cols};
             } else {
                 const void *tokens = A_KMAJOR ? a.x : a.dy;
                 const int64_t ld = A_KMAJOR ? a.x_stride : a.dy_stride;
                 red = A_KMAJOR ? a.K : a.N;
-                A = {we + (A_KMAJOR ? (int64_t)m0 * a.K : m0), a.K, A_KMAJOR ? M - m0 : red, A_KMAJOR ? red : M - m0,
-                     paired(a.w, a.K)};
-                B = {reinterpret_cast<const uint16_t *>(tokens) + n0 * ld, ld, cols, red, paired(tokens, ld)};
+                A = {we + (A_KMAJOR ? (int64_t)m0 * a.K : m0), a.K, A_KMAJOR ? M - m0 : red, A_KMAJOR ? red : M - m0};
+                B = {reinterpret_cast<const uint16_t *>(tokens) + n0 * ld, ld, cols, red};
             }
             const int steps = (red + BK - 1) / BK;
-            if (warp < kLoadWarps) {
-                const int pieces = WG ? w / 8 : (w - warp + 7) / 8;
-                for (int k = 0; k < steps; ++k) {
-                    uint32_t va[kPerWarp], vb[kPerWarp];
-                    load_pieces<A_KMAJOR>(va, A, k * BK, warp, lane);
-                    load_pieces<B_KMAJOR>(vb, B, k * BK, warp, lane);
-                    if (wait(&empty[stage], phase ^ 1u, TF_DEVERR_PRODUCER_WAIT)) {
-                        const uint32_t tile = ptx::smem_u32(ring + stage * kStageBytes);
-                        store_pieces(va, tile, kPerWarp, warp, lane);
-                        store_pieces(vb, tile + kOperandBytes, pieces, warp, lane);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(&full[stage]);
-                    }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            } else {
-                const uint32_t id = idesc(TILE, w, a.dtype == TF_BF16, !A_KMAJOR, !B_KMAJOR);
-                for (int k = 0; k < steps; ++k) {
-                    if (wait(&full[stage], phase, TF_DEVERR_MMA_WAIT)) {
-                        ptx::tc_fence_after();
-                        const uint32_t tile = ptx::smem_u32(ring + stage * kStageBytes);
-                        const uint32_t al = desc_low(tile, A_KMAJOR), bl = desc_low(tile + kOperandBytes, B_KMAJOR);
-                        if (issuer) {
+            const int pieces = WG ? w / 8 : (w - warp + 7) / 8;
+            const uint32_t id = idesc(TILE, w, a.dtype == TF_BF16, !A_KMAJOR, !B_KMAJOR);
+            int mma_stage = stage;
+            uint32_t mma_phase = phase;
+            auto multiply = [&](int k) {   // warp 0: the K step's MMAs
+                if (wait(&full[mma_stage], mma_phase, TF_DEVERR_MMA_WAIT)) {
+                    ptx::tc_fence_after();
+                    const uint32_t tile = ptx::smem_u32(ring + mma_stage * kStageBytes);
+                    const uint32_t al = desc_low(tile, A_KMAJOR), bl = desc_low(tile + kOperandBytes, B_KMAJOR);
+                    if (issuer) {
 #pragma unroll
-                            for (int i = 0; i < BK / UMMA_K; ++i)
-                                ptx::umma_bf16(tmem, desc_of(al + i * desc_step(A_KMAJOR)), desc_of(bl + i * desc_step(B_KMAJOR)),
-                                               id, k > 0 || i > 0);
-                            ptx::umma_commit(&empty[stage]);
-                            if (k == steps - 1) ptx::umma_commit(&done);
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < BK / UMMA_K; ++i)
+                            ptx::umma_bf16(tmem, desc_of(al + i * desc_step(A_KMAJOR)), desc_of(bl + i * desc_step(B_KMAJOR)),
+                                           id, k > 0 || i > 0);
+                        ptx::umma_commit(&empty[mma_stage]);
+                        if (k == steps - 1) ptx::umma_commit(&done);
                     }
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    __syncwarp();
+                }
+                if (++mma_stage == kStages) {
+                    mma_stage = 0;
+                    mma_phase ^= 1u;
+                }
+            };
+            for (int k = 0; k < steps; ++k) {
+                Pieces va, vb;
+                load_pieces<A_KMAJOR>(va, A, k * BK, warp, lane);
+                load_pieces<B_KMAJOR>(vb, B, k * BK, warp, lane);
+                if (warp == 0 && k > 0) multiply(k - 1);   // (one step behind, so as not to wait for the other warps)
+                if (wait(&empty[stage], phase ^ 1u, TF_DEVERR_PRODUCER_WAIT)) {
+                    const uint32_t tile = ptx::smem_u32(ring + stage * kStageBytes);
+                    store_pieces(va, tile, kPerWarp, warp, lane);
+                    store_pieces(vb, tile + kOperandBytes, pieces, warp, lane);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&full[stage]);
+                }
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            const bool ready = steps > 0 && warp < kLoadWarps && wait(&done, done_phase, TF_DEVERR_EPILOGUE_WAIT);
+            if (warp == 0 && steps > 0) multiply(steps - 1);
+            const bool ready = steps > 0 && wait(&done, done_phase, TF_DEVERR_EPILOGUE_WAIT);
             if (steps > 0) done_phase ^= 1u;
             const bool add = WG && (a.accumulate || part > 0);
-            if (ready || (WG && steps == 0 && !add && warp < kLoadWarps)) {
+            if (ready || (WG && steps == 0 && !add)) {
                 ptx::tc_fence_after();
                 // warps w and w + 4 read TMEM lanes 32*(w%4) and on, each 64 of the columns
                 const int m = m0 + (warp & 3) * 32 + lane;
@@ -242,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_unaligned_kernel(const Gr
             ptx::tc_fence_after();
         }
     }
-    if (warp == kLoadWarps) {
+    if (warp == 0) {
         if (*(volatile int *)&dead) {   // MMAs may still be reading the ring
             if (issuer) ptx::umma_commit(&drain);
             __syncwarp();
