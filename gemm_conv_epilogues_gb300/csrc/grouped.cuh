@@ -262,7 +262,7 @@ __device__ __forceinline__ uint32_t idesc(int m, int n, bool bf16, bool a_mmajor
 // their loops with the whole warp and let one lane issue: in code that a single
 // lane runs the compiler cannot keep what these instructions take in uniform
 // registers, and a K step then takes its issuer ~600 cycles (the tensor cores
-// 512 for the widest tile).
+// 512 for the widest tile): 212 us against 189 for 16384 rows of 4096 x 2048.
 __device__ __forceinline__ bool elect_one()
 {
     uint32_t p;

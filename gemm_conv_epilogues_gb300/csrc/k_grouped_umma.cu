@@ -21,8 +21,20 @@
 //   3     lists the CTA's coming items, 32 at a time, so that the issuing warps
 //         do not stop for their searches and divisions
 //   4-11  epilogue: TMEM -> registers -> bias, activation -> y
-//   12-15 WGRAD: the bias gradient, from dy itself, beside the products (a kernel
-//         of its own cost 38 us of 230: it reads dy once more)
+//   12-15 WGRAD: the bias gradient, from dy itself, beside the products (188 us
+//         without it, 195 with it, 228 in a kernel of its own, which reads dy
+//         once more)
+//
+// What bounds it, at 16384 rows in 16 uneven groups, bf16, weights 4096 x 2048
+// (275 GFLOP; 142.7 us at the tensor cores' burst rate, 157.5 at the sustained one):
+//   FORWARD with bias, GELU and the pre-activation saved: 174-178 us, 1.55-1.58
+//     PFLOP/s, tensor pipe 75% busy; 159 without the epilogue's stores, and the
+//     operands' loads alone take 146 (64 bytes per clock and SM from L2)
+//   DGRAD with GELU's slope: 174-177 us
+//   WGRAD with dbias: 246-250 us; the fp32 dw, 128 KB per tile, leaves the SM at
+//     about 13 bytes per clock whichever way it is stored (fragments, 128-byte
+//     rows or TMA), and the writes keep the loads waiting
+//   16 rows in 16 groups of 2048 x 4096 (decoding): 39.5 us, 6.0 TB/s of weights
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the
 // device error word and winds down.
 #include <cuda.h>
@@ -366,7 +378,9 @@ __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int 
 }
 
 // KSUB: K blocks of 64 per stage.  Handing a stage over takes its issuers ~300
-// cycles, so small tiles take four; pairs two.
+// cycles, so FORWARD and DGRAD take two (pairs, 16384 rows: 185 us against 189
+// with one, DGRAD 186 against 195; single CTAs, 16 rows: 39.5 against 43.0, and
+// 41.3 with four).  WGRAD, whose last block may be ragged, takes one.
 template <int MODE, int CG, int KSUB>
 __global__ void __launch_bounds__(threads_of(MODE), 1)
     grouped_umma_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -1055,7 +1069,13 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
         const cudaError_t e = pair ? launch_mode<MODE, 2, 1>(a, kMaxBN, st, splits) : launch_mode<MODE, 1, 1>(a, kMaxBN, st, splits);
         return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);
     } else {
-        // A group's tiles of `bn` rows each, half a tile more on average for the ragged end.
+        // Pairs move the fewest operand bytes per product, which is what bounds large calls (16 groups of
+        // 512 rows, 2048 x 2048: 57 us; single CTAs with tiles of 128 rows 65, of 256 rows 62).  Smaller tiles
+        // win while they fill no more than one wave of SMs (8 groups of 128 rows, 1024 x 4096: 18.0 us, pairs
+        // 24.3; 256 rows: 34 and 25), and where a group's rows would leave the wide one mostly empty (16 groups
+        // of 32 rows, 2048 x 2048: 25.6 us with 64, 26.6 with 128, 28.0 on pairs; of 96 rows: 32.6, 28.2, 31.3;
+        // 4 groups of one row, 4096 x 4096: 23.9 with 16 and 29.9 with 64, whose stages are larger and fewer).
+        // A group's tiles of `bn` rows each, half a tile more on average for the ragged end:
         auto one_wave = [&](int bn) { return (M + BM - 1) / BM * (a.rows / bn + (a.groups + 1) / 2) <= sm_count(); };
         if (M > BM && avg > 96 && !one_wave(128)) return launch_mode<MODE, 2, 2>(a, kMaxBN, st);
         return launch_mode<MODE, 1, 2>(a, avg <= 8 ? 16 : avg <= 48 || one_wave(64) ? 64 : 128, st);
