@@ -1006,15 +1006,15 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     return counted(cudaLaunchKernelEx(&cfg, grouped_umma_kernel<MODE, CG, KSUB>, ta, tb, p));
 }
 
-// WGRAD with fewer tiles than CTAs (pairs) and long groups: every group's rows in
-// `splits` runs, whose products a second kernel adds.  At least 256 rows per
-// run on average, as far as the host knows.
+// WGRAD with fewer tiles than CTAs and long groups: every group's rows in
+// `splits` runs, whose products a second kernel adds.  At least 512 rows per run
+// on average, as far as the host knows (2 groups of 8000 rows, 256 x 320: 13.2
+// us, 15.5 with 256 rows, 56 without splits; no difference at 4000 rows in 8 groups).
 int wgrad_splits(int64_t rows, int groups, int64_t N, int64_t K)
 {
-    const bool pair = N > BM && K > 128;
-    const int64_t tiles = (int64_t)groups * ((N + (pair ? 2 * BM : BM) - 1) / (pair ? 2 * BM : BM)) * ((K + kMaxBN - 1) / kMaxBN);
-    int64_t s = sm_count() / (pair ? 2 : 1) / tiles;
-    if (s > rows / groups / 256) s = rows / groups / 256;
+    const int64_t tiles = (int64_t)groups * ((N + BM - 1) / BM) * ((K + kMaxBN - 1) / kMaxBN);
+    int64_t s = sm_count() / tiles;
+    if (s > rows / groups / 512) s = rows / groups / 512;
     if (s > kGroupedMaxGroups / groups) s = kGroupedMaxGroups / groups;
     return s < 2 ? 1 : (int)s;
 }
@@ -1063,8 +1063,10 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
     const int64_t M = MODE == GROUPED_DGRAD ? a.K : a.N;
     const int64_t avg = a.rows / a.groups;   // rows per group, as far as the host knows
     if constexpr (MODE == GROUPED_WGRAD) {
-        const bool pair = M > BM && a.K > 128;
         int splits = wgrad_splits(a.rows, a.groups, a.N, a.K);
+        // Pairs for long groups only (16 groups of 2048 x 2048: of 2048 rows 219 us, single CTAs 226; of 1024
+        // rows 123-128 and 122; of 256 rows 70 and 59): two CTAs' epilogues have to end before either goes on.
+        const bool pair = M > BM && a.K > 128 && avg > 1024 && splits == 1;
         if (a.ws_bytes < split_bytes(splits, a.groups, a.N, a.K)) splits = 1;
         const cudaError_t e = pair ? launch_mode<MODE, 2, 1>(a, kMaxBN, st, splits) : launch_mode<MODE, 1, 1>(a, kMaxBN, st, splits);
         return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);

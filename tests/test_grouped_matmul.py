@@ -268,6 +268,13 @@ def test_wgrad_long_groups(b, counts, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts,N,K", [([1500, 0, 2607], 1288, 1032), ([2100], 4104, 776)])
+def test_wgrad_long_groups_of_many_tiles(b, counts, N, K):
+    _check_wgrad(b, counts, N, K, "bf16")
+    _check_wgrad(b, counts, N, K, "fp16", pad=8, before=3, after=2)
+
+
+@pytest.mark.gpu
 def test_more_tiles_than_a_wave(b):
     counts = [300, 1, 777, 0, 513, 1200]
     _check_forward(b, counts, 1032, 200, "bf16", "silu", True, True)
