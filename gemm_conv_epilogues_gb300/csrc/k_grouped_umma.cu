@@ -1025,11 +1025,19 @@ int64_t split_bytes(int splits, int groups, int64_t N, int64_t K)
     return splits < 2 ? 0 : (int64_t)splits * groups * N * (K + 1) * 4;
 }
 
-// dst[e][i] (+)= the sum over s of src[e*splits + s][i], in order; 4 values per thread.
-__global__ void __launch_bounds__(256) split_sum_kernel(float *dw, float *dbias, const float *ws, int splits, int groups,
-                                                        int64_t NK, int64_t N, int accumulate)
+// dst[e][i] (+)= the sum over s of src[e*splits + s][i], in order; 4 values per
+// thread.  Nothing with invalid offsets, for which there are no partial sums.
+__global__ void __launch_bounds__(256) split_sum_kernel(float *dw, float *dbias, const float *ws, const int *offsets,
+                                                        int rows, int splits, int groups, int64_t NK, int64_t N,
+                                                        int accumulate)
 {
     pdl_begin();
+    bool wrong = false;
+    for (int i = threadIdx.x; i <= groups; i += 256) {
+        const int v = offsets[i];
+        wrong |= v < 0 || v > rows || (i > 0 && offsets[i - 1] > v);
+    }
+    if (__syncthreads_or(wrong)) return;
     const int64_t step = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
     auto add = [&](float *dst, const float *src, int64_t n) {   // n values per group, a multiple of 4
         for (int64_t i = first; i < groups * n / 4; i += step) {
@@ -1054,7 +1062,7 @@ cudaError_t launch_sum(const GroupedArgs &a, int splits, cudaStream_t st)
 {
     const int64_t NK = (int64_t)a.N * a.K, blocks = (a.groups * NK / 4 + 255) / 256, most = 8 * (int64_t)sm_count();
     return launch_pdl(split_sum_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, st, a.dw, a.dbias,
-                      static_cast<const float *>(a.ws), splits, a.groups, NK, (int64_t)a.N, a.accumulate);
+                      static_cast<const float *>(a.ws), a.offsets, a.rows, splits, a.groups, NK, (int64_t)a.N, a.accumulate);
 }
 
 template <int MODE>
@@ -1064,9 +1072,10 @@ cudaError_t launch_auto(const GroupedArgs &a, cudaStream_t st)
     const int64_t avg = a.rows / a.groups;   // rows per group, as far as the host knows
     if constexpr (MODE == GROUPED_WGRAD) {
         int splits = wgrad_splits(a.rows, a.groups, a.N, a.K);
-        // Pairs for long groups only (16 groups of 2048 x 2048: of 2048 rows 219 us, single CTAs 226; of 1024
-        // rows 123-128 and 122; of 256 rows 70 and 59): two CTAs' epilogues have to end before either goes on.
-        const bool pair = M > BM && a.K > 128 && avg > 1024 && splits == 1;
+        // Pairs for long groups only (16 groups of 2048 x 2048: of 2048 rows 219 us, single CTAs 226; of 512
+        // rows 85 and 79; of 256 rows 70 and 59; 4096 x 2048 of 1024 rows 257 and 262): two CTAs' epilogues have
+        // to end before either goes on.
+        const bool pair = M > BM && a.K > 128 && avg >= 1024 && splits == 1;
         if (a.ws_bytes < split_bytes(splits, a.groups, a.N, a.K)) splits = 1;
         const cudaError_t e = pair ? launch_mode<MODE, 2, 1>(a, kMaxBN, st, splits) : launch_mode<MODE, 1, 1>(a, kMaxBN, st, splits);
         return e != cudaSuccess || splits == 1 ? e : launch_sum(a, splits, st);

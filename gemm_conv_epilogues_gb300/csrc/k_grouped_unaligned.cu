@@ -16,7 +16,7 @@
 // Bound by the loads' way through the L1: a K step of both operands is 256
 // pieces, the MMAs on it take 128 cycles.  16384 rows, 16 groups, bf16: forward
 // 401 us for 2047 x 1001, 242 us (278 TFLOP/s) for 2046 x 1002, whose rows are
-// whole words; the same product on the CUDA cores took over 4 ms.  All of a K
+// whole words; on the CUDA cores either took 2.9 ms.  All of a K
 // step's loads are under way at once; joining the values of a word as they come
 // took 1343 and 306 us.  A ninth warp for the MMAs (96 registers instead of
 // 128): 526 and 226 us.

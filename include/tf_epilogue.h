@@ -261,7 +261,8 @@ int tf_residual_layernorm_select(int64_t hidden);
  * the unrounded s.  Any hidden from 1 to 131072, up to 2^30 rows, any row stride (below 2^31)
  * and the alignment of an element; rows whose start is not a multiple of 16
  * bytes take a slower kernel.  rows may be 0 (nothing is read or written).
- * Elements between `hidden` and the stride are not touched. */
+ * Elements between `hidden` and the stride are not touched.  y and sum may lie
+ * in the place of x or res (the same address and stride), each in its own. */
 int tf_layernorm_forward(const void *x, int64_t x_stride, const void *res, int64_t res_stride, const float *gamma,
                          const float *beta, void *y, int64_t y_stride, void *sum, int64_t sum_stride, float *mean,
                          float *rstd, int64_t rows, int64_t hidden, float eps, int dtype, tf_stream_t stream);
@@ -286,7 +287,7 @@ int64_t tf_layernorm_backward_workspace_size(int64_t rows, int64_t hidden, int d
  * are NULL) is in use until the stream reaches the end of the call; calls that
  * may overlap need one each, captured graphs too.  TF_ERR_INVALID_ARG when it
  * is missing or too small.  rows may be 0: dgamma and dbeta become 0, or stay
- * as they are with `accumulate`. */
+ * as they are with `accumulate`.  dx may lie in the place of dy, x or dres. */
 int tf_layernorm_backward(const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const float *gamma,
                           const float *mean, const float *rstd, const void *dres, int64_t dres_stride, void *dx,
                           int64_t dx_stride, float *dgamma, float *dbeta, int64_t rows, int64_t hidden, int accumulate,
@@ -307,7 +308,7 @@ int tf_layernorm_backward(const void *dy, int64_t dy_stride, const void *x, int6
  * groups up to 1024, N and K up to 65536, rows up to 4194304; row strides (in
  * elements, below 2^31) of their own.  The tensor-core kernels need every row
  * and base address to be a multiple of 16 bytes (N % 8 == 0, K % 8 == 0,
- * strides % 8 == 0); other operands take a much slower kernel.  rows may be 0.
+ * strides % 8 == 0); other operands take a slower kernel.  rows may be 0.
  * A row's result depends on that row and its group's weights only: infinities
  * or NaN in one group do not reach another.  Equal calls give equal bits. */
 

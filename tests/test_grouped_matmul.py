@@ -407,6 +407,21 @@ def test_bad_offsets_write_nothing(b, offsets, N, K):
 
 
 @pytest.mark.gpu
+def test_bad_offsets_with_split_sums(b):
+    rows, N, K = 6000, 128, 256
+    size = b.tf_grouped_matmul_wgrad_workspace_size(rows, 1, N, K, b.TF_BF16)
+    assert size > 0
+    dy, x = _rand(rows, N, "bf16"), _rand(rows, K, "bf16")
+    ws = torch.full((size // 4,), 3.0, device="cuda")
+    for accumulate in (0, 1):
+        dw, db = torch.full((1, N, K), 7.0, device="cuda"), torch.full((1, N), 7.0, device="cuda")
+        b.tf_grouped_matmul_wgrad(dy, N, x, K, torch.tensor([0, rows + 1], dtype=torch.int32, device="cuda"), dw, db,
+                                  rows, 1, N, K, accumulate, b.TF_BF16, ws, size)
+        assert b.tf_read_device_error() == (b.TF_ERR_TIMEOUT, b.TF_DEVERR_OFFSETS)
+        assert (dw == 7).all() and (db == 7).all()
+
+
+@pytest.mark.gpu
 def test_no_rows(b):
     dev = torch.zeros(4, dtype=torch.int32, device="cuda")
     z = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")

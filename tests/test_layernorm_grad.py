@@ -350,3 +350,33 @@ def test_captured_and_replayed(b, hidden):
         step()
         for g, w in zip(got, (y, s, mean, rstd, dx, dg, db)):
             assert torch.equal(g, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,hidden,name,pad", [(700, 256, "bf16", 0), (400, 640, "fp16", 8), (333, 1001, "bf16", 0),
+                                                  (200, 5003, "fp32", 3), (64, 9001, "fp16", 0), (64, 16384, "bf16", 0)])
+def test_outputs_in_the_place_of_inputs(b, rows, hidden, name, pad):
+    """The residual stream updated where it lies, and a gradient over either of its inputs: the same bits."""
+    d = _inputs(rows, hidden, name, pad)
+    st, code = d["x"].stride(0), CODES[name]
+    place = lambda t: torch.empty_strided((rows, hidden), (st, 1), dtype=t.dtype, device="cuda").copy_(t)
+    y, s, mean, rstd = _forward(b, d, name, pad=pad)
+    x, res = place(d["x"]), place(d["res"])
+    m, r = torch.empty_like(mean), torch.empty_like(rstd)
+    b.tf_layernorm_forward(x, st, res, st, d["gamma"], d["beta"], x, st, res, st, m, r, rows, hidden, EPS, code)
+    for got, want in ((x, y), (res, s), (m, mean), (r, rstd)):
+        assert torch.equal(got, want)
+    size = b.tf_layernorm_backward_workspace_size(rows, hidden, code)
+    ws = torch.empty(size // 4, device="cuda")
+
+    def backward(dy, xx, dres, dx):
+        dg, db = torch.empty(hidden, device="cuda"), torch.empty(hidden, device="cuda")
+        b.tf_layernorm_backward(dy, st, xx, st, d["gamma"], mean, rstd, dres, st, dx, st, dg, db, rows, hidden, 0, code,
+                                ws, size)
+        return dx.clone(), dg, db
+
+    want = backward(place(d["dy"]), place(s), place(d["dres"]), place(d["dy"]))
+    for i in range(3):
+        t = [place(d["dy"]), place(s), place(d["dres"])]
+        for got, w in zip(backward(*t, t[i]), want):
+            assert torch.equal(got, w)
