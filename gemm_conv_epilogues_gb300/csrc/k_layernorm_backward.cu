@@ -51,15 +51,16 @@ int cols_for(int64_t hidden, int size, bool aligned, int tensors)
     return 16;
 }
 
-// GROUP: threads per row where the columns are element-wise (a constant makes
-// them immediate offsets), 0 for 16-byte vectors.
-template <typename T, int GROUP, bool CLUSTER, int NT, int COLS>
+// GROUP: threads per row where the columns are element-wise or pairs (a constant
+// makes them immediate offsets), 0 for 16-byte vectors.
+template <typename T, int GROUP, bool CLUSTER, int NT, int COLS, int VEC = 16 / (int)sizeof(T)>
 __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 1)
     norm_backward_kernel(const __grid_constant__ NormGradArgs a, const __grid_constant__ Sources src,
                          const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
     constexpr bool ALIGNED = GROUP == 0;
-    using C = Cols<T, ALIGNED, COLS>;
+    static_assert(ALIGNED == kAligned<T, VEC>, "GROUP and VEC");
+    using C = Cols<T, VEC, COLS>;
     constexpr int PAIRS = C::PAIRS;
     constexpr bool HELD = COLS <= 16;   // gamma in registers
     pdl_begin();
@@ -70,7 +71,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 
     const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0;
     const int gsize = ALIGNED ? g.group : GROUP, gt = threadIdx.x % gsize, c0 = rank * g.slice;
     const int unit = (int)blockIdx.x / g.csize, units = (int)gridDim.x / g.csize;
-    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, unit, units, c0, err, wait_ns,
+    auto ring = start_ring<T, VEC, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, unit, units, c0, err, wait_ns,
                                                     xbar);
     Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 
         return v;
     };
     const float inv_h = 1.0f / (float)a.hidden;
-    Edge<T> ed, ex, er;
+    Edge<T, VEC> ed, ex, er;
     load_edge(ring, 0, ring.first, gt, gsize, ed);
     load_edge(ring, 1, ring.first, gt, gsize, ex);
     if (NT > 2) load_edge(ring, 2, ring.first, gt, gsize, er);
@@ -239,11 +240,12 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
     }
 }
 
-Geometry geometry_for(int64_t rows, int64_t hidden, int size, bool aligned, int tensors)
+Geometry geometry_for(int64_t rows, int64_t hidden, int size, int vec, int tensors)
 {
+    const bool aligned = vec * size == 16;
     const int cols = cols_for(hidden, size, aligned, tensors);
     const int group = (int)(hidden + cols - 1) / cols;   // (rounded up by geometry())
-    return geometry(hidden, size, aligned, cols, tensors, sm_threads(cols, aligned, group, tensors), true, rows, cols > 16 ? 1 : 0);
+    return geometry(hidden, size, vec, cols, tensors, sm_threads(cols, aligned, group, tensors), true, rows, cols > 16 ? 1 : 0);
 }
 
 // The most partial sums that any alignment and number of operands gives.
@@ -252,8 +254,8 @@ int64_t most_units(int64_t rows, int64_t hidden, int dtype)
     const int size = dtype == TF_FP32 ? 4 : 2;
     int64_t most = 0;
     for (int tensors : {2, 3})
-        for (bool aligned : {false, true}) {
-            const int64_t u = launch_units(geometry_for(rows, hidden, size, aligned, tensors), rows);
+        for (int vec : {1, 2, 16 / size}) {
+            const int64_t u = launch_units(geometry_for(rows, hidden, size, vec, tensors), rows);
             if (u > most) most = u;
         }
     return most;
@@ -265,11 +267,15 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
     constexpr int size = (int)sizeof(T);
     uint32_t *err = device_error_word();
     if (!err) return cudaErrorInitializationError;
-    const bool aligned = a.hidden * size % 16 == 0 && aligned_rows(a.dy, a.dy_stride, size) &&
-                         aligned_rows(a.x, a.x_stride, size) && aligned_rows(a.dres, a.dres_stride, size) &&
-                         aligned_rows(a.dx, a.dx_stride, size);
+    auto whole = [&](int bytes) {   // every row starts and ends on a multiple of `bytes`
+        return a.hidden * size % bytes == 0 && aligned_rows(a.dy, a.dy_stride, size, bytes) &&
+               aligned_rows(a.x, a.x_stride, size, bytes) && aligned_rows(a.dres, a.dres_stride, size, bytes) &&
+               aligned_rows(a.dx, a.dx_stride, size, bytes);
+    };
+    const bool aligned = whole(16);
+    const int vec = aligned ? 16 / size : size == 2 && whole(4) ? 2 : 1;
     const Sources src = {{a.dy, a.x, a.dres}, {a.dy_stride, a.x_stride, a.dres_stride}};
-    const Geometry g = geometry_for(a.rows, a.hidden, size, aligned, a.dres ? 3 : 2);
+    const Geometry g = geometry_for(a.rows, a.hidden, size, vec, a.dres ? 3 : 2);
     *units = launch_units(g, a.rows);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
@@ -281,21 +287,26 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
             default: return norm_backward_kernel<T, 0, false, NT, 16>;
             }
         }
-        if (cols_for(a.hidden, size, false, NT) == 16)
-            return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16> : norm_backward_kernel<T, 512, false, NT, 16>;
-        switch (g.group) {
-        case 32: return norm_backward_kernel<T, 32, false, NT, 8>;
-        case 64: return norm_backward_kernel<T, 64, false, NT, 8>;
-        case 128: return norm_backward_kernel<T, 128, false, NT, 8>;
-        case 192: return norm_backward_kernel<T, 192, false, NT, 8>;
-        case 256: return norm_backward_kernel<T, 256, false, NT, 8>;
-        case 320: return norm_backward_kernel<T, 320, false, NT, 8>;
-        case 384: return norm_backward_kernel<T, 384, false, NT, 8>;
-        case 448: return norm_backward_kernel<T, 448, false, NT, 8>;
-        case 512: return norm_backward_kernel<T, 512, false, NT, 8>;
-        case 640: return norm_backward_kernel<T, 640, false, NT, 8>;
-        default: return norm_backward_kernel<T, 768, false, NT, 8>;
-        }
+        auto unaligned = [&](auto v) {
+            constexpr int VEC = decltype(v)::value;
+            if (cols_for(a.hidden, size, false, NT) == 16)
+                return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16, VEC>
+                                   : norm_backward_kernel<T, 512, false, NT, 16, VEC>;
+            switch (g.group) {
+            case 32: return norm_backward_kernel<T, 32, false, NT, 8, VEC>;
+            case 64: return norm_backward_kernel<T, 64, false, NT, 8, VEC>;
+            case 128: return norm_backward_kernel<T, 128, false, NT, 8, VEC>;
+            case 192: return norm_backward_kernel<T, 192, false, NT, 8, VEC>;
+            case 256: return norm_backward_kernel<T, 256, false, NT, 8, VEC>;
+            case 320: return norm_backward_kernel<T, 320, false, NT, 8, VEC>;
+            case 384: return norm_backward_kernel<T, 384, false, NT, 8, VEC>;
+            case 448: return norm_backward_kernel<T, 448, false, NT, 8, VEC>;
+            case 512: return norm_backward_kernel<T, 512, false, NT, 8, VEC>;
+            case 640: return norm_backward_kernel<T, 640, false, NT, 8, VEC>;
+            default: return norm_backward_kernel<T, 768, false, NT, 8, VEC>;
+            }
+        };
+        return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());
     };
     return launch_rows(a.dres ? pick(std::integral_constant<int, 3>()) : pick(std::integral_constant<int, 2>()), g,
                        *units, st, a, src, g, err, wait_limit_ns());

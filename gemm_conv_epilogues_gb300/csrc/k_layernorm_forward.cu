@@ -27,10 +27,10 @@ int cols_of(bool aligned, int size, int64_t hidden)
 }
 constexpr int sm_threads(int cols) { return cols == 8 ? 1024 : 512; }
 
-// GROUP: threads per row where the columns are element-wise (a constant makes
-// them immediate offsets), 0 for 16-byte vectors.  SPAN: 0 for at most 256
+// GROUP: threads per row where the columns are element-wise or pairs (a constant
+// makes them immediate offsets), 0 for 16-byte vectors.  SPAN: 0 for at most 256
 // threads per row, 1 for up to 512, 2 for a cluster of such CTAs.
-template <typename T, int GROUP, int SPAN, int NT, int COLS>
+template <typename T, int GROUP, int SPAN, int NT, int COLS, int VEC = 16 / (int)sizeof(T)>
 __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ? 512 : 256,
                                   GROUP > 512   ? 1
                                   : GROUP > 256 ? (COLS == 8 ? 2 : 1)
@@ -42,7 +42,8 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
                         const __grid_constant__ Geometry g, uint32_t *err, uint64_t wait_ns)
 {
     constexpr bool ALIGNED = GROUP == 0, CLUSTER = SPAN == 2;
-    using C = Cols<T, ALIGNED, COLS>;
+    static_assert(ALIGNED == kAligned<T, VEC>, "GROUP and VEC");
+    using C = Cols<T, VEC, COLS>;
     constexpr int PAIRS = C::PAIRS;
     constexpr bool HELD = COLS <= 16;   // gamma and beta in registers
     pdl_begin();
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
     __shared__ __align__(8) uint64_t xbar[2];
     const int rank = CLUSTER ? (int)ptx::cluster_ctarank() : 0;
     const int gsize = ALIGNED ? g.group : GROUP, gt = threadIdx.x % gsize, c0 = rank * g.slice;
-    auto ring = start_ring<T, ALIGNED, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, (int)blockIdx.x / g.csize,
+    auto ring = start_ring<T, VEC, CLUSTER, NT>(g, smem, src, a.hidden, (int)a.rows, (int)blockIdx.x / g.csize,
                                                     (int)gridDim.x / g.csize, c0, err, wait_ns, xbar);
     Exchange xch = {slot, xbar, (uint32_t)rank, (uint32_t)g.csize, wait_ns, err, false};
     const int width = ring.width;
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(GROUP > 512 ? 1024 : GROUP > 256 || SPAN > 0 ?
     }
     const float inv_h = 1.0f / (float)a.hidden, inv_n = 1.0f / (float)width;
 
-    Edge<T> ex, er;
+    Edge<T, VEC> ex, er;
     load_edge(ring, 0, ring.first, gt, gsize, ex);
     if (NT > 1) load_edge(ring, 1, ring.first, gt, gsize, er);
     for (int row = ring.first, it = 0; row < ring.rows; row += ring.step, ++it, ring.advance()) {
@@ -144,12 +145,16 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
     constexpr int size = (int)sizeof(T);
     uint32_t *err = device_error_word();
     if (!err) return cudaErrorInitializationError;
-    const bool aligned = a.hidden * size % 16 == 0 && aligned_rows(a.x, a.x_stride, size) &&
-                         aligned_rows(a.res, a.res_stride, size) && aligned_rows(a.y, a.y_stride, size) &&
-                         aligned_rows(a.sum, a.sum_stride, size);
+    auto whole = [&](int bytes) {   // every row starts and ends on a multiple of `bytes`
+        return a.hidden * size % bytes == 0 && aligned_rows(a.x, a.x_stride, size, bytes) &&
+               aligned_rows(a.res, a.res_stride, size, bytes) && aligned_rows(a.y, a.y_stride, size, bytes) &&
+               aligned_rows(a.sum, a.sum_stride, size, bytes);
+    };
+    const bool aligned = whole(16);
+    const int vec = aligned ? 16 / size : size == 2 && whole(4) ? 2 : 1;
     const Sources src = {{a.x, a.res}, {a.x_stride, a.res_stride}};
     const int cols = cols_of(aligned, size, a.hidden);
-    const Geometry g = geometry(a.hidden, size, aligned, cols, a.res ? 2 : 1, sm_threads(cols), false, a.rows,
+    const Geometry g = geometry(a.hidden, size, vec, cols, a.res ? 2 : 1, sm_threads(cols), false, a.rows,
                                 cols > 16 ? 2 : 0);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
@@ -159,22 +164,26 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
             if (cols == 24) return norm_forward_kernel<T, 0, 0, NT, size == 2 ? 24 : 16>;
             return g.group > 256 ? norm_forward_kernel<T, 0, 1, NT, 16> : norm_forward_kernel<T, 0, 0, NT, 16>;
         }
-        if (g.csize > 1) return norm_forward_kernel<T, 512, 2, NT, 16>;
-        switch (g.group) {
-        case 32: return norm_forward_kernel<T, 32, 0, NT, 8>;
-        case 64: return norm_forward_kernel<T, 64, 0, NT, 8>;
-        case 128: return norm_forward_kernel<T, 128, 0, NT, 8>;
-        case 192: return norm_forward_kernel<T, 192, 0, NT, 8>;
-        case 256: return norm_forward_kernel<T, 256, 0, NT, 8>;
-        case 320: return norm_forward_kernel<T, 320, 0, NT, 8>;
-        case 384: return norm_forward_kernel<T, 384, 0, NT, 8>;
-        case 448: return norm_forward_kernel<T, 448, 0, NT, 8>;
-        case 512: return norm_forward_kernel<T, 512, 0, NT, 8>;
-        case 640: return norm_forward_kernel<T, 640, 0, NT, 8>;
-        case 768: return norm_forward_kernel<T, 768, 0, NT, 8>;
-        case 896: return norm_forward_kernel<T, 896, 0, NT, 8>;
-        default: return norm_forward_kernel<T, 1024, 0, NT, 8>;
-        }
+        auto unaligned = [&](auto v) {
+            constexpr int VEC = decltype(v)::value;
+            if (g.csize > 1) return norm_forward_kernel<T, 512, 2, NT, 16, VEC>;
+            switch (g.group) {
+            case 32: return norm_forward_kernel<T, 32, 0, NT, 8, VEC>;
+            case 64: return norm_forward_kernel<T, 64, 0, NT, 8, VEC>;
+            case 128: return norm_forward_kernel<T, 128, 0, NT, 8, VEC>;
+            case 192: return norm_forward_kernel<T, 192, 0, NT, 8, VEC>;
+            case 256: return norm_forward_kernel<T, 256, 0, NT, 8, VEC>;
+            case 320: return norm_forward_kernel<T, 320, 0, NT, 8, VEC>;
+            case 384: return norm_forward_kernel<T, 384, 0, NT, 8, VEC>;
+            case 448: return norm_forward_kernel<T, 448, 0, NT, 8, VEC>;
+            case 512: return norm_forward_kernel<T, 512, 0, NT, 8, VEC>;
+            case 640: return norm_forward_kernel<T, 640, 0, NT, 8, VEC>;
+            case 768: return norm_forward_kernel<T, 768, 0, NT, 8, VEC>;
+            case 896: return norm_forward_kernel<T, 896, 0, NT, 8, VEC>;
+            default: return norm_forward_kernel<T, 1024, 0, NT, 8, VEC>;
+            }
+        };
+        return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());
     };
     return launch_rows(a.res ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>()), g,
                        launch_units(g, a.rows), st, a, src, g, err, wait_limit_ns());

@@ -10,12 +10,14 @@
 // CTAs per SM, were slower: 161 against 110 us for 8192 x 8192 bf16, forward
 // with residual; the exchange lengthens every row.)
 //
-// Alignment.  With every row start a multiple of 16 bytes (ALIGNED) a row is
+// Alignment.  With every row start and length a multiple of 16 bytes a row is
 // one bulk copy and a thread's columns are 16-byte vectors.  Otherwise the
 // copy takes the 16-byte pieces that lie inside the row, at the same offset
 // from a 16-byte boundary in shared memory as in global memory; the up to 15
 // bytes before and behind them are loaded one row ahead by the threads whose
-// columns they are (copying them too would read past the tensor's ends).
+// columns they are (copying them too would read past the tensor's ends).  A
+// thread's columns are then single ones, or pairs where 16-bit rows consist of
+// whole words (6000 x 5002 bf16 with residual, forward: 76 us, 100 one by one).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -97,9 +99,17 @@ struct Sources {
     int64_t stride[kMaxTensors];
 };
 
+// VEC: neighbouring columns that a thread moves at once.  16 bytes of them for
+// aligned rows; else one, or two of 16 bits (a word).
+template <typename T, int VEC>
+constexpr bool kAligned = VEC * (int)sizeof(T) == 16;
+template <typename T, int VEC>
+using Unit = typename std::conditional<VEC == 2, uint32_t, T>::type;   // of unaligned rows
+
 // What one thread knows of its row group's ring of NT tensors.
-template <typename T, bool ALIGNED, int NT>
+template <typename T, int VEC, int NT>
 struct Ring {
+    static constexpr bool ALIGNED = kAligned<T, VEC>;
     const Sources &src;
     unsigned char *mem;
     uint64_t *full;
@@ -180,43 +190,44 @@ struct Ring {
                     atomicOr(err, TF_DEVERR_DRAIN_WAIT);
     }
 
-    // Columns of row `it` of tensor i that lie before and behind the copied pieces.
+    // Units of row `it` of tensor i that lie before and behind the copied pieces.
     __device__ __forceinline__ void edges(int i, int64_t row, int &head, int &tail) const
     {
+        constexpr int size = (int)sizeof(Unit<T, VEC>);
         const uint64_t a = reinterpret_cast<uint64_t>(at(i, row)), bytes = (uint64_t)width * sizeof(T);
         const uint64_t lo = (a + 15) & ~15ull, hi = (a + bytes) & ~15ull;
-        head = min(width, (int)((lo - a) / sizeof(T)));
-        tail = hi > lo ? (int)((a + bytes - hi) / sizeof(T)) : width - head;
+        head = min(width / VEC, (int)((lo - a) / size));
+        tail = hi > lo ? (int)((a + bytes - hi) / size) : width / VEC - head;
     }
 };
 
-// The edge elements of one tensor's row that are this thread's columns (at
-// most one of either edge), loaded a row ahead and put into the row's stage
-// before the thread reads it: a thread reads its own columns only, so no
-// barrier lies between.
-template <typename T>
+// The edge units of one tensor's row that are this thread's columns (at most
+// one of either edge), loaded a row ahead and put into the row's stage before
+// the thread reads it: a thread reads its own columns only, so no barrier lies
+// between.
+template <typename T, int VEC>
 struct Edge {
-    T head, tail;
-    int head_at, tail_at;   // columns, or -1
+    Unit<T, VEC> head, tail;
+    int head_at, tail_at;   // units, or -1
 };
 
-template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ void load_edge(const Ring<T, ALIGNED, NT> &ring, int i, int64_t row, int gt, int gsize,
-                                          Edge<T> &e)
+template <typename T, int VEC, int NT>
+__device__ __forceinline__ void load_edge(const Ring<T, VEC, NT> &ring, int i, int64_t row, int gt, int gsize,
+                                          Edge<T, VEC> &e)
 {
-    if constexpr (!ALIGNED) {
+    if constexpr (!kAligned<T, VEC>) {
         e.head_at = e.tail_at = -1;
         if (row < ring.rows) {
             int head, tail;
             ring.edges(i, row, head, tail);
-            const T *p = ring.at(i, row);
+            const Unit<T, VEC> *p = reinterpret_cast<const Unit<T, VEC> *>(ring.at(i, row));
             if (gt < head) {
                 e.head_at = gt;
                 e.head = p[gt];
             }
-            // the last columns, at most 15: those congruent to gt modulo the group's size
-            const int t0 = ring.width - tail, d = (gt - t0) % gsize, c = t0 + (d < 0 ? d + gsize : d);
-            if (c < ring.width) {
+            // the last units, at most 15: those congruent to gt modulo the group's size
+            const int n = ring.width / VEC, t0 = n - tail, d = (gt - t0) % gsize, c = t0 + (d < 0 ? d + gsize : d);
+            if (c < n) {
                 e.tail_at = c;
                 e.tail = p[c];
             }
@@ -225,19 +236,19 @@ __device__ __forceinline__ void load_edge(const Ring<T, ALIGNED, NT> &ring, int 
 }
 
 // Tensor i of the current row `row` in its stage.
-template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ T *stage_row(const Ring<T, ALIGNED, NT> &ring, int i, int row)
+template <typename T, int VEC, int NT>
+__device__ __forceinline__ T *stage_row(const Ring<T, VEC, NT> &ring, int i, int row)
 {
     unsigned char *s = ring.mem + (ring.stage * NT + i) * ring.tensor_bytes;
-    if constexpr (!ALIGNED) s += reinterpret_cast<uint64_t>(ring.at(i, row)) & 15u;
+    if constexpr (!kAligned<T, VEC>) s += reinterpret_cast<uint64_t>(ring.at(i, row)) & 15u;
     return reinterpret_cast<T *>(s);
 }
 
-template <typename T, bool ALIGNED, int NT>
-__device__ __forceinline__ void put_edge(const Ring<T, ALIGNED, NT> &ring, int i, int row, const Edge<T> &edge)
+template <typename T, int VEC, int NT>
+__device__ __forceinline__ void put_edge(const Ring<T, VEC, NT> &ring, int i, int row, const Edge<T, VEC> &edge)
 {
-    if constexpr (!ALIGNED) {
-        T *p = stage_row(ring, i, row);
+    if constexpr (!kAligned<T, VEC>) {
+        auto *p = reinterpret_cast<Unit<T, VEC> *>(stage_row(ring, i, row));
         if (edge.head_at >= 0) p[edge.head_at] = edge.head;
         if (edge.tail_at >= 0) p[edge.tail_at] = edge.tail;
     }
@@ -252,20 +263,30 @@ __device__ __forceinline__ float2 widen2(uint32_t u, __nv_bfloat16)
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
-// A thread's COLS columns of one row, in the storage type; zero past the slice.
-// ALIGNED: 16-byte vectors gt, gt + gsize, ...; else elements gt, gt + gsize, ...
-// The arithmetic goes over pairs (packed fp32): the kernels are close to the
-// issue rate.
-template <typename T, bool ALIGNED, int COLS>
+__device__ __forceinline__ uint32_t narrow2(float2 f, __half)
+{
+    const __half2 h = __floats2half2_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t narrow2(float2 f, __nv_bfloat16)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// A thread's COLS columns of one row, in the storage type; zero past the slice:
+// the vectors (units) gt, gt + gsize, ... of VEC columns.  The arithmetic goes
+// over pairs (packed fp32): the kernels are close to the issue rate.
+template <typename T, int VEC, int COLS>
 struct Cols {
-    static constexpr int VEC = ALIGNED ? 16 / (int)sizeof(T) : 1;
+    static constexpr bool ALIGNED = kAligned<T, VEC>;
     static constexpr int NVEC = COLS / VEC;
     static constexpr int PAIRS = COLS / 2;
     uint4 v[ALIGNED ? NVEC : 1];
-    T e[ALIGNED ? 1 : COLS];
+    Unit<T, VEC> e[ALIGNED ? 1 : NVEC];
 
     template <int NT>
-    __device__ __forceinline__ void load(const Ring<T, ALIGNED, NT> &ring, int i, int row, int gt, int gsize)
+    __device__ __forceinline__ void load(const Ring<T, VEC, NT> &ring, int i, int row, int gt, int gsize)
     {
         const T *p = stage_row(ring, i, row);
         const int n = ring.width / VEC;
@@ -273,6 +294,7 @@ struct Cols {
         for (int k = 0; k < NVEC; ++k) {
             const int c = gt + k * gsize;
             if constexpr (ALIGNED) v[k] = c < n ? reinterpret_cast<const uint4 *>(p)[c] : make_uint4(0, 0, 0, 0);
+            else if constexpr (VEC == 2) e[k] = c < n ? reinterpret_cast<const uint32_t *>(p)[c] : 0u;
             else if (c < n) e[k] = p[c];
             else narrow(e[k], 0.0f);
         }
@@ -280,7 +302,9 @@ struct Cols {
     // values 2p and 2p + 1
     __device__ __forceinline__ float2 get(int p) const
     {
-        if constexpr (!ALIGNED) {
+        if constexpr (VEC == 2) {
+            return widen2(e[p], T());
+        } else if constexpr (VEC == 1) {
             return make_float2(widen(e[2 * p]), widen(e[2 * p + 1]));
         } else {
             constexpr int PER = VEC / 2;   // pairs per vector
@@ -316,6 +340,10 @@ struct Cols {
                 }
                 if (c < n) st_stream(dst + c * VEC, repack<T>(w));
             }
+        } else if constexpr (VEC == 2) {
+#pragma unroll
+            for (int p = 0; p < PAIRS; ++p)
+                if (gt + p * gsize < width / 2) reinterpret_cast<uint32_t *>(dst)[gt + p * gsize] = narrow2(f[p], T());
         } else {
 #pragma unroll
             for (int p = 0; p < PAIRS; ++p) {
@@ -437,13 +465,13 @@ __device__ __forceinline__ uint32_t cluster_nctarank()
 
 // Shared set-up of both kernels: this thread's ring, with its barriers
 // initialised and the first rows on their way.
-template <typename T, bool ALIGNED, bool CLUSTER, int NT>
-__device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, unsigned char *smem, const Sources &src,
+template <typename T, int VEC, bool CLUSTER, int NT>
+__device__ __forceinline__ Ring<T, VEC, NT> start_ring(const Geometry &g, unsigned char *smem, const Sources &src,
                                                            int hidden, int rows, int unit, int units, int c0,
                                                            uint32_t *err, uint64_t wait_ns, uint64_t *xbar)
 {
     const int gid = threadIdx.x / g.group, ngroups = g.threads / g.group;
-    Ring<T, ALIGNED, NT> r{src,
+    Ring<T, VEC, NT> r{src,
                            smem + (size_t)gid * g.stages * NT * g.tensor_bytes,
                            reinterpret_cast<uint64_t *>(smem + g.bar_off) + gid * g.stages,
                            g.stages,
@@ -475,14 +503,14 @@ __device__ __forceinline__ Ring<T, ALIGNED, NT> start_ring(const Geometry &g, un
 // ---------------------------------------------------------------- host side
 
 // Rows of `hidden` columns, `tensors` of them streaming in, in a kernel whose
-// threads take `cols` columns and of which an SM holds `sm_threads` threads.
-// MERGED: all the row groups of an SM in one CTA (whose column sums then leave
+// threads take `cols` columns, `vec` at once, and of which an SM holds
+// `sm_threads` threads.  MERGED: all the row groups of an SM in one CTA (whose column sums then leave
 // the SM once).
-inline Geometry geometry(int64_t hidden, int size, bool aligned, int cols, int tensors, int sm_threads, bool merged,
+inline Geometry geometry(int64_t hidden, int size, int vec, int cols, int tensors, int sm_threads, bool merged,
                          int64_t rows, int tables = 0)
 {
     Geometry g;
-    const int vec = aligned ? 16 / size : 1;
+    const bool aligned = vec * size == 16;
     const int csize = (int)((hidden + kSlice - 1) / kSlice);
     const int64_t slice = ((hidden + csize - 1) / csize + vec - 1) / vec * vec;
     g.csize = (int)((hidden + slice - 1) / slice);   // no CTA without columns
@@ -562,9 +590,9 @@ cudaError_t launch_rows(void (*kern)(KArgs...), const Geometry &g, int64_t units
     return counted(cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...));
 }
 
-inline bool aligned_rows(const void *p, int64_t stride, int size)
+inline bool aligned_rows(const void *p, int64_t stride, int size, int bytes)
 {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride * size % 16 == 0);
+    return !p || (reinterpret_cast<uintptr_t>(p) % (unsigned)bytes == 0 && stride * size % bytes == 0);
 }
 
 }  // namespace norm

@@ -380,3 +380,31 @@ def test_outputs_in_the_place_of_inputs(b, rows, hidden, name, pad):
         t = [place(d["dy"]), place(s), place(d["dres"])]
         for got, w in zip(backward(*t, t[i]), want):
             assert torch.equal(got, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,hidden", [(9, 2), (300, 30), (257, 66), (70, 258), (900, 316), (65, 514), (400, 1002),
+                                         (31, 2502), (60, 3498), (20, 5002), (7, 6146), (5, 8190), (3, 10002),
+                                         (2, 65534)])
+def test_rows_of_whole_words(b, rows, hidden, name):
+    """16-bit rows on 4-byte boundaries that are no multiples of 16 bytes, packed and in wider rows, then shifted to 2 bytes."""
+    for pad in (0, 6, 3):
+        d = _inputs(rows, hidden, name, pad)
+        _check_forward(b, d, name, pad=pad)
+        _check_forward(b, d, name, res=False, pad=pad)
+        _check_backward(b, d, name, pad=pad)
+        _check_backward(b, d, name, dres=False, pad=pad)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shift", [1, 2, 6])
+def test_rows_from_shifted_bases(b, shift):
+    """Whole rows whose buffer starts 2, 4 or 12 bytes past a 16-byte boundary."""
+    d = _inputs(90, 1002, "bf16", 0)
+    for key in ("x", "res", "dy", "dres"):
+        buf = torch.full((d[key].numel() + shift,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        e = dict(d)
+        e[key] = buf[shift:].view(d[key].shape).copy_(d[key])
+        _check_forward(b, e, "bf16")
+        _check_backward(b, e, "bf16")
