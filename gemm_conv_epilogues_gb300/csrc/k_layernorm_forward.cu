@@ -185,8 +185,9 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
         };
         return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());
     };
+    int64_t units = launch_units(g, a.rows);
     return launch_rows(a.res ? pick(std::integral_constant<int, 2>()) : pick(std::integral_constant<int, 1>()), g,
-                       launch_units(g, a.rows), st, a, src, g, err, wait_limit_ns());
+                       units, st, a, src, g, err, wait_limit_ns());
 }
 
 }  // namespace
