@@ -569,8 +569,9 @@ inline int64_t launch_units(const Geometry &g, int64_t rows)
 // than its SMs would make, since a cluster lies in one GPC.  (Too many run as a
 // second wave: 2048 x 32768 bf16 forward took 190 us instead of 105.)  Asked once per device.
 template <typename... KArgs>
-cudaError_t resident_clusters(int *clusters, const cudaLaunchConfig_t &cfg, void (*kern)(KArgs...), int csize)
+cudaError_t resident_clusters(int *clusters, cudaLaunchConfig_t cfg, void (*kern)(KArgs...), int csize)
 {
+    cfg.blockDim = dim3(kClusterGroup);   // whose registers fill an SM, whatever the rows' width
     static std::mutex mu;
     static int known[64][kMaxRanks + 1];
     int d = 0;
