@@ -23,7 +23,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "ptx_sm100.cuh"
@@ -567,26 +566,18 @@ inline int64_t launch_units(const Geometry &g, int64_t rows)
 
 // Clusters of this many CTAs, one CTA per SM, that the GPU holds at once: fewer
 // than its SMs would make, since a cluster lies in one GPC.  (Too many run as a
-// second wave: 2048 x 32768 bf16 forward took 190 us instead of 105.)  Asked once per device.
+// second wave: 2048 x 32768 bf16 forward took 190 us instead of 105.)
 template <typename... KArgs>
 cudaError_t resident_clusters(int *clusters, cudaLaunchConfig_t cfg, void (*kern)(KArgs...), int csize)
 {
+    const void *key = reinterpret_cast<const void *>(kern);
+    if (recall(key, FACT_CLUSTERS + csize, clusters)) return cudaSuccess;
     cfg.blockDim = dim3(kClusterGroup);   // whose registers fill an SM, whatever the rows' width
-    static std::mutex mu;
-    static int known[64][kMaxRanks + 1];
-    int d = 0;
-    const cudaError_t e = cudaGetDevice(&d);
-    if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!known[d][csize]) {
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            return cudaErrorNotSupported;
-        }
-        known[d][csize] = n;
+    if (cudaOccupancyMaxActiveClusters(clusters, kern, &cfg) != cudaSuccess || *clusters < 1) {
+        cudaGetLastError();
+        return cudaErrorNotSupported;
     }
-    *clusters = known[d][csize];
+    remember(key, FACT_CLUSTERS + csize, *clusters);
     return cudaSuccess;
 }
 
@@ -594,8 +585,13 @@ cudaError_t resident_clusters(int *clusters, cudaLaunchConfig_t cfg, void (*kern
 template <typename... KArgs, typename... Args>
 cudaError_t launch_rows(void (*kern)(KArgs...), const Geometry &g, int64_t &units, cudaStream_t st, Args... args)
 {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, g.smem);
-    if (e == cudaSuccess && g.csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const void *key = reinterpret_cast<const void *>(kern);
+    cudaError_t e = raise_smem_limit(key);
+    int allowed = 0;
+    if (e == cudaSuccess && g.csize > 8 && !recall(key, FACT_WIDE_CLUSTERS, &allowed)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) remember(key, FACT_WIDE_CLUSTERS, 1);
+    }
     if (e != cudaSuccess) {
         cudaGetLastError();   // a refused attribute is not an error of the caller's stream
         return cudaErrorNotSupported;

@@ -60,6 +60,62 @@ int sm_count()
     return g_sms[d];
 }
 
+namespace {
+// Open addressing over (kernel, device, item); a full table remembers no more.
+struct Fact {
+    const void *kern;
+    int key, value;
+};
+constexpr int kFacts = 4096;
+Fact g_facts[kFacts];
+
+Fact *fact_slot(const void *kern, int key)   // with g_mu held; null when the table is full
+{
+    uint64_t h = (reinterpret_cast<uintptr_t>(kern) >> 4) * 0x9E3779B97F4A7C15ull + (uint64_t)key * 0xC2B2AE3D27D4EB4Full;
+    for (int i = 0; i < kFacts; ++i) {
+        Fact &f = g_facts[((h >> 40) + i) % kFacts];
+        if (!f.kern || (f.kern == kern && f.key == key)) return &f;
+    }
+    return nullptr;
+}
+}  // namespace
+
+bool recall(const void *kern, int item, int *value)
+{
+    const int d = current_device();
+    if (d < 0) return false;
+    std::lock_guard<std::mutex> lock(g_mu);
+    const Fact *f = fact_slot(kern, item * kMaxDevices + d);
+    if (!f || !f->kern) return false;
+    *value = f->value;
+    return true;
+}
+
+void remember(const void *kern, int item, int value)
+{
+    const int d = current_device();
+    if (d < 0) return;
+    const int key = item * kMaxDevices + d;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (Fact *f = fact_slot(kern, key)) *f = {kern, key, value};
+}
+
+cudaError_t raise_smem_limit(const void *kern)
+{
+    int limit = 0;
+    if (recall(kern, FACT_SMEM_RAISED, &limit)) return cudaSuccess;
+    int d = 0;
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&limit, cudaDevAttrMaxSharedMemoryPerBlockOptin, d);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    limit -= (int)fa.sharedSizeBytes;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+    if (e == cudaSuccess) remember(kern, FACT_SMEM_RAISED, limit);
+    return e;
+}
+
 }  // namespace tf
 
 using namespace tf;

@@ -18,6 +18,18 @@ uint32_t *device_error_word();
 uint64_t wait_limit_ns();
 int sm_count();
 
+// Numbers asked once of the runtime about a kernel on the current device, by
+// item: recall() is false where none has been remembered.
+enum { FACT_SMEM_RAISED = 0, FACT_WIDE_CLUSTERS = 1, FACT_CLUSTERS = 16 /* + CTAs per cluster */ };
+bool recall(const void *kern, int item, int *value);
+void remember(const void *kern, int item, int value);
+
+// Lets a kernel's launches take as much dynamic shared memory as the current
+// device has beside the kernel's static memory.  The limit belongs to the
+// kernel, not to a launch: set to what one launch takes, it would refuse a
+// larger one that another host thread is about to make.
+cudaError_t raise_smem_limit(const void *kern);
+
 // Conv launchers.  `epilogue` is 1 for the fused BN+SiLU epilogue, 0 for a
 // plain bf16 store of the accumulator (the unfused chain's first kernel).
 struct ConvArgs {
