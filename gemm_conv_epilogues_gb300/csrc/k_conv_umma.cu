@@ -875,6 +875,8 @@ cudaError_t launch_conv_umma(const ConvArgs &a, cudaStream_t st)
     if (!conv_umma_supports(s, a.Ho, a.Wo)) return cudaErrorNotSupported;
     EncodeTiledFn tiled = encode_tiled();
     if (!tiled) return cudaErrorNotSupported;
+    const cudaError_t bound = bind_context();
+    if (bound != cudaSuccess) return bound;
     // a 2-CTA cluster always runs the paired MMA (each CTA holds half of B)
     const int cl = a.cluster == 2 ? 2 : 1;
     const bool pair = cl == 2;

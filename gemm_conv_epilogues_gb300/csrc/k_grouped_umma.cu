@@ -967,6 +967,8 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     p.off_sched = p.off_bar + kNumBars * 8 + 16;
     const int smem = p.off_sched + sched;
 
+    cudaError_t e = bind_context();
+    if (e != cudaSuccess) return e;
     const CUtensorMapDataType type = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap ta, tb;
     bool ok;
@@ -982,7 +984,7 @@ cudaError_t launch_mode(const GroupedArgs &a, int bn, cudaStream_t st, int split
     if (!ok) return cudaErrorInvalidValue;
 
     int units = 0;
-    cudaError_t e = resident<MODE, CG, KSUB>(&units);
+    e = resident<MODE, CG, KSUB>(&units);
     if (e != cudaSuccess) return e;
     const int64_t mt = (p.M + BM * CG - 1) / (BM * CG);
     const int64_t most = WG ? (int64_t)p.groups * mt * ((a.K + kMaxBN - 1) / kMaxBN)

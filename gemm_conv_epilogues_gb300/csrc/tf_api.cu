@@ -1,6 +1,7 @@
 // The C ABI of libtf_epilogue.so: argument validation, kernel selection and
 // launch.  Every check runs on the host before anything is launched; an
 // unsupported case is an error, never a silent fallback.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -114,6 +115,24 @@ cudaError_t raise_smem_limit(const void *kern)
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
     if (e == cudaSuccess) remember(kern, FACT_SMEM_RAISED, limit);
     return e;
+}
+
+cudaError_t bind_context()
+{
+    using CurrentFn = CUresult (*)(CUcontext *);
+    static const CurrentFn current = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return (CurrentFn) nullptr;
+        return reinterpret_cast<CurrentFn>(f);
+    }();
+    CUcontext c = nullptr;
+    if (current && current(&c) == CUDA_SUCCESS && c) return cudaSuccess;
+    int d = 0;
+    const cudaError_t e = cudaGetDevice(&d);
+    return e == cudaSuccess ? cudaSetDevice(d) : e;
 }
 
 }  // namespace tf

@@ -30,6 +30,11 @@ void remember(const void *kern, int item, int value);
 // larger one that another host thread is about to make.
 cudaError_t raise_smem_limit(const void *kern);
 
+// Makes the current device's context the calling thread's, where the thread
+// has none: tensor maps are encoded by the driver, which, unlike the runtime's
+// calls, does not do so itself for a new host thread.
+cudaError_t bind_context();
+
 // Conv launchers.  `epilogue` is 1 for the fused BN+SiLU epilogue, 0 for a
 // plain bf16 store of the accumulator (the unfused chain's first kernel).
 struct ConvArgs {

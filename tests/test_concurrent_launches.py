@@ -1,5 +1,6 @@
-"""Two host threads calling one kernel at sizes that need different amounts of
-shared memory: neither thread's launches depend on the other's sizes."""
+"""Calls from several host threads: two threads that call one kernel at sizes
+that need different amounts of shared memory, neither of whose launches depends
+on the other's sizes, and the first calls of a new thread."""
 import sys
 import threading
 import time
@@ -79,3 +80,37 @@ def test_norm_backward(b, sizes):
                                                rows, hidden, 0, b.TF_FP16, ws, size, 0, check=False)
 
     assert _refused([call(*s) for s in NORMS[sizes]]) == [[], []]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["conv", "norm", "product", "input gradient", "weight gradient"])
+def test_first_calls_of_a_thread(b, what):
+    """A host thread that has called nothing of CUDA before gets what the main thread gets."""
+    off = torch.tensor([0, 40, 64], dtype=torch.int32, device="cuda")
+    x, dy = torch.randn(64, 128, device="cuda").bfloat16(), torch.randn(64, 256, device="cuda").bfloat16()
+    w = torch.randn(2, 256, 128, device="cuda").bfloat16()
+    shape = b.conv_shape(1, 8, 16, 64, 64, 1, 1)
+    image, filt = x.view(torch.int16)[:, :64].repeat(2, 1), w.view(torch.int16)[0, :64, :64].contiguous()
+    f = torch.ones(2, 64, device="cuda")
+    out = {"conv": filt.new_zeros(128, 64), "norm": torch.zeros_like(x), "product": torch.zeros_like(dy),
+           "input gradient": torch.zeros_like(x), "weight gradient": torch.zeros(2, 256, 128, device="cuda")}[what]
+    call = {
+        "conv": lambda: b.tf_conv2d_bn_silu_variant(image, filt, f[0], f[1], out, shape, b.TF_CONV_UMMA, 0, check=False),
+        "norm": lambda: b.tf_layernorm_forward(x, 128, None, 0, None, None, out, 128, None, 0, None, None, 64, 128, 1e-5,
+                                               b.TF_BF16, 0, check=False),
+        "product": lambda: b.tf_grouped_matmul(x, 128, w, None, off, out, 256, None, 0, 64, 2, 256, 128, 0, b.TF_BF16, 0,
+                                               check=False),
+        "input gradient": lambda: b.tf_grouped_matmul_dgrad(dy, 256, w, off, None, 0, out, 128, 64, 2, 256, 128, 0,
+                                                            b.TF_BF16, 0, check=False),
+        "weight gradient": lambda: b.tf_grouped_matmul_wgrad(dy, 256, x, 128, off, out, None, 64, 2, 256, 128, 0,
+                                                             b.TF_BF16, None, 0, 0, check=False)}[what]
+    assert call() == 0
+    torch.cuda.synchronize()
+    want, codes = out.clone(), []
+    out.zero_()
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=lambda: codes.extend([call(), call()]))
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert codes == [0, 0] and torch.equal(out, want) and want.any()
