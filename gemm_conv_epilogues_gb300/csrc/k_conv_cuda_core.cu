@@ -222,7 +222,7 @@ cudaError_t launch_conv_tiled(const ConvArgs &a, cudaStream_t st)
     const size_t smem = sizeof(uint4) * ((size_t)halo_h * halo_w + (size_t)CO_T * s.KH * s.KW);
     if (smem > 200 * 1024 || s.N > 65535 || (s.C_out + CO_T - 1) / CO_T > 65535) return cudaErrorNotSupported;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(conv_tiled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(conv_tiled_kernel));
         if (e != cudaSuccess) return e;
     }
     const dim3 grid((unsigned)(((a.Ho + TH - 1) / TH) * ((a.Wo + TW - 1) / TW)), (unsigned)s.N,

@@ -752,8 +752,7 @@ cudaError_t launch_bn(const CUtensorMap &ta, const CUtensorMap &tb, const CUtens
     if (CG == 2 && p.num_n_tiles * BN != p.C_out) return cudaErrorNotSupported;
     if (!plan_smem<BN, EPI, MH, CG>(p.num_kb, want_bres && p.splits == 1, p.sm))
         return cudaErrorNotSupported;
-    // Per-function, per-device attribute; cheap enough to set on every launch.
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, p.sm.alloc);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern));
     if (e != cudaSuccess) return e;
     // programmatic dependent launch: the kernel's set-up may overlap the
     // previous kernel of the stream (it waits before touching global memory)

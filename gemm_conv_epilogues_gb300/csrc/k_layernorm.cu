@@ -570,7 +570,7 @@ cudaError_t launch_ln_cta(const void *a, const void *b, const float *gamma, cons
     stages = stages < 2 ? 2 : (stages > 4 ? 4 : stages);
     const size_t smem = (size_t)stages * stage_bytes + 8 * (size_t)stages;
     auto kern = layernorm_kernel<2, RESIDUAL, AFFINE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern));
     if (e != cudaSuccess) return e;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem) != cudaSuccess || per_sm < 1)
@@ -628,7 +628,7 @@ cudaError_t launch_ln_cluster_with(const void *a, const void *b, const float *ga
     stages = stages < 2 ? 2 : (stages > 4 ? 4 : stages);
     const size_t smem = (size_t)stages * stage_bytes + 8 * (size_t)stages;
     auto kern = layernorm_cluster_kernel<RESIDUAL, AFFINE, NV, MAXT, REGP>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void *>(kern));
     if (e == cudaSuccess && csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) {
         cudaGetLastError();   // a refused attribute is not an error of the caller's stream

@@ -114,3 +114,26 @@ def test_first_calls_of_a_thread(b, what):
     thread.join()
     torch.cuda.synchronize()
     assert codes == [0, 0] and torch.equal(out, want) and want.any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("widths", [(2048, 8192), (24576, 65536)])
+def test_residual_layernorm(b, widths):
+    def call(hidden):
+        act, res, y = _half(4, hidden), _half(4, hidden), _half(4, hidden)
+        f = torch.ones(2, hidden, device="cuda")
+        return lambda: b.tf_residual_layernorm(act, res, f[0], f[1], y, 4, hidden, 1e-5, 0, check=False)
+
+    assert _refused([call(w) for w in widths]) == [[], []]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("variant,kernels", [("TF_CONV_UMMA", [(1, 64), (1, 256)]), ("TF_CONV_TILED", [(13, 8), (15, 8)])])
+def test_conv(b, variant, kernels):
+    def call(k, c_in):
+        shape = b.conv_shape(1, 8, 16, c_in, 64, k, k, (1, 1), (k // 2, k // 2))
+        x, w, y = (torch.zeros(n, dtype=torch.int16, device="cuda") for n in (128 * c_in, 64 * k * k * c_in, 128 * 64))
+        f = torch.ones(2, 64, device="cuda")
+        return lambda: b.tf_conv2d_bn_silu_variant(x, w, f[0], f[1], y, shape, getattr(b, variant), 0, check=False)
+
+    assert _refused([call(*s) for s in kernels]) == [[], []]
