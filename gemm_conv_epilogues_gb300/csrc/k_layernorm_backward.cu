@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 
         load_edge(ring, 0, next, gt, gsize, ed);
         load_edge(ring, 1, next, gt, gsize, ex);
         if (NT > 2) load_edge(ring, 2, next, gt, gsize, er);
-        const float2 scale = make_float2(rstd, rstd), shift = make_float2(-mean * rstd, -mean * rstd);
+        const float2 scale = make_float2(rstd, rstd), centre = make_float2(mean, mean);
+        // (the difference first: x*rstd - mean*rstd would lose the digits of a row far from zero)
+        auto normalised = [&](int p) { return fmul2(fsub2(x.get(p), centre), scale); };
         if (next < ring.rows) {
             mean = __ldg(a.mean + next);
             rstd = __ldg(a.rstd + next);
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 
         float2 c1 = make_float2(0.0f, 0.0f), c2 = c1;
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {   // past the slice dy is zero and adds nothing
-            const float2 fd = d.get(p), xh = ffma2(x.get(p), scale, shift), w = fmul2(fd, gamma2(p));
+            const float2 fd = d.get(p), xh = normalised(p), w = fmul2(fd, gamma2(p));
             dg[p] = ffma2(fd, xh, dg[p]);
             db[p] = fadd2(db[p], fd);
             c1 = fadd2(c1, w);
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(CLUSTER ? 512 : cta_threads(COLS, GROUP, NT), 
         float2 out[PAIRS];
 #pragma unroll
         for (int p = 0; p < PAIRS; ++p) {
-            const float2 xh = ffma2(x.get(p), scale, shift);
+            const float2 xh = normalised(p);
             out[p] = ffma2(fmul2(d.get(p), gamma2(p)), scale, ffma2(xh, k2, k1));
             if (NT > 2) out[p] = fadd2(out[p], r.get(p));
         }

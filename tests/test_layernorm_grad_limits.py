@@ -1,0 +1,32 @@
+"""Layer norm with its gradients where rounding adds up or the launch changes
+form."""
+import pytest
+import torch
+
+import test_layernorm_grad as base
+import train_reference as ref
+
+
+@pytest.fixture(scope="module")
+def b(cuda_ready):
+    from gemm_conv_epilogues_gb300 import binding
+    yield binding
+    assert binding.tf_read_device_error() == (0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name,offset", [("fp32", 100.0), ("fp32", 1e4), ("bf16", 300.0), ("fp16", 2000.0)])
+@pytest.mark.parametrize("rows,hidden,dres", [(50, 4096, True), (40, 640, False), (30, 1001, True), (9, 20480, False)])
+def test_backward_far_from_zero(b, rows, hidden, dres, name, offset):
+    """x - mean is one rounding of its own value, not of x: xh keeps its digits however far the row lies from zero."""
+    d = base._inputs(rows, hidden, name, 0, offset=offset)
+    _, mean, rstd, _ = ref.norm_forward(d["x"], None, None, None, base.EPS)
+    mean, rstd = mean.float(), rstd.float()
+    dx, dgamma, dbeta = base._backward(b, d, name, mean, rstd, dres)
+    dr = d["dres"] if dres else None
+    rx, rg, rb = ref.norm_backward(d["dy"], d["x"], d["gamma"], mean, rstd, dr)
+    # the bounds of rows around zero, whose xh is off by 2u*rstd*|x - mean| and its own two roundings
+    near = d["x"].double() - mean.double()[:, None]
+    bx, bg, bb = ref.norm_backward_bounds(name, d["dy"], near, d["gamma"], torch.zeros_like(mean), rstd, dr, rx)
+    for got, want, bound, what in ((dx, rx, bx, "dx"), (dgamma, rg, bg, "dgamma"), (dbeta, rb, bb, "dbeta")):
+        base._within(got, want, bound, what)
