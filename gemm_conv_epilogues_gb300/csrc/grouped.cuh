@@ -159,6 +159,35 @@ __device__ __forceinline__ float2 act_slope2(float2 z)
     }
 }
 
+// ---------------------------------------------------------------- column sums
+
+// total += the sum over rows first, first + step, ... < end, where at(m, sum)
+// sets `sum` to one step's rows' sum.  In three levels, of 64 steps, of 64 such sums
+// and of those: in one level a long group's running sum outgrows its terms, and
+// equal ones lose 2e-3 over 2^20 rows (1e-2 over 2^22).
+template <int N, typename F>
+__device__ __forceinline__ void sum_rows(float2 (&total)[N], int first, int end, int step, F at)
+{
+    constexpr int FAN = 64;
+    auto into = [](float2 (&dst)[N], const float2 (&src)[N]) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) dst[k] = fadd2(dst[k], src[k]);
+    };
+    for (int m = first; m < end;) {
+        float2 mid[N] = {};
+        for (int j = 0; j < FAN && m < end; ++j) {
+            float2 low[N] = {};
+            for (int i = 0; i < FAN && m < end; ++i, m += step) {
+                float2 sum[N];
+                at(m, sum);
+                into(low, sum);
+            }
+            into(mid, low);
+        }
+        into(total, mid);
+    }
+}
+
 // ---------------------------------------------------------------- tile schedule
 
 // The groups' rows and the running count of their tiles, in shared memory.

@@ -332,8 +332,8 @@ __device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const uint32_t (
 
 // dbias[e][n] = sum of dy[m][n] over group e's rows, without the pipeline: a warp
 // takes 64 columns of a group (16 where that leaves warps without work), 16
-// bytes per lane, eight loads in flight, fp32 sums, the lanes' rows added in a
-// fixed order.
+// bytes per lane, eight loads in flight, fp32 sums in levels, the lanes' rows
+// added in a fixed order.
 template <typename T>
 __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int warp)
 {
@@ -345,7 +345,7 @@ __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int 
         const int lo = s.row[e], hi = s.row[e + 1];
         const uint16_t *src = reinterpret_cast<const uint16_t *>(p.dy) + n;
         float2 sum[4] = {};
-        for (int m = lo + r0; m < hi && n < p.M; m += 8 * down) {
+        sum_rows(sum, lo + r0, n < p.M ? hi : lo, 8 * down, [&](int m, float2 (&rows)[4]) {
             uint4 v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -353,12 +353,12 @@ __device__ __forceinline__ void bias_grad(const UmmaArgs &p, const Plan &s, int 
                                          : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum[0] = fadd2(sum[0], Half2Of<T>::unpack(v[i].x));
-                sum[1] = fadd2(sum[1], Half2Of<T>::unpack(v[i].y));
-                sum[2] = fadd2(sum[2], Half2Of<T>::unpack(v[i].z));
-                sum[3] = fadd2(sum[3], Half2Of<T>::unpack(v[i].w));
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    rows[j] = i == 0 ? Half2Of<T>::unpack(w[j]) : fadd2(rows[j], Half2Of<T>::unpack(w[j]));
             }
-        }
+        });
         __syncwarp();
         for (int o = across; o < 32; o <<= 1)
 #pragma unroll

@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) grouped_unaligned_kernel(const Gr
 
 // dbias[e][n] = sum of dy[m][n] over group e's rows.  A CTA takes 64 columns of
 // one group: VEC columns per thread (8: 16-byte loads), 64/VEC threads side by
-// side, the others on rows of their own, four loads each in flight; the CTA's
-// partial sums are added in order.  Bound by HBM: dy once.
+// side, the others on rows of their own, four loads each in flight, sums in
+// levels; the CTA's partial sums are added in order.  Bound by HBM: dy once.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(256) grouped_bias_grad_kernel(const GroupedArgs a, uint32_t *err)
 {
@@ -298,33 +298,32 @@ __global__ void __launch_bounds__(256) grouped_bias_grad_kernel(const GroupedArg
     const int e = blockIdx.y, q = threadIdx.x / ACROSS, c = (int)threadIdx.x % ACROSS * VEC, n = blockIdx.x * 64 + c;
     const int lo = a.offsets[e], hi = a.offsets[e + 1];
     const T *dy = reinterpret_cast<const T *>(a.dy) + n;
-    float sum[VEC] = {};
-    if (n < a.N)   // (N is a multiple of VEC)
-        for (int m = lo + q; m < hi; m += 4 * DOWN) {
-            if constexpr (VEC == 8) {
-                uint4 v[4];
+    constexpr int PAIRS = (VEC + 1) / 2;   // (of a single column the second value stays zero)
+    float2 sum[PAIRS] = {};
+    // (N is a multiple of VEC)
+    sum_rows(sum, lo + q, n < a.N ? hi : lo, 4 * DOWN, [&](int m, float2 (&rows)[PAIRS]) {
+        if constexpr (VEC == 8) {
+            uint4 v[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = m + i * DOWN < hi ? __ldg(reinterpret_cast<const uint4 *>(dy + (int64_t)(m + i * DOWN) * a.dy_stride))
-                                             : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i)
+                v[i] = m + i * DOWN < hi ? __ldg(reinterpret_cast<const uint4 *>(dy + (int64_t)(m + i * DOWN) * a.dy_stride))
+                                         : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = Half2Of<T>::unpack(w[j]);
-                        sum[2 * j] += f.x;
-                        sum[2 * j + 1] += f.y;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (m + i * DOWN < hi) sum[0] += Half2Of<T>::widen(dy[(int64_t)(m + i * DOWN) * a.dy_stride]);
+                for (int j = 0; j < 4; ++j)
+                    rows[j] = i == 0 ? Half2Of<T>::unpack(w[j]) : fadd2(rows[j], Half2Of<T>::unpack(w[j]));
             }
-        }
+        } else {
+            rows[0] = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) red[q][c + j] = sum[j];
+            for (int i = 0; i < 4; ++i)
+                if (m + i * DOWN < hi) rows[0].x += Half2Of<T>::widen(dy[(int64_t)(m + i * DOWN) * a.dy_stride]);
+        }
+    });
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) red[q][c + j] = j % 2 ? sum[j / 2].y : sum[j / 2].x;
     cta_sync();
     if (threadIdx.x < 64 && blockIdx.x * 64 + threadIdx.x < (unsigned)a.N) {
         float t = 0.0f;
