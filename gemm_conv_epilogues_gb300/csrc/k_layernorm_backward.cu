@@ -250,10 +250,15 @@ Geometry geometry_for(int64_t rows, int64_t hidden, int size, int vec, int tenso
     return geometry(hidden, size, vec, cols, tensors, sm_threads(cols, aligned, group, tensors), true, rows, cols > 16 ? 1 : 0);
 }
 
-// The most partial sums that any alignment and number of operands gives.
+// The most partial sums that any alignment, number of operands and number of
+// rows up to `rows` gives.  One row per CTA gives the most, as long as there are
+// SMs: with more rows a CTA takes several, and 153 rows may have half the partial
+// sums of 152.
 int64_t most_units(int64_t rows, int64_t hidden, int dtype)
 {
     const int size = dtype == TF_FP32 ? 4 : 2;
+    const int64_t sms = sm_count();
+    if (rows > sms) rows = sms;
     int64_t most = 0;
     for (int tensors : {2, 3})
         for (int vec : {1, 2, 16 / size}) {

@@ -268,8 +268,9 @@ int tf_layernorm_forward(const void *x, int64_t x_stride, const void *res, int64
                          float *rstd, int64_t rows, int64_t hidden, float eps, int dtype, tf_stream_t stream);
 
 /* Bytes of device workspace tf_layernorm_backward needs when dgamma or dbeta
- * is wanted (fp32 column sums of the rows each CTA takes).  Host only; depends
- * on the current device's SM count. */
+ * is wanted (fp32 column sums of the rows each CTA takes).  It does not fall as
+ * rows grow: a workspace for the largest batch serves every smaller one.  Host
+ * only; depends on the current device's SM count. */
 int64_t tf_layernorm_backward_workspace_size(int64_t rows, int64_t hidden, int dtype);
 
 /* Gradients of tf_layernorm_forward.  With xh = (x - mean)*rstd, w = dy*gamma:

@@ -30,3 +30,12 @@ def test_backward_far_from_zero(b, rows, hidden, dres, name, offset):
     bx, bg, bb = ref.norm_backward_bounds(name, d["dy"], near, d["gamma"], torch.zeros_like(mean), rstd, dr, rx)
     for got, want, bound, what in ((dx, rx, bx, "dx"), (dgamma, rg, bg, "dgamma"), (dbeta, rb, bb, "dbeta")):
         base._within(got, want, bound, what)
+
+
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+@pytest.mark.parametrize("hidden", [8, 100, 640, 641, 1024, 4096, 5003, 20480])
+def test_workspace_of_a_larger_batch_serves_a_smaller_one(native_lib, hidden, dtype):
+    from gemm_conv_epilogues_gb300 import binding as b
+    sizes = [b.tf_layernorm_backward_workspace_size(rows, hidden, dtype) for rows in range(6000)]
+    assert sizes[0] == 0 and sizes[1] == 8 * hidden
+    assert all(p <= q for p, q in zip(sizes, sizes[1:]))
