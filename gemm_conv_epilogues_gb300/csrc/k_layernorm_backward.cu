@@ -7,6 +7,7 @@
 // group takes; the row groups of an SM form one CTA and add their sums in
 // shared memory, one set per SM goes to the workspace, and a second, small
 // kernel adds those in order, so that equal calls give equal bits (no atomics).
+// Very many rows take several such launches.
 // Bound by HBM: 16384 x 4096 bf16 with dres in 90 us, 80 of them this pass at
 // 6.7 TB/s, the rest the second kernel; narrow rows by the issue slots (50001 x
 // 640 fp16: 45 us, 4.3 TB/s), odd widths by their element-wise columns (1999 x
@@ -242,6 +243,12 @@ __global__ void __launch_bounds__(kSumWarps * 32) norm_weight_grad_kernel(const 
     }
 }
 
+cudaError_t launch_weight_grad(const NormGradArgs &a, int64_t units, cudaStream_t st)
+{
+    return launch_pdl(norm_weight_grad_kernel, dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(kSumWarps * 32), 0, st, a,
+                      (int)units);
+}
+
 Geometry geometry_for(int64_t rows, int64_t hidden, int size, int vec, int tensors)
 {
     const bool aligned = vec * size == 16;
@@ -268,8 +275,17 @@ int64_t most_units(int64_t rows, int64_t hidden, int dtype)
     return most;
 }
 
+// Rows that one launch takes where column sums are wanted: up to 1024 for each
+// of its row groups.  A thread adds its rows one after the other, and equal
+// terms of a much longer sum lose digits: 3e-4 over 37000 rows each, below 1e-5
+// over 1024.  (Of 4096 16-bit columns a launch takes 311,000 rows, over 1 ms.)
+int64_t rows_per_launch(const Geometry &g, const NormGradArgs &a)
+{
+    return a.ws ? 1024 * launch_units(g, a.rows) * (g.threads / g.group) : a.rows;
+}
+
 template <typename T>
-cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
+cudaError_t launch_typed(const NormGradArgs &a, cudaStream_t st)
 {
     constexpr int size = (int)sizeof(T);
     uint32_t *err = device_error_word();
@@ -281,9 +297,7 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
     };
     const bool aligned = whole(16);
     const int vec = aligned ? 16 / size : size == 2 && whole(4) ? 2 : 1;
-    const Sources src = {{a.dy, a.x, a.dres}, {a.dy_stride, a.x_stride, a.dres_stride}};
     const Geometry g = geometry_for(a.rows, a.hidden, size, vec, a.dres ? 3 : 2);
-    *units = launch_units(g, a.rows);
     auto pick = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
         if (aligned) {
@@ -315,8 +329,27 @@ cudaError_t launch_typed(const NormGradArgs &a, int64_t *units, cudaStream_t st)
         };
         return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());
     };
-    return launch_rows(a.dres ? pick(std::integral_constant<int, 3>()) : pick(std::integral_constant<int, 2>()), g,
-                       *units, st, a, src, g, err, wait_limit_ns());
+    auto kern = a.dres ? pick(std::integral_constant<int, 3>()) : pick(std::integral_constant<int, 2>());
+    const int64_t run = rows_per_launch(g, a);
+    NormGradArgs p = a;
+    for (int64_t left = a.rows;;) {
+        p.rows = left < run ? left : run;
+        const Sources src = {{p.dy, p.x, p.dres}, {a.dy_stride, a.x_stride, a.dres_stride}};
+        int64_t units = launch_units(g, p.rows);
+        cudaError_t e = launch_rows(kern, g, units, st, p, src, g, err, wait_limit_ns());
+        if (e == cudaSuccess && a.ws) e = launch_weight_grad(p, units, st);
+        if (e != cudaSuccess || (left -= p.rows) == 0) return e;
+        auto skip = [&](const void *&q, int64_t stride) {
+            if (q) q = static_cast<const T *>(q) + p.rows * stride;
+        };
+        skip(p.dy, a.dy_stride);
+        skip(p.x, a.x_stride);
+        skip(p.dres, a.dres_stride);
+        p.dx = static_cast<T *>(p.dx) + p.rows * a.dx_stride;
+        p.mean += p.rows;
+        p.rstd += p.rows;
+        p.accumulate = 1;
+    }
 }
 
 }  // namespace
@@ -328,15 +361,11 @@ int64_t layernorm_backward_workspace(int64_t rows, int64_t hidden, int dtype)
 
 cudaError_t launch_layernorm_backward(const NormGradArgs &a, cudaStream_t st)
 {
-    int64_t units = 0;   // with no rows there are no partial sums, and the gradients become zero
-    cudaError_t e = cudaSuccess;
-    if (a.rows > 0)
-        e = a.dtype == TF_FP32   ? launch_typed<float>(a, &units, st)
-            : a.dtype == TF_BF16 ? launch_typed<__nv_bfloat16>(a, &units, st)
-                                 : launch_typed<__half>(a, &units, st);
-    if (e != cudaSuccess || (!a.dgamma && !a.dbeta)) return e;
-    return launch_pdl(norm_weight_grad_kernel, dim3((unsigned)((a.hidden + 31) / 32), 2), dim3(kSumWarps * 32), 0, st, a,
-                      (int)units);
+    // with no rows there are no partial sums, and the gradients become zero
+    if (a.rows == 0) return launch_weight_grad(a, 0, st);
+    return a.dtype == TF_FP32   ? launch_typed<float>(a, st)
+           : a.dtype == TF_BF16 ? launch_typed<__nv_bfloat16>(a, st)
+                                : launch_typed<__half>(a, st);
 }
 
 }  // namespace tf

@@ -5,6 +5,7 @@ import torch
 
 import test_layernorm_grad as base
 import train_reference as ref
+from train_reference import U
 
 
 @pytest.fixture(scope="module")
@@ -30,6 +31,30 @@ def test_backward_far_from_zero(b, rows, hidden, dres, name, offset):
     bx, bg, bb = ref.norm_backward_bounds(name, d["dy"], near, d["gamma"], torch.zeros_like(mean), rstd, dr, rx)
     for got, want, bound, what in ((dx, rx, bx, "dx"), (dgamma, rg, bg, "dgamma"), (dbeta, rb, bb, "dbeta")):
         base._within(got, want, bound, what)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hidden,rows", [(8, 1 << 27), (1, (1 << 27) + 3)])
+def test_weight_gradients_of_many_rows(b, hidden, rows):
+    """Equal terms, whose roundings do not cancel.  No term passes more than about 1024 additions of a row
+    group, 64 of the groups' and CTAs' sums and 256 of what further runs of rows add."""
+    dy = torch.full((rows, hidden), 0.1, device="cuda")
+    x, mean, rstd = torch.ones(rows, hidden, device="cuda"), torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dgamma, dbeta = torch.empty(hidden, device="cuda"), torch.full((hidden,), 3.0, device="cuda")
+    size = b.tf_layernorm_backward_workspace_size(rows, hidden, b.TF_FP32)
+    ws = torch.full((size // 4,), float("nan"), device="cuda")
+    args = (dy, hidden, x, hidden, None, mean, rstd, None, 0, dy, hidden)
+    # dbeta alone, added to what it holds, then both; dx takes dy's place
+    keep = dy.clone()
+    b.tf_layernorm_backward(*args, None, dbeta, rows, hidden, 1, b.TF_FP32, ws, size)
+    dy.copy_(keep)
+    del keep
+    want = rows * float(torch.tensor(0.1))
+    bound = (1024 + 64 + 256) * U * (want + 3)
+    assert (dbeta.double() - want - 3).abs().max() <= bound
+    b.tf_layernorm_backward(*args, dgamma, dbeta, rows, hidden, 0, b.TF_FP32, ws, size)
+    assert (dbeta.double() - want).abs().max() <= bound
+    assert (dgamma.double() - want).abs().max() <= bound
 
 
 @pytest.mark.parametrize("dtype", [0, 1, 2])
