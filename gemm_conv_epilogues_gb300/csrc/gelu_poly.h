@@ -14,3 +14,8 @@
 #define TF_GELU_C5 -0.04057419300079346f
 #define TF_GELU_C6 0.016779523342847824f
 #define TF_GELU_C7 -0.004253455437719822f
+// t*Q(t)*sqrt(2 pi)*exp(t^2/2) in 1/t^2, for t in [TF_GELU_TMAX, TF_GELU_TFAR]
+#define TF_GELU_TFAR 15.0f
+#define TF_GELU_FAR0 0.9999721646308899f
+#define TF_GELU_FAR1 -0.9923630952835083f
+#define TF_GELU_FAR2 2.4148473739624023f

@@ -12,6 +12,12 @@ T_CLAMP = 12 rather than 6: for 6 < t <= 12 the exact |s*Q(t)| is below
 2^P(3) ~ 2^-111 makes s*Q vanish, so every such output rounds to +-0 in fp16
 (and GELU(+inf) = +inf) without a separate test for large |s|.
 
+bf16 has the exponents that fp16 lacks: there s*Q(-s) is a number down to
+s = -13.5.  Below -6 the kernels that store bf16 take
+t*Q(t) = S(1/t^2) * 2^(-t^2/2 * log2 e) / sqrt(2 pi), the scale of Q's asymptotic
+series, with S a quadratic fitted on t in [6, 15]; with phi the density,
+Q(t) - t*phi(t), the slope of GELU at -t, is t*phi(t)*(S/t^2 - 1).
+
 The script also checks the whole fp32 evaluation, emulated in numpy, against
 s*ndtr(s) on every finite fp16 input: the result must stay within 1 fp16 ulp
 of the correctly rounded value (the GPU tests allow 2).
@@ -25,6 +31,8 @@ from scipy.special import log_ndtr, ndtr
 T_MAX = 6.0
 T_CLAMP = 12.0
 DEGREE = 7
+T_FAR = 15.0       # fp32's and bf16's t*Q(t) is zero from 14.4 on
+FAR_SCALE = 32     # the exponent is evaluated 2^32 too high: ex2 flushes what fp32 still holds
 
 
 def fit():
@@ -33,6 +41,30 @@ def fit():
     v = t / (T_MAX / 2.0) - 1.0
     c = np.polynomial.chebyshev.chebfit(v, g, DEGREE)
     return np.polynomial.chebyshev.cheb2poly(c).astype(np.float32)
+
+
+def fit_far():
+    """S(u), u = 1/t^2, at the Chebyshev points of u over t in [T_MAX, T_FAR]; power basis."""
+    lo, hi = 1 / T_FAR ** 2, 1 / T_MAX ** 2
+    u = (lo + hi) / 2 + (hi - lo) / 2 * np.cos(np.pi * (np.arange(2000) + 0.5) / 2000)
+    t = 1 / np.sqrt(u)
+    s = np.exp(log_ndtr(-t) + 0.5 * t * t) * t * np.sqrt(2 * np.pi)
+    return np.polynomial.Polynomial.fit(u, s, 2, domain=[lo, hi]).convert().coef.astype(np.float32)
+
+
+def far_fp32(s32, c):
+    """(GELU(s), GELU'(s)) for s < -T_MAX, the kernels' arithmetic step by step in fp32 (ex2 and the
+    reciprocal taken exact, results below the smallest normal number of ex2 flushed)."""
+    f32, f64 = np.float32, np.float64
+    fma = lambda a, b, d: (a.astype(f64) * f64(b) + f64(d)).astype(f32)
+    t = np.minimum(np.abs(s32), f32(T_FAR))
+    t2 = (t * t).astype(f32)
+    e = np.exp2(fma(t2, f32(-0.5 / np.log(2)), f32(FAR_SCALE - 0.5 * np.log2(2 * np.pi))).astype(f64))
+    e = np.where(e < 2.0 ** -126, 0, e).astype(f32)
+    u = (1 / t2.astype(f64)).astype(f32)
+    s = fma(fma(np.full_like(u, c[2]), u.astype(f64), c[1]), u.astype(f64), c[0])
+    small = f32(2.0 ** -FAR_SCALE)
+    return (-(e * s) * small).astype(f32), ((e * t) * fma(s, u.astype(f64), -1) * small).astype(f32)
 
 
 def gelu_fp32(s32, p):
@@ -62,7 +94,7 @@ def check(p):
 
 
 def main():
-    p = fit()
+    p, far = fit(), fit_far()
     worst, frac = check(p)
     assert worst <= 1, worst
     here = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +109,10 @@ def main():
         f.write(f"#define TF_GELU_POLY_DEGREE {DEGREE}\n")
         for k, c in enumerate(p):
             f.write(f"#define TF_GELU_C{k} {float(c)!r}f\n")
+        f.write("// t*Q(t)*sqrt(2 pi)*exp(t^2/2) in 1/t^2, for t in [TF_GELU_TMAX, TF_GELU_TFAR]\n")
+        f.write(f"#define TF_GELU_TFAR {T_FAR:.1f}f\n")
+        for k, c in enumerate(far):
+            f.write(f"#define TF_GELU_FAR{k} {float(c)!r}f\n")
     print(f"max {worst} ulp, {100 * frac:.2f}% off by one")
 
 

@@ -27,6 +27,11 @@ struct Half2Of<__half> {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
     __device__ static float2 unpack(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2 *>(&u)); }
+    __device__ static uint32_t min2(uint32_t a, uint32_t b)
+    {
+        const __half2 h = __hmin2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
     __device__ static __half round(float a) { return __float2half_rn(a); }
     __device__ static float widen(__half a) { return __half2float(a); }
 };
@@ -40,6 +45,11 @@ struct Half2Of<__nv_bfloat16> {
     __device__ static float2 unpack(uint32_t u)
     {
         return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+    __device__ static uint32_t min2(uint32_t a, uint32_t b)
+    {
+        const __nv_bfloat162 h = __hmin2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
     __device__ static __nv_bfloat16 round(float a) { return __float2bfloat16_rn(a); }
     __device__ static float widen(__nv_bfloat16 a) { return __bfloat162float(a); }
@@ -62,7 +72,8 @@ __device__ __forceinline__ float max_nan(float a, float b)
 }
 
 // Q(t), the upper tail of the standard normal at t in [0, 12]: the fit of
-// gelu_f32 (relative error below 1e-5 on [0, 6], below 2^-29 in value beyond).
+// gelu_f32 (relative error below 1e-5 on [0, 6], below 2^-29 in value beyond:
+// nothing beside 1, but see far_value()).
 __device__ __forceinline__ float normal_tail(float t)
 {
     const float v = fmaf(t, 1.0f / (TF_GELU_TMAX * 0.5f), -1.0f);
@@ -77,17 +88,66 @@ __device__ __forceinline__ float normal_tail(float t)
     return ex2_approx(acc);
 }
 
+// Activation and slope far below zero, where they are numbers that only the
+// exponents of bf16 hold: GELU below -6 by the scale of the tail's asymptotic
+// series (gen_gelu_poly.py), SiLU below -80 as z e^z and (1 + z) e^z.  The
+// exponentials are taken 2^32 too high, since ex2 flushes what an fp32 product
+// still holds.  Relative error below 1e-4 down to the smallest bf16; at the
+// clamps all is zero.  Such values are rare, so the epilogues look at the least
+// of 32 values and leave these branches out where FAR is false (tested value by
+// value they took 21.8 us instead of 17.5 for 4096 rows of 2048 x 512 with GELU).
+constexpr float kFarScale = 32.0f, kFarUnscale = 1.0f / 4294967296.0f;
+__host__ __device__ constexpr float far_from(int act) { return act == TF_ACT_GELU ? -TF_GELU_TMAX : -80.0f; }
+
+// t*Q(t) = tail_scale(t, s) * s * kFarUnscale
+__device__ __forceinline__ float tail_scale(float t, float &s, float &u)
+{
+    const float t2 = t * t;
+    u = rcp_approx(t2);
+    s = fmaf(fmaf(TF_GELU_FAR2, u, TF_GELU_FAR1), u, TF_GELU_FAR0);
+    return ex2_approx(fmaf(t2, -0.5f * kLog2e, kFarScale - 1.3257480647f));   // log2 sqrt(2 pi)
+}
+
+template <int ACT>
+__device__ __forceinline__ float far_value(float z)
+{
+    if constexpr (ACT == TF_ACT_GELU) {
+        float s, u;
+        const float e = tail_scale(fminf(-z, TF_GELU_TFAR), s, u);
+        return -(e * s) * kFarUnscale;
+    } else {
+        const float v = fmaxf(z, -200.0f);
+        return v * ex2_approx(fmaf(v, kLog2e, kFarScale)) * kFarUnscale;
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ float far_slope(float z)
+{
+    if constexpr (ACT == TF_ACT_GELU) {
+        float s, u;
+        const float t = fminf(-z, TF_GELU_TFAR), e = tail_scale(t, s, u);
+        return e * t * fmaf(s, u, -1.0f) * kFarUnscale;
+    } else {
+        const float v = fmaxf(z, -200.0f);
+        return (1.0f + v) * ex2_approx(fmaf(v, kLog2e, kFarScale)) * kFarUnscale;
+    }
+}
+
 // The pre-activation is an fp32 sum of any size (it need not be a finite
-// fp16), so both arguments are clamped where the function has reached its
-// limit: |z| at 12 in GELU(z) = max(z, 0) - |z| Q(|z|), z at -100 in SiLU,
-// which gives the limits at the infinities.  NaN stays NaN (min.NaN, max.NaN).
+// fp16), so the arguments are clamped where the function has reached its
+// limit, which gives the limits at the infinities: |z| at 12 in
+// GELU(z) = max(z, 0) - |z| Q(|z|), z at 100 in SiLU's slope, and those of
+// far_value().  NaN stays NaN (min.NaN, max.NaN).
+template <bool FAR>
 __device__ __forceinline__ float act_value(int act, float z)
 {
     if (act == TF_ACT_SILU) {
-        const float v = max_nan(z, -100.0f);
-        return v * rcp_approx(1.0f + ex2_approx(-kLog2e * v));
+        if (FAR && z < far_from(TF_ACT_SILU)) return far_value<TF_ACT_SILU>(z);
+        return silu_f32(z);
     }
     if (act == TF_ACT_GELU) {
+        if (FAR && z < far_from(TF_ACT_GELU)) return far_value<TF_ACT_GELU>(z);
         const float t = min_nan(fabsf(z), TF_GELU_TCLAMP);
         return fmaf(-t, normal_tail(t), max_nan(z, 0.0f));
     }
@@ -96,14 +156,17 @@ __device__ __forceinline__ float act_value(int act, float z)
 
 // d act/dz.  SiLU: s + z s (1 - s), s = sigmoid(z).  GELU: Phi(z) + z phi(z),
 // that is h = Q(t) - t phi(t) for z < 0 and 1 - h for z >= 0, t = |z|.
+template <bool FAR>
 __device__ __forceinline__ float act_slope(int act, float z)
 {
     if (act == TF_ACT_SILU) {
-        const float v = min_nan(max_nan(z, -100.0f), 100.0f);
+        if (FAR && z < far_from(TF_ACT_SILU)) return far_slope<TF_ACT_SILU>(z);
+        const float v = min_nan(z, 100.0f);
         const float s = rcp_approx(1.0f + ex2_approx(-kLog2e * v));
         return fmaf(v * s, 1.0f - s, s);
     }
     if (act == TF_ACT_GELU) {
+        if (FAR && z < far_from(TF_ACT_GELU)) return far_slope<TF_ACT_GELU>(z);
         const float t = min_nan(fabsf(z), TF_GELU_TCLAMP);
         const float phi = 0.3989422804f * ex2_approx(-0.5f * kLog2e * t * t);
         const float h = fmaf(-t, phi, normal_tail(t));
@@ -128,32 +191,42 @@ __device__ __forceinline__ float2 normal_tail2(float2 t)
     return make_float2(ex2_approx(acc.x), ex2_approx(acc.y));
 }
 
-template <int ACT>
+// f2 of a pair, with f1 in place of the values far below zero
+template <int ACT, bool FAR, typename F1>
+__device__ __forceinline__ float2 with_far(float2 z, float2 f2, F1 f1)
+{
+    if (FAR && z.x < far_from(ACT)) f2.x = f1(z.x);
+    if (FAR && z.y < far_from(ACT)) f2.y = f1(z.y);
+    return f2;
+}
+
+template <int ACT, bool FAR>
 __device__ __forceinline__ float2 act_value2(float2 z)
 {
+    auto far = [](float v) { return far_value<ACT>(v); };
     if constexpr (ACT == TF_ACT_SILU) {
-        const float2 v = make_float2(max_nan(z.x, -100.0f), max_nan(z.y, -100.0f));
-        return silu_f32x2(v);
+        return with_far<ACT, FAR>(z, silu_f32x2(z), far);
     } else if constexpr (ACT == TF_ACT_GELU) {
         const float2 t = make_float2(min_nan(fabsf(z.x), TF_GELU_TCLAMP), min_nan(fabsf(z.y), TF_GELU_TCLAMP));
         const float2 r = make_float2(max_nan(z.x, 0.0f), max_nan(z.y, 0.0f));
-        return ffma2(make_float2(-t.x, -t.y), normal_tail2(t), r);
+        return with_far<ACT, FAR>(z, ffma2(make_float2(-t.x, -t.y), normal_tail2(t), r), far);
     } else {
         return z;
     }
 }
 
-template <int ACT>
+template <int ACT, bool FAR>
 __device__ __forceinline__ float2 act_slope2(float2 z)
 {
     if constexpr (ACT == TF_ACT_SILU) {
-        return make_float2(act_slope(TF_ACT_SILU, z.x), act_slope(TF_ACT_SILU, z.y));
+        return make_float2(act_slope<FAR>(TF_ACT_SILU, z.x), act_slope<FAR>(TF_ACT_SILU, z.y));
     } else if constexpr (ACT == TF_ACT_GELU) {
         const float2 t = make_float2(min_nan(fabsf(z.x), TF_GELU_TCLAMP), min_nan(fabsf(z.y), TF_GELU_TCLAMP));
         const float2 u = fmul2(fmul2(t, t), dup2(-0.5f * kLog2e));
         const float2 phi = make_float2(-0.3989422804f * ex2_approx(u.x), -0.3989422804f * ex2_approx(u.y));
         const float2 h = ffma2(t, phi, normal_tail2(t));
-        return make_float2(z.x >= 0.0f ? 1.0f - h.x : h.x, z.y >= 0.0f ? 1.0f - h.y : h.y);
+        const float2 f = make_float2(z.x >= 0.0f ? 1.0f - h.x : h.x, z.y >= 0.0f ? 1.0f - h.y : h.y);
+        return with_far<ACT, FAR>(z, f, [](float v) { return far_slope<ACT>(v); });
     } else {
         return dup2(1.0f);
     }

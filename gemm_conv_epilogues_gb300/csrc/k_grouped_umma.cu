@@ -301,7 +301,21 @@ __device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const uint32_t (
             store_box(dst, stride, box, n0, p.M, token, count);
         };
         if (p.pre) emit([](float2 z) { return z; }, p.pre, p.pre_stride);
-        emit([](float2 z) { return act_value2<ACT>(z); }, p.y, p.y_stride);
+        bool far = false;
+        if (ACT != TF_ACT_NONE) {
+            float least[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                least[j] = INFINITY;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) least[j] = fminf(least[j], fminf(pair(b, j).x, pair(b, j).y));
+                least[j] += bias[j];   // (adding keeps the order)
+            }
+            const float all = fminf(fminf(least[0], least[1]), fminf(least[2], least[3]));
+            far = __any_sync(0xffffffffu, all < far_from(ACT));
+        }
+        if (far) emit([](float2 z) { return act_value2<ACT, true>(z); }, p.y, p.y_stride);
+        else emit([](float2 z) { return act_value2<ACT, false>(z); }, p.y, p.y_stride);
     } else {
         __syncwarp();
         if (ACT != TF_ACT_NONE) {
@@ -312,19 +326,33 @@ __device__ __forceinline__ void finish_chunk(const UmmaArgs &p, const uint32_t (
             }
             __syncwarp();
         }
+        auto emit = [&](auto far) {
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t z[4], w[4];
-            if (ACT != TF_ACT_NONE) ldmatrix_x4_trans(at + b * 512, z);
+            for (int b = 0; b < 4; ++b) {
+                uint32_t z[4], w[4];
+                if (ACT != TF_ACT_NONE) ldmatrix_x4_trans(at + b * 512, z);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 v = pair(b, j);
-                if (ACT != TF_ACT_NONE) v = fmul2(v, act_slope2<ACT>(Half2Of<T>::unpack(z[j])));
-                w[j] = Half2Of<T>::pack(v.x, v.y);
+                for (int j = 0; j < 4; ++j) {
+                    float2 v = pair(b, j);
+                    if (ACT != TF_ACT_NONE) v = fmul2(v, act_slope2<ACT, decltype(far)::value>(Half2Of<T>::unpack(z[j])));
+                    w[j] = Half2Of<T>::pack(v.x, v.y);
+                }
+                __syncwarp();   // (a block's four rows are read before they are replaced)
+                stmatrix_x4_trans(at + b * 512, w[0], w[1], w[2], w[3]);
             }
-            __syncwarp();   // (a block's four rows are read before they are replaced)
-            stmatrix_x4_trans(at + b * 512, w[0], w[1], w[2], w[3]);
+        };
+        bool far = false;
+        if (ACT != TF_ACT_NONE) {
+            uint32_t least = Half2Of<T>::min2(pre[0].x, pre[0].y);
+            least = Half2Of<T>::min2(least, Half2Of<T>::min2(pre[0].z, pre[0].w));
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                least = Half2Of<T>::min2(least, Half2Of<T>::min2(Half2Of<T>::min2(pre[i].x, pre[i].y), Half2Of<T>::min2(pre[i].z, pre[i].w)));
+            const float2 f = Half2Of<T>::unpack(least);
+            far = __any_sync(0xffffffffu, fminf(f.x, f.y) < far_from(ACT));
         }
+        if (far) emit(std::true_type());
+        else emit(std::false_type());
         __syncwarp();
         store_box(p.y, p.y_stride, box, n0, p.M, token, count);
     }
