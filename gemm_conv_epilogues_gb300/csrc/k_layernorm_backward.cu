@@ -310,9 +310,12 @@ cudaError_t launch_typed(const NormGradArgs &a, cudaStream_t st)
         }
         auto unaligned = [&](auto v) {
             constexpr int VEC = decltype(v)::value;
-            if (cols_for(a.hidden, size, false, NT) == 16)
+            decltype(&norm_backward_kernel<T, 32, false, NT, 8, VEC>) none = nullptr;   // refused by launch_rows()
+            if (cols_for(a.hidden, size, false, NT) == 16) {
+                if (g.group != 512) return none;
                 return g.csize > 1 ? norm_backward_kernel<T, 512, true, NT, 16, VEC>
                                    : norm_backward_kernel<T, 512, false, NT, 16, VEC>;
+            }
             switch (g.group) {
             case 32: return norm_backward_kernel<T, 32, false, NT, 8, VEC>;
             case 64: return norm_backward_kernel<T, 64, false, NT, 8, VEC>;
@@ -324,7 +327,8 @@ cudaError_t launch_typed(const NormGradArgs &a, cudaStream_t st)
             case 448: return norm_backward_kernel<T, 448, false, NT, 8, VEC>;
             case 512: return norm_backward_kernel<T, 512, false, NT, 8, VEC>;
             case 640: return norm_backward_kernel<T, 640, false, NT, 8, VEC>;
-            default: return norm_backward_kernel<T, 768, false, NT, 8, VEC>;
+            case 768: return norm_backward_kernel<T, 768, false, NT, 8, VEC>;
+            default: return none;
             }
         };
         return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());

@@ -166,7 +166,8 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
         }
         auto unaligned = [&](auto v) {
             constexpr int VEC = decltype(v)::value;
-            if (g.csize > 1) return norm_forward_kernel<T, 512, 2, NT, 16, VEC>;
+            decltype(&norm_forward_kernel<T, 32, 0, NT, 8, VEC>) none = nullptr;   // refused by launch_rows()
+            if (g.csize > 1) return g.group == 512 ? norm_forward_kernel<T, 512, 2, NT, 16, VEC> : none;
             switch (g.group) {
             case 32: return norm_forward_kernel<T, 32, 0, NT, 8, VEC>;
             case 64: return norm_forward_kernel<T, 64, 0, NT, 8, VEC>;
@@ -180,7 +181,8 @@ cudaError_t launch_typed(const NormArgs &a, cudaStream_t st)
             case 640: return norm_forward_kernel<T, 640, 0, NT, 8, VEC>;
             case 768: return norm_forward_kernel<T, 768, 0, NT, 8, VEC>;
             case 896: return norm_forward_kernel<T, 896, 0, NT, 8, VEC>;
-            default: return norm_forward_kernel<T, 1024, 0, NT, 8, VEC>;
+            case 1024: return norm_forward_kernel<T, 1024, 0, NT, 8, VEC>;
+            default: return none;
             }
         };
         return vec == 2 ? unaligned(std::integral_constant<int, size == 2 ? 2 : 1>()) : unaligned(std::integral_constant<int, 1>());

@@ -581,10 +581,13 @@ cudaError_t resident_clusters(int *clusters, cudaLaunchConfig_t cfg, void (*kern
     return cudaSuccess;
 }
 
-// `units` CTAs or clusters, at most as many as run at once.
+// `units` CTAs or clusters, at most as many as run at once.  No kernel (null)
+// where none is built for the geometry's row groups: one built for others would
+// wait at its barriers for threads that are not there.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_rows(void (*kern)(KArgs...), const Geometry &g, int64_t &units, cudaStream_t st, Args... args)
 {
+    if (!kern) return cudaErrorNotSupported;
     const void *key = reinterpret_cast<const void *>(kern);
     cudaError_t e = raise_smem_limit(key);
     int allowed = 0;

@@ -64,3 +64,15 @@ def test_workspace_of_a_larger_batch_serves_a_smaller_one(native_lib, hidden, dt
     sizes = [b.tf_layernorm_backward_workspace_size(rows, hidden, dtype) for rows in range(6000)]
     assert sizes[0] == 0 and sizes[1] == 8 * hidden
     assert all(p <= q for p, q in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["bf16", "fp32"])
+@pytest.mark.parametrize("hidden", [8 * g - s for g in (32, 64, 128, 192, 256, 320, 384, 448, 512, 640, 768, 896, 1024)
+                                    for s in (1, 2)])
+def test_every_row_group_of_single_columns(b, hidden, name):
+    """Each number of threads that an unaligned row may take has its kernels, for single columns and for pairs."""
+    d = base._inputs(5, hidden, name, 0)
+    for extra in (False, True):
+        base._check_forward(b, d, name, res=extra)
+        base._check_backward(b, d, name, dres=extra)
