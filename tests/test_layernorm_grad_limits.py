@@ -66,6 +66,19 @@ def test_workspace_of_a_larger_batch_serves_a_smaller_one(native_lib, hidden, dt
     assert all(p <= q for p, q in zip(sizes, sizes[1:]))
 
 
+# rows of every number of slices from 2 to 16, whole 16-byte rows and odd ones
+CLUSTERS = [(2, 8192 * n - s) for n in range(2, 17) for s in (3000, 2991)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,hidden", CLUSTERS)
+def test_every_cluster_size(b, rows, hidden):
+    name = ("bf16", "fp16", "fp32")[hidden // 8192 % 3]
+    d = base._inputs(rows, hidden, name, 0)
+    base._check_forward(b, d, name, res=hidden % 2 == 0)
+    base._check_backward(b, d, name, dres=hidden % 2 == 0)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", ["bf16", "fp32"])
 @pytest.mark.parametrize("hidden", [8 * g - s for g in (32, 64, 128, 192, 256, 320, 384, 448, 512, 640, 768, 896, 1024)
