@@ -456,13 +456,6 @@ struct Exchange {
     }
 };
 
-__device__ __forceinline__ uint32_t cluster_nctarank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-
 // Shared set-up of both kernels: this thread's ring, with its barriers
 // initialised and the first rows on their way.
 template <typename T, int VEC, bool CLUSTER, int NT>
