@@ -27,13 +27,16 @@
 //
 // What bounds it, at 16384 rows in 16 uneven groups, bf16, weights 4096 x 2048
 // (275 GFLOP; 142.7 us at the tensor cores' burst rate, 157.5 at the sustained one):
-//   FORWARD with bias, GELU and the pre-activation saved: 174-178 us, 1.55-1.58
+//   FORWARD with bias, GELU and the pre-activation saved: 174-178 us (207 in a
+//     loop, under the power cap), 1.55-1.58
 //     PFLOP/s, tensor pipe 75% busy; 159 without the epilogue's stores, and the
 //     operands' loads alone take 146 (64 bytes per clock and SM from L2)
-//   DGRAD with GELU's slope: 174-177 us
-//   WGRAD with dbias: 246-250 us; the fp32 dw, 128 KB per tile, leaves the SM at
+//   DGRAD with GELU's slope: 174-178 us (206 in a loop)
+//   WGRAD with dbias: 251-256 us; the fp32 dw, 128 KB per tile, leaves the SM at
 //     about 13 bytes per clock whichever way it is stored (fragments, 128-byte
-//     rows or TMA), and the writes keep the loads waiting
+//     rows or TMA), and the writes keep the loads waiting.  For a group of more
+//     than 1024 rows (half of the rows here) the epilogue holds both accumulators
+//     until its last store, so that the next item's MMAs do not run under it
 //   16 rows in 16 groups of 2048 x 4096 (decoding): 39.5 us, 6.0 TB/s of weights
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the
 // device error word and winds down.

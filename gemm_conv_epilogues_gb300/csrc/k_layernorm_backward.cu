@@ -8,10 +8,11 @@
 // shared memory, one set per SM goes to the workspace, and a second, small
 // kernel adds those in order, so that equal calls give equal bits (no atomics).
 // Very many rows take several such launches.
-// Bound by HBM: 16384 x 4096 bf16 with dres in 90 us, 80 of them this pass at
-// 6.7 TB/s, the rest the second kernel; narrow rows by the issue slots (50001 x
-// 640 fp16: 45 us, 4.3 TB/s), odd widths by their element-wise columns (1999 x
-// 5003 fp32: 32 us).
+// Bound by HBM: 16384 x 4096 bf16 with dres in 89 us, 80 of them this pass at
+// 6.7 TB/s, the rest the second kernel; narrow rows by the chain of wait,
+// shuffles and store of the one row that each of an SM's sixteen warps has in
+// flight (50001 x 640 fp16: 45 us, 4.2 TB/s, 0.55 instructions per cycle and
+// scheduler), odd widths by their element-wise columns (1999 x 5003 fp32: 32 us).
 #include "norm_rows.cuh"
 
 namespace tf {

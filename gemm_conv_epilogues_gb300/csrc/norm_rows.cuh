@@ -276,7 +276,7 @@ __device__ __forceinline__ uint32_t narrow2(float2 f, __nv_bfloat16)
 
 // A thread's COLS columns of one row, in the storage type; zero past the slice:
 // the vectors (units) gt, gt + gsize, ... of VEC columns.  The arithmetic goes
-// over pairs (packed fp32): the kernels are close to the issue rate.
+// over pairs (packed fp32), which halves its instructions.
 template <typename T, int VEC, int COLS>
 struct Cols {
     static constexpr bool ALIGNED = kAligned<T, VEC>;
@@ -607,7 +607,7 @@ cudaError_t launch_rows(void (*kern)(KArgs...), const Geometry &g, int64_t &unit
     cfg.attrs = attr;
     cfg.numAttrs = g.csize > 1 ? 2 : 1;
     // Clusters of 3, 5, 6 or 7 CTAs wait for the previous kernel's end: placed while its CTAs leave one by one,
-    // fewer of them find room (3300 x 20480 bf16, backward: 200 us instead of 146).
+    // fewer of them find room (3300 x 20480 bf16, backward: 200 us instead of 148).
     if (g.csize & (g.csize - 1)) {
         cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
