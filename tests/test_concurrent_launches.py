@@ -1,6 +1,7 @@
 """Calls from several host threads: two threads that call one kernel at sizes
 that need different amounts of shared memory, neither of whose launches depends
-on the other's sizes, and the first calls of a new thread."""
+on the other's sizes, the first calls of a new thread, and graphs replayed over each
+other."""
 import sys
 import threading
 import time
@@ -137,3 +138,50 @@ def test_conv(b, variant, kernels):
         return lambda: b.tf_conv2d_bn_silu_variant(x, w, f[0], f[1], y, shape, getattr(b, variant), 0, check=False)
 
     assert _refused([call(*s) for s in kernels]) == [[], []]
+
+
+@pytest.mark.gpu
+def test_two_graphs_replayed_at_once(b):
+    """Captured gradient steps with workspaces of their own, replayed over each other on two streams: the bits of
+    eager calls."""
+    rows, hidden, N, K = 6000, 1024, 128, 256
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    jobs = []
+    for i in range(2):
+        g = torch.Generator("cuda").manual_seed(i)
+        rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+        job = dict(x=rnd(rows, hidden), dy=rnd(rows, hidden), dx=rnd(rows, hidden), stats=torch.ones(2, rows, device="cuda"),
+                   grads=torch.zeros(2, hidden, device="cuda"), a=rnd(rows, N), c=rnd(rows, K),
+                   dw=torch.zeros(1, N, K, device="cuda"), db=torch.zeros(1, N, device="cuda"))
+        job["sizes"] = (b.tf_layernorm_backward_workspace_size(rows, hidden, b.TF_BF16),
+                        b.tf_grouped_matmul_wgrad_workspace_size(rows, 1, N, K, b.TF_BF16))
+        assert all(job["sizes"])
+        job["ws"] = [torch.empty(s, dtype=torch.uint8, device="cuda") for s in job["sizes"]]
+        jobs.append(job)
+
+    def step(j):
+        b.tf_layernorm_backward(j["dy"], hidden, j["x"], hidden, None, j["stats"][0], j["stats"][1], None, 0, j["dx"], hidden,
+                                j["grads"][0], j["grads"][1], rows, hidden, 0, b.TF_BF16, j["ws"][0], j["sizes"][0])
+        b.tf_grouped_matmul_wgrad(j["a"], N, j["c"], K, off, j["dw"], j["db"], rows, 1, N, K, 0, b.TF_BF16, j["ws"][1],
+                                  j["sizes"][1])
+
+    outs = lambda j: [j["dx"], j["grads"], j["dw"], j["db"]]
+    for j in jobs:
+        step(j)
+        j["want"] = [t.clone() for t in outs(j)]
+    torch.cuda.synchronize()
+    for j in jobs:
+        j["graph"], j["stream"] = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(j["graph"]):
+            for _ in range(3):
+                step(j)
+        for t in outs(j):
+            t.fill_(7)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for j in jobs:
+            with torch.cuda.stream(j["stream"]):
+                j["graph"].replay()
+    torch.cuda.synchronize()
+    for j in jobs:
+        assert all(torch.equal(t, w) for t, w in zip(outs(j), j["want"]))
