@@ -20,9 +20,12 @@ TF_OK, TF_ERR_INVALID_ARG, TF_ERR_UNSUPPORTED, TF_ERR_CUDA, TF_ERR_TIMEOUT = 0, 
 TF_LN_AUTO, TF_LN_WARP, TF_LN_CTA, TF_LN_CLUSTER = -1, 0, 1, 2
 TF_FP16, TF_BF16, TF_FP32 = 0, 1, 2
 TF_ACT_NONE, TF_ACT_SILU, TF_ACT_GELU = 0, 1, 2
+TF_INT32, TF_INT64 = 0, 1
+TF_NO_INDEX = -(1 << 63)
 TF_DEVERR_PRODUCER_WAIT, TF_DEVERR_MMA_WAIT, TF_DEVERR_EPILOGUE_WAIT = 0x1, 0x2, 0x4
 TF_DEVERR_DRAIN_WAIT, TF_DEVERR_PROBE_WAIT, TF_DEVERR_EXCHANGE_WAIT = 0x8, 0x10, 0x20
 TF_DEVERR_PAIR_TMEM, TF_DEVERR_SMEM_ALIGN, TF_DEVERR_OFFSETS = 0x40, 0x80, 0x100
+TF_DEVERR_INDEX = 0x200
 
 
 class TfError(RuntimeError):
@@ -75,6 +78,9 @@ _SIGS = {
     "tf_grouped_matmul_wgrad_workspace_size": ([_i64, _i64, _i64, _i64, _i], _i64),
     "tf_grouped_matmul_wgrad": ([_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i, _i, _vp, _i64, _vp],
                                 _i),
+    "tf_embedding_forward": ([_vp, _i, _vp, _vp, _i64, _i64, _i64, _i64, _f, _i64, _i, _vp], _i),
+    "tf_embedding_backward_workspace_size": ([_i64, _i64, _i64], _i64),
+    "tf_embedding_backward": ([_vp, _i64, _vp, _i, _vp, _i64, _i64, _i64, _f, _i64, _i, _i, _vp, _i64, _vp], _i),
     "tf_set_wait_limit_ns": ([_u64], None),
     "tf_get_wait_limit_ns": ([], _u64),
     "tf_read_device_error": ([ctypes.POINTER(ctypes.c_uint32)], _i),
@@ -260,6 +266,25 @@ def tf_grouped_matmul_wgrad(dy, dy_stride, x, x_stride, offsets, dw, dbias, rows
     return _check(_lib.tf_grouped_matmul_wgrad(dy, dy_stride, x, x_stride, offsets, dw, dbias, rows, groups, N, K,
                                                accumulate, dtype, workspace, workspace_bytes, _stream(stream)),
                   "tf_grouped_matmul_wgrad", check)
+
+
+def tf_embedding_forward(tokens, index, table, y, y_stride, rows, vocab, hidden, scale, padding, dtype, stream=None,
+                         check=True):
+    tokens, table, y = _ptrs(tokens, table, y)
+    return _check(_lib.tf_embedding_forward(tokens, index, table, y, y_stride, rows, vocab, hidden, scale, padding, dtype,
+                                            _stream(stream)), "tf_embedding_forward", check)
+
+
+def tf_embedding_backward_workspace_size(rows, vocab, hidden) -> int:
+    return int(_lib.tf_embedding_backward_workspace_size(rows, vocab, hidden))
+
+
+def tf_embedding_backward(dy, dy_stride, tokens, index, dtable, rows, vocab, hidden, scale, padding, accumulate, dtype,
+                          workspace, workspace_bytes, stream=None, check=True):
+    dy, tokens, dtable, workspace = _ptrs(dy, tokens, dtable, workspace)
+    return _check(_lib.tf_embedding_backward(dy, dy_stride, tokens, index, dtable, rows, vocab, hidden, scale, padding,
+                                             accumulate, dtype, workspace, workspace_bytes, _stream(stream)),
+                  "tf_embedding_backward", check)
 
 
 def tf_unfused_conv2d(x, w_ohwi, t1, shape, variant=TF_CONV_AUTO, stream=None, check=True):

@@ -93,6 +93,12 @@ typedef enum {
 /* Storage types of the calls that take a `dtype`. */
 typedef enum { TF_FP16 = 0, TF_BF16 = 1, TF_FP32 = 2 } tf_dtype;
 
+/* Types of tokens and targets. */
+typedef enum { TF_INT32 = 0, TF_INT64 = 1 } tf_index;
+
+/* As a padding token or an ignored target: none. */
+#define TF_NO_INDEX INT64_MIN
+
 /* Activations of the grouped products' epilogues: none, z*sigmoid(z), and
  * z*Phi(z) with the normal distribution function (the erf form). */
 typedef enum { TF_ACT_NONE = 0, TF_ACT_SILU = 1, TF_ACT_GELU = 2 } tf_act;
@@ -357,6 +363,42 @@ int tf_grouped_matmul_wgrad(const void *dy, int64_t dy_stride, const void *x, in
                             float *dw, float *dbias, int64_t rows, int64_t groups, int64_t N, int64_t K, int accumulate,
                             int dtype, void *workspace, int64_t workspace_bytes, tf_stream_t stream);
 
+/* ---------------------------------------------------------------- embedding */
+
+/* y[i] = scale * table[tokens[i]], rounded once.
+ *   tokens : int32 or int64 (tf_index) [rows] on the device
+ *   table  : dtype (TF_FP16, TF_BF16 or TF_FP32) [vocab][hidden], contiguous
+ *   y      : dtype [rows][hidden], row i at i*y_stride elements
+ * A token equal to `padding` gives a row of zeros and reads no row of the table; it need
+ * not be a row's number (-1, say; TF_NO_INDEX: no such token).  Any other token
+ * outside [0, vocab) gives a row of zeros too and sets TF_DEVERR_INDEX in the
+ * device error word.  Any hidden to 131072, any stride (below 2^31) and the
+ * alignment of an element; rows and bases that are not multiples of 16 bytes
+ * take a slower kernel.  Up to 2^30 rows and 2^31 - 2 words; rows may be 0. */
+int tf_embedding_forward(const void *tokens, int index, const void *table, void *y, int64_t y_stride, int64_t rows,
+                         int64_t vocab, int64_t hidden, float scale, int64_t padding, int dtype, tf_stream_t stream);
+
+/* Bytes of device workspace tf_embedding_backward needs (two lists of the
+ * tokens, and fp32 partial sums).  It does not fall as rows grow.  Host only. */
+int64_t tf_embedding_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden);
+
+/* Gradient of the table: dtable[v] = scale * the sum of dy[i] over the rows i
+ * with tokens[i] = v, 0 for words that do not occur.  With `accumulate` != 0 the
+ * sums are added to what dtable holds, and the rows of other words are not
+ * touched (a head that shares its weights with the embedding leaves its own
+ * gradient there, tf_linear_cross_entropy_backward).
+ *   dy     : dtype [rows][hidden], row i at i*dy_stride elements
+ *   dtable : fp32 [vocab][hidden], contiguous
+ * Tokens, sizes and alignment as above: the rows of dy of padding and of tokens
+ * outside [0, vocab) are not read.  Sums are fp32, in an order that
+ * depends on the tokens and sizes alone: equal calls give equal bits.  The
+ * workspace (16-byte aligned) is in use until the stream reaches the end of the
+ * call; calls that may overlap need one each, captured graphs too.  rows may be
+ * 0: dtable becomes 0, or stays as it is with `accumulate`. */
+int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens, int index, float *dtable, int64_t rows,
+                          int64_t vocab, int64_t hidden, float scale, int64_t padding, int accumulate, int dtype,
+                          void *workspace, int64_t workspace_bytes, tf_stream_t stream);
+
 /* ---------------------------------------------------------------- unfused chains */
 
 /* The separate kernels that the fused calls replace, for the traffic and time
@@ -423,6 +465,9 @@ uint64_t tf_get_wait_limit_ns(void);
 
 #define TF_DEVERR_OFFSETS 0x100u      /* grouped products: the row offsets fall or leave [0, rows]
                                          (the call wrote nothing) */
+
+#define TF_DEVERR_INDEX 0x200u        /* embedding, cross entropy: a token or target outside [0, vocab) that
+                                         is not the padding (its row counts as padding) */
 
 /* Synchronises the current device, copies the device error word of the
  * current device into *word (may be NULL), clears it, and returns TF_OK if it
