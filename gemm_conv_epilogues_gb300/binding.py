@@ -81,6 +81,12 @@ _SIGS = {
     "tf_embedding_forward": ([_vp, _i, _vp, _vp, _i64, _i64, _i64, _i64, _f, _i64, _i, _vp], _i),
     "tf_embedding_backward_workspace_size": ([_i64, _i64, _i64], _i64),
     "tf_embedding_backward": ([_vp, _i64, _vp, _i, _vp, _i64, _i64, _i64, _f, _i64, _i, _i, _vp, _i64, _vp], _i),
+    "tf_linear_cross_entropy_forward_workspace_size": ([_i64, _i64, _i64, _i], _i64),
+    "tf_linear_cross_entropy_forward": ([_vp, _i64, _vp, _vp, _i, _vp, _vp, _i64, _i64, _i64, _f, _i64, _i, _vp, _i64, _vp],
+                                        _i),
+    "tf_linear_cross_entropy_backward_workspace_size": ([_i64, _i64, _i64, _i], _i64),
+    "tf_linear_cross_entropy_backward": ([_vp, _i64, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _f, _i64,
+                                          _i, _i, _i, _vp, _i64, _vp], _i),
     "tf_set_wait_limit_ns": ([_u64], None),
     "tf_get_wait_limit_ns": ([], _u64),
     "tf_read_device_error": ([ctypes.POINTER(ctypes.c_uint32)], _i),
@@ -285,6 +291,32 @@ def tf_embedding_backward(dy, dy_stride, tokens, index, dtable, rows, vocab, hid
     return _check(_lib.tf_embedding_backward(dy, dy_stride, tokens, index, dtable, rows, vocab, hidden, scale, padding,
                                              accumulate, dtype, workspace, workspace_bytes, _stream(stream)),
                   "tf_embedding_backward", check)
+
+
+def tf_linear_cross_entropy_forward_workspace_size(rows, vocab, hidden, dtype) -> int:
+    return int(_lib.tf_linear_cross_entropy_forward_workspace_size(rows, vocab, hidden, dtype))
+
+
+def tf_linear_cross_entropy_forward(x, x_stride, w, targets, index, loss, lse, rows, vocab, hidden, scale, ignore, dtype,
+                                    workspace, workspace_bytes, stream=None, check=True):
+    x, w, targets, loss, lse, workspace = _ptrs(x, w, targets, loss, lse, workspace)
+    return _check(_lib.tf_linear_cross_entropy_forward(x, x_stride, w, targets, index, loss, lse, rows, vocab, hidden,
+                                                       scale, ignore, dtype, workspace, workspace_bytes, _stream(stream)),
+                  "tf_linear_cross_entropy_forward", check)
+
+
+def tf_linear_cross_entropy_backward_workspace_size(rows, vocab, hidden, dtype) -> int:
+    return int(_lib.tf_linear_cross_entropy_backward_workspace_size(rows, vocab, hidden, dtype))
+
+
+def tf_linear_cross_entropy_backward(x, x_stride, w, targets, index, lse, dloss, dlse, dx, dx_stride, dw, rows, vocab,
+                                     hidden, scale, ignore, accumulate, dw_dtype, dtype, workspace, workspace_bytes,
+                                     stream=None, check=True):
+    x, w, targets, lse, dloss, dlse, dx, dw, workspace = _ptrs(x, w, targets, lse, dloss, dlse, dx, dw, workspace)
+    return _check(_lib.tf_linear_cross_entropy_backward(x, x_stride, w, targets, index, lse, dloss, dlse, dx, dx_stride, dw,
+                                                        rows, vocab, hidden, scale, ignore, accumulate, dw_dtype, dtype,
+                                                        workspace, workspace_bytes, _stream(stream)),
+                  "tf_linear_cross_entropy_backward", check)
 
 
 def tf_unfused_conv2d(x, w_ohwi, t1, shape, variant=TF_CONV_AUTO, stream=None, check=True):

@@ -109,7 +109,8 @@ cudaError_t embed_typed(const EmbedArgs &a, cudaStream_t st)
     };
     constexpr int FULL = 16 / (int)sizeof(T);
     if (fits(FULL)) return launch_embed<T, FULL>(a, st);
-    if (sizeof(T) == 2 && fits(2)) return launch_embed<T, 2>(a, st);
+    if constexpr (sizeof(T) == 2)
+        if (fits(2)) return launch_embed<T, 2>(a, st);
     return launch_embed<T, 1>(a, st);
 }
 
@@ -429,7 +430,8 @@ cudaError_t sums_typed(const EmbedArgs &a, const SumArgs &s, cudaStream_t st)
     };
     constexpr int FULL = 16 / (int)sizeof(T);
     if (fits(FULL)) return launch_sums<T, FULL>(a, s, st);
-    if (sizeof(T) == 2 && fits(2)) return launch_sums<T, 2>(a, s, st);
+    if constexpr (sizeof(T) == 2)
+        if (fits(2)) return launch_sums<T, 2>(a, s, st);
     return launch_sums<T, 1>(a, s, st);
 }
 

@@ -1,0 +1,782 @@
+// The products of the cross entropy over a vocabulary on the 5th-generation
+// tensor cores.  Logits never reach memory:
+//   STATS    D[t][v] = sum_h x[t][h] w[v][h]; the epilogue keeps, per row and
+//            stretch of the tile's words, the largest sum and the sum of exponentials
+//   DLOGITS  the same sums again; the epilogue turns them into the gradients of
+//            the logits, dl = e^(l - lse) ca - [v = target] cb, in the operands' type,
+//            for one piece of the vocabulary
+//   GRADS    of that piece, in one launch:
+//              DX[t][h] = sum_v dl[t][v] w[v][h]   A = dl (K-major), B = w (N-major)
+//              DW[v][h] = sum_t dl[t][v] x[t][h]   A = dl (M-major), B = x (N-major)
+//
+// Rows (DW: words) are the MMA's M side, so that a thread of the epilogue has a row
+// of the tile to itself and reduces over the vocabulary in its registers.
+//
+// Persistent kernel, one CTA (CG = 1) or CTA pair (CG = 2, cta_group::2) per SM
+// (pair).  A pair takes tiles of 512 x 256: two 256-row MMAs share a K step's B
+// tile, which takes 48 KB of operands per CTA for 1024 cycles of MMAs (tiles of
+// 256 x 256 would take 64 bytes per clock, all that an SM gets from L2).  The two
+// accumulators fill the TMEM; the epilogue empties the first before the second, and
+// the next tile's MMAs into the first begin meanwhile, on as many K steps as the ring
+// holds.  Warps:
+//   0     TMA producer of a ring of K steps (64 deep, 128-byte swizzle)
+//   1     TMEM allocator and MMA issuer
+//   4-11  epilogue
+// Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
+// error word and winds down.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "grouped.cuh"
+#include "lm_internal.h"
+#include "ptx_sm100.cuh"
+#include "tensor_maps.h"
+
+namespace tf {
+namespace {
+
+using grouped::BK;
+using grouped::desc_low;
+using grouped::desc_of;
+using grouped::desc_step;
+using grouped::elect_one;
+using grouped::Half2Of;
+using grouped::idesc;
+using grouped::kChunkBytes;
+using grouped::UMMA_K;
+
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
+constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
+constexpr int kTileN = 256;
+constexpr int kABytes = 128 * BK * 2;               // 128 rows of a K step
+constexpr int kStageBytes = 48 * 1024;              // pair: 2 x 128 rows of A and 128 of B; single CTA: 128 and 256
+constexpr int kBoxBytes = 32 * 128;                 // an epilogue warp's box: 32 rows of 128 bytes
+constexpr int kOffBox = kStages * kStageBytes, kOffBar = kOffBox + kEpiWarps * kBoxBytes;
+constexpr int kNumBars = 2 * kStages + 5;
+constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
+constexpr int kNarrowRows = 256;                    // up to here tiles of 128 rows on single CTAs
+constexpr uint32_t kTmemCols = 512;
+constexpr int kEpilogueCost = 6;                    // an epilogue's time in K steps, for sharing out the tiles
+
+struct VocabArgs {
+    LceProduct a;
+    uint32_t *err;
+    uint64_t wait_ns;
+    int bn;            // columns per tile
+    int a_box;         // rows that a load of A brings (STATS, DLOGITS)
+    int group;         // STATS, DLOGITS: row tiles that share a sweep over the vocabulary
+    int split_steps;   // DX: K steps per split
+};
+
+// A tile: rows [m0, +128*CG*CG), columns [n0, +bn), K steps [k0, k0 + nk).
+struct Tile {
+    int kind, m0, n0, k0, nk, slot;
+};
+enum { TILE_LOGITS = 0, TILE_DX = 1, TILE_DW = 2 };
+
+__device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Which tiles this CTA or pair takes, the j-th of them by at(); the same in all of its roles.
+template <int MODE, int CG>
+struct Share {
+    static constexpr int ROWS = 128 * CG * CG;
+    int cid, ncl, tiles;
+    int row_tiles, col_tiles;      // STATS, DLOGITS
+    int nd, nw, rest, lead;        // GRADS: tiles of either kind; pairs with a DX tile more; DW tiles that the others take first
+    int dw_steps, dx_steps;
+
+    __device__ __forceinline__ void init(const VocabArgs &p, int count, int cid_, int ncl_)
+    {
+        cid = cid_;
+        ncl = ncl_;
+        if constexpr (MODE != LCE_GRADS) {
+            row_tiles = div_up(count, ROWS);
+            col_tiles = div_up(p.a.words, p.bn);
+            tiles = row_tiles * col_tiles;
+        } else {
+            // DX tiles in turn; the pairs that have one less take DW tiles for its
+            // time before the rest of those goes round
+            row_tiles = div_up(count, ROWS);
+            col_tiles = div_up(p.a.hidden, p.bn);
+            dw_steps = div_up(count, BK);
+            dx_steps = div_up(p.a.words, BK);
+            nd = p.a.dx ? p.a.splits * row_tiles * col_tiles : 0;
+            nw = p.a.dw ? div_up(p.a.words, ROWS) * col_tiles : 0;
+            rest = nd % ncl;
+            lead = 0;
+            if (rest > 0) {
+                const int cw = dw_steps + kEpilogueCost;
+                lead = min((p.split_steps + kEpilogueCost + cw / 2) / cw, div_up(nw, ncl - rest));
+            }
+        }
+    }
+
+    __device__ __forceinline__ bool at(const VocabArgs &p, int j, Tile *t) const
+    {
+        if constexpr (MODE != LCE_GRADS) {
+            const int i = cid + j * ncl;
+            if (i >= tiles) return false;
+            const int g = i / (p.group * col_tiles), r = i - g * p.group * col_tiles;
+            const int size = min(p.group, row_tiles - g * p.group);
+            const int v = r / size;
+            *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v};
+            return true;
+        } else {
+            const int own = nd / ncl + (cid < rest ? 1 : 0);
+            if (j < own) {
+                const int i = cid + j * ncl, s = i / (row_tiles * col_tiles), r = i - s * row_tiles * col_tiles;
+                const int k0 = s * p.split_steps;
+                *t = {TILE_DX, r / col_tiles * ROWS, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s};
+                return true;
+            }
+            j -= own;
+            const int mine = rest > 0 && cid >= rest ? lead : 0;
+            const int i = j < mine ? j * (ncl - rest) + cid - rest
+                                   : (rest > 0 ? lead * (ncl - rest) : 0) + (j - mine) * ncl + (cid - rest + ncl) % ncl;
+            if (i >= nw) return false;
+            *t = {TILE_DW, i / col_tiles * ROWS, i % col_tiles * p.bn, 0, dw_steps, 0};
+            return true;
+        }
+    }
+};
+
+// Arrives once on the mbarrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void commit_both(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     ptx::smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// The box: row `lane`'s piece i of 16 bytes on the way in, row 4i + lane/8's piece
+// lane%8 on the way out; the pieces are swizzled so that neither side meets a bank twice.
+__device__ __forceinline__ void box_put(uint8_t *box, int lane, int i, uint4 v)
+{
+    *reinterpret_cast<uint4 *>(box + lane * 128 + ((i ^ (lane & 7)) * 16)) = v;
+}
+__device__ __forceinline__ uint4 box_get(const uint8_t *box, int row, int piece)
+{
+    return *reinterpret_cast<const uint4 *>(box + row * 128 + ((piece ^ (row & 7)) * 16));
+}
+
+// ---------------------------------------------------------------- epilogues
+
+// The columns [n0 + c, +32) of one row join its running maximum and sum of exponentials.
+__device__ __forceinline__ void join_stats(const uint32_t (&r)[32], int left, float factor, float &top, float &sum)
+{
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = j < left ? __uint_as_float(r[j]) : -INFINITY;
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 4; j < 32; ++j) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    const float most = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+    const float base = most == -INFINITY ? 0.0f : most;
+    // the difference before the factor: a sure word's exponential is one, however large its logit
+    const float2 base2 = make_float2(base, base), factor2 = make_float2(factor, factor);
+    float s[4] = {sum * ex2_approx((top - base) * factor), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 d = fmul2(fsub2(make_float2(v[j], v[j + 1]), base2), factor2);
+        s[j & 2] += ex2_approx(d.x);
+        s[(j & 2) + 1] += ex2_approx(d.y);
+    }
+    sum = (s[0] + s[1]) + (s[2] + s[3]);
+    top = most;
+}
+
+// r[i] of a register array, i the same for no two lanes in general.
+__device__ __forceinline__ float pick(const uint32_t (&r)[32], int i)
+{
+    uint32_t v = r[0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) v = j == i ? r[j] : v;
+    return __uint_as_float(v);
+}
+
+template <int MODE, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    vocab_umma_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_x, const __grid_constant__ VocabArgs p)
+{
+    constexpr bool PAIR = CG == 2;
+    constexpr int SUB = CG;                       // M side: accumulators per tile
+    constexpr int SUB_ROWS = 128 * CG;            // rows of an accumulator, over the pair
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *empty = full + kStages;
+    uint64_t *tfull = empty + kStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = PAIR ? (int)ptx::cluster_ctarank() : 0;
+    const bool leader = crank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&tfull[i], 1);
+            ptx::mbar_init(&tempty[i], CG * kEpiWarps);   // one lane per epilogue warp of either CTA
+        }
+        ptx::mbar_init(drain, 1);
+        ptx::mbar_init_fence();
+        ptx::prefetch_tensormap(&map_a);
+        ptx::prefetch_tensormap(&map_w);
+        ptx::prefetch_tensormap(&map_x);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(tmem_slot, kTmemCols);
+            ptx::tmem_relinquish();
+        }
+    }
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    ptx::tc_fence_before();
+    cta_sync();
+    ptx::tc_fence_after();
+    if constexpr (PAIR) ptx::cluster_sync();   // the peer's barriers exist
+    const uint32_t tmem_base = *tmem_slot;
+    bool sound = true;
+    if ((ptx::smem_u32(smem) & 1023u) != 0) {
+        sound = false;
+        if (threadIdx.x == 0) atomicOr(p.err, TF_DEVERR_SMEM_ALIGN);
+    }
+    if constexpr (PAIR) {
+        if (ptx::ld_shared_cluster_u32(ptx::mapa_shared(tmem_slot, (uint32_t)crank ^ 1u)) != tmem_base) {
+            sound = false;
+            if (threadIdx.x == 0) atomicOr(p.err, TF_DEVERR_PAIR_TMEM);
+        }
+    }
+    const int count = *p.a.count;
+    Share<MODE, CG> share;
+    share.init(p, count, (int)blockIdx.x / CG, (int)gridDim.x / CG);
+
+    if (!sound) {
+        // nothing has been issued
+    } else if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        int stage = 0;
+        uint32_t phase = 0, issued = 0, last_phase = 0;
+        bool ok = true;
+        const bool issuer = elect_one();
+        const int half = p.bn / CG;   // columns of B that this CTA loads
+        Tile t;
+        for (int j = 0; ok && share.at(p, j, &t); ++j) {
+            for (int kb = 0; kb < t.nk; ++kb) {
+                const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                if (issuer) {
+                    uint64_t *bar = &full[stage];
+                    uint8_t *a_dst = smem + stage * kStageBytes, *b_dst = a_dst + SUB * kABytes;
+                    const int k = (t.k0 + kb) * BK, row = t.m0 + crank * 128;
+                    const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, 0) : 0u;
+                    auto load = [&](void *dst, const CUtensorMap *map, int c0, int c1) {
+                        if constexpr (PAIR) ptx::tma_load_2d_pair(dst, map, bar_cl, c0, c1);
+                        else ptx::tma_load_2d(dst, map, bar, c0, c1);
+                    };
+                    if constexpr (MODE != LCE_GRADS) {
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (SUB * p.a_box + half) * (BK * 2)));
+#pragma unroll
+                        for (int s = 0; s < SUB; ++s) load(a_dst + s * kABytes, &map_a, k, row + s * SUB_ROWS);
+                        load(b_dst, &map_w, k, t.n0 + crank * half);
+                    } else {
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (SUB * 128 + half) * (BK * 2)));
+                        const CUtensorMap *map_b = t.kind == TILE_DX ? &map_w : &map_x;
+#pragma unroll
+                        for (int i = 0; i < 2 * SUB; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
+                            const int m = row + (i >> 1) * SUB_ROWS + (i & 1) * 64;
+                            if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
+                            else load(a_dst + i * kChunkBytes, &map_a, m, k);
+                        }
+                        for (int i = 0; i < half / 64; ++i) load(b_dst + i * kChunkBytes, map_b, t.n0 + crank * half + 64 * i, k);
+                    }
+                }
+                __syncwarp();
+                issued |= 1u << stage;
+                last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
+        // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
+        for (int s = 0; s < kStages; ++s)
+            if (leader && ((issued >> s) & 1u))
+                if (!ptx::mbar_wait<PAIR>(&full[s], (last_phase >> s) & 1u, p.wait_ns) && lane == 0)
+                    atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (leader) {
+            int stage = 0, b = 0;
+            uint32_t phase = 0, taken = 0;   // taken: parity of the uses of either accumulator
+            bool ok = true;
+            const bool issuer = elect_one(), bf16 = p.a.dtype == TF_BF16;
+            const uint32_t base = ptx::smem_u32(smem);
+            Tile t;
+            for (int j = 0; ok && share.at(p, j, &t); ++j) {
+                if (t.nk == 0) continue;
+                const bool a_mn = t.kind == TILE_DW, b_mn = MODE == LCE_GRADS;
+                const uint32_t id = idesc(128 * CG, p.bn, bf16, a_mn, b_mn);
+                const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
+                const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + SUB * kABytes, !b_mn);
+                const int c0 = SUB == 2 ? 0 : b;
+                auto issue = [&](int at, int sub, uint32_t acc) {   // one K step into one accumulator
+                    const uint32_t a = a_low + (uint32_t)at * (kStageBytes >> 4) + (uint32_t)sub * (kABytes >> 4);
+                    const uint32_t bb = b_low + (uint32_t)at * (kStageBytes >> 4);
+                    const uint32_t d = tmem_base + (uint32_t)((SUB == 2 ? sub : c0) * kTileN);
+                    if (issuer) {
+#pragma unroll
+                        for (int k = 0; k < BK / UMMA_K; ++k) {
+                            if constexpr (PAIR)
+                                ptx::umma_bf16_pair(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, k == 0 ? acc : 1u);
+                            else
+                                ptx::umma_bf16(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, k == 0 ? acc : 1u);
+                        }
+                    }
+                    __syncwarp();
+                };
+                auto commit = [&](uint64_t *bar) {
+                    if (issuer) {
+                        if constexpr (PAIR) commit_both(bar);
+                        else ptx::umma_commit(bar);
+                    }
+                    __syncwarp();
+                };
+                bool got = ptx::mbar_wait<PAIR>(&tempty[c0], ((taken >> c0) & 1u) ^ 1u, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                bool second = SUB == 1;   // the second accumulator is free
+                int late = 0;             // K steps that it has yet to take
+                for (int kb = 0; kb < t.nk; ++kb) {
+                    got = ptx::mbar_wait(&full[stage], phase, p.wait_ns);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    issue(stage, 0, kb > 0 ? 1u : 0u);
+                    const bool last = kb == t.nk - 1;
+                    if (last) commit(&tfull[c0]);
+                    if constexpr (SUB == 2) {
+                        if (!second) {
+                            const uint32_t par = ((taken >> 1) & 1u) ^ 1u;
+                            if (last || late == kStages - 1) {
+                                got = ptx::mbar_wait<PAIR>(&tempty[1], par, p.wait_ns);
+                                if (!__all_sync(0xffffffffu, got)) {
+                                    ok = false;
+                                    break;
+                                }
+                                second = true;
+                            } else {
+                                second = __all_sync(0xffffffffu, mbar_test(&tempty[1], par));
+                            }
+                            if (second) ptx::tc_fence_after();
+                        }
+                        if (second) {
+                            for (; late >= 0; --late) {
+                                const int at = stage >= late ? stage - late : stage - late + kStages;
+                                issue(at, 1, kb - late > 0 ? 1u : 0u);
+                                commit(&empty[at]);
+                            }
+                            late = 0;
+                            if (last) commit(&tfull[1]);
+                        } else {
+                            ++late;
+                        }
+                    } else {
+                        commit(&empty[stage]);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (SUB == 2) {
+                    taken ^= 3u;
+                } else {
+                    taken ^= 1u << c0;
+                    b ^= 1;
+                }
+            }
+            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+            if (issuer) {   // (the lane that issued the MMAs)
+                if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
+                else ptx::umma_commit(drain);
+            }
+            __syncwarp();
+            if (!ptx::mbar_wait(drain, 0, p.wait_ns) && lane == 0) atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
+        }
+    } else if (warp >= kFirstEpiWarp) {
+        // ------------------------------------------------------------ epilogue
+        // Warp w reads TMEM lanes 32*(w%4) .. +31, one row per lane; h tells its columns.
+        const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
+        uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
+        const bool bf16 = p.a.dtype == TF_BF16;
+        int b = 0;
+        uint32_t seen = 0;   // parity of the results of either accumulator
+        bool ok = true;
+        Tile t;
+        auto pack = [&](float x, float y) { return bf16 ? Half2Of<__nv_bfloat16>::pack(x, y) : Half2Of<__half>::pack(x, y); };
+        for (int j = 0; ok && share.at(p, j, &t); ++j) {
+            for (int sub = 0; sub < SUB; ++sub) {
+                const int acc = SUB == 2 ? sub : b;
+                const int row0 = t.m0 + sub * SUB_ROWS + crank * 128 + q * 32, row = row0 + lane;
+                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN);
+                int target = -1;
+                float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
+                if constexpr (MODE != LCE_GRADS) {
+                    if (row < count) {
+                        target = __ldg(p.a.target + row) - p.a.v0 - t.n0;   // its column of the tile
+                        if constexpr (MODE == LCE_DLOGITS) {
+                            l2 = __ldg(p.a.l2 + row);
+                            ca = __ldg(p.a.ca + row);
+                            cb = __ldg(p.a.cb + row);
+                        }
+                    }
+                }
+                if (t.nk > 0) {
+                    const bool got = ptx::mbar_wait(&tfull[acc], (seen >> acc) & 1u, p.wait_ns);
+                    if (!__all_sync(0xffffffffu, got)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                }
+                if constexpr (MODE == LCE_STATS) {
+                    const int width = min(p.bn, p.a.words - t.n0), mid = (p.bn / 2 + 31) & ~31;
+                    float top = -INFINITY, sum = 0.0f;
+                    const int end = min(width, h ? p.bn : mid);
+#pragma unroll 1
+                    for (int c = h * mid; c < end; c += 32) {
+                        uint32_t r[32];
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
+                        ptx::tmem_ld_wait();
+                        const int left = end - c;
+                        if (left >= 32) join_stats(r, 32, p.a.factor, top, sum);
+                        else join_stats(r, left, p.a.factor, top, sum);
+                        const int at = target - c;
+                        const bool hit = at >= 0 && at < min(32, left);
+                        if (__any_sync(0xffffffffu, hit)) {
+                            const float v = pick(r, at);
+                            if (hit) p.a.at_target[row] = v;
+                        }
+                    }
+                    if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
+                } else if constexpr (MODE == LCE_DLOGITS) {
+                    const int width = min(p.bn, p.a.words - t.n0);
+#pragma unroll 1
+                    for (int c = h * 64; c < width; c += 128) {
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            uint32_t r[32];
+                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 32 * part), r);
+                            ptx::tmem_ld_wait();
+                            const int at = target - c - 32 * part, left = width - c - 32 * part;
+                            const bool whole = row < count && left >= 32;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float v = ex2_approx(fmaf(__uint_as_float(r[i]), p.a.factor, -l2)) * ca;
+                                r[i] = whole || (row < count && i < left) ? __float_as_uint(v) : 0u;
+                            }
+                            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i == at && i < left) r[i] = __float_as_uint(__uint_as_float(r[i]) - cb);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    w[k] = pack(__uint_as_float(r[8 * i + 2 * k]), __uint_as_float(r[8 * i + 2 * k + 1]));
+                                box_put(box, lane, part * 4 + i, make_uint4(w[0], w[1], w[2], w[3]));
+                            }
+                        }
+                        __syncwarp();
+                        const int piece = lane & 7, col = t.n0 + c + 8 * piece;
+                        uint16_t *out = static_cast<uint16_t *>(p.a.dl) + col;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 4 * i + (lane >> 3);
+                            if (row0 + r < p.a.rows && c + 8 * piece < p.bn && col < p.a.dl_pitch)
+                                *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + r) * p.a.dl_pitch) = box_get(box, r, piece);
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    const bool dx = t.kind == TILE_DX;
+                    const int width = min(p.bn, p.a.hidden - t.n0);
+                    const float mult = p.a.factor * (p.a.unit ? __ldg(p.a.unit + 1) : 1.0f);
+                    const int rows = dx ? count : p.a.words;   // of this tile's M side
+                    const bool wide = dx || p.a.dw_f32;        // 32-bit results
+                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                    const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
+                    uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
+                                      : static_cast<uint8_t *>(p.a.dw);
+                    // rows that 16-byte words make up
+                    const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
+                    const int cols = wide ? 32 : 64, per = wide ? 4 : 8, piece = lane & 7;
+                    if (t.nk > 0 || !add) {
+#pragma unroll 1
+                        for (int c = h * cols; c < width && row0 < rows; c += 2 * cols) {
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                if (part == 1 && wide) break;
+                                uint32_t r[32];
+                                if (t.nk > 0) {
+                                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 32 * part), r);
+                                    ptx::tmem_ld_wait();
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) r[i] = 0u;
+                                }
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * mult);
+                                if (wide) {
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        box_put(box, lane, i, make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
+                                } else {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        uint32_t w[4];
+#pragma unroll
+                                        for (int k = 0; k < 4; ++k)
+                                            w[k] = pack(__uint_as_float(r[8 * i + 2 * k]), __uint_as_float(r[8 * i + 2 * k + 1]));
+                                        box_put(box, lane, part * 4 + i, make_uint4(w[0], w[1], w[2], w[3]));
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                            const int col0 = t.n0 + c;
+                            if (words) {
+                                const int col = col0 + per * piece;
+                                uint8_t *dst = out + (int64_t)col * (wide ? 4 : 2);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int r = 4 * i + (lane >> 3);
+                                    if (row0 + r >= rows || col >= pitch) continue;
+                                    uint4 *at = reinterpret_cast<uint4 *>(dst + (int64_t)(row0 + r) * pitch * (wide ? 4 : 2));
+                                    uint4 v = box_get(box, r, piece);
+                                    if (add) {
+                                        const uint4 o = *at;
+                                        v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
+                                        v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
+                                        v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
+                                        v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
+                                    }
+                                    *at = v;
+                                }
+                            } else {
+                                for (int r = 0; r < min(32, rows - row0); ++r) {
+                                    for (int e = lane; e < cols && col0 + e < pitch; e += 32) {
+                                        const int64_t at = (int64_t)(row0 + r) * pitch + col0 + e;
+                                        const uint8_t *src = box + r * 128 + (((e / per) ^ (r & 7)) * 16);
+                                        if (wide) {
+                                            const float v = reinterpret_cast<const float *>(src)[e % per];
+                                            float *dst = reinterpret_cast<float *>(out) + at;
+                                            *dst = add ? *dst + v : v;
+                                        } else {
+                                            reinterpret_cast<uint16_t *>(out)[at] = reinterpret_cast<const uint16_t *>(src)[e % per];
+                                        }
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
+                if (t.nk > 0) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
+                        else ptx::mbar_arrive(&tempty[acc]);
+                    }
+                    seen ^= 1u << acc;
+                    if (SUB == 1) b ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
+    }
+
+    ptx::tc_fence_before();
+    cta_sync();
+    if constexpr (PAIR) ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
+        else ptx::tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+// CTAs (or pairs) that can be resident at once, by device; the kernel's
+// shared-memory limit is raised on the way.
+template <int MODE, int CG>
+cudaError_t resident(int *units)
+{
+    static std::mutex mu;
+    static int known[64];
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
+    if (e != cudaSuccess || d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!known[d]) {
+        auto kern = vocab_umma_kernel<MODE, CG>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        int n = sm_count();
+        if (CG == 2) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(n / 2 * 2));
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kSmemBytes;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess) return e;
+            if (n < 1) return cudaErrorNotSupported;
+        }
+        known[d] = n;
+    }
+    *units = known[d];
+    return cudaSuccess;
+}
+
+template <int MODE, int CG>
+cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
+{
+    constexpr int ROWS = 128 * CG * CG;
+    VocabArgs p = {};
+    p.a = a;
+    p.err = device_error_word();
+    p.wait_ns = wait_limit_ns();
+    if (!p.err) return cudaErrorInitializationError;
+    const int row_tiles = (a.rows + ROWS - 1) / ROWS;
+    int64_t tiles;
+    if (MODE == LCE_GRADS) {
+        const int nh = (a.hidden + kTileN - 1) / kTileN, step = 64 * CG;   // equal widths, in whole boxes of either CTA
+        p.bn = ((a.hidden + nh - 1) / nh + step - 1) / step * step;
+        p.split_steps = ((a.words + BK - 1) / BK + a.splits - 1) / a.splits;
+        const int64_t cols = (a.hidden + p.bn - 1) / p.bn;
+        tiles = ((a.dx ? (int64_t)a.splits * row_tiles : 0) + (a.dw ? (a.words + ROWS - 1) / ROWS : 0)) * cols;
+    } else {
+        p.bn = lce_word_tile(a.rows, a.words);
+        p.a_box = CG == 2 || a.rows >= 128 ? 128 : (a.rows + 7) / 8 * 8;
+        // rows whose tiles of x stay in L2 while the vocabulary goes past
+        const int64_t fit = ((int64_t)32 << 20) / ((int64_t)ROWS * a.x_pitch * 2);
+        p.group = fit < 1 ? 1 : fit > row_tiles ? row_tiles : (int)fit;
+        if (p.group < 1) p.group = 1;
+        tiles = (int64_t)row_tiles * ((a.words + p.bn - 1) / p.bn);
+    }
+    if (tiles == 0) return cudaSuccess;
+    if (tiles >= (int64_t)1 << 31) return cudaErrorNotSupported;
+
+    cudaError_t e = bind_context();
+    if (e != cudaSuccess) return e;
+    const CUtensorMapDataType type = a.dtype == TF_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap ma, mw, mx;
+    const int rows = a.rows > 0 ? a.rows : 1;   // (dw without rows: nothing is loaded)
+    bool ok;
+    if (MODE == LCE_GRADS) {
+        ok = encode_rows(&ma, type, a.dl, rows, a.words, a.dl_pitch, 64, 64) &&
+             encode_rows(&mw, type, a.w, a.words, a.hidden, a.w_pitch, 64, 64) &&
+             encode_rows(&mx, type, a.x, rows, a.hidden, a.x_pitch, 64, 64);
+    } else {
+        ok = encode_rows(&ma, type, a.x, rows, a.hidden, a.x_pitch, BK, p.a_box) &&
+             encode_rows(&mw, type, a.w, a.words, a.hidden, a.w_pitch, BK, p.bn / CG);
+        mx = ma;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+
+    int units = 0;
+    e = resident<MODE, CG>(&units);
+    if (e != cudaSuccess) return e;
+    if (units > tiles) units = (int)tiles;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * CG));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    return counted(cudaLaunchKernelEx(&cfg, vocab_umma_kernel<MODE, CG>, ma, mw, mx, p));
+}
+
+template <int MODE>
+cudaError_t launch_rows(const LceProduct &a, cudaStream_t st)
+{
+    return a.rows <= kNarrowRows ? launch_mode<MODE, 1>(a, st) : launch_mode<MODE, 2>(a, st);
+}
+
+}  // namespace
+
+int lce_row_tile(int64_t rows) { return rows <= kNarrowRows ? 128 : 512; }
+int lce_units(int64_t rows) { return rows <= kNarrowRows ? sm_count() : sm_count() / 2; }
+
+// Single CTAs share the words out evenly, so that the last wave is as full as the others.
+int lce_word_tile(int64_t rows, int64_t words)
+{
+    if (rows > kNarrowRows) return kTileN;
+    const int64_t n = sm_count(), waves = (words + n * kTileN - 1) / (n * kTileN);
+    const int64_t bn = ((words + n * waves - 1) / (n * waves) + 15) / 16 * 16;
+    return bn < 64 ? 64 : (int)bn;
+}
+
+cudaError_t launch_lce_product(int mode, const LceProduct &a, cudaStream_t st)
+{
+    if (mode == LCE_STATS) return launch_rows<LCE_STATS>(a, st);
+    if (mode == LCE_DLOGITS) return launch_rows<LCE_DLOGITS>(a, st);
+    return launch_rows<LCE_GRADS>(a, st);
+}
+
+}  // namespace tf

@@ -399,6 +399,61 @@ int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens,
                           int64_t vocab, int64_t hidden, float scale, int64_t padding, int accumulate, int dtype,
                           void *workspace, int64_t workspace_bytes, tf_stream_t stream);
 
+/* ---------------------------------------------------------------- linear cross entropy */
+
+/* Softmax cross entropy of the logits scale * x w^T over a vocabulary (a language
+ * model's head), without the logits in memory:
+ *   l[i][v] = scale * sum over h of x[i][h]*w[v][h]
+ *   lse[i]  = log(sum over v of exp(l[i][v]));  loss[i] = lse[i] - l[i][targets[i]]
+ *   x       : dtype (TF_FP16 or TF_BF16; TF_ERR_UNSUPPORTED for TF_FP32) [rows][hidden],
+ *             row i at i*x_stride elements
+ *   w       : dtype [vocab][hidden], contiguous (16-byte aligned where hidden % 8 == 0)
+ *   targets : int32 or int64 (tf_index) [rows] on the device
+ *   loss, lse : fp32 [rows];  scale > 0
+ * Rows whose target is `ignore` (-100, say; TF_NO_INDEX: none) cost nothing and
+ * get a loss and lse of 0; what x holds there, NaN included, is not read.
+ * Other targets outside [0, vocab) are ignored likewise and set TF_DEVERR_INDEX.
+ * Sums are fp32; equal calls give equal bits.  The tensor cores truncate where
+ * fp32 additions round (see the grouped products): logits whose terms cancel are off by up
+ * to 6e-8 of their largest partial sum for every 16 terms.
+ * Any hidden to 65536, any row stride (below 2^31) and the alignment of an
+ * element; where hidden is not a multiple of 8 the weights are copied on the
+ * way.  Up to 4194304 rows and words; rows may be 0.
+ * The workspace (16-byte aligned) is in use until the stream reaches the end of
+ * the call; calls that may overlap need one each, captured graphs too.
+ * TF_ERR_INVALID_ARG when it is missing or too small.  Its size does not fall as rows
+ * grow; host only, depends on the current device's SM count. */
+int64_t tf_linear_cross_entropy_forward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden, int dtype);
+int tf_linear_cross_entropy_forward(const void *x, int64_t x_stride, const void *w, const void *targets, int index,
+                                    float *loss, float *lse, int64_t rows, int64_t vocab, int64_t hidden, float scale,
+                                    int64_t ignore, int dtype, void *workspace, int64_t workspace_bytes,
+                                    tf_stream_t stream);
+
+/* Gradients of tf_linear_cross_entropy_forward, one piece of the vocabulary after the
+ * other: the logits are computed again, and no more than 256 MB of their
+ * gradients (more only above 262144 rows: 1 KB per row) are in memory at once.
+ *   dl[i][v] = exp(l[i][v] - lse[i])*(dloss[i] + dlse[i]) - [v = targets[i]]*dloss[i]
+ *   dx = scale * dl w;  dw = scale * dl^T x
+ *   lse    : fp32 [rows], from the forward pass
+ *   dloss, dlse : fp32 [rows], the gradients that reach loss and lse; dloss may be
+ *            NULL (1), dlse may be NULL (0)
+ *   dx     : dtype [rows][hidden], row i at i*dx_stride elements, or NULL (not wanted);
+ *            0 for ignored rows, whose lse, dloss and dlse are not read
+ *   dw     : dw_dtype [vocab][hidden], contiguous, or NULL; dw_dtype is dtype or
+ *            TF_FP32.  With `accumulate` != 0 (TF_FP32 only) it is added to what
+ *            dw holds.
+ * dl is rounded to dtype, the matrix products' operand type: a relative 2^-9 (bf16) or 2^-12
+ * (fp16) of each term at most, in dx and dw, also where dw is fp32.  fp16 holds
+ * dl in units of a power of two that puts the largest |dloss| + |dlse| below
+ * 2^15, so that terms down to 2^-29 of it keep their digits and
+ * none below 2^-40 of it counts.  Sums are fp32.  Workspace as above. */
+int64_t tf_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden, int dtype);
+int tf_linear_cross_entropy_backward(const void *x, int64_t x_stride, const void *w, const void *targets, int index,
+                                     const float *lse, const float *dloss, const float *dlse, void *dx,
+                                     int64_t dx_stride, void *dw, int64_t rows, int64_t vocab, int64_t hidden,
+                                     float scale, int64_t ignore, int accumulate, int dw_dtype, int dtype,
+                                     void *workspace, int64_t workspace_bytes, tf_stream_t stream);
+
 /* ---------------------------------------------------------------- unfused chains */
 
 /* The separate kernels that the fused calls replace, for the traffic and time
