@@ -6,14 +6,15 @@
 // Both are bound by HBM.  The backward pass brings equal tokens together, so
 // that every row of dtable is written once and in a fixed order of additions,
 // which atomics would not give:
-//   1  the keys (token, position) are sorted in chunks of 2048 in shared memory
-//   2  32 sorted runs at a time become one: a key's place is the sum of its
-//      places in all of them, found by binary search (keys are unique)
-//   3  the sorted list is cut into pieces of equal length, whatever the words'
+//   1  a stable counting sort of (token, position): every CTA owns a range of the
+//      vocabulary, reads all tokens (they are few beside the rows) and places those of
+//      its range, so that no CTA waits for another
+//   2  the sorted list is cut into pieces of equal length, whatever the words'
 //      frequencies; a thread adds its columns of a piece's rows of dy and writes
-//      a row of dtable where the word changes.  Words that cross a piece's ends
-//      leave partial sums.  Other CTAs write the zeros of words that do not occur.
-//   4  the partial sums of crossing words are added in order
+//      a row of dtable where the word changes.  A word that goes on for less than a
+//      piece is finished where it began; longer ones leave partial sums.  Other
+//      CTAs write the zeros of words that do not occur.
+//   3  the partial sums of the long words are added in order
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -119,49 +120,119 @@ cudaError_t embed_typed(const EmbedArgs &a, cudaStream_t st)
 // A key holds the token in its upper and the row of dy in its lower half; tokens
 // that have no gradient come last.
 constexpr uint32_t kNone = 0xffffffffu;
-constexpr int kSortThreads = 1024, kChunk = 2 * kSortThreads, kFanIn = 32;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kDigitBits = 18;   // words per pass: the counters of 2^18/152 words and 32 warps fill the shared memory
 
 __device__ __forceinline__ uint32_t word_of(uint64_t key) { return (uint32_t)(key >> 32); }
 
-// Bitonic sort of a chunk in shared memory: a warp owns 64 neighbouring keys, so
-// that steps of up to 32 need no barrier of the CTA.
-__global__ void __launch_bounds__(kSortThreads) sort_chunks_kernel(const __grid_constant__ EmbedArgs a, uint64_t *out)
+// One pass of the stable counting sort, by the digit (word >> shift) & mask: the
+// first takes the tokens, a second one, for more than 2^18 words, the first one's
+// keys.  A warp has a stretch of the list and counters of its own, so that places
+// follow the order of the list: below this CTA's range, smaller digits, earlier
+// warps, earlier in the warp.  16384 tokens, 32000 words: 9 us (sorting chunks and
+// merging them took 32).
+template <bool FIRST>
+__global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_constant__ EmbedArgs a, const uint64_t *in,
+                                                                  uint64_t *out, int *long_words, int shift, int range)
 {
     pdl_begin();
-    __shared__ uint64_t s[kChunk];
-    const int64_t first = (int64_t)blockIdx.x * kChunk;
-    const int n = (int)min((int64_t)kChunk, a.rows - first), t = threadIdx.x;
-    int span = 64;
-    while (span < n) span *= 2;
-    for (int i = t; i < span; i += kSortThreads) {
-        uint64_t key = ~0ull;
-        if (i < n) {
-            const int64_t token = a.tokens.at(first + i);
-            const bool inside = token >= 0 && token < a.vocab, none = token == a.padding;
-            if (!inside && !none) atomicOr(a.err, TF_DEVERR_INDEX);
-            key = (uint64_t)(inside && !none ? (uint32_t)token : kNone) << 32 | (uint32_t)(first + i);
-        }
-        s[i] = key;
-    }
+    extern __shared__ uint32_t cnt[];   // [kSortWarps][range]
+    __shared__ uint32_t warp_sums[kSortWarps], below_sums[kSortWarps], total;
+    constexpr int UNROLL = 8;
+    constexpr uint32_t mask = (1u << kDigitBits) - 1;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const uint32_t d0 = blockIdx.x * (uint32_t)range, d1 = d0 + (uint32_t)range;
+    const bool last = blockIdx.x == gridDim.x - 1;
+    const int64_t seg = ((a.rows + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int64_t lo = warp * seg, hi = min(a.rows, lo + seg);
+    for (int i = t; i < kSortWarps * range; i += kSortThreads) cnt[i] = 0;
+    if (blockIdx.x == 0 && t == 0) *long_words = 0;
     __syncthreads();
-    for (int k = 2; k <= span; k *= 2) {
-        for (int j = k / 2; j > 0; j /= 2) {
-            if (t < span / 2) {
-                const int i = 2 * t - (t & (j - 1));
-                const uint64_t x = s[i], y = s[i + j];
-                if ((x > y) == ((i & k) == 0)) {
-                    s[i] = y;
-                    s[i + j] = x;
-                }
-            }
-            if (j > 32 || (j == 1 && k >= 64)) __syncthreads();
-            else __syncwarp();
+    uint32_t *mine = cnt + warp * range;
+    auto key_at = [&](int64_t i) -> uint64_t {
+        if (i >= hi) return ~0ull;
+        if constexpr (FIRST) {
+            const int64_t token = a.tokens.at(i);
+            const bool inside = token >= 0 && token < a.vocab, none = token == a.padding;
+            if (!inside && !none && blockIdx.x == 0) atomicOr(a.err, TF_DEVERR_INDEX);
+            return (uint64_t)(inside && !none ? (uint32_t)token : kNone) << 32 | (uint32_t)i;
+        } else {
+            return in[i];
+        }
+    };
+    uint32_t low = 0;
+    for (int64_t i = lo; i < hi; i += 32 * UNROLL) {
+        uint64_t key[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + u * 32 + lane);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const uint32_t digit = (word_of(key[u]) >> shift) & mask;
+            if (word_of(key[u]) == kNone) continue;
+            low += digit < d0;
+            if (digit >= d0 && digit < d1) atomicAdd(mine + (digit - d0), 1u);
         }
     }
-    for (int i = t; i < n; i += kSortThreads) out[first + i] = s[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) low += __shfl_xor_sync(0xffffffffu, low, o);
+    if (lane == 0) below_sums[warp] = low;
+    __syncthreads();
+    uint32_t base = 0;
+    for (int w = 0; w < kSortWarps; ++w) base += below_sums[w];
+    // counters become places, a thread per digit
+    for (int d = 0; d < range; d += kSortThreads) {
+        uint32_t sum = 0;
+        if (d + t < range)
+            for (int w = 0; w < kSortWarps; ++w) sum += cnt[w * range + d + t];
+        uint32_t scan = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += up;
+        }
+        if (lane == 31) warp_sums[warp] = scan;
+        __syncthreads();
+        uint32_t at = base + scan - sum, all = 0;
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warp) at += warp_sums[w];
+            all += warp_sums[w];
+        }
+        base += all;
+        if (d + t < range)
+            for (int w = 0; w < kSortWarps; ++w) {
+                const uint32_t n = cnt[w * range + d + t];
+                cnt[w * range + d + t] = at;
+                at += n;
+            }
+        __syncthreads();
+    }
+    if (t == 0) total = base;
+    __syncthreads();
+    for (int64_t i = lo; i < hi; i += 32 * UNROLL) {
+        uint64_t key[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + u * 32 + lane);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const uint32_t digit = (word_of(key[u]) >> shift) & mask;
+            const bool in_range = word_of(key[u]) != kNone && digit >= d0 && digit < d1;
+            const unsigned active = __ballot_sync(0xffffffffu, in_range);
+            if (active == 0) continue;
+            if (in_range) {
+                const unsigned same = __match_any_sync(active, digit);
+                const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[digit - d0];
+                out[first + before] = key[u];
+                __syncwarp(active);
+                if (before == 0) mine[digit - d0] = first + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    if (last)   // the rest have no gradient
+        for (int64_t i = total + t; i < a.rows; i += kSortThreads) out[i] = ~0ull;
 }
 
-// Keys of run [lo, hi) below `key`.
+// Keys of [lo, hi) below `key`.
 __device__ __forceinline__ int64_t below(const uint64_t *keys, int64_t lo, int64_t hi, uint64_t key)
 {
     const int64_t start = lo;
@@ -172,78 +243,47 @@ __device__ __forceinline__ int64_t below(const uint64_t *keys, int64_t lo, int64
     return lo - start;
 }
 
-// Groups of up to kFanIn sorted runs of `len` keys become one run each.  Four
-// searches at a time, whose loads do not wait for one another; neighbouring
-// threads' keys take nearly the same path.
-__global__ void __launch_bounds__(kThreads) merge_runs_kernel(const uint64_t *in, uint64_t *out, int64_t n, int64_t len)
-{
-    pdl_begin();
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= n) return;
-    const uint64_t key = in[i];
-    const int64_t run = i / len, group = run / kFanIn * kFanIn, base = group * len;
-    int64_t place = i - run * len;
-    for (int64_t r = group; r < group + kFanIn && r * len < n; r += 4) {
-        int64_t lo[4], hi[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            lo[u] = min((r + u) * len, n);
-            hi[u] = r + u < group + kFanIn && r + u != run ? min((r + u + 1) * len, n) : lo[u];
-            place -= lo[u];
-        }
-        bool more = true;
-        while (more) {
-            uint64_t v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = lo[u] < hi[u] ? __ldg(in + ((lo[u] + hi[u]) >> 1)) : 0;
-            more = false;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (lo[u] >= hi[u]) continue;
-                const int64_t mid = (lo[u] + hi[u]) >> 1;
-                if (v[u] < key) lo[u] = mid + 1; else hi[u] = mid;
-                more |= lo[u] < hi[u];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) place += lo[u];
-    }
-    out[base + place] = key;
-}
-
 // ---------------------------------------------------------------- backward: sums
 
 constexpr int kSumThreads = 128;
 constexpr int kFillRows = 64;      // rows of dtable per zeroing CTA
-constexpr int kMinPiece = 32, kMaxPiece = 1024;
-constexpr int kLevel = 64;         // rows added before their sum joins the piece's: long sums of equal terms keep their digits
+constexpr int kMinPiece = 8, kMaxPiece = 1024;
+constexpr int kLevel = 64;         // terms added before their sum joins the next level's: long sums of equal terms keep their digits
+constexpr int64_t kMostPieces = 32768;
 
 struct SumArgs {
     const uint64_t *keys;
     const void *dy;
-    float *dtable, *part;          // part: [pieces][2][pitch], of the words that go on before and behind the piece
+    float *dtable, *part;          // part: [pieces][2][pitch], of long words that go on before and behind the piece
+    int *long_words;               // their number, then the pieces that they begin in
     int64_t dy_stride, n, vocab, pitch;
     int hidden, accumulate, piece, pieces, lanes, sum_blocks;
     float scale;
 };
 
+// A row's columns.  Adding to what is there is left to the L2, which does not make
+// the thread wait for the old values; every element of dtable gets one such
+// addition in a call, so that their order does not matter.
 template <int VEC>
 __device__ __forceinline__ void put_row(float *dst, const float (&sum)[VEC], float scale, bool add)
 {
     if constexpr (VEC % 4 == 0) {
 #pragma unroll
         for (int k = 0; k < VEC; k += 4) {
-            float4 v = make_float4(sum[k] * scale, sum[k + 1] * scale, sum[k + 2] * scale, sum[k + 3] * scale);
-            float4 *p = reinterpret_cast<float4 *>(dst + k);
-            if (add) {
-                const float4 o = *p;
-                v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-            }
-            *p = v;
+            const float4 v = make_float4(sum[k] * scale, sum[k + 1] * scale, sum[k + 2] * scale, sum[k + 3] * scale);
+            if (add)
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + k), "f"(v.x), "f"(v.y), "f"(v.z),
+                             "f"(v.w)
+                             : "memory");
+            else
+                *reinterpret_cast<float4 *>(dst + k) = v;
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) dst[k] = add ? dst[k] + sum[k] * scale : sum[k] * scale;
+        for (int k = 0; k < VEC; ++k) {
+            if (add) atomicAdd(dst + k, sum[k] * scale);
+            else dst[k] = sum[k] * scale;
+        }
     }
 }
 
@@ -287,40 +327,60 @@ __global__ void __launch_bounds__(kSumThreads) sum_pieces_kernel(const __grid_co
     if (p >= a.pieces || c >= a.hidden) return;
     const int64_t first = (int64_t)p * a.piece, end = min(first + a.piece, a.n);
     const T *dy = static_cast<const T *>(a.dy) + c;
+    auto word_at = [&](int64_t i) { return i >= 0 && i < a.n ? word_of(__ldg(a.keys + i)) : kNone; };
+    // A word that goes on behind the piece it begins in for `piece` rows or more is long: each
+    // of its pieces leaves a partial sum.  Otherwise the piece that it begins in finishes it.
+    uint32_t word = word_at(first);
+    const uint32_t final = word_at(end - 1);
+    const bool head = word != kNone && word_at(first - 1) == word;
+    const bool head_long = head && (word_at(first + a.piece - 1) == word || word_at(first - a.piece - 1) == word);
+    const bool tail = final != kNone && word_at(end) == final;
+    const bool tail_long = tail && (word_at(end + a.piece - 1) == final || (head && final == word));
+    const int64_t limit = tail && !tail_long ? min(end + a.piece, a.n) : end;
     float sum[VEC] = {}, low[VEC] = {};
     int held = 0;
-    uint32_t word = word_of(__ldg(a.keys + first));
-    bool head = first > 0 && word_of(__ldg(a.keys + first - 1)) == word;   // the word goes on from the piece before
+    bool at_head = head;
     auto flush = [&](bool goes_on) {
-        if (word != kNone) {
+        if (word != kNone && (!at_head || head_long)) {
 #pragma unroll
             for (int k = 0; k < VEC; ++k) sum[k] += low[k];
-            if (head || goes_on)
-                put_row<VEC>(a.part + ((int64_t)p * 2 + (head ? 0 : 1)) * a.pitch + c, sum, 1.0f, false);
+            if (at_head || goes_on)
+                put_row<VEC>(a.part + ((int64_t)p * 2 + (at_head ? 0 : 1)) * a.pitch + c, sum, 1.0f, false);
             else
                 put_row<VEC>(a.dtable + (int64_t)word * a.hidden + c, sum, a.scale, a.accumulate != 0);
+            if (goes_on && !at_head && c == 0) a.long_words[1 + atomicAdd(a.long_words, 1)] = p;
         }
 #pragma unroll
         for (int k = 0; k < VEC; ++k) sum[k] = low[k] = 0.0f;
         held = 0;
-        head = false;
+        at_head = false;
     };
-    for (int64_t i = first; i < end; i += UNROLL) {
-        uint64_t key[UNROLL];
+    const uint32_t skipped = head && !head_long ? word : kNone;   // finished by the piece before
+    auto key_at = [&](int64_t i) {
+        const uint64_t key = i < limit ? __ldg(a.keys + i) : ~0ull;
+        return i < end || word_of(key) == final ? key : ~0ull;
+    };
+    uint64_t key[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) key[u] = key_at(first + u);
+    for (int64_t i = first; i < limit; i += UNROLL) {
         P v[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) key[u] = i + u < end ? __ldg(a.keys + i + u) : ~0ull;
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
-            if (word_of(key[u]) != kNone) v[u] = *reinterpret_cast<const P *>(dy + (int64_t)(uint32_t)key[u] * a.dy_stride);
+        uint32_t w[UNROLL];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            if (i + u >= end) break;
-            if (word_of(key[u]) != word) {
+            w[u] = word_of(key[u]);
+            if (w[u] != kNone && w[u] != skipped) v[u] = *reinterpret_cast<const P *>(dy + (int64_t)(uint32_t)key[u] * a.dy_stride);
+        }
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + UNROLL + u);   // the next ones, while the rows are under way
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (w[u] == kNone) break;   // (the last of the list, or of the word that went on)
+            if (w[u] != word) {
                 flush(false);
-                word = word_of(key[u]);
+                word = w[u];
             }
-            if (word == kNone) continue;
+            if (w[u] == skipped) continue;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) low[k] += widen<T>(v[u].v[k]);
             if (++held == kLevel) {
@@ -333,33 +393,42 @@ __global__ void __launch_bounds__(kSumThreads) sum_pieces_kernel(const __grid_co
             }
         }
     }
-    flush(end < a.n && word_of(__ldg(a.keys + end)) == word);
+    flush(tail_long);
 }
 
-constexpr int kJoinCols = 32, kJoinSplits = 8, kJoinPieces = 4;
+constexpr int kJoinCols = 32, kJoinSplits = 8, kJoinThreads = kJoinCols * kJoinSplits;
 
-// Words that cross the ends of pieces: the CTA of the piece where the word
-// begins adds its partial sums, in kJoinSplits stretches that are joined in order.
-__global__ void __launch_bounds__(kJoinCols * kJoinSplits) join_pieces_kernel(const __grid_constant__ SumArgs a)
+// Long words: a CTA adds 128 columns of one word's partial sums, in kJoinSplits
+// stretches that are joined in order.
+__global__ void __launch_bounds__(kJoinThreads) join_pieces_kernel(const __grid_constant__ SumArgs a)
 {
     pdl_begin();
     __shared__ float4 red[kJoinSplits][kJoinCols];
     const int col = threadIdx.x % kJoinCols, split = threadIdx.x / kJoinCols;
-    const int c = ((int)blockIdx.y * kJoinCols + col) * 4;
-    for (int p = (int)blockIdx.x * kJoinPieces; p < min(((int)blockIdx.x + 1) * kJoinPieces, a.pieces - 1); ++p) {
-        const int64_t first = (int64_t)p * a.piece, end = first + a.piece;   // (the next piece exists)
-        const uint32_t word = word_of(__ldg(a.keys + end - 1));
-        if (word == kNone || word_of(__ldg(a.keys + end)) != word) continue;
-        if (p > 0 && word_of(__ldg(a.keys + first)) == word && word_of(__ldg(a.keys + first - 1)) == word) continue;
-        const int64_t last = below(a.keys, 0, a.n, ((uint64_t)word + 1) << 32) - 1;   // its last key
-        const int64_t count = last / a.piece - p + 1, per = (count + kJoinSplits - 1) / kJoinSplits;
+    const int across = (a.hidden + 4 * kJoinCols - 1) / (4 * kJoinCols), items = *a.long_words * across;
+    for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
+        const int p = a.long_words[1 + item / across], c = (item % across * kJoinCols + col) * 4;
+        const uint32_t word = word_of(__ldg(a.keys + (int64_t)(p + 1) * a.piece - 1));
+        int count = 1;   // pieces: those behind p that begin with the word follow one another
+        for (int q = p + 1;; q += kJoinThreads) {
+            const int64_t at = (int64_t)(q + (int)threadIdx.x) * a.piece;
+            const int n = __syncthreads_count(at < a.n && word_of(__ldg(a.keys + at)) == word);
+            count += n;
+            if (n < kJoinThreads) break;
+        }
+        const int per = (count + kJoinSplits - 1) / kJoinSplits;
         float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (c < a.hidden) {
-            const float *src = a.part + c;
+            const float *src = a.part + (int64_t)p * 2 * a.pitch + c;
+            const int end = min((split + 1) * per, count);
+            for (int q0 = split * per; q0 < end; q0 += kLevel) {
+                float4 low = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-            for (int64_t q = split * per; q < min((split + 1) * per, count); ++q) {
-                const float4 v = *reinterpret_cast<const float4 *>(src + ((p + q) * 2 + (q == 0 ? 1 : 0)) * a.pitch);
-                t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
+                for (int q = q0; q < min(q0 + kLevel, end); ++q) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + (2 * (int64_t)q + (q == 0 ? 1 : 0)) * a.pitch);
+                    low.x += v.x; low.y += v.y; low.z += v.z; low.w += v.w;
+                }
+                t.x += low.x; t.y += low.y; t.z += low.z; t.w += low.w;
             }
         }
         red[split][col] = t;
@@ -386,14 +455,15 @@ int lanes_of(int words)
     return lanes;
 }
 
-// Pieces that fill the SMs (32 CTAs each) where the list is long enough, of 32
-// to 1024 keys.  Sized for 8 columns per thread, whatever the type, so that the
+// Pieces that fill the SMs where the list is long enough (16 CTAs each, and no more
+// pieces than a long word's join adds quickly), of 8 to 1024 keys.  Sized for 8 columns per thread, whatever the type, so that the
 // workspace depends on the sizes alone.
 int64_t piece_target(int64_t hidden)
 {
     const int lanes = lanes_of((int)((hidden + 7) / 8));
     const int64_t slices = (hidden + 8 * lanes - 1) / (8 * lanes), per_block = kSumThreads / lanes;
-    return (32 * 152 + slices - 1) / slices * per_block;
+    const int64_t fill = (16 * 152 + slices - 1) / slices * per_block;
+    return fill < kMostPieces ? fill : kMostPieces;
 }
 int64_t piece_of(int64_t rows, int64_t hidden)
 {
@@ -409,6 +479,7 @@ int64_t most_pieces(int64_t rows, int64_t hidden)
 }
 int64_t pitch_of(int64_t hidden) { return (hidden + 7) / 8 * 8; }
 int64_t keys_bytes(int64_t rows) { return (rows * 8 + 255) / 256 * 256; }
+int64_t list_bytes(int64_t pieces) { return ((pieces + 1) * 4 + 255) / 256 * 256; }
 
 template <typename T, int VEC>
 cudaError_t launch_sums(const EmbedArgs &a, SumArgs s, cudaStream_t st)
@@ -443,41 +514,45 @@ cudaError_t launch_embedding_forward(const EmbedArgs &a, cudaStream_t st)
     return a.dtype == TF_BF16 ? embed_typed<__nv_bfloat16>(a, st) : embed_typed<__half>(a, st);
 }
 
-// Two lists of keys, then the partial sums.
-int64_t embedding_backward_workspace(int64_t rows, int64_t, int64_t hidden)
+// The keys (twice for two passes), the long words' list, then the partial sums.
+int64_t embedding_backward_workspace(int64_t rows, int64_t vocab, int64_t hidden)
 {
-    return 2 * keys_bytes(rows) + most_pieces(rows, hidden) * 2 * pitch_of(hidden) * 4;
+    const int passes = vocab > (int64_t)1 << kDigitBits ? 2 : 1;
+    const int64_t pieces = most_pieces(rows, hidden);
+    return rows == 0 ? 0 : passes * keys_bytes(rows) + list_bytes(pieces) + pieces * 2 * pitch_of(hidden) * 4;
 }
 
 cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
 {
-    uint64_t *from = static_cast<uint64_t *>(a.ws), *to = from + keys_bytes(a.rows) / 8;
+    const int passes = a.vocab > (int64_t)1 << kDigitBits ? 2 : 1;
+    char *ws = static_cast<char *>(a.ws);
+    uint64_t *keys = reinterpret_cast<uint64_t *>(ws), *first = reinterpret_cast<uint64_t *>(ws + (passes - 1) * keys_bytes(a.rows));
     SumArgs s = {};
-    s.part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + 2 * keys_bytes(a.rows));
+    s.keys = keys;
+    s.long_words = reinterpret_cast<int *>(ws + passes * keys_bytes(a.rows));
+    s.part = reinterpret_cast<float *>(ws + passes * keys_bytes(a.rows) + list_bytes(most_pieces(a.rows, a.hidden)));
     s.dy = a.dy; s.dtable = a.dtable; s.dy_stride = a.dy_stride; s.n = a.rows; s.vocab = a.vocab;
     s.pitch = pitch_of(a.hidden); s.hidden = a.hidden; s.accumulate = a.accumulate; s.scale = a.scale;
     s.piece = (int)piece_of(a.rows, a.hidden);
     s.pieces = (int)((a.rows + s.piece - 1) / s.piece);
     cudaError_t e = cudaSuccess;
-    if (a.rows > 0) {
-        const int64_t chunks = (a.rows + kChunk - 1) / kChunk;
-        e = launch_pdl(sort_chunks_kernel, dim3((unsigned)chunks), dim3(kSortThreads), 0, st, a, from);
-        for (int64_t len = kChunk; e == cudaSuccess && len < a.rows; len *= kFanIn) {
-            e = launch_pdl(merge_runs_kernel, dim3((unsigned)((a.rows + kThreads - 1) / kThreads)), dim3(kThreads), 0, st,
-                           static_cast<const uint64_t *>(from), to, a.rows, len);
-            uint64_t *t = from;
-            from = to;
-            to = t;
-        }
-        if (e != cudaSuccess) return e;
+    for (int pass = 0; a.rows > 0 && e == cudaSuccess && pass < passes; ++pass) {
+        const int64_t all = ((a.vocab - 1) >> (pass * kDigitBits)) + 1, most = (int64_t)1 << kDigitBits;
+        const int64_t digits = all < most ? all : most, sms = sm_count() > 152 ? 152 : sm_count();
+        const int64_t range = (digits + sms - 1) / sms < 64 ? 64 : (digits + sms - 1) / sms;
+        const dim3 grid((unsigned)((digits + range - 1) / range));
+        const size_t smem = (size_t)(kSortWarps * range * 4);
+        auto kern = pass == 0 ? count_sort_kernel<true> : count_sort_kernel<false>;
+        e = raise_smem_limit(reinterpret_cast<const void *>(kern));
+        if (e == cudaSuccess)
+            e = launch_pdl(kern, grid, dim3(kSortThreads), smem, st, a, static_cast<const uint64_t *>(first),
+                           pass == 0 ? first : keys, s.long_words, pass * kDigitBits, (int)range);
     }
-    s.keys = from;
+    if (e != cudaSuccess) return e;
     if (a.dtype == TF_FP32) e = sums_typed<float>(a, s, st);
     else e = a.dtype == TF_BF16 ? sums_typed<__nv_bfloat16>(a, s, st) : sums_typed<__half>(a, s, st);
     if (e != cudaSuccess || s.pieces < 2) return e;
-    const unsigned across = (unsigned)((a.hidden + 4 * kJoinCols - 1) / (4 * kJoinCols));
-    return launch_pdl(join_pieces_kernel, dim3((unsigned)((s.pieces - 1 + kJoinPieces - 1) / kJoinPieces), across),
-                      dim3(kJoinCols * kJoinSplits), 0, st, s);
+    return launch_pdl(join_pieces_kernel, dim3((unsigned)(4 * sm_count())), dim3(kJoinThreads), 0, st, s);
 }
 
 }  // namespace tf

@@ -185,49 +185,93 @@ __global__ void __launch_bounds__(1024) unit_kernel(const __grid_constant__ LceA
 // ---------------------------------------------------------------- loss
 
 struct LossArgs {
-    const int *count, *index;
+    const int *count, *index, *target;
     const float2 *part;
     const float *at_target;
+    const uint16_t *x, *w;
     float *loss, *lse;
-    int rows, slots;
+    int64_t x_pitch;
+    int rows, slots, per_block, hidden, bf16;
     float scale;
 };
 
-// 32 rows per CTA, a row's slots over 32 threads.  The loss is taken from the
-// maximum, so that a sure target's does not drown in the logits' size.
-__global__ void __launch_bounds__(1024) loss_kernel(const __grid_constant__ LossArgs p)
+// `per_block` rows per CTA (one, or four, whose neighbouring slots fill a sector), a
+// row's slots over the CTA's threads.
+//
+// The target's logit is taken again, in fp32 from the operands: the tensor cores'
+// truncation leaves it 1e-5 low, which is what the loss would be off by (relative
+// error of 4096 rows' losses, 4096 terms per logit: 1.3e-6, and 9e-7 so).  It takes the
+// place of the products' own in the loss.  With m the largest logit, t
+// the target's, A the others' sum e^(l - m) and d = m - t the loss is
+// log(1 + A e^d), so that a sure target's loss keeps its digits.  lse stays that of the
+// products' logits, which the backward pass takes it from: what both are off by
+// cancels in 1 - e^(l - lse), of which a sure target's gradient consists.
+__global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ LossArgs p)
 {
     pdl_begin();
-    __shared__ float2 red[32][33];
-    const int count = *p.count;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, row = (int)blockIdx.x * 32 + x;
-    if ((int)blockIdx.x * 32 >= count) return;
+    constexpr int WARPS = kThreads / 32;
+    __shared__ float2 red[WARPS][4];
+    __shared__ float dots[WARPS];
+    const int count = *p.count, per = p.per_block, row0 = (int)blockIdx.x * per;
+    if (row0 >= count) return;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, x = t % per, row = row0 + x;
     const float c = p.scale * kLog2e;
     auto join = [&](float2 s, float2 v) {
         const float m = fmaxf(s.x, v.x), base = m == -INFINITY ? 0.0f : m;
         return make_float2(m, s.y * ex2_approx((s.x - base) * c) + v.y * ex2_approx((v.x - base) * c));
     };
+    // the target's logit, by WARPS/per warps
+    const int wide = WARPS / per, mine = row0 + warp / wide;
+    float dot = 0.0f;
+    if (mine < count) {
+        const uint16_t *a = p.x + mine * p.x_pitch, *b = p.w + (int64_t)p.target[mine] * p.hidden;
+        auto both = [&](uint32_t u, uint32_t v) {
+            const float2 f = p.bf16 ? Half2Of<__nv_bfloat16>::unpack(u) : Half2Of<__half>::unpack(u);
+            const float2 g = p.bf16 ? Half2Of<__nv_bfloat16>::unpack(v) : Half2Of<__half>::unpack(v);
+            return fmaf(f.x, g.x, f.y * g.y);
+        };
+        float s[4] = {};
+        const int at = (warp % wide) * 32 + lane, step = wide * 32;
+        if (p.hidden % 8 == 0)
+            for (int k = at; k < p.hidden / 8; k += step) {
+                const uint4 u = reinterpret_cast<const uint4 *>(a)[k], v = reinterpret_cast<const uint4 *>(b)[k];
+                s[0] += both(u.x, v.x);
+                s[1] += both(u.y, v.y);
+                s[2] += both(u.z, v.z);
+                s[3] += both(u.w, v.w);
+            }
+        else
+            for (int k = at; k < p.hidden; k += step) s[0] += both(a[k], b[k]);
+        dot = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) dots[warp] = dot;
     float2 s = make_float2(-INFINITY, 0.0f);
+    const int lanes = kThreads / per;
     if (row < count)
-        for (int k = y; k < p.slots; k += 4 * 32) {
+        for (int k = t / per; k < p.slots; k += 4 * lanes) {
             float2 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                v[u] = k + u * 32 < p.slots ? p.part[(int64_t)(k + u * 32) * p.rows + row] : make_float2(-INFINITY, 0.0f);
+                v[u] = k + u * lanes < p.slots ? p.part[(int64_t)(k + u * lanes) * p.rows + row] : make_float2(-INFINITY, 0.0f);
             s = join(s, join(join(v[0], v[1]), join(v[2], v[3])));
         }
-    red[y][x] = s;
+    for (int o = 16; o >= per; o >>= 1)
+        s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    if (lane < per) red[warp][lane] = s;
     __syncthreads();
-    s = red[x][y];   // this warp's row, a stretch of its slots per lane
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s = join(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
-    const int mine = (int)blockIdx.x * 32 + y;
-    if (x == 0 && mine < count) {
-        const float over = logf(s.y);
-        const int64_t i = p.index[mine];
-        p.loss[i] = fmaf(p.scale, s.x - p.at_target[mine], over);
-        p.lse[i] = fmaf(p.scale, s.x, over);
-    }
+    if (t >= per || row >= count) return;
+    for (int w = 1; w < WARPS; ++w) s = join(s, red[w][t]);
+    dot = 0.0f;
+    for (int w = 0; w < wide; ++w) dot += dots[t * wide + w];
+    const float target = p.scale * dot, d = p.scale * s.x - target;
+    float others = s.y - ex2_approx((p.at_target[row] - s.x) * c);
+    if (others < 0.0f) others = 0.0f;   // (not a NaN)
+    const float loss = d > 60.0f ? d + logf(others + expf(-d)) : log1pf(others * expf(d));
+    const int64_t i = p.index[row];
+    p.loss[i] = loss;
+    p.lse[i] = fmaf(p.scale, s.x, logf(s.y));
 }
 
 // ---------------------------------------------------------------- dx
@@ -448,8 +492,12 @@ cudaError_t launch_lce_forward(const LceArgs &a, cudaStream_t st)
         m.slot0 += 2 * (int)((words + bn - 1) / bn);
     }
     if (e != cudaSuccess) return e;
-    LossArgs l = {m.count, at<int>(a.ws, p.index), m.part, m.at_target, a.loss, a.lse, (int)a.rows, m.slot0, a.scale};
-    return launch_pdl(loss_kernel, dim3((unsigned)((a.rows + 31) / 32)), dim3(1024), 0, st, l);
+    LossArgs l = {};
+    l.count = m.count; l.index = at<int>(a.ws, p.index); l.target = m.target; l.part = m.part; l.at_target = m.at_target;
+    l.x = static_cast<const uint16_t *>(m.x); l.w = static_cast<const uint16_t *>(a.w); l.loss = a.loss; l.lse = a.lse;
+    l.x_pitch = p.x_pitch; l.rows = (int)a.rows; l.slots = m.slot0; l.per_block = a.rows < 512 ? 1 : 4;
+    l.hidden = a.hidden; l.bf16 = a.dtype == TF_BF16; l.scale = a.scale;
+    return launch_pdl(loss_kernel, dim3((unsigned)((a.rows + l.per_block - 1) / l.per_block)), dim3(kThreads), 0, st, l);
 }
 
 cudaError_t launch_lce_backward(const LceArgs &a, cudaStream_t st)

@@ -70,9 +70,10 @@ struct VocabArgs {
     int split_steps;   // DX: K steps per split
 };
 
-// A tile: rows [m0, +128*CG*CG), columns [n0, +bn), K steps [k0, k0 + nk).
+// A tile: rows [m0, +128*CG*CG), columns [n0, +bn), K steps [k0, k0 + nk); `subs` of its
+// accumulators have rows that exist.
 struct Tile {
-    int kind, m0, n0, k0, nk, slot;
+    int kind, m0, n0, k0, nk, slot, subs;
 };
 enum { TILE_LOGITS = 0, TILE_DX = 1, TILE_DW = 2 };
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 template <int MODE, int CG>
 struct Share {
     static constexpr int ROWS = 128 * CG * CG;
-    int cid, ncl, tiles;
+    int cid, ncl, tiles, rows;
     int row_tiles, col_tiles;      // STATS, DLOGITS
     int nd, nw, rest, lead;        // GRADS: tiles of either kind; pairs with a DX tile more; DW tiles that the others take first
     int dw_steps, dx_steps;
@@ -91,6 +92,7 @@ struct Share {
     {
         cid = cid_;
         ncl = ncl_;
+        rows = count;
         if constexpr (MODE != LCE_GRADS) {
             row_tiles = div_up(count, ROWS);
             col_tiles = div_up(p.a.words, p.bn);
@@ -113,6 +115,8 @@ struct Share {
         }
     }
 
+    __device__ __forceinline__ int subs(int m0, int end) const { return CG == 2 && m0 + 128 * CG < end ? 2 : 1; }
+
     __device__ __forceinline__ bool at(const VocabArgs &p, int j, Tile *t) const
     {
         if constexpr (MODE != LCE_GRADS) {
@@ -121,14 +125,15 @@ struct Share {
             const int g = i / (p.group * col_tiles), r = i - g * p.group * col_tiles;
             const int size = min(p.group, row_tiles - g * p.group);
             const int v = r / size;
-            *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v};
+            const int m0 = (g * p.group + r - v * size) * ROWS;
+            *t = {TILE_LOGITS, m0, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v, subs(m0, rows)};
             return true;
         } else {
             const int own = nd / ncl + (cid < rest ? 1 : 0);
             if (j < own) {
                 const int i = cid + j * ncl, s = i / (row_tiles * col_tiles), r = i - s * row_tiles * col_tiles;
-                const int k0 = s * p.split_steps;
-                *t = {TILE_DX, r / col_tiles * ROWS, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s};
+                const int k0 = s * p.split_steps, m0 = r / col_tiles * ROWS;
+                *t = {TILE_DX, m0, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s, subs(m0, rows)};
                 return true;
             }
             j -= own;
@@ -136,7 +141,8 @@ struct Share {
             const int i = j < mine ? j * (ncl - rest) + cid - rest
                                    : (rest > 0 ? lead * (ncl - rest) : 0) + (j - mine) * ncl + (cid - rest + ncl) % ncl;
             if (i >= nw) return false;
-            *t = {TILE_DW, i / col_tiles * ROWS, i % col_tiles * p.bn, 0, dw_steps, 0};
+            const int m0 = i / col_tiles * ROWS;
+            *t = {TILE_DW, m0, i % col_tiles * p.bn, 0, dw_steps, 0, subs(m0, p.a.words)};
             return true;
         }
     }
@@ -304,15 +310,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else ptx::tma_load_2d(dst, map, bar, c0, c1);
                     };
                     if constexpr (MODE != LCE_GRADS) {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (SUB * p.a_box + half) * (BK * 2)));
-#pragma unroll
-                        for (int s = 0; s < SUB; ++s) load(a_dst + s * kABytes, &map_a, k, row + s * SUB_ROWS);
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (t.subs * p.a_box + half) * (BK * 2)));
+                        for (int s = 0; s < t.subs; ++s) load(a_dst + s * kABytes, &map_a, k, row + s * SUB_ROWS);
                         load(b_dst, &map_w, k, t.n0 + crank * half);
                     } else {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (SUB * 128 + half) * (BK * 2)));
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (t.subs * 128 + half) * (BK * 2)));
                         const CUtensorMap *map_b = t.kind == TILE_DX ? &map_w : &map_x;
-#pragma unroll
-                        for (int i = 0; i < 2 * SUB; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
+                        for (int i = 0; i < 2 * t.subs; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
                             const int m = row + (i >> 1) * SUB_ROWS + (i & 1) * 64;
                             if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
                             else load(a_dst + i * kChunkBytes, &map_a, m, k);
@@ -391,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     issue(stage, 0, kb > 0 ? 1u : 0u);
                     const bool last = kb == t.nk - 1;
                     if (last) commit(&tfull[c0]);
-                    if constexpr (SUB == 2) {
+                    if (SUB == 2 && t.subs == 2) {
                         if (!second) {
                             const uint32_t par = ((taken >> 1) & 1u) ^ 1u;
                             if (last || late == kStages - 1) {
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (SUB == 2) {
-                    taken ^= 3u;
+                    taken ^= t.subs == 2 ? 3u : 1u;
                 } else {
                     taken ^= 1u << c0;
                     b ^= 1;
@@ -442,25 +446,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kFirstEpiWarp) {
         // ------------------------------------------------------------ epilogue
-        // Warp w reads TMEM lanes 32*(w%4) .. +31, one row per lane; h tells its columns.
+        // Warp w reads TMEM lanes 32*(w%4) .. +31, one row per lane, and one half of the
+        // columns, 64 at a time; the accumulator is free when the last of them are in
+        // registers.  (All 128 at once, to free it at the start, make straight-line code of
+        // all that follows: 4-8% slower in STATS, 25% in small calls.)
         const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
         uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
         const bool bf16 = p.a.dtype == TF_BF16;
+        const int c0 = h * ((p.bn / 2 + 63) & ~63), c1 = h ? p.bn : (p.bn / 2 + 63) & ~63;   // this warp's columns of a tile
+        const float mult = p.a.factor * (MODE == LCE_GRADS && p.a.unit ? __ldg(p.a.unit + 1) : 1.0f);
         int b = 0;
         uint32_t seen = 0;   // parity of the results of either accumulator
         bool ok = true;
         Tile t;
-        auto pack = [&](float x, float y) { return bf16 ? Half2Of<__nv_bfloat16>::pack(x, y) : Half2Of<__half>::pack(x, y); };
+        auto pack = [&](uint32_t x, uint32_t y) {
+            const float a = __uint_as_float(x), b = __uint_as_float(y);
+            return bf16 ? Half2Of<__nv_bfloat16>::pack(a, b) : Half2Of<__half>::pack(a, b);
+        };
+        // 32 columns as 16-bit values into one half of the box's rows
+        auto put_half = [&](const uint32_t (&r)[32], int part) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                box_put(box, lane, part * 4 + i, make_uint4(pack(r[8 * i], r[8 * i + 1]), pack(r[8 * i + 2], r[8 * i + 3]),
+                                                            pack(r[8 * i + 4], r[8 * i + 5]), pack(r[8 * i + 6], r[8 * i + 7])));
+        };
         for (int j = 0; ok && share.at(p, j, &t); ++j) {
-            for (int sub = 0; sub < SUB; ++sub) {
+            for (int sub = 0; sub < t.subs; ++sub) {
                 const int acc = SUB == 2 ? sub : b;
                 const int row0 = t.m0 + sub * SUB_ROWS + crank * 128 + q * 32, row = row0 + lane;
-                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN);
+                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN + c0);
+                const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
+                const int left = min(width, c1) - c0;   // columns with results, up to 128
                 int target = -1;
                 float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
                 if constexpr (MODE != LCE_GRADS) {
                     if (row < count) {
-                        target = __ldg(p.a.target + row) - p.a.v0 - t.n0;   // its column of the tile
+                        target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
                         if constexpr (MODE == LCE_DLOGITS) {
                             l2 = __ldg(p.a.l2 + row);
                             ca = __ldg(p.a.ca + row);
@@ -475,143 +496,139 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     ptx::tc_fence_after();
+                    seen ^= 1u << acc;
+                    if (SUB == 1) b ^= 1;
                 }
-                if constexpr (MODE == LCE_STATS) {
-                    const int width = min(p.bn, p.a.words - t.n0), mid = (p.bn / 2 + 31) & ~31;
-                    float top = -INFINITY, sum = 0.0f;
-                    const int end = min(width, h ? p.bn : mid);
+                auto release = [&]() {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
+                        else ptx::mbar_arrive(&tempty[acc]);
+                    }
+                };
+                if (t.nk > 0 && left <= 0) release();
+                float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-                    for (int c = h * mid; c < end; c += 32) {
-                        uint32_t r[32];
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)c, r);
+                for (int u = 0; u < left; u += 64) {
+                    uint32_t r[2][32];
+                    if (t.nk > 0) {
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
                         ptx::tmem_ld_wait();
-                        const int left = end - c;
-                        if (left >= 32) join_stats(r, 32, p.a.factor, top, sum);
-                        else join_stats(r, left, p.a.factor, top, sum);
-                        const int at = target - c;
-                        const bool hit = at >= 0 && at < min(32, left);
-                        if (__any_sync(0xffffffffu, hit)) {
-                            const float v = pick(r, at);
-                            if (hit) p.a.at_target[row] = v;
-                        }
+                        if (u + 64 >= left) release();
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
                     }
-                    if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
-                } else if constexpr (MODE == LCE_DLOGITS) {
-                    const int width = min(p.bn, p.a.words - t.n0);
-#pragma unroll 1
-                    for (int c = h * 64; c < width; c += 128) {
+                    if constexpr (MODE == LCE_STATS) {
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            uint32_t r[32];
-                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 32 * part), r);
-                            ptx::tmem_ld_wait();
-                            const int at = target - c - 32 * part, left = width - c - 32 * part;
-                            const bool whole = row < count && left >= 32;
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float v = ex2_approx(fmaf(__uint_as_float(r[i]), p.a.factor, -l2)) * ca;
-                                r[i] = whole || (row < count && i < left) ? __float_as_uint(v) : 0u;
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = u + 32 * i;
+                            if (c + 32 <= left) join_stats(r[i], 32, p.a.factor, top, sum);
+                            else join_stats(r[i], left - c, p.a.factor, top, sum);
+                            const int at = target - c;
+                            const bool hit = at >= 0 && at < 32 && target < left;
+                            if (__any_sync(0xffffffffu, hit)) {
+                                const float v = pick(r[i], at);
+                                if (hit) p.a.at_target[row] = v;
                             }
-                            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+                        }
+                    } else if constexpr (MODE == LCE_DLOGITS) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    if (i == at && i < left) r[i] = __float_as_uint(__uint_as_float(r[i]) - cb);
+                        for (int i = 0; i < 2; ++i) {
+                            const int c = u + 32 * i;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
+                            const int at = target - c;
+                            const bool hit = at >= 0 && at < 32 && target < left;
+                            if (__any_sync(0xffffffffu, hit)) {
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (hit && k == at) r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) - cb);
                             }
+                            // columns behind the piece's words, and rows behind those that count, which
+                            // dw's last K step reads: zeros
+                            if (c + 32 > left || row0 + 32 > count) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4];
+                                for (int k = 0; k < 32; ++k) r[i][k] = row < count && c + k < left ? r[i][k] : 0u;
+                            }
+                            put_half(r[i], i);
+                        }
+                        __syncwarp();
+                        const int piece = lane & 7, c = c0 + u + 8 * piece;
+                        uint16_t *out = static_cast<uint16_t *>(p.a.dl) + t.n0 + c;
+                        if (c < c1 && t.n0 + c < p.a.dl_pitch) {
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    w[k] = pack(__uint_as_float(r[8 * i + 2 * k]), __uint_as_float(r[8 * i + 2 * k + 1]));
-                                box_put(box, lane, part * 4 + i, make_uint4(w[0], w[1], w[2], w[3]));
+                            for (int i = 0; i < 8; ++i) {
+                                const int at = 4 * i + (lane >> 3);
+                                if (row0 + at < p.a.rows)
+                                    *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
                             }
                         }
                         __syncwarp();
-                        const int piece = lane & 7, col = t.n0 + c + 8 * piece;
-                        uint16_t *out = static_cast<uint16_t *>(p.a.dl) + col;
+                    } else {
+                        const bool dx = t.kind == TILE_DX;
+                        const int rows = dx ? count : p.a.words;   // of this tile's M side
+                        const bool wide = dx || p.a.dw_f32;        // 32-bit results
+                        const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                        if ((t.nk == 0 && add) || row0 >= rows) continue;
+                        const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
+                        uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
+                                          : static_cast<uint8_t *>(p.a.dw);
+                        // rows that 16-byte words make up
+                        const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 4 * i + (lane >> 3);
-                            if (row0 + r < p.a.rows && c + 8 * piece < p.bn && col < p.a.dl_pitch)
-                                *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + r) * p.a.dl_pitch) = box_get(box, r, piece);
+                        for (int k = 0; k < 32; ++k) {
+                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
+                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
                         }
-                        __syncwarp();
-                    }
-                } else {
-                    const bool dx = t.kind == TILE_DX;
-                    const int width = min(p.bn, p.a.hidden - t.n0);
-                    const float mult = p.a.factor * (p.a.unit ? __ldg(p.a.unit + 1) : 1.0f);
-                    const int rows = dx ? count : p.a.words;   // of this tile's M side
-                    const bool wide = dx || p.a.dw_f32;        // 32-bit results
-                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
-                    const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
-                    uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
-                                      : static_cast<uint8_t *>(p.a.dw);
-                    // rows that 16-byte words make up
-                    const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
-                    const int cols = wide ? 32 : 64, per = wide ? 4 : 8, piece = lane & 7;
-                    if (t.nk > 0 || !add) {
-#pragma unroll 1
-                        for (int c = h * cols; c < width && row0 < rows; c += 2 * cols) {
+                        if (!wide) {
+                            put_half(r[0], 0);
+                            put_half(r[1], 1);
+                        }
+                        const int per = wide ? 4 : 8, size = wide ? 4 : 2;
 #pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                if (part == 1 && wide) break;
-                                uint32_t r[32];
-                                if (t.nk > 0) {
-                                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(c + 32 * part), r);
-                                    ptx::tmem_ld_wait();
-                                } else {
+                        for (int i = 0; i < 2; ++i) {
+                            if (i == 1 && (!wide || u + 32 >= left)) break;
+                            if (wide) {
 #pragma unroll
-                                    for (int i = 0; i < 32; ++i) r[i] = 0u;
-                                }
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * mult);
-                                if (wide) {
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        box_put(box, lane, i, make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]));
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        uint32_t w[4];
-#pragma unroll
-                                        for (int k = 0; k < 4; ++k)
-                                            w[k] = pack(__uint_as_float(r[8 * i + 2 * k]), __uint_as_float(r[8 * i + 2 * k + 1]));
-                                        box_put(box, lane, part * 4 + i, make_uint4(w[0], w[1], w[2], w[3]));
-                                    }
-                                }
+                                for (int k = 0; k < 8; ++k)
+                                    box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
                             }
                             __syncwarp();
-                            const int col0 = t.n0 + c;
+                            // the box's rows, of 128 bytes from column c on
+                            const int c = t.n0 + c0 + u + 32 * i;
                             if (words) {
-                                const int col = col0 + per * piece;
-                                uint8_t *dst = out + (int64_t)col * (wide ? 4 : 2);
+                                const int piece = lane & 7, col = c + per * piece;
+                                uint8_t *dst = out + ((int64_t)(row0 + (lane >> 3)) * pitch + col) * size;
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const int r = 4 * i + (lane >> 3);
-                                    if (row0 + r >= rows || col >= pitch) continue;
-                                    uint4 *at = reinterpret_cast<uint4 *>(dst + (int64_t)(row0 + r) * pitch * (wide ? 4 : 2));
-                                    uint4 v = box_get(box, r, piece);
+                                for (int k = 0; k < 8; ++k) {
+                                    const int at = 4 * k + (lane >> 3);
+                                    if (row0 + at >= rows || col >= pitch) continue;
+                                    uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
+                                    uint4 v = box_get(box, at, piece);
                                     if (add) {
-                                        const uint4 o = *at;
+                                        const uint4 o = *to;
                                         v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
                                         v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
                                         v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
                                         v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
                                     }
-                                    *at = v;
+                                    *to = v;
                                 }
                             } else {
-                                for (int r = 0; r < min(32, rows - row0); ++r) {
-                                    for (int e = lane; e < cols && col0 + e < pitch; e += 32) {
-                                        const int64_t at = (int64_t)(row0 + r) * pitch + col0 + e;
-                                        const uint8_t *src = box + r * 128 + (((e / per) ^ (r & 7)) * 16);
+                                for (int at = 0; at < min(32, rows - row0); ++at) {
+                                    for (int e = lane; e < 8 * per && c + e < pitch; e += 32) {
+                                        const int64_t to = (int64_t)(row0 + at) * pitch + c + e;
+                                        const uint8_t *src = box + at * 128 + (((e / per) ^ (at & 7)) * 16);
                                         if (wide) {
                                             const float v = reinterpret_cast<const float *>(src)[e % per];
-                                            float *dst = reinterpret_cast<float *>(out) + at;
+                                            float *dst = reinterpret_cast<float *>(out) + to;
                                             *dst = add ? *dst + v : v;
                                         } else {
-                                            reinterpret_cast<uint16_t *>(out)[at] = reinterpret_cast<const uint16_t *>(src)[e % per];
+                                            reinterpret_cast<uint16_t *>(out)[to] = reinterpret_cast<const uint16_t *>(src)[e % per];
                                         }
                                     }
                                 }
@@ -620,16 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (t.nk > 0) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
-                        else ptx::mbar_arrive(&tempty[acc]);
-                    }
-                    seen ^= 1u << acc;
-                    if (SUB == 1) b ^= 1;
-                }
+                if constexpr (MODE == LCE_STATS)
+                    if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
