@@ -131,59 +131,90 @@ __device__ __forceinline__ uint32_t word_of(uint64_t key) { return (uint32_t)(ke
 // follow the order of the list: below this CTA's range, smaller digits, earlier
 // warps, earlier in the warp.  16384 tokens, 32000 words: 9 us (sorting chunks and
 // merging them took 32).
-template <bool FIRST>
-__global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_constant__ EmbedArgs a, const uint64_t *in,
-                                                                  uint64_t *out, int *long_words, int shift, int range)
+struct SortArgs {
+    Indices tokens;
+    const uint64_t *in;
+    uint64_t *out;
+    int *long_words;
+    uint32_t *err;
+    int64_t vocab;
+    uint32_t padding;   // a word of the vocabulary, or kNone
+    int n, shift, range;
+    int64_t listed_padding;
+};
+
+template <bool FIRST, bool WIDE>
+__global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_constant__ SortArgs a)
 {
     pdl_begin();
     extern __shared__ uint32_t cnt[];   // [kSortWarps][range]
-    __shared__ uint32_t warp_sums[kSortWarps], below_sums[kSortWarps], total;
+    __shared__ uint32_t warp_sums[kSortWarps], below_sums[kSortWarps];
     constexpr int UNROLL = 8;
     constexpr uint32_t mask = (1u << kDigitBits) - 1;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const uint32_t d0 = blockIdx.x * (uint32_t)range, d1 = d0 + (uint32_t)range;
-    const bool last = blockIdx.x == gridDim.x - 1;
-    const int64_t seg = ((a.rows + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const int64_t lo = warp * seg, hi = min(a.rows, lo + seg);
-    for (int i = t; i < kSortWarps * range; i += kSortThreads) cnt[i] = 0;
-    if (blockIdx.x == 0 && t == 0) *long_words = 0;
+    const uint32_t range = (uint32_t)a.range, d0 = blockIdx.x * range;
+    const int seg = ((a.n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+    const int lo = min(a.n, warp * seg), hi = min(a.n, lo + seg);
+    for (int i = t; i < kSortWarps * a.range; i += kSortThreads) cnt[i] = 0;
+    if (blockIdx.x == 0 && t == 0) *a.long_words = 0;
     __syncthreads();
-    uint32_t *mine = cnt + warp * range;
-    auto key_at = [&](int64_t i) -> uint64_t {
-        if (i >= hi) return ~0ull;
-        if constexpr (FIRST) {
-            const int64_t token = a.tokens.at(i);
-            const bool inside = token >= 0 && token < a.vocab, none = token == a.padding;
-            if (!inside && !none && blockIdx.x == 0) atomicOr(a.err, TF_DEVERR_INDEX);
-            return (uint64_t)(inside && !none ? (uint32_t)token : kNone) << 32 | (uint32_t)i;
+    uint32_t *mine = cnt + warp * a.range;
+    // 32*UNROLL entries from i on: their words (kNone: not there) and, of keys, their rows
+    auto load = [&](int i, uint32_t (&word)[UNROLL], uint32_t (&row)[UNROLL]) {
+        if constexpr (!FIRST) {
+            uint64_t v[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? a.in[i + 32 * u] : ~0ull;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                word[u] = word_of(v[u]);
+                row[u] = (uint32_t)v[u];
+            }
+        } else if constexpr (WIDE) {
+            uint64_t v[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? static_cast<const uint64_t *>(a.tokens.p)[i + 32 * u] : ~0ull;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint64_t)a.vocab && (uint32_t)v[u] != a.padding ? (uint32_t)v[u] : kNone;
         } else {
-            return in[i];
+            uint32_t v[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? static_cast<const uint32_t *>(a.tokens.p)[i + 32 * u] : kNone;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint32_t)a.vocab && v[u] != a.padding ? v[u] : kNone;
         }
     };
     uint32_t low = 0;
-    for (int64_t i = lo; i < hi; i += 32 * UNROLL) {
-        uint64_t key[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + u * 32 + lane);
+    for (int i = lo + lane; i < hi; i += 32 * UNROLL) {
+        uint32_t word[UNROLL], row[UNROLL];
+        load(i, word, row);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const uint32_t digit = (word_of(key[u]) >> shift) & mask;
-            if (word_of(key[u]) == kNone) continue;
-            low += digit < d0;
-            if (digit >= d0 && digit < d1) atomicAdd(mine + (digit - d0), 1u);
+            const uint32_t digit = (word[u] >> a.shift) & mask, at = digit - d0;
+            low += word[u] != kNone && digit < d0;
+            if (word[u] != kNone && at < range) atomicAdd(mine + at, 1u);
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low += __shfl_xor_sync(0xffffffffu, low, o);
     if (lane == 0) below_sums[warp] = low;
+    if (FIRST && blockIdx.x == 0)   // one CTA reports the tokens that are neither words nor the padding
+        for (int i = t; i < a.n; i += kSortThreads) {
+            const int64_t token = a.tokens.at(i);
+            if ((token < 0 || token >= a.vocab) && token != a.listed_padding) atomicOr(a.err, TF_DEVERR_INDEX);
+        }
     __syncthreads();
-    uint32_t base = 0;
-    for (int w = 0; w < kSortWarps; ++w) base += below_sums[w];
-    // counters become places, a thread per digit
-    for (int d = 0; d < range; d += kSortThreads) {
+    uint32_t base = below_sums[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) base += __shfl_xor_sync(0xffffffffu, base, o);
+    // counters become places: a warp per 32 digits' sums, then a thread per digit
+    for (int d = 0; d < a.range; d += kSortThreads) {
+        const bool live = d + t < a.range;
         uint32_t sum = 0;
-        if (d + t < range)
-            for (int w = 0; w < kSortWarps; ++w) sum += cnt[w * range + d + t];
+        if (live) {
+#pragma unroll
+            for (int w = 0; w < kSortWarps; ++w) sum += cnt[w * a.range + d + t];
+        }
         uint32_t scan = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -192,44 +223,50 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
         }
         if (lane == 31) warp_sums[warp] = scan;
         __syncthreads();
-        uint32_t at = base + scan - sum, all = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
-            if (w < warp) at += warp_sums[w];
-            all += warp_sums[w];
+        uint32_t before = warp_sums[lane], all = before;   // this lane's warp; those before this warp, and all
+        before = lane < warp ? before : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            all += __shfl_xor_sync(0xffffffffu, all, o);
         }
+        uint32_t at = base + before + scan - sum;
         base += all;
-        if (d + t < range)
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t n = cnt[w * range + d + t];
-                cnt[w * range + d + t] = at;
-                at += n;
+        if (live) {
+            for (int w = 0; w < kSortWarps; w += 8) {
+                uint32_t n[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) n[k] = cnt[(w + k) * a.range + d + t];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    cnt[(w + k) * a.range + d + t] = at;
+                    at += n[k];
+                }
             }
+        }
         __syncthreads();
     }
-    if (t == 0) total = base;
-    __syncthreads();
-    for (int64_t i = lo; i < hi; i += 32 * UNROLL) {
-        uint64_t key[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + u * 32 + lane);
+    for (int i0 = lo; i0 < hi; i0 += 32 * UNROLL) {
+        uint32_t word[UNROLL], row[UNROLL];
+        load(i0 + lane, word, row);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const uint32_t digit = (word_of(key[u]) >> shift) & mask;
-            const bool in_range = word_of(key[u]) != kNone && digit >= d0 && digit < d1;
+            const uint32_t at = ((word[u] >> a.shift) & mask) - d0;
+            const bool in_range = word[u] != kNone && at < range;
             const unsigned active = __ballot_sync(0xffffffffu, in_range);
             if (active == 0) continue;
             if (in_range) {
-                const unsigned same = __match_any_sync(active, digit);
-                const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[digit - d0];
-                out[first + before] = key[u];
+                const unsigned same = __match_any_sync(active, at);
+                const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[at];
+                a.out[first + before] = (uint64_t)word[u] << 32 | (FIRST ? (uint32_t)(i0 + 32 * u + lane) : row[u]);
                 __syncwarp(active);
-                if (before == 0) mine[digit - d0] = first + __popc(same);
+                if (before == 0) mine[at] = first + __popc(same);
             }
             __syncwarp();
         }
     }
-    if (last)   // the rest have no gradient
-        for (int64_t i = total + t; i < a.rows; i += kSortThreads) out[i] = ~0ull;
+    if (blockIdx.x == gridDim.x - 1)   // the rest have no gradient
+        for (int64_t i = (int64_t)base + t; i < a.n; i += kSortThreads) a.out[i] = ~0ull;
 }
 
 // Keys of [lo, hi) below `key`.
@@ -313,21 +350,21 @@ __device__ __forceinline__ void fill_zeros(const SumArgs &a, int64_t v0)
 // `lanes` threads per piece, each with VEC neighbouring columns of a slice of
 // lanes*VEC; the CTA's other threads take further pieces.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kSumThreads) sum_pieces_kernel(const __grid_constant__ SumArgs a)
+__global__ void __launch_bounds__(kSumThreads, 5) sum_pieces_kernel(const __grid_constant__ SumArgs a)
 {
     pdl_begin();
     if ((int)blockIdx.x >= a.sum_blocks) {
         if (blockIdx.y == 0) fill_zeros(a, (int64_t)((int)blockIdx.x - a.sum_blocks) * kFillRows);
         return;
     }
-    constexpr int UNROLL = 8;
+    constexpr int UNROLL = VEC * sizeof(T) == 16 ? 4 : 8;
     using P = Pack<T, VEC>;
     const int p = (int)blockIdx.x * (kSumThreads / a.lanes) + (int)threadIdx.x / a.lanes;
     const int c = ((int)blockIdx.y * a.lanes + (int)threadIdx.x % a.lanes) * VEC;
     if (p >= a.pieces || c >= a.hidden) return;
-    const int64_t first = (int64_t)p * a.piece, end = min(first + a.piece, a.n);
+    const int first = p * a.piece, n = (int)a.n, end = min(first + a.piece, n);   // (n + 2*piece fits)
     const T *dy = static_cast<const T *>(a.dy) + c;
-    auto word_at = [&](int64_t i) { return i >= 0 && i < a.n ? word_of(__ldg(a.keys + i)) : kNone; };
+    auto word_at = [&](int i) { return i >= 0 && i < n ? word_of(__ldg(a.keys + i)) : kNone; };
     // A word that goes on behind the piece it begins in for `piece` rows or more is long: each
     // of its pieces leaves a partial sum.  Otherwise the piece that it begins in finishes it.
     uint32_t word = word_at(first);
@@ -336,7 +373,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_pieces_kernel(const __grid_co
     const bool head_long = head && (word_at(first + a.piece - 1) == word || word_at(first - a.piece - 1) == word);
     const bool tail = final != kNone && word_at(end) == final;
     const bool tail_long = tail && (word_at(end + a.piece - 1) == final || (head && final == word));
-    const int64_t limit = tail && !tail_long ? min(end + a.piece, a.n) : end;
+    const int limit = tail && !tail_long ? min(end + a.piece, n) : end;
     float sum[VEC] = {}, low[VEC] = {};
     int held = 0;
     bool at_head = head;
@@ -356,14 +393,14 @@ __global__ void __launch_bounds__(kSumThreads) sum_pieces_kernel(const __grid_co
         at_head = false;
     };
     const uint32_t skipped = head && !head_long ? word : kNone;   // finished by the piece before
-    auto key_at = [&](int64_t i) {
+    auto key_at = [&](int i) {
         const uint64_t key = i < limit ? __ldg(a.keys + i) : ~0ull;
         return i < end || word_of(key) == final ? key : ~0ull;
     };
     uint64_t key[UNROLL];
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) key[u] = key_at(first + u);
-    for (int64_t i = first; i < limit; i += UNROLL) {
+    for (int i = first; i < limit; i += UNROLL) {
         P v[UNROLL];
         uint32_t w[UNROLL];
 #pragma unroll
@@ -541,12 +578,14 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
         const int64_t digits = all < most ? all : most, sms = sm_count() > 152 ? 152 : sm_count();
         const int64_t range = (digits + sms - 1) / sms < 64 ? 64 : (digits + sms - 1) / sms;
         const dim3 grid((unsigned)((digits + range - 1) / range));
-        const size_t smem = (size_t)(kSortWarps * range * 4);
-        auto kern = pass == 0 ? count_sort_kernel<true> : count_sort_kernel<false>;
+        SortArgs q = {};
+        q.tokens = a.tokens; q.in = first; q.out = pass == 0 ? first : keys; q.long_words = s.long_words; q.err = a.err;
+        q.vocab = a.vocab; q.listed_padding = a.padding;
+        q.padding = a.padding >= 0 && a.padding < a.vocab ? (uint32_t)a.padding : kNone;
+        q.n = (int)a.rows; q.shift = pass * kDigitBits; q.range = (int)range;
+        auto kern = pass > 0 ? count_sort_kernel<false, false> : a.tokens.wide ? count_sort_kernel<true, true> : count_sort_kernel<true, false>;
         e = raise_smem_limit(reinterpret_cast<const void *>(kern));
-        if (e == cudaSuccess)
-            e = launch_pdl(kern, grid, dim3(kSortThreads), smem, st, a, static_cast<const uint64_t *>(first),
-                           pass == 0 ? first : keys, s.long_words, pass * kDigitBits, (int)range);
+        if (e == cudaSuccess) e = launch_pdl(kern, grid, dim3(kSortThreads), (size_t)(kSortWarps * range * 4), st, q);
     }
     if (e != cudaSuccess) return e;
     if (a.dtype == TF_FP32) e = sums_typed<float>(a, s, st);
