@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include "lm_internal.h"
+#include "ptx_sm100.cuh"
 
 namespace tf {
 namespace {
@@ -296,6 +297,8 @@ struct SumArgs {
     int64_t dy_stride, n, vocab, pitch;
     int hidden, accumulate, piece, pieces, lanes, sum_blocks;
     float scale;
+    uint32_t *err;
+    uint64_t wait_ns;
 };
 
 // A row's columns.  Adding to what is there is left to the L2, which does not make
@@ -348,20 +351,33 @@ __device__ __forceinline__ void fill_zeros(const SumArgs &a, int64_t v0)
 }
 
 // `lanes` threads per piece, each with VEC neighbouring columns of a slice of
-// lanes*VEC; the CTA's other threads take further pieces.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kSumThreads, 5) sum_pieces_kernel(const __grid_constant__ SumArgs a)
+// lanes*VEC; the CTA's other threads take further pieces.  RING: the rows come through
+// shared memory by bulk copies, two batches of eight ahead, which keeps more of them under
+// way than registers could (16384 rows of 4096 bf16 into 32000 words: 74 us with registers).
+template <typename T, int VEC, bool RING>
+__global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(const __grid_constant__ SumArgs a)
 {
     pdl_begin();
     if ((int)blockIdx.x >= a.sum_blocks) {
         if (blockIdx.y == 0) fill_zeros(a, (int64_t)((int)blockIdx.x - a.sum_blocks) * kFillRows);
         return;
     }
-    constexpr int UNROLL = VEC * sizeof(T) == 16 ? 4 : 8;
+    constexpr int UNROLL = RING || VEC * sizeof(T) < 16 ? 8 : 4;
     using P = Pack<T, VEC>;
-    const int p = (int)blockIdx.x * (kSumThreads / a.lanes) + (int)threadIdx.x / a.lanes;
-    const int c = ((int)blockIdx.y * a.lanes + (int)threadIdx.x % a.lanes) * VEC;
-    if (p >= a.pieces || c >= a.hidden) return;
+    const int member = (int)threadIdx.x % a.lanes, group = (int)threadIdx.x / a.lanes;
+    const int p = (int)blockIdx.x * (kSumThreads / a.lanes) + group;
+    const int slice = (int)blockIdx.y * a.lanes * VEC, c = slice + member * VEC;
+    __shared__ __align__(128) P ring[RING ? 2 * UNROLL * kSumThreads : 1];
+    __shared__ __align__(8) uint64_t full[kSumThreads / 32][2];
+    if (RING) {
+        if (threadIdx.x < kSumThreads / 32 * 2) {
+            ptx::mbar_init(&full[threadIdx.x / 2][threadIdx.x % 2], 1);
+            ptx::mbar_init_fence();
+        }
+        __syncthreads();
+    }
+    if (p >= a.pieces || (!RING && c >= a.hidden)) return;
+    const bool live = c < a.hidden;   // (RING: the others take part in the barriers)
     const int first = p * a.piece, n = (int)a.n, end = min(first + a.piece, n);   // (n + 2*piece fits)
     const T *dy = static_cast<const T *>(a.dy) + c;
     auto word_at = [&](int i) { return i >= 0 && i < n ? word_of(__ldg(a.keys + i)) : kNone; };
@@ -378,7 +394,7 @@ __global__ void __launch_bounds__(kSumThreads, 5) sum_pieces_kernel(const __grid
     int held = 0;
     bool at_head = head;
     auto flush = [&](bool goes_on) {
-        if (word != kNone && (!at_head || head_long)) {
+        if (live && word != kNone && (!at_head || head_long)) {
 #pragma unroll
             for (int k = 0; k < VEC; ++k) sum[k] += low[k];
             if (at_head || goes_on)
@@ -397,36 +413,84 @@ __global__ void __launch_bounds__(kSumThreads, 5) sum_pieces_kernel(const __grid
         const uint64_t key = i < limit ? __ldg(a.keys + i) : ~0ull;
         return i < end || word_of(key) == final ? key : ~0ull;
     };
-    uint64_t key[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) key[u] = key_at(first + u);
-    for (int i = first; i < limit; i += UNROLL) {
-        P v[UNROLL];
-        uint32_t w[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            w[u] = word_of(key[u]);
-            if (w[u] != kNone && w[u] != skipped) v[u] = *reinterpret_cast<const P *>(dy + (int64_t)(uint32_t)key[u] * a.dy_stride);
+    auto add_row = [&](uint32_t w, const P &v) {
+        if (w != word) {
+            flush(false);
+            word = w;
         }
+        if (w == skipped) return;
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + UNROLL + u);   // the next ones, while the rows are under way
+        for (int k = 0; k < VEC; ++k) low[k] += widen<T>(v.v[k]);
+        if (++held == kLevel) {
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            if (w[u] == kNone) break;   // (the last of the list, or of the word that went on)
-            if (w[u] != word) {
-                flush(false);
-                word = w[u];
+            for (int k = 0; k < VEC; ++k) {
+                sum[k] += low[k];
+                low[k] = 0.0f;
             }
-            if (w[u] == skipped) continue;
+            held = 0;
+        }
+    };
+    if constexpr (RING) {
+        const uint32_t bytes = (uint32_t)(min(a.lanes * VEC, a.hidden - slice) * (int)sizeof(T));
+        // the first thread of the piece asks for a batch's rows
+        auto fetch = [&](int i, int half) {
+            if (member != 0) return;
+            uint64_t key[UNROLL];
+            uint32_t rows = 0;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) low[k] += widen<T>(v[u].v[k]);
-            if (++held == kLevel) {
+            for (int u = 0; u < UNROLL; ++u) {
+                key[u] = key_at(i + u);
+                const uint32_t w = word_of(key[u]);
+                if (w == kNone || w == skipped) key[u] = ~0ull;
+                else ++rows;
+            }
+            ptx::mbar_arrive_expect_tx(&full[group][half], rows * bytes);
+            const T *src = static_cast<const T *>(a.dy) + slice;
 #pragma unroll
-                for (int k = 0; k < VEC; ++k) {
-                    sum[k] += low[k];
-                    low[k] = 0.0f;
-                }
-                held = 0;
+            for (int u = 0; u < UNROLL; ++u)
+                if (key[u] != ~0ull)
+                    ptx::bulk_load(&ring[(half * UNROLL + u) * kSumThreads + group * a.lanes],
+                                   src + (int64_t)(uint32_t)key[u] * a.dy_stride, bytes, &full[group][half]);
+        };
+        bool ok = true;   // after a wait that ran out no other is made, and the loop goes on to its end
+        fetch(first, 0);
+        if (first + UNROLL < limit) fetch(first + UNROLL, 1);
+        int batch = 0;
+        for (int i = first; i < limit; i += UNROLL, ++batch) {
+            const int half = batch & 1;
+            uint32_t w[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) w[u] = word_of(key_at(i + u));
+            if (ok && !(ok = ptx::mbar_wait(&full[group][half], (uint32_t)(batch >> 1) & 1u, a.wait_ns)))
+                atomicOr(a.err, TF_DEVERR_PRODUCER_WAIT);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                if (w[u] == kNone) break;   // (the last of the list, or of the word that went on)
+                add_row(w[u], ring[(half * UNROLL + u) * kSumThreads + threadIdx.x]);
+            }
+            // the piece's threads have read the batch
+            __syncwarp();
+            if (a.lanes > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(a.lanes) : "memory");
+            if (i + 2 * UNROLL < limit) fetch(i + 2 * UNROLL, half);
+        }
+    } else {
+        uint64_t key[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) key[u] = key_at(first + u);
+        for (int i = first; i < limit; i += UNROLL) {
+            P v[UNROLL];
+            uint32_t w[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                w[u] = word_of(key[u]);
+                if (w[u] != kNone && w[u] != skipped) v[u] = *reinterpret_cast<const P *>(dy + (int64_t)(uint32_t)key[u] * a.dy_stride);
+            }
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + UNROLL + u);   // the next ones, while the rows are under way
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                if (w[u] == kNone) break;
+                add_row(w[u], v[u]);
             }
         }
     }
@@ -525,8 +589,10 @@ cudaError_t launch_sums(const EmbedArgs &a, SumArgs s, cudaStream_t st)
     const int slices = (a.hidden + s.lanes * VEC - 1) / (s.lanes * VEC), per_block = kSumThreads / s.lanes;
     s.sum_blocks = (s.pieces + per_block - 1) / per_block;
     const int64_t fill = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
-    return launch_pdl(sum_pieces_kernel<T, VEC>, dim3((unsigned)(s.sum_blocks + fill), (unsigned)slices), dim3(kSumThreads),
-                      0, st, s);
+    const dim3 grid((unsigned)(s.sum_blocks + fill), (unsigned)slices);
+    if constexpr (VEC * sizeof(T) == 16)
+        if (s.lanes >= 32) return launch_pdl(sum_pieces_kernel<T, VEC, true>, grid, dim3(kSumThreads), 0, st, s);
+    return launch_pdl(sum_pieces_kernel<T, VEC, false>, grid, dim3(kSumThreads), 0, st, s);
 }
 
 template <typename T>
@@ -572,6 +638,8 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
     s.pitch = pitch_of(a.hidden); s.hidden = a.hidden; s.accumulate = a.accumulate; s.scale = a.scale;
     s.piece = (int)piece_of(a.rows, a.hidden);
     s.pieces = (int)((a.rows + s.piece - 1) / s.piece);
+    s.err = a.err;
+    s.wait_ns = wait_limit_ns();
     cudaError_t e = cudaSuccess;
     for (int pass = 0; a.rows > 0 && e == cudaSuccess && pass < passes; ++pass) {
         const int64_t all = ((a.vocab - 1) >> (pass * kDigitBits)) + 1, most = (int64_t)1 << kDigitBits;

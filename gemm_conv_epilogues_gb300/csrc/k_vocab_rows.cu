@@ -18,6 +18,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "grouped.cuh"
 #include "lm_internal.h"
 
@@ -37,11 +39,12 @@ struct GatherArgs {
     LceArgs a;
     int *count, *index, *target;
     float *l2, *ca, *cb;       // backward
-    const float *unit;         // fp16's, else null
+    float *unit;               // backward
+    int unit_given;            // fp16: unit_kernel has been there
+    float *dot;                // forward: x w[target], in fp32
     uint16_t *x;
     int64_t x_pitch;
     int per_block;             // rows
-    int backward;
 };
 
 // 1: counts, 0: ignored (or outside the vocabulary, which the error word tells)
@@ -55,30 +58,60 @@ __device__ __forceinline__ bool counts(const LceArgs &a, int64_t i, int64_t *tar
     return false;
 }
 
-// A row of 16-bit values, by the widest words that fit it.
-__device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int n, int lane, int lanes)
+// The sum of two products of 16-bit pairs.
+template <typename T>
+__device__ __forceinline__ float pair_product(uint32_t u, uint32_t v)
 {
+    const float2 f = Half2Of<T>::unpack(u), g = Half2Of<T>::unpack(v);
+    return fmaf(f.x, g.x, f.y * g.y);
+}
+
+// `lanes` threads copy a row of 16-bit values, by the widest words that fit it; with a
+// type T, a thread returns its share of the row's product with `w`.
+template <typename T>
+__device__ __forceinline__ float copy_row(uint16_t *dst, const uint16_t *src, const uint16_t *w, int n, int lane, int lanes)
+{
+    constexpr bool DOT = !std::is_void<T>::value;
+    constexpr int UNROLL = DOT ? 2 : 4;
+    using P = typename std::conditional<DOT, T, __half>::type;
+    float sum[2] = {};
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0 && n % 8 == 0) {
-        for (int c = lane; c < n / 8; c += 4 * lanes) {
-            uint4 v[4];
+        for (int c = lane; c < n / 8; c += UNROLL * lanes) {
+            uint4 v[UNROLL], f[UNROLL];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (c + u * lanes < n / 8) v[u] = reinterpret_cast<const uint4 *>(src)[c + u * lanes];
+            for (int u = 0; u < UNROLL; ++u)
+                if (c + u * lanes < n / 8) {
+                    v[u] = reinterpret_cast<const uint4 *>(src)[c + u * lanes];
+                    if (DOT) f[u] = reinterpret_cast<const uint4 *>(w)[c + u * lanes];   // (weights of such widths are aligned)
+                }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (c + u * lanes < n / 8) reinterpret_cast<uint4 *>(dst)[c + u * lanes] = v[u];
+            for (int u = 0; u < UNROLL; ++u) {
+                if (c + u * lanes >= n / 8) break;
+                reinterpret_cast<uint4 *>(dst)[c + u * lanes] = v[u];
+                if (DOT) {
+                    sum[0] += pair_product<P>(v[u].x, f[u].x) + pair_product<P>(v[u].y, f[u].y);
+                    sum[1] += pair_product<P>(v[u].z, f[u].z) + pair_product<P>(v[u].w, f[u].w);
+                }
+            }
         }
     } else {
-        for (int c = lane; c < n; c += 8 * lanes) {
-            uint16_t v[8];
+        for (int c = lane; c < n; c += 4 * lanes) {
+            uint16_t v[4], f[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u * lanes < n) v[u] = src[c + u * lanes];
+            for (int u = 0; u < 4; ++u)
+                if (c + u * lanes < n) {
+                    v[u] = src[c + u * lanes];
+                    if (DOT) f[u] = w[c + u * lanes];
+                }
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u * lanes < n) dst[c + u * lanes] = v[u];
+            for (int u = 0; u < 4; ++u) {
+                if (c + u * lanes >= n) break;
+                dst[c + u * lanes] = v[u];
+                if (DOT) sum[u & 1] += pair_product<P>(v[u], f[u]);
+            }
         }
     }
+    return sum[0] + sum[1];
 }
 
 __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lanes)
@@ -91,11 +124,14 @@ __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lan
 
 // A CTA takes per_block rows; it counts those that count before them itself,
 // which reads the targets once per CTA, but needs no CTA to wait for another.
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs g)
+// T: the operands' type in the forward pass, void in the backward pass.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_constant__ GatherArgs g)
 {
     pdl_begin();
+    constexpr bool BACKWARD = std::is_void<T>::value;
     __shared__ int warps[kThreads / 32];
-    __shared__ int place[kThreads];
+    __shared__ int place[kThreads], hit[kThreads];
     const LceArgs &a = g.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t first = (int64_t)blockIdx.x * g.per_block, end = min(first + g.per_block, a.rows);
@@ -110,6 +146,34 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     __syncthreads();
     before = 0;
     for (int w = 0; w < kThreads / 32; ++w) before += warps[w];
+    // bf16's unit of the gradients of the logits: the first row's |dloss|
+    float unit = 1.0f;
+    if (BACKWARD) {
+        if (g.unit_given) {
+            unit = g.unit[0];
+        } else if (a.dloss) {
+            __shared__ int where;
+            for (int64_t base = 0; base < a.rows; base += kThreads) {
+                if (t == 0) where = kThreads;
+                __syncthreads();
+                int64_t target;
+                if (base + t < a.rows && counts(a, base + t, &target, false)) atomicMin(&where, t);
+                __syncthreads();
+                if (where < kThreads) {
+                    const float d = fabsf(a.dloss[base + where]);
+                    if (d > 0x1p-40f && d < 0x1p40f) unit = 1.0f / d;
+                    break;
+                }
+                __syncthreads();
+            }
+            if (end == a.rows && t == 0) {
+                g.unit[0] = unit;
+                g.unit[1] = 1.0f / unit;
+            }
+        } else if (end == a.rows && t == 0) {
+            g.unit[0] = g.unit[1] = 1.0f;
+        }
+    }
     for (int64_t base = first; base < end; base += kThreads) {
         const int64_t i = base + t;
         int64_t target = 0;
@@ -124,26 +188,42 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
             before += warps[w];
         }
         place[t] = used ? at : -1;
+        hit[t] = (int)target;
         if (used) {
             g.index[at] = (int)i;
             g.target[at] = (int)target;
-            if (g.backward) {
-                const float d = a.dloss ? a.dloss[i] : 1.0f, unit = g.unit ? g.unit[0] : 1.0f;
+            if (BACKWARD) {
+                const float d = a.dloss ? a.dloss[i] : 1.0f;
                 g.l2[at] = a.lse[i] * kLog2e;
                 g.ca[at] = (a.dlse ? d + a.dlse[i] : d) * unit;
                 g.cb[at] = d * unit;
             }
-        } else if (live && !g.backward) {
+        } else if (live && !BACKWARD) {
             a.loss[i] = 0.0f;
             a.lse[i] = 0.0f;
         }
         __syncthreads();
-        for (int r = warp; r < (int)min((int64_t)kThreads, end - base); r += kThreads / 32) {
+        const int lanes = g.per_block == 1 ? kThreads : 32, member = t % lanes;   // a row to a warp, or to the CTA
+        for (int r = t / lanes; r < (int)min((int64_t)kThreads, end - base); r += kThreads / lanes) {
             const int64_t row = base + r;
-            if (place[r] >= 0)
-                copy_row(g.x + place[r] * g.x_pitch, static_cast<const uint16_t *>(a.x) + row * a.x_stride, a.hidden, lane, 32);
-            else if (a.dx)
-                zero_row(static_cast<uint16_t *>(a.dx) + row * a.dx_stride, a.hidden, lane, 32);
+            if (place[r] >= 0) {
+                float dot = copy_row<T>(g.x + place[r] * g.x_pitch, static_cast<const uint16_t *>(a.x) + row * a.x_stride,
+                                        static_cast<const uint16_t *>(a.w) + (int64_t)hit[r] * a.hidden, a.hidden, member, lanes);
+                if (!BACKWARD) {
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+                    if (lanes > 32) {   // (the CTA's only row)
+                        __shared__ float dots[kThreads / 32];
+                        if (lane == 0) dots[warp] = dot;
+                        __syncthreads();
+                        dot = 0.0f;
+                        for (int w = 0; w < kThreads / 32; ++w) dot += dots[w];
+                    }
+                    if (member == 0) g.dot[place[r]] = dot;
+                }
+            } else if (a.dx) {
+                zero_row(static_cast<uint16_t *>(a.dx) + row * a.dx_stride, a.hidden, member, lanes);
+            }
         }
     }
     if (end == a.rows) {   // the last CTA
@@ -154,101 +234,79 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     }
 }
 
-// fp16 holds the gradients of the logits times a power of two that puts the
-// largest they can be below 2^15: a word's share of 1e-5 in a mean over 16384 rows would
-// otherwise lie far below fp16's smallest.  unit[0] is that power, unit[1] its inverse.
+// The gradients of the logits are held in units of a typical |dloss|, which is often
+// that of all rows: a target's (p - 1) dloss is then rounded near one, where it is
+// off by no more than p, and not by dloss's own rounding, the same in every row (dx of 3300 rows
+// with a mean's weights: relative error 2.9e-3 without, 1.9e-3 with units).  bf16 takes the first
+// row's.  fp16, whose exponents are few, takes the largest, times 2^14:
+// a word's share of 1e-5 would otherwise lie far below its smallest.  unit[0] is
+// the factor, unit[1] its inverse.
 __global__ void __launch_bounds__(1024) unit_kernel(const __grid_constant__ LceArgs a, float *unit)
 {
     pdl_begin();
-    __shared__ float warps[32];
-    float most = 0.0f;
+    __shared__ float2 warps[32];
+    float most = 0.0f, both = 0.0f;   // the largest |dloss|, and |dloss| + |dlse|, which bounds the gradients
     for (int64_t i = threadIdx.x; i < a.rows; i += 1024) {
         int64_t target;
         if (!counts(a, i, &target, false)) continue;
-        const float d = a.dloss ? a.dloss[i] : 1.0f;
-        most = fmaxf(most, fabsf(d) + (a.dlse ? fabsf(a.dlse[i]) : 0.0f));
+        const float d = a.dloss ? fabsf(a.dloss[i]) : 1.0f;
+        most = fmaxf(most, d);
+        both = fmaxf(both, d + (a.dlse ? fabsf(a.dlse[i]) : 0.0f));
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
+    for (int o = 16; o > 0; o >>= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        both = fmaxf(both, __shfl_xor_sync(0xffffffffu, both, o));
+    }
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = make_float2(most, both);
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 0; w < 32; ++w) most = fmaxf(most, warps[w]);
-        // most < 2^(exponent + 1); both powers of two are normal numbers
-        const int exponent = (int)((__float_as_uint(most) >> 23) & 255u) - 127;
-        const int power = most > 0.0f && exponent < 128 ? min(max(14 - exponent, -126), 126) : 0;
-        unit[0] = __uint_as_float((uint32_t)(power + 127) << 23);
-        unit[1] = __uint_as_float((uint32_t)(127 - power) << 23);
+        for (int w = 0; w < 32; ++w) {
+            most = fmaxf(most, warps[w].x);
+            both = fmaxf(both, warps[w].y);
+        }
+        const float size = both <= 2.0f * most ? most : both;   // (2^15 and 2^14 at most)
+        // (both are normal numbers)
+        unit[0] = size > 0x1p-100f && size < 0x1p100f ? 0x1p14f / size : 1.0f;
+        unit[1] = 1.0f / unit[0];
     }
 }
 
 // ---------------------------------------------------------------- loss
 
 struct LossArgs {
-    const int *count, *index, *target;
+    const int *count, *index;
     const float2 *part;
-    const float *at_target;
-    const uint16_t *x, *w;
+    const float *at_target, *dot;
     float *loss, *lse;
-    int64_t x_pitch;
-    int rows, slots, per_block, hidden, bf16;
+    int rows, slots, per_block;
     float scale;
 };
 
 // `per_block` rows per CTA (one, or four, whose neighbouring slots fill a sector), a
 // row's slots over the CTA's threads.
 //
-// The target's logit is taken again, in fp32 from the operands: the tensor cores'
-// truncation leaves it 1e-5 low, which is what the loss would be off by (relative
-// error of 4096 rows' losses, 4096 terms per logit: 1.3e-6, and 9e-7 so).  It takes the
-// place of the products' own in the loss.  With m the largest logit, t
-// the target's, A the others' sum e^(l - m) and d = m - t the loss is
-// log(1 + A e^d), so that a sure target's loss keeps its digits.  lse stays that of the
-// products' logits, which the backward pass takes it from: what both are off by
-// cancels in 1 - e^(l - lse), of which a sure target's gradient consists.
+// The target's logit is the one that `gather` has taken in fp32 from the operands:
+// the tensor cores' truncation leaves theirs 1e-5 low, which is what the loss would be
+// off by (relative error of 4096 rows' losses, 4096 terms per logit: 1.3e-6, and 9e-7
+// so).  With m the largest logit, t the target's, A the others' sum e^(l - m) and
+// d = m - t the loss is log(1 + A e^d), so that a sure target's loss keeps its digits.
+// lse stays that of the products' logits, which the backward pass takes it from: what
+// both are off by cancels in 1 - e^(l - lse), of which a sure target's gradient consists.
 __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ LossArgs p)
 {
     pdl_begin();
     constexpr int WARPS = kThreads / 32;
     __shared__ float2 red[WARPS][4];
-    __shared__ float dots[WARPS];
     const int count = *p.count, per = p.per_block, row0 = (int)blockIdx.x * per;
     if (row0 >= count) return;
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, x = t % per, row = row0 + x;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = row0 + t % per, lanes = kThreads / per;
     const float c = p.scale * kLog2e;
     auto join = [&](float2 s, float2 v) {
         const float m = fmaxf(s.x, v.x), base = m == -INFINITY ? 0.0f : m;
         return make_float2(m, s.y * ex2_approx((s.x - base) * c) + v.y * ex2_approx((v.x - base) * c));
     };
-    // the target's logit, by WARPS/per warps
-    const int wide = WARPS / per, mine = row0 + warp / wide;
-    float dot = 0.0f;
-    if (mine < count) {
-        const uint16_t *a = p.x + mine * p.x_pitch, *b = p.w + (int64_t)p.target[mine] * p.hidden;
-        auto both = [&](uint32_t u, uint32_t v) {
-            const float2 f = p.bf16 ? Half2Of<__nv_bfloat16>::unpack(u) : Half2Of<__half>::unpack(u);
-            const float2 g = p.bf16 ? Half2Of<__nv_bfloat16>::unpack(v) : Half2Of<__half>::unpack(v);
-            return fmaf(f.x, g.x, f.y * g.y);
-        };
-        float s[4] = {};
-        const int at = (warp % wide) * 32 + lane, step = wide * 32;
-        if (p.hidden % 8 == 0)
-            for (int k = at; k < p.hidden / 8; k += step) {
-                const uint4 u = reinterpret_cast<const uint4 *>(a)[k], v = reinterpret_cast<const uint4 *>(b)[k];
-                s[0] += both(u.x, v.x);
-                s[1] += both(u.y, v.y);
-                s[2] += both(u.z, v.z);
-                s[3] += both(u.w, v.w);
-            }
-        else
-            for (int k = at; k < p.hidden; k += step) s[0] += both(a[k], b[k]);
-        dot = (s[0] + s[1]) + (s[2] + s[3]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if (lane == 0) dots[warp] = dot;
     float2 s = make_float2(-INFINITY, 0.0f);
-    const int lanes = kThreads / per;
     if (row < count)
         for (int k = t / per; k < p.slots; k += 4 * lanes) {
             float2 v[4];
@@ -263,14 +321,11 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     __syncthreads();
     if (t >= per || row >= count) return;
     for (int w = 1; w < WARPS; ++w) s = join(s, red[w][t]);
-    dot = 0.0f;
-    for (int w = 0; w < wide; ++w) dot += dots[t * wide + w];
-    const float target = p.scale * dot, d = p.scale * s.x - target;
+    const float d = p.scale * (s.x - p.dot[row]);
     float others = s.y - ex2_approx((p.at_target[row] - s.x) * c);
     if (others < 0.0f) others = 0.0f;   // (not a NaN)
-    const float loss = d > 60.0f ? d + logf(others + expf(-d)) : log1pf(others * expf(d));
     const int64_t i = p.index[row];
-    p.loss[i] = loss;
+    p.loss[i] = d > 60.0f ? d + logf(others + expf(-d)) : log1pf(others * expf(d));
     p.lse[i] = fmaf(p.scale, s.x, logf(s.y));
 }
 
@@ -320,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const uint16_t *w, 
     pdl_begin();
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
     for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step)
-        copy_row(out + r * pitch, w + r * hidden, hidden, threadIdx.x & 31, 32);
+        copy_row<void>(out + r * pitch, w + r * hidden, nullptr, hidden, threadIdx.x & 31, 32);
 }
 
 cudaError_t launch_pack(const LceArgs &a, int64_t v0, int64_t words, int64_t pitch, void *out, cudaStream_t st)
@@ -340,7 +395,7 @@ struct Plan {
     int64_t x_pitch, w_pitch, dl_pitch, dx_pitch;
     int64_t piece;          // words
     int splits;             // of dx
-    int64_t count, unit, index, target, l2, ca, cb, at_target, part, x, dl, dx, pack, bytes;
+    int64_t count, unit, index, target, l2, ca, cb, at_target, dot, part, x, dl, dx, pack, bytes;
 };
 
 // Words per piece where `most` bytes hold `per_word` each: as few pieces as fit, of
@@ -377,6 +432,7 @@ Plan plan_of(bool backward, int64_t rows, int64_t vocab, int64_t hidden)
     if (pack) p.piece = piece_of(vocab, p.w_pitch * 2, kPackBytes);
     if (!backward) {
         p.at_target = take(4 * rows);
+        p.dot = take(4 * rows);
         // two slots per tile of 256 words, for few rows of as little as 64
         const int64_t pieces = (vocab + p.piece - 1) / p.piece, few = rows < 256 ? rows : 256;
         const int64_t wide = 2 * (vocab / 256 + pieces) * rows, narrow = 2 * (vocab / 64 + pieces) * few;
@@ -390,14 +446,9 @@ Plan plan_of(bool backward, int64_t rows, int64_t vocab, int64_t hidden)
         p.dl_pitch = up(p.piece, 64);
         const int64_t all = 2 * rows * up(vocab, 64), least = 2 * rows * 512, cap = kDlBytes > least ? kDlBytes : least;
         p.dl = take(all < cap ? all : cap);
-        // splits: at least two waves of tiles, of at least eight K steps
-        const int64_t tile = lce_row_tile(rows), tiles = (rows + tile - 1) / tile * ((hidden + 255) / 256);
-        int64_t s = (2 * (int64_t)lce_units(rows) + tiles - 1) / tiles;
-        const int64_t row_bytes = p.dx_pitch * 4 * rows, by_bytes = kSplitBytes / row_bytes, by_steps = p.piece / (64 * 8);
-        s = s < by_bytes ? s : by_bytes;
-        s = s < by_steps ? s : by_steps;
-        s = s < 16 ? s : 16;
-        p.splits = s < 1 ? 1 : (int)s;
+        const int64_t row_bytes = p.dx_pitch * 4 * rows, by_bytes = kSplitBytes / row_bytes;
+        const int64_t splits = lce_splits(rows, p.piece, hidden);
+        p.splits = (int)(splits < by_bytes ? splits : by_bytes < 1 ? 1 : by_bytes);
         const int64_t most = 16 * row_bytes < kSplitBytes ? 16 * row_bytes : kSplitBytes;
         p.dx = take(row_bytes > most ? row_bytes : most);
     }
@@ -421,23 +472,21 @@ cudaError_t launch_gather(const LceArgs &a, const Plan &p, bool backward, cudaSt
     g.target = at<int>(a.ws, p.target);
     g.x = at<uint16_t>(a.ws, p.x);
     g.x_pitch = p.x_pitch;
-    g.backward = backward;
-    cudaError_t e = cudaSuccess;
-    if (backward) {
-        g.l2 = at<float>(a.ws, p.l2);
-        g.ca = at<float>(a.ws, p.ca);
-        g.cb = at<float>(a.ws, p.cb);
-        if (a.dtype == TF_FP16) {
-            float *unit = at<float>(a.ws, p.unit);
-            e = launch_pdl(unit_kernel, dim3(1), dim3(1024), 0, st, a, unit);
-            g.unit = unit;
-        }
+    // a row per CTA while they all run at once, a row per warp, or more where counting what lies
+    // before would take longer than that
+    g.per_block = a.rows <= 4 * sm_count() ? 1 : a.rows <= 16384 ? 8 : (int)up((a.rows + 2047) / 2048, 8);
+    const dim3 grid((unsigned)(a.rows ? (a.rows + g.per_block - 1) / g.per_block : 1));
+    if (!backward) {
+        g.dot = at<float>(a.ws, p.dot);
+        return launch_pdl(a.dtype == TF_BF16 ? gather_kernel<__nv_bfloat16> : gather_kernel<__half>, grid, dim3(kThreads), 0, st, g);
     }
-    if (e != cudaSuccess) return e;
-    // a row or two per warp, more where counting what lies before would take longer than that
-    g.per_block = a.rows <= 16384 ? 8 : (int)up((a.rows + 2047) / 2048, 8);
-    const int64_t blocks = a.rows ? (a.rows + g.per_block - 1) / g.per_block : 1;
-    return launch_pdl(gather_kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, g);
+    g.l2 = at<float>(a.ws, p.l2);
+    g.ca = at<float>(a.ws, p.ca);
+    g.cb = at<float>(a.ws, p.cb);
+    g.unit = at<float>(a.ws, p.unit);
+    g.unit_given = a.dtype == TF_FP16;
+    const cudaError_t e = g.unit_given ? launch_pdl(unit_kernel, dim3(1), dim3(1024), 0, st, a, g.unit) : cudaSuccess;
+    return e != cudaSuccess ? e : launch_pdl(gather_kernel<void>, grid, dim3(kThreads), 0, st, g);
 }
 
 LceProduct product_of(const LceArgs &a, const Plan &p)
@@ -493,10 +542,9 @@ cudaError_t launch_lce_forward(const LceArgs &a, cudaStream_t st)
     }
     if (e != cudaSuccess) return e;
     LossArgs l = {};
-    l.count = m.count; l.index = at<int>(a.ws, p.index); l.target = m.target; l.part = m.part; l.at_target = m.at_target;
-    l.x = static_cast<const uint16_t *>(m.x); l.w = static_cast<const uint16_t *>(a.w); l.loss = a.loss; l.lse = a.lse;
-    l.x_pitch = p.x_pitch; l.rows = (int)a.rows; l.slots = m.slot0; l.per_block = a.rows < 512 ? 1 : 4;
-    l.hidden = a.hidden; l.bf16 = a.dtype == TF_BF16; l.scale = a.scale;
+    l.count = m.count; l.index = at<int>(a.ws, p.index); l.part = m.part; l.at_target = m.at_target;
+    l.dot = at<float>(a.ws, p.dot); l.loss = a.loss; l.lse = a.lse; l.rows = (int)a.rows; l.slots = m.slot0;
+    l.per_block = a.rows < 512 ? 1 : 4; l.scale = a.scale;
     return launch_pdl(loss_kernel, dim3((unsigned)((a.rows + l.per_block - 1) / l.per_block)), dim3(kThreads), 0, st, l);
 }
 
@@ -508,7 +556,7 @@ cudaError_t launch_lce_backward(const LceArgs &a, cudaStream_t st)
     m.l2 = at<float>(a.ws, p.l2);
     m.ca = at<float>(a.ws, p.ca);
     m.cb = at<float>(a.ws, p.cb);
-    m.unit = a.dtype == TF_FP16 ? at<float>(a.ws, p.unit) : nullptr;
+    m.unit = at<float>(a.ws, p.unit);
     m.dl = at<void>(a.ws, p.dl);
     m.dl_pitch = p.dl_pitch;
     m.dx = a.dx ? at<float>(a.ws, p.dx) : nullptr;

@@ -12,16 +12,19 @@
 // Rows (DW: words) are the MMA's M side, so that a thread of the epilogue has a row
 // of the tile to itself and reduces over the vocabulary in its registers.
 //
-// Persistent kernel, one CTA (CG = 1) or CTA pair (CG = 2, cta_group::2) per SM
-// (pair).  A pair takes tiles of 512 x 256: two 256-row MMAs share a K step's B
-// tile, which takes 48 KB of operands per CTA for 1024 cycles of MMAs (tiles of
-// 256 x 256 would take 64 bytes per clock, all that an SM gets from L2).  The two
-// accumulators fill the TMEM; the epilogue empties the first before the second, and
-// the next tile's MMAs into the first begin meanwhile, on as many K steps as the ring
-// holds.  Warps:
+// Persistent kernel, one CTA (CG = 1, tiles of 128 rows, for few rows) or CTA pair
+// (CG = 2, cta_group::2, tiles of 256 rows) per SM (pair), with two 256-column fp32
+// accumulators, so that the epilogue of one tile overlaps the main loop of the
+// next.  (Pairs with tiles of 512 x 256, which load a quarter less per product but
+// fill the TMEM with one tile: 1152 us instead of 1064 for a step of 8192 rows, 3300 of
+// which count, over 32000 words of 2048; 5047 instead of 5005 for 4096 rows, 64000 words of 4096.)  Warps:
 //   0     TMA producer of a ring of K steps (64 deep, 128-byte swizzle)
 //   1     TMEM allocator and MMA issuer
 //   4-11  epilogue
+// Few rows leave the tensor cores idle, so that their logits' tiles take 128 words and
+// either half of K has an accumulator of its own, which the epilogue adds: the truncation
+// that every 16 terms bring shrinks with the partial sums (relative error of four rows' losses,
+// 4096 terms: 1.1e-6 without, see below with).
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
 // error word and winds down.
 #include <cuda.h>
@@ -46,19 +49,22 @@ using grouped::idesc;
 using grouped::kChunkBytes;
 using grouped::UMMA_K;
 
-constexpr int kStages = 4;
+constexpr int kMaxStages = 6, kRingBytes = 192 * 1024;
 constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kTileN = 256;
 constexpr int kABytes = 128 * BK * 2;               // 128 rows of a K step
-constexpr int kStageBytes = 48 * 1024;              // pair: 2 x 128 rows of A and 128 of B; single CTA: 128 and 256
+// B: half of a pair's 256 columns, all of a single CTA's 256, or of its 128 (the logits of few rows)
+constexpr int stage_bytes(int mode, int cg) { return kABytes + (cg == 2 || mode != LCE_GRADS ? 128 : 256) * BK * 2; }
 constexpr int kBoxBytes = 32 * 128;                 // an epilogue warp's box: 32 rows of 128 bytes
-constexpr int kOffBox = kStages * kStageBytes, kOffBar = kOffBox + kEpiWarps * kBoxBytes;
-constexpr int kNumBars = 2 * kStages + 5;
+constexpr int kOffBox = kRingBytes, kOffBar = kOffBox + kEpiWarps * kBoxBytes;
+constexpr int kNumBars = 2 * kMaxStages + 5;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
-constexpr int kNarrowRows = 256;                    // up to here tiles of 128 rows on single CTAs
+constexpr int kNarrowRows = 128;                    // up to here tiles of 128 rows on single CTAs
 constexpr uint32_t kTmemCols = 512;
-constexpr int kEpilogueCost = 6;                    // an epilogue's time in K steps, for sharing out the tiles
+
+// a tile's time in K steps, for sharing out the work: the epilogue's, where the K loop is shorter
+__host__ __device__ constexpr int tile_cost(int steps) { return (steps > 10 ? steps : 10) + 1; }
 
 struct VocabArgs {
     LceProduct a;
@@ -70,10 +76,9 @@ struct VocabArgs {
     int split_steps;   // DX: K steps per split
 };
 
-// A tile: rows [m0, +128*CG*CG), columns [n0, +bn), K steps [k0, k0 + nk); `subs` of its
-// accumulators have rows that exist.
+// A tile: rows [m0, +128*CG), columns [n0, +bn), K steps [k0, k0 + nk).
 struct Tile {
-    int kind, m0, n0, k0, nk, slot, subs;
+    int kind, m0, n0, k0, nk, slot;
 };
 enum { TILE_LOGITS = 0, TILE_DX = 1, TILE_DW = 2 };
 
@@ -82,8 +87,8 @@ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 // Which tiles this CTA or pair takes, the j-th of them by at(); the same in all of its roles.
 template <int MODE, int CG>
 struct Share {
-    static constexpr int ROWS = 128 * CG * CG;
-    int cid, ncl, tiles, rows;
+    static constexpr int ROWS = 128 * CG;
+    int cid, ncl, tiles;
     int row_tiles, col_tiles;      // STATS, DLOGITS
     int nd, nw, rest, lead;        // GRADS: tiles of either kind; pairs with a DX tile more; DW tiles that the others take first
     int dw_steps, dx_steps;
@@ -92,7 +97,6 @@ struct Share {
     {
         cid = cid_;
         ncl = ncl_;
-        rows = count;
         if constexpr (MODE != LCE_GRADS) {
             row_tiles = div_up(count, ROWS);
             col_tiles = div_up(p.a.words, p.bn);
@@ -109,13 +113,11 @@ struct Share {
             rest = nd % ncl;
             lead = 0;
             if (rest > 0) {
-                const int cw = dw_steps + kEpilogueCost;
-                lead = min((p.split_steps + kEpilogueCost + cw / 2) / cw, div_up(nw, ncl - rest));
+                const int cw = tile_cost(dw_steps);
+                lead = min((tile_cost(p.split_steps) + cw / 2) / cw, div_up(nw, ncl - rest));
             }
         }
     }
-
-    __device__ __forceinline__ int subs(int m0, int end) const { return CG == 2 && m0 + 128 * CG < end ? 2 : 1; }
 
     __device__ __forceinline__ bool at(const VocabArgs &p, int j, Tile *t) const
     {
@@ -125,15 +127,14 @@ struct Share {
             const int g = i / (p.group * col_tiles), r = i - g * p.group * col_tiles;
             const int size = min(p.group, row_tiles - g * p.group);
             const int v = r / size;
-            const int m0 = (g * p.group + r - v * size) * ROWS;
-            *t = {TILE_LOGITS, m0, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v, subs(m0, rows)};
+            *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v};
             return true;
         } else {
             const int own = nd / ncl + (cid < rest ? 1 : 0);
             if (j < own) {
                 const int i = cid + j * ncl, s = i / (row_tiles * col_tiles), r = i - s * row_tiles * col_tiles;
-                const int k0 = s * p.split_steps, m0 = r / col_tiles * ROWS;
-                *t = {TILE_DX, m0, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s, subs(m0, rows)};
+                const int k0 = s * p.split_steps;
+                *t = {TILE_DX, r / col_tiles * ROWS, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s};
                 return true;
             }
             j -= own;
@@ -141,8 +142,7 @@ struct Share {
             const int i = j < mine ? j * (ncl - rest) + cid - rest
                                    : (rest > 0 ? lead * (ncl - rest) : 0) + (j - mine) * ncl + (cid - rest + ncl) % ncl;
             if (i >= nw) return false;
-            const int m0 = i / col_tiles * ROWS;
-            *t = {TILE_DW, m0, i % col_tiles * p.bn, 0, dw_steps, 0, subs(m0, p.a.words)};
+            *t = {TILE_DW, i / col_tiles * ROWS, i % col_tiles * p.bn, 0, dw_steps, 0};
             return true;
         }
     }
@@ -155,20 +155,6 @@ __device__ __forceinline__ void commit_both(uint64_t *bar)
                      ptx::smem_u32(bar)),
                  "h"((uint16_t)3)
                  : "memory");
-}
-
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
 }
 
 // The box: row `lane`'s piece i of 16 bytes on the way in, row 4i + lane/8's piece
@@ -223,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_x, const __grid_constant__ VocabArgs p)
 {
     constexpr bool PAIR = CG == 2;
-    constexpr int SUB = CG;                       // M side: accumulators per tile
-    constexpr int SUB_ROWS = 128 * CG;            // rows of an accumulator, over the pair
+    constexpr int kStageBytes = stage_bytes(MODE, CG), kStages = kRingBytes / kStageBytes;
+    constexpr bool HALVES = CG == 1 && MODE != LCE_GRADS;   // two sums per accumulator, 128 columns apart
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *empty = full + kStages;
@@ -302,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (issuer) {
                     uint64_t *bar = &full[stage];
-                    uint8_t *a_dst = smem + stage * kStageBytes, *b_dst = a_dst + SUB * kABytes;
+                    uint8_t *a_dst = smem + stage * kStageBytes, *b_dst = a_dst + kABytes;
                     const int k = (t.k0 + kb) * BK, row = t.m0 + crank * 128;
                     const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, 0) : 0u;
                     auto load = [&](void *dst, const CUtensorMap *map, int c0, int c1) {
@@ -310,14 +296,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else ptx::tma_load_2d(dst, map, bar, c0, c1);
                     };
                     if constexpr (MODE != LCE_GRADS) {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (t.subs * p.a_box + half) * (BK * 2)));
-                        for (int s = 0; s < t.subs; ++s) load(a_dst + s * kABytes, &map_a, k, row + s * SUB_ROWS);
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (p.a_box + half) * (BK * 2)));
+                        load(a_dst, &map_a, k, row);
                         load(b_dst, &map_w, k, t.n0 + crank * half);
                     } else {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (t.subs * 128 + half) * (BK * 2)));
+                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (128 + half) * (BK * 2)));
                         const CUtensorMap *map_b = t.kind == TILE_DX ? &map_w : &map_x;
-                        for (int i = 0; i < 2 * t.subs; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
-                            const int m = row + (i >> 1) * SUB_ROWS + (i & 1) * 64;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
+                            const int m = row + 64 * i;
                             if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
                             else load(a_dst + i * kChunkBytes, &map_a, m, k);
                         }
@@ -353,38 +340,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool a_mn = t.kind == TILE_DW, b_mn = MODE == LCE_GRADS;
                 const uint32_t id = idesc(128 * CG, p.bn, bf16, a_mn, b_mn);
                 const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
-                const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + SUB * kABytes, !b_mn);
-                const int c0 = SUB == 2 ? 0 : b;
-                auto issue = [&](int at, int sub, uint32_t acc) {   // one K step into one accumulator
-                    const uint32_t a = a_low + (uint32_t)at * (kStageBytes >> 4) + (uint32_t)sub * (kABytes >> 4);
-                    const uint32_t bb = b_low + (uint32_t)at * (kStageBytes >> 4);
-                    const uint32_t d = tmem_base + (uint32_t)((SUB == 2 ? sub : c0) * kTileN);
-                    if (issuer) {
-#pragma unroll
-                        for (int k = 0; k < BK / UMMA_K; ++k) {
-                            if constexpr (PAIR)
-                                ptx::umma_bf16_pair(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, k == 0 ? acc : 1u);
-                            else
-                                ptx::umma_bf16(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, k == 0 ? acc : 1u);
-                        }
-                    }
-                    __syncwarp();
-                };
+                const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + kABytes, !b_mn);
                 auto commit = [&](uint64_t *bar) {
-                    if (issuer) {
-                        if constexpr (PAIR) commit_both(bar);
-                        else ptx::umma_commit(bar);
-                    }
-                    __syncwarp();
+                    if constexpr (PAIR) commit_both(bar);
+                    else ptx::umma_commit(bar);
                 };
-                bool got = ptx::mbar_wait<PAIR>(&tempty[c0], ((taken >> c0) & 1u) ^ 1u, p.wait_ns);
+                bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
-                bool second = SUB == 1;   // the second accumulator is free
-                int late = 0;             // K steps that it has yet to take
+                const uint32_t d = tmem_base + (uint32_t)(b * kTileN);
                 for (int kb = 0; kb < t.nk; ++kb) {
                     got = ptx::mbar_wait(&full[stage], phase, p.wait_ns);
                     if (!__all_sync(0xffffffffu, got)) {
@@ -392,49 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     ptx::tc_fence_after();
-                    issue(stage, 0, kb > 0 ? 1u : 0u);
-                    const bool last = kb == t.nk - 1;
-                    if (last) commit(&tfull[c0]);
-                    if (SUB == 2 && t.subs == 2) {
-                        if (!second) {
-                            const uint32_t par = ((taken >> 1) & 1u) ^ 1u;
-                            if (last || late == kStages - 1) {
-                                got = ptx::mbar_wait<PAIR>(&tempty[1], par, p.wait_ns);
-                                if (!__all_sync(0xffffffffu, got)) {
-                                    ok = false;
-                                    break;
-                                }
-                                second = true;
-                            } else {
-                                second = __all_sync(0xffffffffu, mbar_test(&tempty[1], par));
-                            }
-                            if (second) ptx::tc_fence_after();
+                    if (issuer) {
+                        const bool upper = HALVES && kb >= (t.nk + 1) / 2, begins = kb == 0 || (HALVES && kb == (t.nk + 1) / 2);
+                        const uint32_t a = a_low + (uint32_t)stage * (kStageBytes >> 4), bb = b_low + (uint32_t)stage * (kStageBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < BK / UMMA_K; ++k) {
+                            const uint32_t acc = k > 0 || !begins ? 1u : 0u, to = d + (upper ? kTileN / 2 : 0u);
+                            if constexpr (PAIR) ptx::umma_bf16_pair(to, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
+                            else ptx::umma_bf16(to, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
                         }
-                        if (second) {
-                            for (; late >= 0; --late) {
-                                const int at = stage >= late ? stage - late : stage - late + kStages;
-                                issue(at, 1, kb - late > 0 ? 1u : 0u);
-                                commit(&empty[at]);
-                            }
-                            late = 0;
-                            if (last) commit(&tfull[1]);
-                        } else {
-                            ++late;
-                        }
-                    } else {
                         commit(&empty[stage]);
+                        if (kb == t.nk - 1) commit(&tfull[b]);
                     }
+                    __syncwarp();
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                if (SUB == 2) {
-                    taken ^= t.subs == 2 ? 3u : 1u;
-                } else {
-                    taken ^= 1u << c0;
-                    b ^= 1;
-                }
+                taken ^= 1u << b;
+                b ^= 1;
             }
             if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
             if (issuer) {   // (the lane that issued the MMAs)
@@ -454,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
         const bool bf16 = p.a.dtype == TF_BF16;
         const int c0 = h * ((p.bn / 2 + 63) & ~63), c1 = h ? p.bn : (p.bn / 2 + 63) & ~63;   // this warp's columns of a tile
-        const float mult = p.a.factor * (MODE == LCE_GRADS && p.a.unit ? __ldg(p.a.unit + 1) : 1.0f);
+        const float mult = p.a.factor * (MODE == LCE_GRADS ? __ldg(p.a.unit + 1) : 1.0f);
         int b = 0;
         uint32_t seen = 0;   // parity of the results of either accumulator
         bool ok = true;
@@ -471,175 +415,184 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                             pack(r[8 * i + 4], r[8 * i + 5]), pack(r[8 * i + 6], r[8 * i + 7])));
         };
         for (int j = 0; ok && share.at(p, j, &t); ++j) {
-            for (int sub = 0; sub < t.subs; ++sub) {
-                const int acc = SUB == 2 ? sub : b;
-                const int row0 = t.m0 + sub * SUB_ROWS + crank * 128 + q * 32, row = row0 + lane;
-                const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN + c0);
-                const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
-                const int left = min(width, c1) - c0;   // columns with results, up to 128
-                int target = -1;
-                float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
-                if constexpr (MODE != LCE_GRADS) {
-                    if (row < count) {
-                        target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
-                        if constexpr (MODE == LCE_DLOGITS) {
-                            l2 = __ldg(p.a.l2 + row);
-                            ca = __ldg(p.a.ca + row);
-                            cb = __ldg(p.a.cb + row);
-                        }
+            const int acc = b;
+            const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
+            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN + c0);
+            const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
+            const int left = min(width, c1) - c0;   // columns with results, up to 128
+            int target = -1;
+            float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
+            if constexpr (MODE != LCE_GRADS) {
+                if (row < count) {
+                    target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
+                    if constexpr (MODE == LCE_DLOGITS) {
+                        l2 = __ldg(p.a.l2 + row);
+                        ca = __ldg(p.a.ca + row);
+                        cb = __ldg(p.a.cb + row);
                     }
                 }
-                if (t.nk > 0) {
-                    const bool got = ptx::mbar_wait(&tfull[acc], (seen >> acc) & 1u, p.wait_ns);
-                    if (!__all_sync(0xffffffffu, got)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                    seen ^= 1u << acc;
-                    if (SUB == 1) b ^= 1;
+            }
+            if (t.nk > 0) {
+                const bool got = ptx::mbar_wait(&tfull[acc], (seen >> acc) & 1u, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
                 }
-                auto release = [&]() {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
-                        else ptx::mbar_arrive(&tempty[acc]);
-                    }
-                };
-                if (t.nk > 0 && left <= 0) release();
-                float top = -INFINITY, sum = 0.0f;
+                ptx::tc_fence_after();
+                seen ^= 1u << acc;
+                b ^= 1;
+            }
+            auto release = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
+                    else ptx::mbar_arrive(&tempty[acc]);
+                }
+            };
+            if (t.nk > 0 && left <= 0) release();
+            float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-                for (int u = 0; u < left; u += 64) {
-                    uint32_t r[2][32];
-                    if (t.nk > 0) {
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
+            for (int u = 0; u < left; u += 64) {
+                uint32_t r[2][32];
+                if (t.nk > 0) {
+                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
+                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
+                    if (HALVES && t.nk > 1) {   // (one K step is all in the lower half)
+                        uint32_t v[2][32];
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + kTileN / 2), v[0]);
+                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + kTileN / 2 + 32), v[1]);
                         ptx::tmem_ld_wait();
-                        if (u + 64 >= left) release();
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
-                    }
-                    if constexpr (MODE == LCE_STATS) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = u + 32 * i;
-                            if (c + 32 <= left) join_stats(r[i], 32, p.a.factor, top, sum);
-                            else join_stats(r[i], left - c, p.a.factor, top, sum);
-                            const int at = target - c;
-                            const bool hit = at >= 0 && at < 32 && target < left;
-                            if (__any_sync(0xffffffffu, hit)) {
-                                const float v = pick(r[i], at);
-                                if (hit) p.a.at_target[row] = v;
-                            }
-                        }
-                    } else if constexpr (MODE == LCE_DLOGITS) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int c = u + 32 * i;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
-                            const int at = target - c;
-                            const bool hit = at >= 0 && at < 32 && target < left;
-                            if (__any_sync(0xffffffffu, hit)) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (hit && k == at) r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) - cb);
-                            }
-                            // columns behind the piece's words, and rows behind those that count, which
-                            // dw's last K step reads: zeros
-                            if (c + 32 > left || row0 + 32 > count) {
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) r[i][k] = row < count && c + k < left ? r[i][k] : 0u;
-                            }
-                            put_half(r[i], i);
-                        }
-                        __syncwarp();
-                        const int piece = lane & 7, c = c0 + u + 8 * piece;
-                        uint16_t *out = static_cast<uint16_t *>(p.a.dl) + t.n0 + c;
-                        if (c < c1 && t.n0 + c < p.a.dl_pitch) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int at = 4 * i + (lane >> 3);
-                                if (row0 + at < p.a.rows)
-                                    *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
-                            }
-                        }
-                        __syncwarp();
-                    } else {
-                        const bool dx = t.kind == TILE_DX;
-                        const int rows = dx ? count : p.a.words;   // of this tile's M side
-                        const bool wide = dx || p.a.dw_f32;        // 32-bit results
-                        const bool add = dx ? !p.a.first : p.a.accumulate != 0;
-                        if ((t.nk == 0 && add) || row0 >= rows) continue;
-                        const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
-                        uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
-                                          : static_cast<uint8_t *>(p.a.dw);
-                        // rows that 16-byte words make up
-                        const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
-                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
-                        }
-                        if (!wide) {
-                            put_half(r[0], 0);
-                            put_half(r[1], 1);
-                        }
-                        const int per = wide ? 4 : 8, size = wide ? 4 : 2;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (i == 1 && (!wide || u + 32 >= left)) break;
-                            if (wide) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
-                            }
-                            __syncwarp();
-                            // the box's rows, of 128 bytes from column c on
-                            const int c = t.n0 + c0 + u + 32 * i;
-                            if (words) {
-                                const int piece = lane & 7, col = c + per * piece;
-                                uint8_t *dst = out + ((int64_t)(row0 + (lane >> 3)) * pitch + col) * size;
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    const int at = 4 * k + (lane >> 3);
-                                    if (row0 + at >= rows || col >= pitch) continue;
-                                    uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
-                                    uint4 v = box_get(box, at, piece);
-                                    if (add) {
-                                        const uint4 o = *to;
-                                        v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
-                                        v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
-                                        v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
-                                        v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
-                                    }
-                                    *to = v;
-                                }
-                            } else {
-                                for (int at = 0; at < min(32, rows - row0); ++at) {
-                                    for (int e = lane; e < 8 * per && c + e < pitch; e += 32) {
-                                        const int64_t to = (int64_t)(row0 + at) * pitch + c + e;
-                                        const uint8_t *src = box + at * 128 + (((e / per) ^ (at & 7)) * 16);
-                                        if (wide) {
-                                            const float v = reinterpret_cast<const float *>(src)[e % per];
-                                            float *dst = reinterpret_cast<float *>(out) + to;
-                                            *dst = add ? *dst + v : v;
-                                        } else {
-                                            reinterpret_cast<uint16_t *>(out)[to] = reinterpret_cast<const uint16_t *>(src)[e % per];
-                                        }
-                                    }
-                                }
-                            }
-                            __syncwarp();
+                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) + __uint_as_float(v[0][k]));
+                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) + __uint_as_float(v[1][k]));
                         }
                     }
+                    ptx::tmem_ld_wait();
+                    if (u + 64 >= left) release();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
                 }
-                if constexpr (MODE == LCE_STATS)
-                    if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
+                if constexpr (MODE == LCE_STATS) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = u + 32 * i;
+                        if (c + 32 <= left) join_stats(r[i], 32, p.a.factor, top, sum);
+                        else join_stats(r[i], left - c, p.a.factor, top, sum);
+                        const int at = target - c;
+                        const bool hit = at >= 0 && at < 32 && target < left;
+                        if (__any_sync(0xffffffffu, hit)) {
+                            const float v = pick(r[i], at);
+                            if (hit) p.a.at_target[row] = v;
+                        }
+                    }
+                } else if constexpr (MODE == LCE_DLOGITS) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int c = u + 32 * i;
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
+                        const int at = target - c;
+                        const bool hit = at >= 0 && at < 32 && target < left;
+                        if (__any_sync(0xffffffffu, hit)) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (hit && k == at) r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) - cb);
+                        }
+                        // columns behind the piece's words, and rows behind those that count, which
+                        // dw's last K step reads: zeros
+                        if (c + 32 > left || row0 + 32 > count) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) r[i][k] = row < count && c + k < left ? r[i][k] : 0u;
+                        }
+                        put_half(r[i], i);
+                    }
+                    __syncwarp();
+                    const int piece = lane & 7, c = c0 + u + 8 * piece;
+                    uint16_t *out = static_cast<uint16_t *>(p.a.dl) + t.n0 + c;
+                    if (c < c1 && t.n0 + c < p.a.dl_pitch) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int at = 4 * i + (lane >> 3);
+                            if (row0 + at < p.a.rows)
+                                *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
+                        }
+                    }
+                    __syncwarp();
+                } else {
+                    const bool dx = t.kind == TILE_DX;
+                    const int rows = dx ? count : p.a.words;   // of this tile's M side
+                    const bool wide = dx || p.a.dw_f32;        // 32-bit results
+                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                    if ((t.nk == 0 && add) || row0 >= rows) continue;
+                    const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
+                    uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
+                                      : static_cast<uint8_t *>(p.a.dw);
+                    // rows that 16-byte words make up
+                    const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
+                        r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
+                    }
+                    if (!wide) {
+                        put_half(r[0], 0);
+                        put_half(r[1], 1);
+                    }
+                    const int per = wide ? 4 : 8, size = wide ? 4 : 2;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (i == 1 && (!wide || u + 32 >= left)) break;
+                        if (wide) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
+                        }
+                        __syncwarp();
+                        // the box's rows, of 128 bytes from column c on
+                        const int c = t.n0 + c0 + u + 32 * i;
+                        if (words) {
+                            const int piece = lane & 7, col = c + per * piece;
+                            uint8_t *dst = out + ((int64_t)(row0 + (lane >> 3)) * pitch + col) * size;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int at = 4 * k + (lane >> 3);
+                                if (row0 + at >= rows || col >= pitch) continue;
+                                uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
+                                uint4 v = box_get(box, at, piece);
+                                if (add) {
+                                    const uint4 o = *to;
+                                    v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
+                                    v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
+                                    v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
+                                    v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
+                                }
+                                *to = v;
+                            }
+                        } else {
+                            for (int at = 0; at < min(32, rows - row0); ++at) {
+                                for (int e = lane; e < 8 * per && c + e < pitch; e += 32) {
+                                    const int64_t to = (int64_t)(row0 + at) * pitch + c + e;
+                                    const uint8_t *src = box + at * 128 + (((e / per) ^ (at & 7)) * 16);
+                                    if (wide) {
+                                        const float v = reinterpret_cast<const float *>(src)[e % per];
+                                        float *dst = reinterpret_cast<float *>(out) + to;
+                                        *dst = add ? *dst + v : v;
+                                    } else {
+                                        reinterpret_cast<uint16_t *>(out)[to] = reinterpret_cast<const uint16_t *>(src)[e % per];
+                                    }
+                                }
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
             }
+            if constexpr (MODE == LCE_STATS)
+                if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
         }
         if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
     }
@@ -697,7 +650,7 @@ cudaError_t resident(int *units)
 template <int MODE, int CG>
 cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
 {
-    constexpr int ROWS = 128 * CG * CG;
+    constexpr int ROWS = 128 * CG;
     VocabArgs p = {};
     p.a = a;
     p.err = device_error_word();
@@ -769,16 +722,28 @@ cudaError_t launch_rows(const LceProduct &a, cudaStream_t st)
 
 }  // namespace
 
-int lce_row_tile(int64_t rows) { return rows <= kNarrowRows ? 128 : 512; }
+int lce_row_tile(int64_t rows) { return rows <= kNarrowRows ? 128 : 256; }
 int lce_units(int64_t rows) { return rows <= kNarrowRows ? sm_count() : sm_count() / 2; }
 
-// Single CTAs share the words out evenly, so that the last wave is as full as the others.
+// As many waves of tiles as the widest take, of tiles as narrow as they then can be.
 int lce_word_tile(int64_t rows, int64_t words)
 {
-    if (rows > kNarrowRows) return kTileN;
-    const int64_t n = sm_count(), waves = (words + n * kTileN - 1) / (n * kTileN);
-    const int64_t bn = ((words + n * waves - 1) / (n * waves) + 15) / 16 * 16;
-    return bn < 64 ? 64 : (int)bn;
+    const bool narrow = rows <= kNarrowRows;
+    const int64_t n = lce_units(rows), down = (rows + lce_row_tile(rows) - 1) / lce_row_tile(rows);
+    const int64_t widest = narrow ? kTileN / 2 : kTileN, step = narrow ? 16 : 32;
+    const int64_t waves = (down * ((words + widest - 1) / widest) + n - 1) / n, across = n * waves / down;
+    const int64_t bn = ((words + across - 1) / across + step - 1) / step * step;
+    return bn < 64 ? 64 : bn > widest ? (int)widest : (int)bn;
+}
+
+// Splits of dx's sums: no longer than a CTA's (pair's) share of both gradients.
+int lce_splits(int64_t rows, int64_t words, int64_t hidden)
+{
+    const int64_t tile = lce_row_tile(rows), across = (hidden + kTileN - 1) / kTileN;
+    const int64_t steps = (words + BK - 1) / BK, dx = (rows + tile - 1) / tile * across, dw = (words + tile - 1) / tile * across;
+    const int64_t share = (dx * tile_cost((int)steps) + dw * tile_cost((int)((rows + BK - 1) / BK))) / lce_units(rows);
+    const int64_t s = (steps + share) / (share + 1);
+    return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
 cudaError_t launch_lce_product(int mode, const LceProduct &a, cudaStream_t st)

@@ -61,7 +61,7 @@ struct LceProduct {
     float2 *part;            // STATS: (maximum, sum) per slot and row
     float *at_target;        // STATS: the target's sum
     const float *l2, *ca, *cb;   // DLOGITS: lse in base 2, and what the probabilities and the target take
-    const float *unit;       // fp16: the power of two that the gradients of the logits are held in, and its inverse
+    const float *unit;       // GRADS: what the gradients of the logits are held times, and its inverse
     void *dl;                // [rows][dl_pitch]
     float *dx;               // GRADS: [splits][rows][dx_pitch], null where not wanted
     void *dw;                // this piece's rows, null where not wanted
@@ -73,8 +73,7 @@ struct LceProduct {
     int dtype, dw_f32, accumulate;
 };
 int lce_word_tile(int64_t rows, int64_t words);   // words per tile of the logits
-int lce_row_tile(int64_t rows);                   // rows per tile
-int lce_units(int64_t rows);                      // CTAs or pairs that work at once
+int lce_splits(int64_t rows, int64_t words, int64_t hidden);   // of dx's sums, at most 16
 cudaError_t launch_lce_product(int mode, const LceProduct &a, cudaStream_t st);
 
 }  // namespace tf
