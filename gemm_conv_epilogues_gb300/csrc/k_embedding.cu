@@ -556,14 +556,14 @@ int lanes_of(int words)
     return lanes;
 }
 
-// Pieces that fill the SMs where the list is long enough (16 CTAs each, and no more
+// Pieces that fill the SMs where the list is long enough (12 CTAs each, in two waves, and no more
 // pieces than a long word's join adds quickly), of 8 to 1024 keys.  Sized for 8 columns per thread, whatever the type, so that the
 // workspace depends on the sizes alone.
 int64_t piece_target(int64_t hidden)
 {
     const int lanes = lanes_of((int)((hidden + 7) / 8));
     const int64_t slices = (hidden + 8 * lanes - 1) / (8 * lanes), per_block = kSumThreads / lanes;
-    const int64_t fill = (16 * 152 + slices - 1) / slices * per_block;
+    const int64_t fill = (12 * 152 + slices - 1) / slices * per_block;
     return fill < kMostPieces ? fill : kMostPieces;
 }
 int64_t piece_of(int64_t rows, int64_t hidden)

@@ -72,7 +72,7 @@ template <typename T>
 __device__ __forceinline__ float copy_row(uint16_t *dst, const uint16_t *src, const uint16_t *w, int n, int lane, int lanes)
 {
     constexpr bool DOT = !std::is_void<T>::value;
-    constexpr int UNROLL = DOT ? 2 : 4;
+    constexpr int UNROLL = 4;
     using P = typename std::conditional<DOT, T, __half>::type;
     float sum[2] = {};
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0 && n % 8 == 0) {
@@ -126,7 +126,7 @@ __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lan
 // which reads the targets once per CTA, but needs no CTA to wait for another.
 // T: the operands' type in the forward pass, void in the backward pass.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_constant__ GatherArgs g)
+__global__ void __launch_bounds__(kThreads, 3) gather_kernel(const __grid_constant__ GatherArgs g)
 {
     pdl_begin();
     constexpr bool BACKWARD = std::is_void<T>::value;
@@ -136,9 +136,13 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t first = (int64_t)blockIdx.x * g.per_block, end = min(first + g.per_block, a.rows);
     int before = 0;
-    for (int64_t i = t; i < first; i += kThreads) {
-        int64_t target;
-        before += counts(a, i, &target, false);
+    for (int64_t i = t; i < first; i += 4 * kThreads) {   // four loads under way at a time
+        int64_t target[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) target[u] = i + u * kThreads < first ? a.targets.at(i + u * kThreads) : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            before += i + u * kThreads < first && target[u] >= 0 && target[u] < a.vocab && target[u] != a.ignore;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -369,13 +373,41 @@ __global__ void __launch_bounds__(kThreads) dx_kernel(const __grid_constant__ Dx
 
 // ---------------------------------------------------------------- weights of odd widths
 
+// A warp per row.  Eight values at any even address come as five aligned 32-bit words,
+// shifted into place; what might lie before the weights or behind them is not read
+// (a row's last one to eight values, and the first eight of all where they begin inside a word).
 __global__ void __launch_bounds__(kThreads) pack_rows_kernel(const uint16_t *w, uint16_t *out, int64_t rows, int hidden,
                                                              int64_t pitch)
 {
     pdl_begin();
+    constexpr int UNROLL = 4;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step)
-        copy_row<void>(out + r * pitch, w + r * hidden, nullptr, hidden, threadIdx.x & 31, 32);
+    const int lane = threadIdx.x & 31, whole = (hidden - 1) / 8;
+    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += step) {
+        const uint16_t *src = w + r * hidden;
+        uint16_t *dst = out + r * pitch;
+        const bool inside = (reinterpret_cast<uintptr_t>(src) & 2u) != 0;
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(src - (inside ? 1 : 0));
+        const int first = r == 0 && inside ? 1 : 0;
+        for (int c = first + lane; c < whole; c += UNROLL * 32) {
+            uint32_t v[UNROLL][5];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+                if (c + u * 32 < whole)
+#pragma unroll
+                    for (int k = 0; k < 5; ++k) v[u][k] = k < 4 || inside ? words[(c + u * 32) * 4 + k] : 0;
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                if (c + u * 32 >= whole) break;
+                const int shift = inside ? 16 : 0;
+                reinterpret_cast<uint4 *>(dst)[c + u * 32] =
+                    make_uint4(__funnelshift_r(v[u][0], v[u][1], shift), __funnelshift_r(v[u][1], v[u][2], shift),
+                               __funnelshift_r(v[u][2], v[u][3], shift), __funnelshift_r(v[u][3], v[u][4], shift));
+            }
+        }
+        if (lane < 8 && first && lane < whole * 8) dst[lane] = src[lane];
+        if (whole * 8 + lane < hidden && lane < 8) dst[whole * 8 + lane] = src[whole * 8 + lane];
+    }
 }
 
 cudaError_t launch_pack(const LceArgs &a, int64_t v0, int64_t words, int64_t pitch, void *out, cudaStream_t st)

@@ -574,16 +574,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         } else {
                             for (int at = 0; at < min(32, rows - row0); ++at) {
-                                for (int e = lane; e < 8 * per && c + e < pitch; e += 32) {
-                                    const int64_t to = (int64_t)(row0 + at) * pitch + c + e;
-                                    const uint8_t *src = box + at * 128 + (((e / per) ^ (at & 7)) * 16);
-                                    if (wide) {
-                                        const float v = reinterpret_cast<const float *>(src)[e % per];
-                                        float *dst = reinterpret_cast<float *>(out) + to;
+                                const int64_t to = (int64_t)(row0 + at) * pitch + c;
+                                const int n = min(8 * per, (int)min(pitch, (int64_t)(1 << 30)) - c);   // columns of this row
+                                const uint8_t *src = box + at * 128;
+                                if (wide) {
+                                    if (lane < n) {
+                                        const float v = *reinterpret_cast<const float *>(src + (((lane >> 2) ^ (at & 7)) * 16) + (lane & 3) * 4);
+                                        float *dst = reinterpret_cast<float *>(out) + to + lane;
                                         *dst = add ? *dst + v : v;
-                                    } else {
-                                        reinterpret_cast<uint16_t *>(out)[to] = reinterpret_cast<const uint16_t *>(src)[e % per];
                                     }
+                                } else {
+                                    // pairs of columns that share a 32-bit word; an odd start leaves its first and last column single
+                                    uint16_t *dst = reinterpret_cast<uint16_t *>(out) + to;
+                                    const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1, e = 2 * lane - odd;
+                                    auto value = [&](int i) {
+                                        return *reinterpret_cast<const uint16_t *>(src + (((i >> 3) ^ (at & 7)) * 16) + (i & 7) * 2);
+                                    };
+                                    if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t *>(dst + e) = value(e) | (uint32_t)value(e + 1) << 16;
+                                    else if (e + 1 < n) dst[e + 1] = value(e + 1);
+                                    else if (e < n) dst[e] = value(e);
+                                    if (odd && lane == 0 && n == 64) dst[63] = value(63);
                                 }
                             }
                         }

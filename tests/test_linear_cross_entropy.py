@@ -429,3 +429,22 @@ def test_gradients_against_differences(b):
     l = torch.softmax(x.double() @ w.double().t(), 1).scatter_add(1, targets[:, None], torch.full((rows, 1), -1.0, device="cuda", dtype=torch.double))
     dx_off = 4 * half_step("fp16") * (l.abs() @ w.double().abs()).sum(1)
     assert ((up - down) / (2 * h) - slope).abs().le(h * h / 60 * span ** 3 + loss_off / h + dx_off).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hidden", [1, 2, 7, 8, 9, 17, 63, 255, 1001])
+@pytest.mark.parametrize("offset", [0, 1, 2, 3])
+def test_weights_at_odd_addresses(b, hidden, offset):
+    """Widths that are copied, from every place inside a 64-bit word; the gradient goes to such a place too."""
+    if hidden % 8 == 0 and offset:
+        pytest.skip("weights of whole 16-byte rows are aligned")
+    rows, vocab = 40, 333
+    x, w, targets = _inputs(rows, vocab, hidden, "fp16", "some", seed=12)
+    flat = torch.full((vocab * hidden + offset + 8,), float("nan"), device="cuda", dtype=torch.float16)
+    view = flat[offset:offset + vocab * hidden].view(vocab, hidden)
+    view.copy_(w)
+    loss, lse = _forward(b, x, view, targets, "fp16")
+    _check_forward(x, w, targets, 1.0, loss, lse)
+    for dw_dtype in ("fp16", "fp32"):
+        dx, dw = _grads(b, x, view, targets, lse, None, None, "fp16", dw_dtype=dw_dtype, offset=offset)
+        _check_grads(x, w, targets, lse, None, None, "fp16", 1.0, dx, dw, dw_dtype)
