@@ -15,9 +15,7 @@
 //      piece is finished where it began; longer ones leave partial sums.  Other
 //      CTAs write the zeros of words that do not occur.
 //   3  the partial sums of the long words are added in order
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+#include "grouped.cuh"
 #include "lm_internal.h"
 #include "ptx_sm100.cuh"
 
@@ -130,8 +128,7 @@ __device__ __forceinline__ uint32_t word_of(uint64_t key) { return (uint32_t)(ke
 // first takes the tokens, a second one, for more than 2^18 words, the first one's
 // keys.  A warp has a stretch of the list and counters of its own, so that places
 // follow the order of the list: below this CTA's range, smaller digits, earlier
-// warps, earlier in the warp.  16384 tokens, 32000 words: 9 us (sorting chunks and
-// merging them took 32).
+// warps, earlier in the warp.  (Sorting chunks and merging them took three times as long.)
 struct SortArgs {
     Indices tokens;
     const uint64_t *in;
@@ -185,22 +182,28 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
             for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint32_t)a.vocab && v[u] != a.padding ? v[u] : kNone;
         }
     };
-    uint32_t low = 0;
-    for (int i = lo + lane; i < hi; i += 32 * UNROLL) {
+    // which of this lane's entries are in the range, where 32 bits hold them: few are, and only those are looked at again
+    const bool marked = seg <= 32 * 32;
+    uint32_t low = 0, marks = 0;
+    int step = 0;
+    for (int i = lo + lane; i < hi; i += 32 * UNROLL, step += UNROLL) {
         uint32_t word[UNROLL], row[UNROLL];
         load(i, word, row);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const uint32_t digit = (word[u] >> a.shift) & mask, at = digit - d0;
             low += word[u] != kNone && digit < d0;
-            if (word[u] != kNone && at < range) atomicAdd(mine + at, 1u);
+            if (word[u] != kNone && at < range) {
+                atomicAdd(mine + at, 1u);
+                marks |= 1u << ((step + u) & 31);
+            }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) low += __shfl_xor_sync(0xffffffffu, low, o);
     if (lane == 0) below_sums[warp] = low;
-    if (FIRST && blockIdx.x == 0)   // one CTA reports the tokens that are neither words nor the padding
-        for (int i = t; i < a.n; i += kSortThreads) {
+    if (FIRST)   // the CTAs look through the tokens together for those that are neither words nor the padding
+        for (int64_t i = (int64_t)blockIdx.x * kSortThreads + t; i < a.n; i += (int64_t)gridDim.x * kSortThreads) {
             const int64_t token = a.tokens.at(i);
             if ((token < 0 || token >= a.vocab) && token != a.listed_padding) atomicOr(a.err, TF_DEVERR_INDEX);
         }
@@ -247,23 +250,37 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
         }
         __syncthreads();
     }
-    for (int i0 = lo; i0 < hi; i0 += 32 * UNROLL) {
-        uint32_t word[UNROLL], row[UNROLL];
-        load(i0 + lane, word, row);
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const uint32_t at = ((word[u] >> a.shift) & mask) - d0;
-            const bool in_range = word[u] != kNone && at < range;
-            const unsigned active = __ballot_sync(0xffffffffu, in_range);
-            if (active == 0) continue;
+    // 32 entries from i0 on, of which this lane has one, in the order of the list
+    auto put = [&](int i, uint32_t word, uint32_t row, bool in_range) {
+        const unsigned active = __ballot_sync(0xffffffffu, in_range);
+        if (active == 0) return;
+        if (in_range) {
+            const uint32_t at = ((word >> a.shift) & mask) - d0;
+            const unsigned same = __match_any_sync(active, at);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[at];
+            a.out[first + before] = (uint64_t)word << 32 | (FIRST ? (uint32_t)i : row);
+            __syncwarp(active);
+            if (before == 0) mine[at] = first + __popc(same);
+        }
+        __syncwarp();
+    };
+    if (marked) {
+        for (int i = lo + lane; i - lane < hi; i += 32, marks >>= 1) {
+            const bool in_range = marks & 1u;
+            uint64_t v = 0;
             if (in_range) {
-                const unsigned same = __match_any_sync(active, at);
-                const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[at];
-                a.out[first + before] = (uint64_t)word[u] << 32 | (FIRST ? (uint32_t)(i0 + 32 * u + lane) : row[u]);
-                __syncwarp(active);
-                if (before == 0) mine[at] = first + __popc(same);
+                if constexpr (!FIRST) v = a.in[i];
+                else v = WIDE ? static_cast<const uint64_t *>(a.tokens.p)[i] : static_cast<const uint32_t *>(a.tokens.p)[i];
             }
-            __syncwarp();
+            put(i, FIRST ? (uint32_t)v : word_of(v), (uint32_t)v, in_range);
+        }
+    } else {
+        for (int i = lo + lane; i - lane < hi; i += 32 * UNROLL) {
+            uint32_t word[UNROLL], row[UNROLL];
+            load(i, word, row);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u)
+                put(i + 32 * u, word[u], row[u], word[u] != kNone && ((word[u] >> a.shift) & mask) - d0 < range);
         }
     }
     if (blockIdx.x == gridDim.x - 1)   // the rest have no gradient
@@ -300,6 +317,25 @@ struct SumArgs {
     uint32_t *err;
     uint64_t wait_ns;
 };
+
+// low += v, two columns at a time where there are as many.
+template <typename T, int VEC>
+__device__ __forceinline__ void add_values(float (&low)[VEC], const Pack<T, VEC> &v)
+{
+    if constexpr (VEC == 1) {
+        low[0] += widen<T>(v.v[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; k += 2) {
+            float2 x;
+            if constexpr (sizeof(T) == 2) x = grouped::Half2Of<T>::unpack(*reinterpret_cast<const uint32_t *>(&v.v[k]));
+            else x = make_float2(v.v[k], v.v[k + 1]);
+            const float2 t = fadd2(make_float2(low[k], low[k + 1]), x);
+            low[k] = t.x;
+            low[k + 1] = t.y;
+        }
+    }
+}
 
 // A row's columns.  Adding to what is there is left to the L2, which does not make
 // the thread wait for the old values; every element of dtable gets one such
@@ -419,8 +455,7 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
             word = w;
         }
         if (w == skipped) return;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) low[k] += widen<T>(v.v[k]);
+        add_values<T, VEC>(low, v);
         if (++held == kLevel) {
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
@@ -659,7 +694,7 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
     if (a.dtype == TF_FP32) e = sums_typed<float>(a, s, st);
     else e = a.dtype == TF_BF16 ? sums_typed<__nv_bfloat16>(a, s, st) : sums_typed<__half>(a, s, st);
     if (e != cudaSuccess || s.pieces < 2) return e;
-    return launch_pdl(join_pieces_kernel, dim3((unsigned)(4 * sm_count())), dim3(kJoinThreads), 0, st, s);
+    return launch_pdl(join_pieces_kernel, dim3((unsigned)(8 * sm_count())), dim3(kJoinThreads), 0, st, s);
 }
 
 }  // namespace tf
