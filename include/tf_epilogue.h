@@ -414,8 +414,10 @@ int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens,
  * get a loss and lse of 0; what x holds there, NaN included, is not read.
  * Other targets outside [0, vocab) are ignored likewise and set TF_DEVERR_INDEX.
  * Sums are fp32; equal calls give equal bits.  The tensor cores truncate where
- * fp32 additions round (see the grouped products): logits whose terms cancel are off by up
- * to 6e-8 of their largest partial sum for every 16 terms.
+ * fp32 additions round (see the grouped products), by up to 6e-8 of the partial sum for
+ * every 16 terms: a logit of 4096 terms of either sign is about 1e-5 too near zero, and lse
+ * with it.  The loss takes its target's logit from an fp32 sum instead, and is log(1 + x) of
+ * the others' share, so that a sure target's small loss keeps its digits.
  * Any hidden to 65536, any row stride (below 2^31) and the alignment of an
  * element; where hidden is not a multiple of 8 the weights are copied on the
  * way.  Up to 4194304 rows and words; rows may be 0.
@@ -443,10 +445,11 @@ int tf_linear_cross_entropy_forward(const void *x, int64_t x_stride, const void 
  *            TF_FP32.  With `accumulate` != 0 (TF_FP32 only) it is added to what
  *            dw holds.
  * dl is rounded to dtype, the matrix products' operand type: a relative 2^-9 (bf16) or 2^-12
- * (fp16) of each term at most, in dx and dw, also where dw is fp32.  fp16 holds
- * dl in units of a power of two that puts the largest |dloss| + |dlse| below
- * 2^15, so that terms down to 2^-29 of it keep their digits and
- * none below 2^-40 of it counts.  Sums are fp32.  Workspace as above. */
+ * (fp16) of each term at most, in dx and dw, also where dw is fp32.  It is held in units
+ * of a typical |dloss|, in which equal weights round to nothing: bf16 takes the first counted row's (where
+ * that lies between 2^-40 and 2^40), fp16 2^-14 of the largest, so that terms down to
+ * 2^-28 of it keep their digits and none below 2^-39 of it counts.  Sums are fp32.
+ * Workspace as above. */
 int64_t tf_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden, int dtype);
 int tf_linear_cross_entropy_backward(const void *x, int64_t x_stride, const void *w, const void *targets, int index,
                                      const float *lse, const float *dloss, const float *dlse, void *dx,

@@ -448,3 +448,73 @@ def test_weights_at_odd_addresses(b, hidden, offset):
     for dw_dtype in ("fp16", "fp32"):
         dx, dw = _grads(b, x, view, targets, lse, None, None, "fp16", dw_dtype=dw_dtype, offset=offset)
         _check_grads(x, w, targets, lse, None, None, "fp16", 1.0, dx, dw, dw_dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("rows", [607, 609, 16385, 20011])
+def test_many_rows(b, rows, dtype):
+    """Rows that are brought together one per CTA, one per warp and several per warp, past the first 256 of a CTA's."""
+    x, w, targets = _inputs(rows, 130, 16, dtype, "some", pad=5, seed=13)
+    targets[:300] = IGNORE            # the first row that counts is not among the first
+    x[:300] = float("nan")
+    loss, lse = _forward(b, x, w, targets, dtype)
+    _check_forward(x, w, targets, 1.0, loss, lse)
+    dloss, dlse = _weights(targets)
+    dx, dw = _grads(b, x, w, targets, lse, dloss, dlse, dtype, dw_dtype="fp32")
+    _check_grads(x, w, targets, lse, dloss, dlse, dtype, 1.0, dx, dw, "fp32")
+
+
+@pytest.mark.gpu
+def test_rows_past_the_first_target_block(b):
+    """More rows per CTA than threads (from 2^19 rows on)."""
+    rows = (1 << 19) + 3
+    x, w, targets = _inputs(rows, 3, 8, "bf16", "some", seed=14)
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    _check_forward(x, w, targets, 1.0, loss, lse)
+    dx, _ = _grads(b, x, w, targets, lse, None, None, "bf16", want=("dx",))
+    _check_grads(x, w, targets, lse, None, None, "bf16", 1.0, dx)
+
+
+@pytest.mark.gpu
+def test_weights_of_any_size_of_dloss(b):
+    """Units of the gradients: a first row's dloss of zero, tiny, huge and negative; and rows that differ by 2^20."""
+    for first in (0.0, 2.0 ** -60, 2.0 ** 60, -3.0):
+        for dtype in HALF:
+            x, w, targets = _inputs(300, 500, 64, dtype, seed=15)
+            loss, lse = _forward(b, x, w, targets, dtype)
+            dloss = torch.full((300,), 0.3, device="cuda")
+            dloss[0] = first
+            dloss[5] = 0.3 * 2.0 ** -20
+            if dtype == "fp16" and first == 2.0 ** 60:
+                continue   # (dx of such a row is not an fp16 number)
+            dx, dw = _grads(b, x, w, targets, lse, dloss, None, dtype, dw_dtype="fp32")
+            _check_grads(x, w, targets, lse, dloss, None, dtype, 1.0, dx, dw, "fp32")
+
+
+@pytest.mark.gpu
+def test_large_offsets(b):
+    """Weights and their gradient past 2^31 elements: zeros but for the last words."""
+    vocab, hidden, rows = 2_100_000, 1040, 3
+    w = torch.zeros(vocab, hidden, dtype=torch.bfloat16, device="cuda")
+    w[-1, :4], w[-2, :4] = 1.0, -0.5
+    x = torch.zeros(rows, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:, :4] = torch.tensor([[2.0], [4.0], [0.0]], device="cuda")
+    targets = torch.tensor([vocab - 1, 7, vocab - 2], device="cuda")
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    l = torch.zeros(rows, 2, dtype=torch.float64, device="cuda")
+    l[:, 0], l[:, 1] = 4 * x[:, 0].double(), -2 * x[:, 0].double()   # the last word's logits, and those of the one before
+    want = torch.log(vocab - 2 + l.exp().sum(1))
+    assert ((lse.double() - want).abs() <= 2.0 ** -18).all()
+    assert ((loss.double() - (want - torch.stack([l[0, 0], 0 * l[1, 0], l[2, 1]]))).abs() <= 2.0 ** -18).all()
+    dx, dw = _grads(b, x, w, targets, lse, None, None, "bf16")
+    p = torch.exp(l - want[:, None])
+    d = p - torch.tensor([[1.0, 0], [0, 0], [0, 1.0]], device="cuda")
+    ref = d.t() @ x[:, :4].double()
+    # one rounding of each gradient of a logit, one of the result
+    bound = 2.0 ** -8 * (d.abs().t() @ x[:, :4].double().abs()) + 2.0 ** -15
+    assert ((dw[[-1, -2], :4].double() - ref).abs() <= bound).all()
+    # the other words' shares, 1/2.1e6 or less of x
+    assert (dw[:-2].abs().amax() <= 4.0 + 1e-3) and (dw[7, 0] + 4.0).abs() <= 0.02
+    others = dw[8:vocab - 2]
+    assert others.abs().amax() <= 6.1 / 2.0e6
