@@ -18,8 +18,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "grouped.cuh"
 #include "lm_internal.h"
 
@@ -41,7 +39,6 @@ struct GatherArgs {
     float *l2, *ca, *cb;       // backward
     float *unit;               // backward
     int unit_given;            // fp16: unit_kernel has been there
-    float *dot;                // forward: x w[target], in fp32
     uint16_t *x;
     int64_t x_pitch;
     int per_block;             // rows
@@ -58,60 +55,30 @@ __device__ __forceinline__ bool counts(const LceArgs &a, int64_t i, int64_t *tar
     return false;
 }
 
-// The sum of two products of 16-bit pairs.
-template <typename T>
-__device__ __forceinline__ float pair_product(uint32_t u, uint32_t v)
+// `lanes` threads copy a row of 16-bit values, by the widest words that fit it.
+__device__ __forceinline__ void copy_row(uint16_t *dst, const uint16_t *src, int n, int lane, int lanes)
 {
-    const float2 f = Half2Of<T>::unpack(u), g = Half2Of<T>::unpack(v);
-    return fmaf(f.x, g.x, f.y * g.y);
-}
-
-// `lanes` threads copy a row of 16-bit values, by the widest words that fit it; with a
-// type T, a thread returns its share of the row's product with `w`.
-template <typename T>
-__device__ __forceinline__ float copy_row(uint16_t *dst, const uint16_t *src, const uint16_t *w, int n, int lane, int lanes)
-{
-    constexpr bool DOT = !std::is_void<T>::value;
-    constexpr int UNROLL = 4;
-    using P = typename std::conditional<DOT, T, __half>::type;
-    float sum[2] = {};
     if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0 && n % 8 == 0) {
-        for (int c = lane; c < n / 8; c += UNROLL * lanes) {
-            uint4 v[UNROLL], f[UNROLL];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-                if (c + u * lanes < n / 8) {
-                    v[u] = reinterpret_cast<const uint4 *>(src)[c + u * lanes];
-                    if (DOT) f[u] = reinterpret_cast<const uint4 *>(w)[c + u * lanes];   // (weights of such widths are aligned)
-                }
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                if (c + u * lanes >= n / 8) break;
-                reinterpret_cast<uint4 *>(dst)[c + u * lanes] = v[u];
-                if (DOT) {
-                    sum[0] += pair_product<P>(v[u].x, f[u].x) + pair_product<P>(v[u].y, f[u].y);
-                    sum[1] += pair_product<P>(v[u].z, f[u].z) + pair_product<P>(v[u].w, f[u].w);
-                }
-            }
-        }
-    } else {
-        for (int c = lane; c < n; c += 4 * lanes) {
-            uint16_t v[4], f[4];
+        for (int c = lane; c < n / 8; c += 4 * lanes) {
+            uint4 v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (c + u * lanes < n) {
-                    v[u] = src[c + u * lanes];
-                    if (DOT) f[u] = w[c + u * lanes];
-                }
+                if (c + u * lanes < n / 8) v[u] = reinterpret_cast<const uint4 *>(src)[c + u * lanes];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                if (c + u * lanes >= n) break;
-                dst[c + u * lanes] = v[u];
-                if (DOT) sum[u & 1] += pair_product<P>(v[u], f[u]);
-            }
+            for (int u = 0; u < 4; ++u)
+                if (c + u * lanes < n / 8) reinterpret_cast<uint4 *>(dst)[c + u * lanes] = v[u];
+        }
+    } else {
+        for (int c = lane; c < n; c += 8 * lanes) {
+            uint16_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u * lanes < n) v[u] = src[c + u * lanes];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u * lanes < n) dst[c + u * lanes] = v[u];
         }
     }
-    return sum[0] + sum[1];
 }
 
 __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lanes)
@@ -124,14 +91,12 @@ __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lan
 
 // A CTA takes per_block rows; it counts those that count before them itself,
 // which reads the targets once per CTA, but needs no CTA to wait for another.
-// T: the operands' type in the forward pass, void in the backward pass.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) gather_kernel(const __grid_constant__ GatherArgs g)
+template <bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_constant__ GatherArgs g)
 {
     pdl_begin();
-    constexpr bool BACKWARD = std::is_void<T>::value;
     __shared__ int warps[kThreads / 32];
-    __shared__ int place[kThreads], hit[kThreads];
+    __shared__ int place[kThreads];
     const LceArgs &a = g.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t first = (int64_t)blockIdx.x * g.per_block, end = min(first + g.per_block, a.rows);
@@ -192,7 +157,6 @@ __global__ void __launch_bounds__(kThreads, 3) gather_kernel(const __grid_consta
             before += warps[w];
         }
         place[t] = used ? at : -1;
-        hit[t] = (int)target;
         if (used) {
             g.index[at] = (int)i;
             g.target[at] = (int)target;
@@ -210,24 +174,10 @@ __global__ void __launch_bounds__(kThreads, 3) gather_kernel(const __grid_consta
         const int lanes = g.per_block == 1 ? kThreads : 32, member = t % lanes;   // a row to a warp, or to the CTA
         for (int r = t / lanes; r < (int)min((int64_t)kThreads, end - base); r += kThreads / lanes) {
             const int64_t row = base + r;
-            if (place[r] >= 0) {
-                float dot = copy_row<T>(g.x + place[r] * g.x_pitch, static_cast<const uint16_t *>(a.x) + row * a.x_stride,
-                                        static_cast<const uint16_t *>(a.w) + (int64_t)hit[r] * a.hidden, a.hidden, member, lanes);
-                if (!BACKWARD) {
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                    if (lanes > 32) {   // (the CTA's only row)
-                        __shared__ float dots[kThreads / 32];
-                        if (lane == 0) dots[warp] = dot;
-                        __syncthreads();
-                        dot = 0.0f;
-                        for (int w = 0; w < kThreads / 32; ++w) dot += dots[w];
-                    }
-                    if (member == 0) g.dot[place[r]] = dot;
-                }
-            } else if (a.dx) {
+            if (place[r] >= 0)
+                copy_row(g.x + place[r] * g.x_pitch, static_cast<const uint16_t *>(a.x) + row * a.x_stride, a.hidden, member, lanes);
+            else if (a.dx)
                 zero_row(static_cast<uint16_t *>(a.dx) + row * a.dx_stride, a.hidden, member, lanes);
-            }
         }
     }
     if (end == a.rows) {   // the last CTA
@@ -281,7 +231,7 @@ __global__ void __launch_bounds__(1024) unit_kernel(const __grid_constant__ LceA
 struct LossArgs {
     const int *count, *index;
     const float2 *part;
-    const float *at_target, *dot;
+    const float *at_target;
     float *loss, *lse;
     int rows, slots, per_block;
     float scale;
@@ -289,14 +239,8 @@ struct LossArgs {
 
 // `per_block` rows per CTA (one, or four, whose neighbouring slots fill a sector), a
 // row's slots over the CTA's threads.
-//
-// The target's logit is the one that `gather` has taken in fp32 from the operands:
-// the tensor cores' truncation leaves theirs 1e-5 low, which is what the loss would be
-// off by (relative error of 4096 rows' losses, 4096 terms per logit: 1.3e-6, and 9e-7
-// so).  With m the largest logit, t the target's, A the others' sum e^(l - m) and
-// d = m - t the loss is log(1 + A e^d), so that a sure target's loss keeps its digits.
-// lse stays that of the products' logits, which the backward pass takes it from: what
-// both are off by cancels in 1 - e^(l - lse), of which a sure target's gradient consists.
+// The loss is taken from the maximum, so that a sure target's, whose sum of exponentials
+// is one, is exactly zero.
 __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ LossArgs p)
 {
     pdl_begin();
@@ -325,12 +269,10 @@ __global__ void __launch_bounds__(kThreads) loss_kernel(const __grid_constant__ 
     __syncthreads();
     if (t >= per || row >= count) return;
     for (int w = 1; w < WARPS; ++w) s = join(s, red[w][t]);
-    const float d = p.scale * (s.x - p.dot[row]);
-    float others = s.y - ex2_approx((p.at_target[row] - s.x) * c);
-    if (others < 0.0f) others = 0.0f;   // (not a NaN)
+    const float over = logf(s.y);
     const int64_t i = p.index[row];
-    p.loss[i] = d > 60.0f ? d + logf(others + expf(-d)) : log1pf(others * expf(d));
-    p.lse[i] = fmaf(p.scale, s.x, logf(s.y));
+    p.loss[i] = fmaf(p.scale, s.x - p.at_target[row], over);
+    p.lse[i] = fmaf(p.scale, s.x, over);
 }
 
 // ---------------------------------------------------------------- dx
@@ -427,7 +369,7 @@ struct Plan {
     int64_t x_pitch, w_pitch, dl_pitch, dx_pitch;
     int64_t piece;          // words
     int splits;             // of dx
-    int64_t count, unit, index, target, l2, ca, cb, at_target, dot, part, x, dl, dx, pack, bytes;
+    int64_t count, unit, index, target, l2, ca, cb, at_target, part, x, dl, dx, pack, bytes;
 };
 
 // Words per piece where `most` bytes hold `per_word` each: as few pieces as fit, of
@@ -464,7 +406,6 @@ Plan plan_of(bool backward, int64_t rows, int64_t vocab, int64_t hidden)
     if (pack) p.piece = piece_of(vocab, p.w_pitch * 2, kPackBytes);
     if (!backward) {
         p.at_target = take(4 * rows);
-        p.dot = take(4 * rows);
         // two slots per tile of 256 words, for few rows of as little as 64
         const int64_t pieces = (vocab + p.piece - 1) / p.piece, few = rows < 256 ? rows : 256;
         const int64_t wide = 2 * (vocab / 256 + pieces) * rows, narrow = 2 * (vocab / 64 + pieces) * few;
@@ -508,17 +449,14 @@ cudaError_t launch_gather(const LceArgs &a, const Plan &p, bool backward, cudaSt
     // before would take longer than that
     g.per_block = a.rows <= 4 * sm_count() ? 1 : a.rows <= 16384 ? 8 : (int)up((a.rows + 2047) / 2048, 8);
     const dim3 grid((unsigned)(a.rows ? (a.rows + g.per_block - 1) / g.per_block : 1));
-    if (!backward) {
-        g.dot = at<float>(a.ws, p.dot);
-        return launch_pdl(a.dtype == TF_BF16 ? gather_kernel<__nv_bfloat16> : gather_kernel<__half>, grid, dim3(kThreads), 0, st, g);
-    }
+    if (!backward) return launch_pdl(gather_kernel<false>, grid, dim3(kThreads), 0, st, g);
     g.l2 = at<float>(a.ws, p.l2);
     g.ca = at<float>(a.ws, p.ca);
     g.cb = at<float>(a.ws, p.cb);
     g.unit = at<float>(a.ws, p.unit);
     g.unit_given = a.dtype == TF_FP16;
     const cudaError_t e = g.unit_given ? launch_pdl(unit_kernel, dim3(1), dim3(1024), 0, st, a, g.unit) : cudaSuccess;
-    return e != cudaSuccess ? e : launch_pdl(gather_kernel<void>, grid, dim3(kThreads), 0, st, g);
+    return e != cudaSuccess ? e : launch_pdl(gather_kernel<true>, grid, dim3(kThreads), 0, st, g);
 }
 
 LceProduct product_of(const LceArgs &a, const Plan &p)
@@ -575,7 +513,7 @@ cudaError_t launch_lce_forward(const LceArgs &a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     LossArgs l = {};
     l.count = m.count; l.index = at<int>(a.ws, p.index); l.part = m.part; l.at_target = m.at_target;
-    l.dot = at<float>(a.ws, p.dot); l.loss = a.loss; l.lse = a.lse; l.rows = (int)a.rows; l.slots = m.slot0;
+    l.loss = a.loss; l.lse = a.lse; l.rows = (int)a.rows; l.slots = m.slot0;
     l.per_block = a.rows < 512 ? 1 : 4; l.scale = a.scale;
     return launch_pdl(loss_kernel, dim3((unsigned)((a.rows + l.per_block - 1) / l.per_block)), dim3(kThreads), 0, st, l);
 }

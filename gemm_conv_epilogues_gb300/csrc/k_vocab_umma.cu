@@ -21,10 +21,10 @@
 //   0     TMA producer of a ring of K steps (64 deep, 128-byte swizzle)
 //   1     TMEM allocator and MMA issuer
 //   4-11  epilogue
-// Few rows leave the tensor cores idle, so that their logits' tiles take 128 words and
-// either half of K has an accumulator of its own, which the epilogue adds: the truncation
-// that every 16 terms bring shrinks with the partial sums (relative error of four rows' losses,
-// 4096 terms: 1.1e-6 without, see below with).
+// The tensor cores truncate where fp32 additions round, so an accumulator's error grows with
+// the number of MMAs it takes.  A logit's sum is cut into parts of 1024 terms, whose
+// accumulators alternate; the epilogue's threads add them in registers while the next part's
+// MMAs run.
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
 // error word and winds down.
 #include <cuda.h>
@@ -54,8 +54,11 @@ constexpr int kEpiWarps = 8, kFirstEpiWarp = 4;
 constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kTileN = 256;
 constexpr int kABytes = 128 * BK * 2;               // 128 rows of a K step
-// B: half of a pair's 256 columns, all of a single CTA's 256, or of its 128 (the logits of few rows)
-constexpr int stage_bytes(int mode, int cg) { return kABytes + (cg == 2 || mode != LCE_GRADS ? 128 : 256) * BK * 2; }
+constexpr int stage_bytes(int cg) { return kABytes + 256 / cg * BK * 2; }
+constexpr int kPartSteps = 16;                      // STATS, DLOGITS: K steps per part of a sum
+// Registers: the epilogue's threads hold 128 sums each while the issuing warps need few.  The
+// kernel starts with 168 per thread, and 88*128 + 208*256 = 168*384.
+constexpr int kIssueRegs = 88, kEpilogueRegs = 208;
 constexpr int kBoxBytes = 32 * 128;                 // an epilogue warp's box: 32 rows of 128 bytes
 constexpr int kOffBox = kRingBytes, kOffBar = kOffBox + kEpiWarps * kBoxBytes;
 constexpr int kNumBars = 2 * kMaxStages + 5;
@@ -209,8 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_x, const __grid_constant__ VocabArgs p)
 {
     constexpr bool PAIR = CG == 2;
-    constexpr int kStageBytes = stage_bytes(MODE, CG), kStages = kRingBytes / kStageBytes;
-    constexpr bool HALVES = CG == 1 && MODE != LCE_GRADS;   // two sums per accumulator, 128 columns apart
+    constexpr int kStageBytes = stage_bytes(CG), kStages = kRingBytes / kStageBytes;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *empty = full + kStages;
@@ -269,342 +271,374 @@ __global__ void __launch_bounds__(kThreads, 1)
     Share<MODE, CG> share;
     share.init(p, count, (int)blockIdx.x / CG, (int)gridDim.x / CG);
 
-    if (!sound) {
-        // nothing has been issued
-    } else if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, last_phase = 0;
-        bool ok = true;
-        const bool issuer = elect_one();
-        const int half = p.bn / CG;   // columns of B that this CTA loads
-        Tile t;
-        for (int j = 0; ok && share.at(p, j, &t); ++j) {
-            for (int kb = 0; kb < t.nk; ++kb) {
-                const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                if (issuer) {
-                    uint64_t *bar = &full[stage];
-                    uint8_t *a_dst = smem + stage * kStageBytes, *b_dst = a_dst + kABytes;
-                    const int k = (t.k0 + kb) * BK, row = t.m0 + crank * 128;
-                    const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, 0) : 0u;
-                    auto load = [&](void *dst, const CUtensorMap *map, int c0, int c1) {
-                        if constexpr (PAIR) ptx::tma_load_2d_pair(dst, map, bar_cl, c0, c1);
-                        else ptx::tma_load_2d(dst, map, bar, c0, c1);
-                    };
-                    if constexpr (MODE != LCE_GRADS) {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (p.a_box + half) * (BK * 2)));
-                        load(a_dst, &map_a, k, row);
-                        load(b_dst, &map_w, k, t.n0 + crank * half);
-                    } else {
-                        if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (128 + half) * (BK * 2)));
-                        const CUtensorMap *map_b = t.kind == TILE_DX ? &map_w : &map_x;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
-                            const int m = row + 64 * i;
-                            if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
-                            else load(a_dst + i * kChunkBytes, &map_a, m, k);
-                        }
-                        for (int i = 0; i < half / 64; ++i) load(b_dst + i * kChunkBytes, map_b, t.n0 + crank * half + 64 * i, k);
-                    }
-                }
-                __syncwarp();
-                issued |= 1u << stage;
-                last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
-                if (++stage == kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
-        // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
-        for (int s = 0; s < kStages; ++s)
-            if (leader && ((issued >> s) & 1u))
-                if (!ptx::mbar_wait<PAIR>(&full[s], (last_phase >> s) & 1u, p.wait_ns) && lane == 0)
-                    atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
-    } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (leader) {
-            int stage = 0, b = 0;
-            uint32_t phase = 0, taken = 0;   // taken: parity of the uses of either accumulator
+    // (one branch per warpgroup, which changes its registers as a whole)
+    if (warp < kFirstEpiWarp) {
+        if constexpr (MODE != LCE_GRADS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (sound && warp == 0) {
+            // ------------------------------------------------------------ producer
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, last_phase = 0;
             bool ok = true;
-            const bool issuer = elect_one(), bf16 = p.a.dtype == TF_BF16;
-            const uint32_t base = ptx::smem_u32(smem);
+            const bool issuer = elect_one();
+            const int half = p.bn / CG;   // columns of B that this CTA loads
             Tile t;
             for (int j = 0; ok && share.at(p, j, &t); ++j) {
-                if (t.nk == 0) continue;
-                const bool a_mn = t.kind == TILE_DW, b_mn = MODE == LCE_GRADS;
-                const uint32_t id = idesc(128 * CG, p.bn, bf16, a_mn, b_mn);
-                const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
-                const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + kABytes, !b_mn);
-                auto commit = [&](uint64_t *bar) {
-                    if constexpr (PAIR) commit_both(bar);
-                    else ptx::umma_commit(bar);
-                };
-                bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d = tmem_base + (uint32_t)(b * kTileN);
                 for (int kb = 0; kb < t.nk; ++kb) {
-                    got = ptx::mbar_wait(&full[stage], phase, p.wait_ns);
+                    const bool got = ptx::mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns);
                     if (!__all_sync(0xffffffffu, got)) {
                         ok = false;
                         break;
                     }
-                    ptx::tc_fence_after();
                     if (issuer) {
-                        const bool upper = HALVES && kb >= (t.nk + 1) / 2, begins = kb == 0 || (HALVES && kb == (t.nk + 1) / 2);
-                        const uint32_t a = a_low + (uint32_t)stage * (kStageBytes >> 4), bb = b_low + (uint32_t)stage * (kStageBytes >> 4);
+                        uint64_t *bar = &full[stage];
+                        uint8_t *a_dst = smem + stage * kStageBytes, *b_dst = a_dst + kABytes;
+                        const int k = (t.k0 + kb) * BK, row = t.m0 + crank * 128;
+                        const uint32_t bar_cl = PAIR ? ptx::mapa_shared(bar, 0) : 0u;
+                        auto load = [&](void *dst, const CUtensorMap *map, int c0, int c1) {
+                            if constexpr (PAIR) ptx::tma_load_2d_pair(dst, map, bar_cl, c0, c1);
+                            else ptx::tma_load_2d(dst, map, bar, c0, c1);
+                        };
+                        if constexpr (MODE != LCE_GRADS) {
+                            if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (p.a_box + half) * (BK * 2)));
+                            load(a_dst, &map_a, k, row);
+                            load(b_dst, &map_w, k, t.n0 + crank * half);
+                        } else {
+                            if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (128 + half) * (BK * 2)));
+                            const CUtensorMap *map_b = t.kind == TILE_DX ? &map_w : &map_x;
 #pragma unroll
-                        for (int k = 0; k < BK / UMMA_K; ++k) {
-                            const uint32_t acc = k > 0 || !begins ? 1u : 0u, to = d + (upper ? kTileN / 2 : 0u);
-                            if constexpr (PAIR) ptx::umma_bf16_pair(to, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
-                            else ptx::umma_bf16(to, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
+                            for (int i = 0; i < 2; ++i) {   // boxes of 64 rows (DX) or 64 words (DW)
+                                const int m = row + 64 * i;
+                                if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
+                                else load(a_dst + i * kChunkBytes, &map_a, m, k);
+                            }
+                            for (int i = 0; i < half / 64; ++i) load(b_dst + i * kChunkBytes, map_b, t.n0 + crank * half + 64 * i, k);
                         }
-                        commit(&empty[stage]);
-                        if (kb == t.nk - 1) commit(&tfull[b]);
                     }
                     __syncwarp();
+                    issued |= 1u << stage;
+                    last_phase = (last_phase & ~(1u << stage)) | (phase << stage);
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
-                taken ^= 1u << b;
-                b ^= 1;
             }
-            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
-            if (issuer) {   // (the lane that issued the MMAs)
-                if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
-                else ptx::umma_commit(drain);
-            }
-            __syncwarp();
-            if (!ptx::mbar_wait(drain, 0, p.wait_ns) && lane == 0) atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
-        }
-    } else if (warp >= kFirstEpiWarp) {
-        // ------------------------------------------------------------ epilogue
-        // Warp w reads TMEM lanes 32*(w%4) .. +31, one row per lane, and one half of the
-        // columns, 64 at a time; the accumulator is free when the last of them are in
-        // registers.  (All 128 at once, to free it at the start, make straight-line code of
-        // all that follows: 4-8% slower in STATS, 25% in small calls.)
-        const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
-        uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
-        const bool bf16 = p.a.dtype == TF_BF16;
-        const int c0 = h * ((p.bn / 2 + 63) & ~63), c1 = h ? p.bn : (p.bn / 2 + 63) & ~63;   // this warp's columns of a tile
-        const float mult = p.a.factor * (MODE == LCE_GRADS ? __ldg(p.a.unit + 1) : 1.0f);
-        int b = 0;
-        uint32_t seen = 0;   // parity of the results of either accumulator
-        bool ok = true;
-        Tile t;
-        auto pack = [&](uint32_t x, uint32_t y) {
-            const float a = __uint_as_float(x), b = __uint_as_float(y);
-            return bf16 ? Half2Of<__nv_bfloat16>::pack(a, b) : Half2Of<__half>::pack(a, b);
-        };
-        // 32 columns as 16-bit values into one half of the box's rows
-        auto put_half = [&](const uint32_t (&r)[32], int part) {
+            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_PRODUCER_WAIT);
+            // every copy has landed before the CTA exits (a pair's complete on the first CTA's barriers)
+            for (int s = 0; s < kStages; ++s)
+                if (leader && ((issued >> s) & 1u))
+                    if (!ptx::mbar_wait<PAIR>(&full[s], (last_phase >> s) & 1u, p.wait_ns) && lane == 0)
+                        atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
+        } else if (sound && warp == 1) {
+            // ------------------------------------------------------------ MMA issuer
+            if (leader) {
+                int stage = 0, b = 0;
+                uint32_t phase = 0, taken = 0;   // taken: parity of the uses of either accumulator
+                bool ok = true;
+                const bool issuer = elect_one(), bf16 = p.a.dtype == TF_BF16;
+                const uint32_t base = ptx::smem_u32(smem);
+                Tile t;
+                for (int j = 0; ok && share.at(p, j, &t); ++j) {
+                    if (t.nk == 0) continue;
+                    const bool a_mn = t.kind == TILE_DW, b_mn = MODE == LCE_GRADS;
+                    const uint32_t id = idesc(128 * CG, p.bn, bf16, a_mn, b_mn);
+                    const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
+                    const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + kABytes, !b_mn);
+                    auto commit = [&](uint64_t *bar) {
+                        if constexpr (PAIR) commit_both(bar);
+                        else ptx::umma_commit(bar);
+                    };
+                    for (int kb = 0; kb < t.nk; ++kb) {
+                        const bool begins = kb == 0 || (MODE != LCE_GRADS && kb % kPartSteps == 0);
+                        const bool ends = kb == t.nk - 1 || (MODE != LCE_GRADS && kb % kPartSteps == kPartSteps - 1);
+                        if (begins) {
+                            const bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
+                            if (!__all_sync(0xffffffffu, got)) {
+                                ok = false;
+                                break;
+                            }
+                        }
+                        const bool got = ptx::mbar_wait(&full[stage], phase, p.wait_ns);
+                        if (!__all_sync(0xffffffffu, got)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        if (issuer) {
+                            const uint32_t a = a_low + (uint32_t)stage * (kStageBytes >> 4), bb = b_low + (uint32_t)stage * (kStageBytes >> 4);
+                            const uint32_t d = tmem_base + (uint32_t)(b * kTileN);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                box_put(box, lane, part * 4 + i, make_uint4(pack(r[8 * i], r[8 * i + 1]), pack(r[8 * i + 2], r[8 * i + 3]),
-                                                            pack(r[8 * i + 4], r[8 * i + 5]), pack(r[8 * i + 6], r[8 * i + 7])));
-        };
-        for (int j = 0; ok && share.at(p, j, &t); ++j) {
-            const int acc = b;
-            const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
-            const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kTileN + c0);
-            const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
-            const int left = min(width, c1) - c0;   // columns with results, up to 128
-            int target = -1;
-            float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
-            if constexpr (MODE != LCE_GRADS) {
-                if (row < count) {
-                    target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
-                    if constexpr (MODE == LCE_DLOGITS) {
-                        l2 = __ldg(p.a.l2 + row);
-                        ca = __ldg(p.a.ca + row);
-                        cb = __ldg(p.a.cb + row);
+                            for (int k = 0; k < BK / UMMA_K; ++k) {
+                                const uint32_t acc = k > 0 || !begins ? 1u : 0u;
+                                if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
+                                else ptx::umma_bf16(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
+                            }
+                            commit(&empty[stage]);
+                            if (ends) commit(&tfull[b]);
+                        }
+                        __syncwarp();
+                        if (ends) {
+                            taken ^= 1u << b;
+                            b ^= 1;
+                        }
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
                 }
-            }
-            if (t.nk > 0) {
-                const bool got = ptx::mbar_wait(&tfull[acc], (seen >> acc) & 1u, p.wait_ns);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
+                if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_MMA_WAIT);
+                if (issuer) {   // (the lane that issued the MMAs)
+                    if constexpr (PAIR) ptx::umma_commit_pair(ptx::smem_u32(drain));
+                    else ptx::umma_commit(drain);
                 }
-                ptx::tc_fence_after();
-                seen ^= 1u << acc;
-                b ^= 1;
-            }
-            auto release = [&]() {
-                ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[acc], 0));
-                    else ptx::mbar_arrive(&tempty[acc]);
-                }
+                if (!ptx::mbar_wait(drain, 0, p.wait_ns) && lane == 0) atomicOr(p.err, TF_DEVERR_DRAIN_WAIT);
+            }
+        }
+    } else {
+        if constexpr (MODE != LCE_GRADS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+        if (sound) {
+            // ------------------------------------------------------------ epilogue
+            // Warp w reads TMEM lanes 32*(w%4) .. +31, one row per lane, and one half of the columns.
+            const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
+            uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
+            const bool bf16 = p.a.dtype == TF_BF16;
+            const int c0 = h * ((p.bn / 2 + 63) & ~63), c1 = h ? p.bn : (p.bn / 2 + 63) & ~63;   // this warp's columns of a tile
+            const float mult = p.a.factor * (MODE == LCE_GRADS ? __ldg(p.a.unit + 1) : 1.0f);
+            int b = 0;
+            uint32_t seen = 0;   // parity of the results of either accumulator
+            bool ok = true;
+            Tile t;
+            auto pack = [&](uint32_t x, uint32_t y) {
+                const float a = __uint_as_float(x), b = __uint_as_float(y);
+                return bf16 ? Half2Of<__nv_bfloat16>::pack(a, b) : Half2Of<__half>::pack(a, b);
             };
-            if (t.nk > 0 && left <= 0) release();
-            float top = -INFINITY, sum = 0.0f;
+            // 32 columns as 16-bit values into one half of the box's rows
+            auto put_half = [&](const uint32_t (&r)[32], int part) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    box_put(box, lane, part * 4 + i, make_uint4(pack(r[8 * i], r[8 * i + 1]), pack(r[8 * i + 2], r[8 * i + 3]),
+                                                                pack(r[8 * i + 4], r[8 * i + 5]), pack(r[8 * i + 6], r[8 * i + 7])));
+            };
+            for (int j = 0; ok && share.at(p, j, &t); ++j) {
+                const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
+                const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
+                const int left = min(width, c1) - c0;   // columns with results, up to 128
+                int target = -1;
+                float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
+                if constexpr (MODE != LCE_GRADS) {
+                    if (row < count) {
+                        target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
+                        if constexpr (MODE == LCE_DLOGITS) {
+                            l2 = __ldg(p.a.l2 + row);
+                            ca = __ldg(p.a.ca + row);
+                            cb = __ldg(p.a.cb + row);
+                        }
+                    }
+                }
+                // waits for the accumulator of the next part (or tile)
+                auto await = [&]() {
+                    const bool got = ptx::mbar_wait(&tfull[b], (seen >> b) & 1u, p.wait_ns);
+                    if (!__all_sync(0xffffffffu, got)) return ok = false;
+                    ptx::tc_fence_after();
+                    seen ^= 1u << b;
+                    return true;
+                };
+                // hands it back
+                auto release = [&]() {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (PAIR) ptx::mbar_arrive_cluster(ptx::mapa_shared(&tempty[b], 0));
+                        else ptx::mbar_arrive(&tempty[b]);
+                    }
+                    b ^= 1;
+                };
+                const uint32_t columns = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
+                if constexpr (MODE != LCE_GRADS) {
+                    uint32_t r[4][32];   // the sums of this row's columns
+                    for (int k0 = 0; k0 < t.nk; k0 += kPartSteps) {
+                        if (!await()) break;
+                        const uint32_t taddr = columns + (uint32_t)(b * kTileN);
+                        if (k0 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (32 * i < left) ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(32 * i), r[i]);
+                            ptx::tmem_ld_wait();
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (32 * i >= left) break;
+                                uint32_t v[32];
+                                ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(32 * i), v);
+                                ptx::tmem_ld_wait();
+#pragma unroll
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 sum = fadd2(make_float2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])),
+                                                             make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                                    r[i][k] = __float_as_uint(sum.x);
+                                    r[i][k + 1] = __float_as_uint(sum.y);
+                                }
+                            }
+                        }
+                        release();
+                    }
+                    if (!ok) break;
+                    if constexpr (MODE == LCE_STATS) {
+                        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int c = 32 * i;
+                            if (c >= left) break;
+                            if (c + 32 <= left) join_stats(r[i], 32, p.a.factor, top, sum);
+                            else join_stats(r[i], left - c, p.a.factor, top, sum);
+                            const int at = target - c;
+                            const bool hit = at >= 0 && at < 32 && target < left;
+                            if (__any_sync(0xffffffffu, hit)) {
+                                const float v = pick(r[i], at);
+                                if (hit) p.a.at_target[row] = v;
+                            }
+                        }
+                        if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            if (64 * u >= left) break;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int i = 2 * u + half, c = 32 * i;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
+                                const int at = target - c;
+                                const bool hit = at >= 0 && at < 32 && target < left;
+                                if (__any_sync(0xffffffffu, hit)) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k)
+                                        if (hit && k == at) r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) - cb);
+                                }
+                                // columns behind the piece's words, and rows behind those that count, which
+                                // dw's last K step reads: zeros
+                                if (c + 32 > left || row0 + 32 > count) {
+#pragma unroll
+                                    for (int k = 0; k < 32; ++k) r[i][k] = row < count && c + k < left ? r[i][k] : 0u;
+                                }
+                                put_half(r[i], half);
+                            }
+                            __syncwarp();
+                            const int piece = lane & 7, c = c0 + 64 * u + 8 * piece;
+                            uint16_t *out = static_cast<uint16_t *>(p.a.dl) + t.n0 + c;
+                            if (c < c1 && t.n0 + c < p.a.dl_pitch) {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const int at = 4 * i + (lane >> 3);
+                                    if (row0 + at < p.a.rows)
+                                        *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                } else {
+                    const uint32_t taddr = columns + (uint32_t)(b * kTileN);
+                    if (t.nk > 0) {
+                        if (!await()) break;
+                        if (left <= 0) release();
+                    }
 #pragma unroll 1
-            for (int u = 0; u < left; u += 64) {
-                uint32_t r[2][32];
-                if (t.nk > 0) {
-                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
-                    ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
-                    if (HALVES && t.nk > 1) {   // (one K step is all in the lower half)
-                        uint32_t v[2][32];
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + kTileN / 2), v[0]);
-                        ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + kTileN / 2 + 32), v[1]);
-                        ptx::tmem_ld_wait();
+                    for (int u = 0; u < left; u += 64) {
+                        uint32_t r[2][32];
+                        if (t.nk > 0) {
+                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
+                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
+                            ptx::tmem_ld_wait();
+                            if (u + 64 >= left) release();
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
+                        }
+                        const bool dx = t.kind == TILE_DX;
+                        const int rows = dx ? count : p.a.words;   // of this tile's M side
+                        const bool wide = dx || p.a.dw_f32;        // 32-bit results
+                        const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                        if ((t.nk == 0 && add) || row0 >= rows) continue;
+                        const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
+                        uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
+                                          : static_cast<uint8_t *>(p.a.dw);
+                        // rows that 16-byte words make up
+                        const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) + __uint_as_float(v[0][k]));
-                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) + __uint_as_float(v[1][k]));
+                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
+                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
                         }
-                    }
-                    ptx::tmem_ld_wait();
-                    if (u + 64 >= left) release();
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
-                }
-                if constexpr (MODE == LCE_STATS) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = u + 32 * i;
-                        if (c + 32 <= left) join_stats(r[i], 32, p.a.factor, top, sum);
-                        else join_stats(r[i], left - c, p.a.factor, top, sum);
-                        const int at = target - c;
-                        const bool hit = at >= 0 && at < 32 && target < left;
-                        if (__any_sync(0xffffffffu, hit)) {
-                            const float v = pick(r[i], at);
-                            if (hit) p.a.at_target[row] = v;
+                        if (!wide) {
+                            put_half(r[0], 0);
+                            put_half(r[1], 1);
                         }
-                    }
-                } else if constexpr (MODE == LCE_DLOGITS) {
+                        const int per = wide ? 4 : 8, size = wide ? 4 : 2;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int c = u + 32 * i;
+                        for (int i = 0; i < 2; ++i) {
+                            if (i == 1 && (!wide || u + 32 >= left)) break;
+                            if (wide) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
-                        const int at = target - c;
-                        const bool hit = at >= 0 && at < 32 && target < left;
-                        if (__any_sync(0xffffffffu, hit)) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (hit && k == at) r[i][k] = __float_as_uint(__uint_as_float(r[i][k]) - cb);
-                        }
-                        // columns behind the piece's words, and rows behind those that count, which
-                        // dw's last K step reads: zeros
-                        if (c + 32 > left || row0 + 32 > count) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) r[i][k] = row < count && c + k < left ? r[i][k] : 0u;
-                        }
-                        put_half(r[i], i);
-                    }
-                    __syncwarp();
-                    const int piece = lane & 7, c = c0 + u + 8 * piece;
-                    uint16_t *out = static_cast<uint16_t *>(p.a.dl) + t.n0 + c;
-                    if (c < c1 && t.n0 + c < p.a.dl_pitch) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int at = 4 * i + (lane >> 3);
-                            if (row0 + at < p.a.rows)
-                                *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
-                        }
-                    }
-                    __syncwarp();
-                } else {
-                    const bool dx = t.kind == TILE_DX;
-                    const int rows = dx ? count : p.a.words;   // of this tile's M side
-                    const bool wide = dx || p.a.dw_f32;        // 32-bit results
-                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
-                    if ((t.nk == 0 && add) || row0 >= rows) continue;
-                    const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
-                    uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
-                                      : static_cast<uint8_t *>(p.a.dw);
-                    // rows that 16-byte words make up
-                    const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
-                        r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
-                    }
-                    if (!wide) {
-                        put_half(r[0], 0);
-                        put_half(r[1], 1);
-                    }
-                    const int per = wide ? 4 : 8, size = wide ? 4 : 2;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (i == 1 && (!wide || u + 32 >= left)) break;
-                        if (wide) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
-                        }
-                        __syncwarp();
-                        // the box's rows, of 128 bytes from column c on
-                        const int c = t.n0 + c0 + u + 32 * i;
-                        if (words) {
-                            const int piece = lane & 7, col = c + per * piece;
-                            uint8_t *dst = out + ((int64_t)(row0 + (lane >> 3)) * pitch + col) * size;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int at = 4 * k + (lane >> 3);
-                                if (row0 + at >= rows || col >= pitch) continue;
-                                uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
-                                uint4 v = box_get(box, at, piece);
-                                if (add) {
-                                    const uint4 o = *to;
-                                    v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
-                                    v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
-                                    v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
-                                    v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
-                                }
-                                *to = v;
+                                for (int k = 0; k < 8; ++k)
+                                    box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
                             }
-                        } else {
-                            for (int at = 0; at < min(32, rows - row0); ++at) {
-                                const int64_t to = (int64_t)(row0 + at) * pitch + c;
-                                const int n = min(8 * per, (int)min(pitch, (int64_t)(1 << 30)) - c);   // columns of this row
-                                const uint8_t *src = box + at * 128;
-                                if (wide) {
-                                    if (lane < n) {
-                                        const float v = *reinterpret_cast<const float *>(src + (((lane >> 2) ^ (at & 7)) * 16) + (lane & 3) * 4);
-                                        float *dst = reinterpret_cast<float *>(out) + to + lane;
-                                        *dst = add ? *dst + v : v;
+                            __syncwarp();
+                            // the box's rows, of 128 bytes from column c on
+                            const int c = t.n0 + c0 + u + 32 * i;
+                            if (words) {
+                                const int piece = lane & 7, col = c + per * piece;
+                                uint8_t *dst = out + ((int64_t)(row0 + (lane >> 3)) * pitch + col) * size;
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    const int at = 4 * k + (lane >> 3);
+                                    if (row0 + at >= rows || col >= pitch) continue;
+                                    uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
+                                    uint4 v = box_get(box, at, piece);
+                                    if (add) {
+                                        const uint4 o = *to;
+                                        v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
+                                        v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
+                                        v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
+                                        v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
                                     }
-                                } else {
-                                    // pairs of columns that share a 32-bit word; an odd start leaves its first and last column single
-                                    uint16_t *dst = reinterpret_cast<uint16_t *>(out) + to;
-                                    const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1, e = 2 * lane - odd;
-                                    auto value = [&](int i) {
-                                        return *reinterpret_cast<const uint16_t *>(src + (((i >> 3) ^ (at & 7)) * 16) + (i & 7) * 2);
-                                    };
-                                    if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t *>(dst + e) = value(e) | (uint32_t)value(e + 1) << 16;
-                                    else if (e + 1 < n) dst[e + 1] = value(e + 1);
-                                    else if (e < n) dst[e] = value(e);
-                                    if (odd && lane == 0 && n == 64) dst[63] = value(63);
+                                    *to = v;
+                                }
+                            } else {
+                                for (int at = 0; at < min(32, rows - row0); ++at) {
+                                    const int64_t to = (int64_t)(row0 + at) * pitch + c;
+                                    const int n = min(8 * per, (int)min(pitch, (int64_t)(1 << 30)) - c);   // columns of this row
+                                    const uint8_t *src = box + at * 128;
+                                    if (wide) {
+                                        if (lane < n) {
+                                            const float v = *reinterpret_cast<const float *>(src + (((lane >> 2) ^ (at & 7)) * 16) + (lane & 3) * 4);
+                                            float *dst = reinterpret_cast<float *>(out) + to + lane;
+                                            *dst = add ? *dst + v : v;
+                                        }
+                                    } else {
+                                        // pairs of columns that share a 32-bit word; an odd start leaves its first and last column single
+                                        uint16_t *dst = reinterpret_cast<uint16_t *>(out) + to;
+                                        const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1, e = 2 * lane - odd;
+                                        auto value = [&](int i) {
+                                            return *reinterpret_cast<const uint16_t *>(src + (((i >> 3) ^ (at & 7)) * 16) + (i & 7) * 2);
+                                        };
+                                        if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t *>(dst + e) = value(e) | (uint32_t)value(e + 1) << 16;
+                                        else if (e + 1 < n) dst[e + 1] = value(e + 1);
+                                        else if (e < n) dst[e] = value(e);
+                                        if (odd && lane == 0 && n == 64) dst[63] = value(63);
+                                    }
                                 }
                             }
+                            __syncwarp();
                         }
-                        __syncwarp();
                     }
                 }
             }
-            if constexpr (MODE == LCE_STATS)
-                if (row < count) p.a.part[(int64_t)(t.slot + h) * p.a.rows + row] = make_float2(top, sum);
+            if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
         }
-        if (!ok && lane == 0) atomicOr(p.err, TF_DEVERR_EPILOGUE_WAIT);
     }
 
     ptx::tc_fence_before();
@@ -634,6 +668,12 @@ cudaError_t resident(int *units)
         auto kern = vocab_umma_kernel<MODE, CG>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
+        // the warpgroups' shares of the registers must not exceed what the kernel starts with
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        if (MODE != LCE_GRADS && kIssueRegs * 32 * kFirstEpiWarp + kEpilogueRegs * 32 * kEpiWarps > fa.numRegs * kThreads)
+            return cudaErrorNotSupported;
         int n = sm_count();
         if (CG == 2) {
             cudaLaunchAttribute attr[1];
@@ -740,10 +780,10 @@ int lce_word_tile(int64_t rows, int64_t words)
 {
     const bool narrow = rows <= kNarrowRows;
     const int64_t n = lce_units(rows), down = (rows + lce_row_tile(rows) - 1) / lce_row_tile(rows);
-    const int64_t widest = narrow ? kTileN / 2 : kTileN, step = narrow ? 16 : 32;
-    const int64_t waves = (down * ((words + widest - 1) / widest) + n - 1) / n, across = n * waves / down;
+    const int64_t step = narrow ? 16 : 32;
+    const int64_t waves = (down * ((words + kTileN - 1) / kTileN) + n - 1) / n, across = n * waves / down;
     const int64_t bn = ((words + across - 1) / across + step - 1) / step * step;
-    return bn < 64 ? 64 : bn > widest ? (int)widest : (int)bn;
+    return bn < 64 ? 64 : bn > kTileN ? kTileN : (int)bn;
 }
 
 // Splits of dx's sums: no longer than a CTA's (pair's) share of both gradients.

@@ -413,11 +413,9 @@ int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens,
  * Rows whose target is `ignore` (-100, say; TF_NO_INDEX: none) cost nothing and
  * get a loss and lse of 0; what x holds there, NaN included, is not read.
  * Other targets outside [0, vocab) are ignored likewise and set TF_DEVERR_INDEX.
- * Sums are fp32; equal calls give equal bits.  The tensor cores truncate where
- * fp32 additions round (see the grouped products), by up to 6e-8 of the partial sum for
- * every 16 terms: a logit of 4096 terms of either sign is about 1e-5 too near zero, and lse
- * with it.  The loss takes its target's logit from an fp32 sum instead, and is log(1 + x) of
- * the others' share, so that a sure target's small loss keeps its digits.
+ * Sums are fp32, a logit's in parts of 1024 terms (the tensor cores truncate where fp32
+ * additions round: see the grouped products); equal calls give equal bits.  A sure target's
+ * loss is exactly 0.
  * Any hidden to 65536, any row stride (below 2^31) and the alignment of an
  * element; where hidden is not a multiple of 8 the weights are copied on the
  * way.  Up to 4194304 rows and words; rows may be 0.
