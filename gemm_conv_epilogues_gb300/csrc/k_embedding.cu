@@ -405,6 +405,7 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
     const int slice = (int)blockIdx.y * a.lanes * VEC, c = slice + member * VEC;
     __shared__ __align__(128) P ring[RING ? 2 * UNROLL * kSumThreads : 1];
     __shared__ __align__(8) uint64_t full[kSumThreads / 32][2];
+    __shared__ uint32_t words[kSumThreads / 32][2][UNROLL];
     if (RING) {
         if (threadIdx.x < kSumThreads / 32 * 2) {
             ptx::mbar_init(&full[threadIdx.x / 2][threadIdx.x % 2], 1);
@@ -467,45 +468,42 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
     };
     if constexpr (RING) {
         const uint32_t bytes = (uint32_t)(min(a.lanes * VEC, a.hidden - slice) * (int)sizeof(T));
-        // the first thread of the piece asks for a batch's rows
+        // The piece's first warp asks for a batch: a row per lane.
         auto fetch = [&](int i, int half) {
-            if (member != 0) return;
-            uint64_t key[UNROLL];
-            uint32_t rows = 0;
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                key[u] = key_at(i + u);
-                const uint32_t w = word_of(key[u]);
-                if (w == kNone || w == skipped) key[u] = ~0ull;
-                else ++rows;
-            }
-            ptx::mbar_arrive_expect_tx(&full[group][half], rows * bytes);
-            const T *src = static_cast<const T *>(a.dy) + slice;
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-                if (key[u] != ~0ull)
-                    ptx::bulk_load(&ring[(half * UNROLL + u) * kSumThreads + group * a.lanes],
-                                   src + (int64_t)(uint32_t)key[u] * a.dy_stride, bytes, &full[group][half]);
+            if (member >= 32) return;
+            const uint64_t key = member < UNROLL ? key_at(i + member) : ~0ull;
+            const uint32_t w = word_of(key);
+            const bool wanted = w != kNone && w != skipped;
+            const unsigned rows = __ballot_sync(0xffffffffu, wanted);
+            if (member < UNROLL) words[group][half][member] = w;
+            if (member == 0) ptx::mbar_arrive_expect_tx(&full[group][half], __popc(rows) * bytes);
+            __syncwarp();
+            if (wanted)
+                ptx::bulk_load(&ring[(half * UNROLL + member) * kSumThreads + group * a.lanes],
+                               static_cast<const T *>(a.dy) + slice + (int64_t)(uint32_t)key * a.dy_stride, bytes, &full[group][half]);
+            __syncwarp();
+        };
+        // the piece's threads meet
+        auto meet = [&]() {
+            __syncwarp();
+            if (a.lanes > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(a.lanes) : "memory");
         };
         bool ok = true;   // after a wait that ran out no other is made, and the loop goes on to its end
         fetch(first, 0);
         if (first + UNROLL < limit) fetch(first + UNROLL, 1);
+        meet();
         int batch = 0;
         for (int i = first; i < limit; i += UNROLL, ++batch) {
             const int half = batch & 1;
-            uint32_t w[UNROLL];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) w[u] = word_of(key_at(i + u));
             if (ok && !(ok = ptx::mbar_wait(&full[group][half], (uint32_t)(batch >> 1) & 1u, a.wait_ns)))
                 atomicOr(a.err, TF_DEVERR_PRODUCER_WAIT);
-#pragma unroll
+#pragma unroll 1
             for (int u = 0; u < UNROLL; ++u) {
-                if (w[u] == kNone) break;   // (the last of the list, or of the word that went on)
-                add_row(w[u], ring[(half * UNROLL + u) * kSumThreads + threadIdx.x]);
+                const uint32_t w = words[group][half][u];
+                if (w == kNone) break;   // (the last of the list, or of the word that went on)
+                add_row(w, ring[(half * UNROLL + u) * kSumThreads + threadIdx.x]);
             }
-            // the piece's threads have read the batch
-            __syncwarp();
-            if (a.lanes > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(a.lanes) : "memory");
+            meet();   // the batch has been read
             if (i + 2 * UNROLL < limit) fetch(i + 2 * UNROLL, half);
         }
     } else {
@@ -591,14 +589,14 @@ int lanes_of(int words)
     return lanes;
 }
 
-// Pieces that fill the SMs where the list is long enough (12 CTAs each, in two waves, and no more
+// Pieces that fill the SMs where the list is long enough (14 CTAs each, and no more
 // pieces than a long word's join adds quickly), of 8 to 1024 keys.  Sized for 8 columns per thread, whatever the type, so that the
 // workspace depends on the sizes alone.
 int64_t piece_target(int64_t hidden)
 {
     const int lanes = lanes_of((int)((hidden + 7) / 8));
     const int64_t slices = (hidden + 8 * lanes - 1) / (8 * lanes), per_block = kSumThreads / lanes;
-    const int64_t fill = (12 * 152 + slices - 1) / slices * per_block;
+    const int64_t fill = (14 * 152 + slices - 1) / slices * per_block;
     return fill < kMostPieces ? fill : kMostPieces;
 }
 int64_t piece_of(int64_t rows, int64_t hidden)
@@ -626,7 +624,17 @@ cudaError_t launch_sums(const EmbedArgs &a, SumArgs s, cudaStream_t st)
     const int64_t fill = a.accumulate ? 0 : (a.vocab + kFillRows - 1) / kFillRows;
     const dim3 grid((unsigned)(s.sum_blocks + fill), (unsigned)slices);
     if constexpr (VEC * sizeof(T) == 16)
-        if (s.lanes >= 32) return launch_pdl(sum_pieces_kernel<T, VEC, true>, grid, dim3(kSumThreads), 0, st, s);
+        if (s.lanes >= 32) {
+            auto kern = sum_pieces_kernel<T, VEC, true>;
+            const void *id = reinterpret_cast<const void *>(kern);
+            int known = 0;
+            if (!recall(id, FACT_CARVEOUT, &known)) {   // shared memory for as many CTAs as the registers allow
+                const cudaError_t e = cudaFuncSetAttribute(id, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+                if (e != cudaSuccess) return e;
+                remember(id, FACT_CARVEOUT, 1);
+            }
+            return launch_pdl(kern, grid, dim3(kSumThreads), 0, st, s);
+        }
     return launch_pdl(sum_pieces_kernel<T, VEC, false>, grid, dim3(kSumThreads), 0, st, s);
 }
 

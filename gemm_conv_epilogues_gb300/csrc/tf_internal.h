@@ -20,7 +20,7 @@ int sm_count();
 
 // Numbers asked once of the runtime about a kernel on the current device, by
 // item: recall() is false where none has been remembered.
-enum { FACT_SMEM_RAISED = 0, FACT_WIDE_CLUSTERS = 1, FACT_CLUSTERS = 16 /* + CTAs per cluster */ };
+enum { FACT_SMEM_RAISED = 0, FACT_WIDE_CLUSTERS = 1, FACT_CARVEOUT = 2, FACT_CLUSTERS = 16 /* + CTAs per cluster */ };
 bool recall(const void *kern, int item, int *value);
 void remember(const void *kern, int item, int value);
 

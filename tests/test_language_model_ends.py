@@ -85,3 +85,58 @@ def test_tied_step(b, rows, vocab, hidden):
         v.fill_(float("nan"))
     graph.replay()
     assert all(torch.equal(u, v) for u, v in zip(first, (loss, dtable, dgamma, dbeta, dw1, db1)))
+
+
+@pytest.mark.gpu
+def test_calls_from_several_host_threads(b):
+    """Threads that never called the library before, each with sizes, a stream and workspaces of its own."""
+    import threading
+
+    sizes = [(5, 900, 64), (200, 1500, 128), (700, 300000, 16), (40, 77, 1002)]
+
+    def inputs(i):
+        rows, vocab, hidden = sizes[i]
+        g = torch.Generator("cuda").manual_seed(i)
+        x = torch.randn(rows, hidden, generator=g, device="cuda").half()
+        w = (torch.randn(vocab, hidden, generator=g, device="cuda") * hidden ** -0.5).half()
+        t = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+        return x, w, t
+
+    def step(i, x, w, t):
+        rows, vocab, hidden = sizes[i]
+        loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        dx, dtable = torch.empty_like(x), torch.empty(vocab, hidden, device="cuda")
+        y = torch.empty_like(x)
+        ws = torch.empty(max(b.tf_linear_cross_entropy_forward_workspace_size(rows, vocab, hidden, 0),
+                             b.tf_linear_cross_entropy_backward_workspace_size(rows, vocab, hidden, 0),
+                             b.tf_embedding_backward_workspace_size(rows, vocab, hidden)), dtype=torch.uint8, device="cuda")
+        n = ws.numel()
+        for _ in range(10):
+            b.tf_embedding_forward(t, 1, w, y, hidden, rows, vocab, hidden, 2.0, -1, 0)
+            b.tf_linear_cross_entropy_forward(x, hidden, w, t, 1, loss, lse, rows, vocab, hidden, 1.0, -1, 0, ws, n)
+            b.tf_linear_cross_entropy_backward(x, hidden, w, t, 1, lse, None, None, dx, hidden, dtable, rows, vocab, hidden, 1.0,
+                                               -1, 0, 2, 0, ws, n)
+            b.tf_embedding_backward(dx, hidden, t, 1, dtable, rows, vocab, hidden, 2.0, -1, 1, 0, ws, n)
+        return y, loss, lse, dx, dtable
+
+    data = [inputs(i) for i in range(len(sizes))]
+    alone = [step(i, *data[i]) for i in range(len(sizes))]
+    torch.cuda.synchronize()
+    got, wrong = [None] * len(sizes), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = step(i, *data[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # (told by the thread that waits)
+            wrong.append((i, e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    for a, g in zip(alone, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, g))
