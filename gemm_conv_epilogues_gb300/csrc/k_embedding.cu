@@ -121,6 +121,7 @@ cudaError_t embed_typed(const EmbedArgs &a, cudaStream_t st)
 constexpr uint32_t kNone = 0xffffffffu;
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kDigitBits = 18;   // words per pass: the counters of 2^18/152 words and 32 warps fill the shared memory
+constexpr int64_t kSortBlocks = 152;
 
 __device__ __forceinline__ uint32_t word_of(uint64_t key) { return (uint32_t)(key >> 32); }
 
@@ -686,8 +687,7 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
     cudaError_t e = cudaSuccess;
     for (int pass = 0; a.rows > 0 && e == cudaSuccess && pass < passes; ++pass) {
         const int64_t all = ((a.vocab - 1) >> (pass * kDigitBits)) + 1, most = (int64_t)1 << kDigitBits;
-        const int64_t digits = all < most ? all : most, sms = sm_count() > 152 ? 152 : sm_count();
-        const int64_t range = (digits + sms - 1) / sms < 64 ? 64 : (digits + sms - 1) / sms;
+        const int64_t digits = all < most ? all : most, even = (digits + kSortBlocks - 1) / kSortBlocks, range = even < 64 ? 64 : even;
         const dim3 grid((unsigned)((digits + range - 1) / range));
         SortArgs q = {};
         q.tokens = a.tokens; q.in = first; q.out = pass == 0 ? first : keys; q.long_words = s.long_words; q.err = a.err;

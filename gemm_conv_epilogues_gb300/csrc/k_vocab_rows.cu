@@ -15,8 +15,7 @@
 //
 // Weights whose rows are not multiples of 16 bytes, which no tensor map can address,
 // are copied piece by piece to rows that are.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include <climits>
 
 #include "grouped.cuh"
 #include "lm_internal.h"
@@ -89,60 +88,52 @@ __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lan
         for (int c = lane; c < n; c += lanes) dst[c] = 0;
 }
 
+// bf16's unit of the gradients of the logits (see unit_kernel).
+__device__ __forceinline__ float unit_of(float typical)
+{
+    return typical > 0x1p-40f && typical < 0x1p40f ? 1.0f / typical : 1.0f;
+}
+
 // A CTA takes per_block rows; it counts those that count before them itself,
 // which reads the targets once per CTA, but needs no CTA to wait for another.
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_constant__ GatherArgs g)
 {
     pdl_begin();
-    __shared__ int warps[kThreads / 32];
+    __shared__ int warps[kThreads / 32], least[kThreads / 32];
     __shared__ int place[kThreads];
+    __shared__ float typical;   // |dloss| of the first row that counts
     const LceArgs &a = g.a;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     const int64_t first = (int64_t)blockIdx.x * g.per_block, end = min(first + g.per_block, a.rows);
-    int before = 0;
+    int before = 0, earliest = INT_MAX;
     for (int64_t i = t; i < first; i += 4 * kThreads) {   // four loads under way at a time
         int64_t target[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) target[u] = i + u * kThreads < first ? a.targets.at(i + u * kThreads) : -1;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            before += i + u * kThreads < first && target[u] >= 0 && target[u] < a.vocab && target[u] != a.ignore;
+            if (i + u * kThreads < first && target[u] >= 0 && target[u] < a.vocab && target[u] != a.ignore) {
+                ++before;
+                earliest = min(earliest, (int)(i + u * kThreads));
+            }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (lane == 0) warps[warp] = before;
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        earliest = min(earliest, __shfl_xor_sync(0xffffffffu, earliest, o));
+    }
+    if (lane == 0) {
+        warps[warp] = before;
+        least[warp] = earliest;
+    }
     __syncthreads();
     before = 0;
-    for (int w = 0; w < kThreads / 32; ++w) before += warps[w];
-    // bf16's unit of the gradients of the logits: the first row's |dloss|
-    float unit = 1.0f;
-    if (BACKWARD) {
-        if (g.unit_given) {
-            unit = g.unit[0];
-        } else if (a.dloss) {
-            __shared__ int where;
-            for (int64_t base = 0; base < a.rows; base += kThreads) {
-                if (t == 0) where = kThreads;
-                __syncthreads();
-                int64_t target;
-                if (base + t < a.rows && counts(a, base + t, &target, false)) atomicMin(&where, t);
-                __syncthreads();
-                if (where < kThreads) {
-                    const float d = fabsf(a.dloss[base + where]);
-                    if (d > 0x1p-40f && d < 0x1p40f) unit = 1.0f / d;
-                    break;
-                }
-                __syncthreads();
-            }
-            if (end == a.rows && t == 0) {
-                g.unit[0] = unit;
-                g.unit[1] = 1.0f / unit;
-            }
-        } else if (end == a.rows && t == 0) {
-            g.unit[0] = g.unit[1] = 1.0f;
-        }
+    for (int w = 0; w < kThreads / 32; ++w) {
+        before += warps[w];
+        earliest = min(earliest, least[w]);
     }
+    if (BACKWARD && t == 0) typical = before > 0 && a.dloss ? fabsf(a.dloss[earliest]) : 1.0f;
     for (int64_t base = first; base < end; base += kThreads) {
         const int64_t i = base + t;
         int64_t target = 0;
@@ -157,11 +148,13 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
             before += warps[w];
         }
         place[t] = used ? at : -1;
+        if (BACKWARD && used && at == 0 && a.dloss) typical = fabsf(a.dloss[i]);   // (the first of all)
+        __syncthreads();
         if (used) {
             g.index[at] = (int)i;
             g.target[at] = (int)target;
             if (BACKWARD) {
-                const float d = a.dloss ? a.dloss[i] : 1.0f;
+                const float d = a.dloss ? a.dloss[i] : 1.0f, unit = g.unit_given ? g.unit[0] : unit_of(typical);
                 g.l2[at] = a.lse[i] * kLog2e;
                 g.ca[at] = (a.dlse ? d + a.dlse[i] : d) * unit;
                 g.cb[at] = d * unit;
@@ -170,7 +163,6 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
             a.loss[i] = 0.0f;
             a.lse[i] = 0.0f;
         }
-        __syncthreads();
         const int lanes = g.per_block == 1 ? kThreads : 32, member = t % lanes;   // a row to a warp, or to the CTA
         for (int r = t / lanes; r < (int)min((int64_t)kThreads, end - base); r += kThreads / lanes) {
             const int64_t row = base + r;
@@ -181,7 +173,13 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
         }
     }
     if (end == a.rows) {   // the last CTA
-        if (t == 0) *g.count = before;
+        if (t == 0) {
+            *g.count = before;
+            if (BACKWARD && !g.unit_given) {
+                g.unit[0] = unit_of(typical);
+                g.unit[1] = 1.0f / g.unit[0];
+            }
+        }
         // the K steps of dw read whole sixty-fours of rows
         for (int64_t r = before + warp; r < min((int64_t)(before + 63) / 64 * 64, a.rows); r += kThreads / 32)
             zero_row(g.x + r * g.x_pitch, (int)g.x_pitch, lane, 32);
