@@ -172,13 +172,16 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
         } else if constexpr (WIDE) {
             uint64_t v[UNROLL];
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? static_cast<const uint64_t *>(a.tokens.p)[i + 32 * u] : ~0ull;
+            for (int u = 0; u < UNROLL; ++u)
+                v[u] = i + 32 * u < hi ? static_cast<const uint64_t *>(a.tokens.p)[i + 32 * u] : ~0ull;
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint64_t)a.vocab && (uint32_t)v[u] != a.padding ? (uint32_t)v[u] : kNone;
+            for (int u = 0; u < UNROLL; ++u)
+                word[u] = v[u] < (uint64_t)a.vocab && (uint32_t)v[u] != a.padding ? (uint32_t)v[u] : kNone;
         } else {
             uint32_t v[UNROLL];
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? static_cast<const uint32_t *>(a.tokens.p)[i + 32 * u] : kNone;
+            for (int u = 0; u < UNROLL; ++u)
+                v[u] = i + 32 * u < hi ? static_cast<const uint32_t *>(a.tokens.p)[i + 32 * u] : kNone;
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint32_t)a.vocab && v[u] != a.padding ? v[u] : kNone;
         }
@@ -304,7 +307,8 @@ __device__ __forceinline__ int64_t below(const uint64_t *keys, int64_t lo, int64
 constexpr int kSumThreads = 128;
 constexpr int kFillRows = 64;      // rows of dtable per zeroing CTA
 constexpr int kMinPiece = 8, kMaxPiece = 1024;
-constexpr int kLevel = 64;         // terms added before their sum joins the next level's: long sums of equal terms keep their digits
+// Terms added before their sum joins the next level's: long sums of equal terms keep their digits.
+constexpr int kLevel = 64;
 constexpr int64_t kMostPieces = 32768;
 
 struct SumArgs {
@@ -390,7 +394,7 @@ __device__ __forceinline__ void fill_zeros(const SumArgs &a, int64_t v0)
 // `lanes` threads per piece, each with VEC neighbouring columns of a slice of
 // lanes*VEC; the CTA's other threads take further pieces.  RING: the rows come through
 // shared memory by bulk copies, two batches of eight ahead, which keeps more of them under
-// way than registers could (16384 rows of 4096 bf16 into 32000 words: 74 us with registers).
+// way than registers could (16384 rows of 4096 bf16 into 32000 words: 59 us, 74 with registers).
 template <typename T, int VEC, bool RING>
 __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(const __grid_constant__ SumArgs a)
 {
@@ -479,9 +483,9 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
             if (member < UNROLL) words[group][half][member] = w;
             if (member == 0) ptx::mbar_arrive_expect_tx(&full[group][half], __popc(rows) * bytes);
             __syncwarp();
+            const T *src = static_cast<const T *>(a.dy) + slice + (int64_t)(uint32_t)key * a.dy_stride;
             if (wanted)
-                ptx::bulk_load(&ring[(half * UNROLL + member) * kSumThreads + group * a.lanes],
-                               static_cast<const T *>(a.dy) + slice + (int64_t)(uint32_t)key * a.dy_stride, bytes, &full[group][half]);
+                ptx::bulk_load(&ring[(half * UNROLL + member) * kSumThreads + group * a.lanes], src, bytes, &full[group][half]);
             __syncwarp();
         };
         // the piece's threads meet
@@ -517,7 +521,8 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
                 w[u] = word_of(key[u]);
-                if (w[u] != kNone && w[u] != skipped) v[u] = *reinterpret_cast<const P *>(dy + (int64_t)(uint32_t)key[u] * a.dy_stride);
+                const T *src = dy + (int64_t)(uint32_t)key[u] * a.dy_stride;
+                if (w[u] != kNone && w[u] != skipped) v[u] = *reinterpret_cast<const P *>(src);
             }
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) key[u] = key_at(i + UNROLL + u);   // the next ones, while the rows are under way
@@ -590,9 +595,10 @@ int lanes_of(int words)
     return lanes;
 }
 
-// Pieces that fill the SMs where the list is long enough (14 CTAs each, and no more
-// pieces than a long word's join adds quickly), of 8 to 1024 keys.  Sized for 8 columns per thread, whatever the type, so that the
-// workspace depends on the sizes alone.
+// Pieces that fill the SMs where the list is long enough (14 CTAs each, and no more pieces than a
+// long word's join adds quickly), of 8 to 1024 keys.  Sized for 8 columns per thread,
+// whatever the type, so that the workspace depends on the sizes alone.  (16384 rows of 4096 into
+// 32000 words: 76.6 us, with 10 to 18 CTAs each 77-81, with 24 87.)
 int64_t piece_target(int64_t hidden)
 {
     const int lanes = lanes_of((int)((hidden + 7) / 8));
@@ -630,7 +636,8 @@ cudaError_t launch_sums(const EmbedArgs &a, SumArgs s, cudaStream_t st)
             const void *id = reinterpret_cast<const void *>(kern);
             int known = 0;
             if (!recall(id, FACT_CARVEOUT, &known)) {   // shared memory for as many CTAs as the registers allow
-                const cudaError_t e = cudaFuncSetAttribute(id, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+                const cudaError_t e = cudaFuncSetAttribute(id, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                           cudaSharedmemCarveoutMaxShared);
                 if (e != cudaSuccess) return e;
                 remember(id, FACT_CARVEOUT, 1);
             }
@@ -673,7 +680,7 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
 {
     const int passes = a.vocab > (int64_t)1 << kDigitBits ? 2 : 1;
     char *ws = static_cast<char *>(a.ws);
-    uint64_t *keys = reinterpret_cast<uint64_t *>(ws), *first = reinterpret_cast<uint64_t *>(ws + (passes - 1) * keys_bytes(a.rows));
+    uint64_t *keys = reinterpret_cast<uint64_t *>(ws), *first = keys + (passes - 1) * keys_bytes(a.rows) / 8;
     SumArgs s = {};
     s.keys = keys;
     s.long_words = reinterpret_cast<int *>(ws + passes * keys_bytes(a.rows));
@@ -687,14 +694,17 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
     cudaError_t e = cudaSuccess;
     for (int pass = 0; a.rows > 0 && e == cudaSuccess && pass < passes; ++pass) {
         const int64_t all = ((a.vocab - 1) >> (pass * kDigitBits)) + 1, most = (int64_t)1 << kDigitBits;
-        const int64_t digits = all < most ? all : most, even = (digits + kSortBlocks - 1) / kSortBlocks, range = even < 64 ? 64 : even;
+        const int64_t digits = all < most ? all : most, even = (digits + kSortBlocks - 1) / kSortBlocks;
+        const int64_t range = even < 64 ? 64 : even;
         const dim3 grid((unsigned)((digits + range - 1) / range));
         SortArgs q = {};
         q.tokens = a.tokens; q.in = first; q.out = pass == 0 ? first : keys; q.long_words = s.long_words; q.err = a.err;
         q.vocab = a.vocab; q.listed_padding = a.padding;
         q.padding = a.padding >= 0 && a.padding < a.vocab ? (uint32_t)a.padding : kNone;
         q.n = (int)a.rows; q.shift = pass * kDigitBits; q.range = (int)range;
-        auto kern = pass > 0 ? count_sort_kernel<false, false> : a.tokens.wide ? count_sort_kernel<true, true> : count_sort_kernel<true, false>;
+        auto kern = pass > 0          ? count_sort_kernel<false, false>
+                    : a.tokens.wide ? count_sort_kernel<true, true>
+                                    : count_sort_kernel<true, false>;
         e = raise_smem_limit(reinterpret_cast<const void *>(kern));
         if (e == cudaSuccess) e = launch_pdl(kern, grid, dim3(kSortThreads), (size_t)(kSortWarps * range * 4), st, q);
     }

@@ -25,6 +25,10 @@
 // the number of MMAs it takes.  A logit's sum is cut into parts of 1024 terms, whose
 // accumulators alternate; the epilogue's threads add them in registers while the next part's
 // MMAs run.
+// What bounds it, 4096 rows, 64000 words of 4096, bf16 (2.15 TFLOP each): STATS 1.02-1.05 ms
+// alone (2.05-2.1 PFLOP/s), DLOGITS in two pieces 1.08-1.10, GRADS 2.23-2.26; the tensor pipe is busy for
+// 95, 93 and 95.5% of the active cycles.  In a loop the power cap holds the clock down: 1.7 PFLOP/s.
+// Four rows over 128000 words: 157 us, 6.7 TB/s of weights.
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
 // error word and winds down.
 #include <cuda.h>
@@ -63,7 +67,9 @@ constexpr int kBoxBytes = 32 * 128;                 // an epilogue warp's box: 3
 constexpr int kOffBox = kRingBytes, kOffBar = kOffBox + kEpiWarps * kBoxBytes;
 constexpr int kNumBars = 2 * kMaxStages + 5;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
-constexpr int kNarrowRows = 128;                    // up to here tiles of 128 rows on single CTAs
+// Up to here tiles of 128 rows on single CTAs (losses over 128000 words of 4096: 4 rows 159 us, 199 on
+// pairs; 128 rows 172 and 181; 200 rows 205 and 185).
+constexpr int kNarrowRows = 128;
 constexpr uint32_t kTmemCols = 512;
 
 // a tile's time in K steps, for sharing out the work: the epilogue's, where the K loop is shorter
@@ -93,7 +99,8 @@ struct Share {
     static constexpr int ROWS = 128 * CG;
     int cid, ncl, tiles;
     int row_tiles, col_tiles;      // STATS, DLOGITS
-    int nd, nw, rest, lead;        // GRADS: tiles of either kind; pairs with a DX tile more; DW tiles that the others take first
+    int nd, nw;                    // GRADS: tiles of either kind
+    int rest, lead;                // pairs with a DX tile more; DW tiles that each of the others takes first
     int dw_steps, dx_steps;
 
     __device__ __forceinline__ void init(const VocabArgs &p, int count, int cid_, int ncl_)
@@ -169,6 +176,28 @@ __device__ __forceinline__ void box_put(uint8_t *box, int lane, int i, uint4 v)
 __device__ __forceinline__ uint4 box_get(const uint8_t *box, int row, int piece)
 {
     return *reinterpret_cast<const uint4 *>(box + row * 128 + ((piece ^ (row & 7)) * 16));
+}
+
+// The first n of row `at`'s columns to where no 16-byte words lie: 32 of 32 bits one by one, or
+// 64 of 16 bits in pairs that share a 32-bit word (an odd start leaves its first and
+// its last column single).
+__device__ __forceinline__ void put_single(float *dst, const uint8_t *box, int at, int n, bool add)
+{
+    const int lane = threadIdx.x & 31;
+    if (lane >= n) return;
+    const float v = *reinterpret_cast<const float *>(box + at * 128 + ((lane >> 2) ^ (at & 7)) * 16 + (lane & 3) * 4);
+    dst[lane] = add ? dst[lane] + v : v;
+}
+__device__ __forceinline__ void put_pairs(uint16_t *dst, const uint8_t *box, int at, int n)
+{
+    auto value = [&](int i) {
+        return *reinterpret_cast<const uint16_t *>(box + at * 128 + ((i >> 3) ^ (at & 7)) * 16 + (i & 7) * 2);
+    };
+    const int lane = threadIdx.x & 31, odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1, e = 2 * lane - odd;
+    if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t *>(dst + e) = value(e) | (uint32_t)value(e + 1) << 16;
+    else if (e + 1 < n) dst[e + 1] = value(e + 1);
+    else if (e < n) dst[e] = value(e);
+    if (odd && lane == 0 && n == 64) dst[63] = value(63);
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -311,7 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (t.kind == TILE_DX) load(a_dst + i * kChunkBytes, &map_a, k, m);
                                 else load(a_dst + i * kChunkBytes, &map_a, m, k);
                             }
-                            for (int i = 0; i < half / 64; ++i) load(b_dst + i * kChunkBytes, map_b, t.n0 + crank * half + 64 * i, k);
+                            for (int i = 0; i < half / 64; ++i)
+                                load(b_dst + i * kChunkBytes, map_b, t.n0 + crank * half + 64 * i, k);
                         }
                     }
                     __syncwarp();
@@ -365,13 +395,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         ptx::tc_fence_after();
                         if (issuer) {
-                            const uint32_t a = a_low + (uint32_t)stage * (kStageBytes >> 4), bb = b_low + (uint32_t)stage * (kStageBytes >> 4);
-                            const uint32_t d = tmem_base + (uint32_t)(b * kTileN);
+                            const uint32_t at = (uint32_t)stage * (kStageBytes >> 4), d = tmem_base + (uint32_t)(b * kTileN);
 #pragma unroll
                             for (int k = 0; k < BK / UMMA_K; ++k) {
+                                const uint64_t a = desc_of(a_low + at + k * a_step), bb = desc_of(b_low + at + k * b_step);
                                 const uint32_t acc = k > 0 || !begins ? 1u : 0u;
-                                if constexpr (PAIR) ptx::umma_bf16_pair(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
-                                else ptx::umma_bf16(d, desc_of(a + k * a_step), desc_of(bb + k * b_step), id, acc);
+                                if constexpr (PAIR) ptx::umma_bf16_pair(d, a, bb, id, acc);
+                                else ptx::umma_bf16(d, a, bb, id, acc);
                             }
                             commit(&empty[stage]);
                             if (ends) commit(&tfull[b]);
@@ -404,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int q = warp & 3, h = (warp - kFirstEpiWarp) >> 2;
             uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
             const bool bf16 = p.a.dtype == TF_BF16;
-            const int c0 = h * ((p.bn / 2 + 63) & ~63), c1 = h ? p.bn : (p.bn / 2 + 63) & ~63;   // this warp's columns of a tile
+            const int mid = (p.bn / 2 + 63) & ~63, c0 = h ? mid : 0, c1 = h ? p.bn : mid;   // this warp's columns of a tile
             const float mult = p.a.factor * (MODE == LCE_GRADS ? __ldg(p.a.unit + 1) : 1.0f);
             int b = 0;
             uint32_t seen = 0;   // parity of the results of either accumulator
@@ -417,9 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 32 columns as 16-bit values into one half of the box's rows
             auto put_half = [&](const uint32_t (&r)[32], int part) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    box_put(box, lane, part * 4 + i, make_uint4(pack(r[8 * i], r[8 * i + 1]), pack(r[8 * i + 2], r[8 * i + 3]),
-                                                                pack(r[8 * i + 4], r[8 * i + 5]), pack(r[8 * i + 6], r[8 * i + 7])));
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = pack(r[8 * i + 2 * k], r[8 * i + 2 * k + 1]);
+                    box_put(box, lane, part * 4 + i, make_uint4(w[0], w[1], w[2], w[3]));
+                }
             };
             for (int j = 0; ok && share.at(p, j, &t); ++j) {
                 const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
@@ -475,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ptx::tmem_ld_wait();
 #pragma unroll
                                 for (int k = 0; k < 32; k += 2) {
-                                    const float2 sum = fadd2(make_float2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1])),
-                                                             make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
+                                    const float2 old = make_float2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1]));
+                                    const float2 sum = fadd2(old, make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])));
                                     r[i][k] = __float_as_uint(sum.x);
                                     r[i][k + 1] = __float_as_uint(sum.y);
                                 }
@@ -533,8 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int i = 0; i < 8; ++i) {
                                     const int at = 4 * i + (lane >> 3);
-                                    if (row0 + at < p.a.rows)
-                                        *reinterpret_cast<uint4 *>(out + (int64_t)(row0 + at) * p.a.dl_pitch) = box_get(box, at, piece);
+                                    uint16_t *to = out + (int64_t)(row0 + at) * p.a.dl_pitch;
+                                    if (row0 + at < p.a.rows) *reinterpret_cast<uint4 *>(to) = box_get(box, at, piece);
                                 }
                             }
                             __syncwarp();
@@ -583,8 +616,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (i == 1 && (!wide || u + 32 >= left)) break;
                             if (wide) {
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    box_put(box, lane, k, make_uint4(r[i][4 * k], r[i][4 * k + 1], r[i][4 * k + 2], r[i][4 * k + 3]));
+                                for (int k = 0; k < 8; ++k) {
+                                    const uint32_t *v = &r[i][4 * k];
+                                    box_put(box, lane, k, make_uint4(v[0], v[1], v[2], v[3]));
+                                }
                             }
                             __syncwarp();
                             // the box's rows, of 128 bytes from column c on
@@ -608,28 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     *to = v;
                                 }
                             } else {
+                                const int n = (int)min((int64_t)(8 * per), pitch - c);   // columns of a row
                                 for (int at = 0; at < min(32, rows - row0); ++at) {
-                                    const int64_t to = (int64_t)(row0 + at) * pitch + c;
-                                    const int n = min(8 * per, (int)min(pitch, (int64_t)(1 << 30)) - c);   // columns of this row
-                                    const uint8_t *src = box + at * 128;
-                                    if (wide) {
-                                        if (lane < n) {
-                                            const float v = *reinterpret_cast<const float *>(src + (((lane >> 2) ^ (at & 7)) * 16) + (lane & 3) * 4);
-                                            float *dst = reinterpret_cast<float *>(out) + to + lane;
-                                            *dst = add ? *dst + v : v;
-                                        }
-                                    } else {
-                                        // pairs of columns that share a 32-bit word; an odd start leaves its first and last column single
-                                        uint16_t *dst = reinterpret_cast<uint16_t *>(out) + to;
-                                        const int odd = (int)(reinterpret_cast<uintptr_t>(dst) >> 1) & 1, e = 2 * lane - odd;
-                                        auto value = [&](int i) {
-                                            return *reinterpret_cast<const uint16_t *>(src + (((i >> 3) ^ (at & 7)) * 16) + (i & 7) * 2);
-                                        };
-                                        if (e >= 0 && e + 1 < n) *reinterpret_cast<uint32_t *>(dst + e) = value(e) | (uint32_t)value(e + 1) << 16;
-                                        else if (e + 1 < n) dst[e + 1] = value(e + 1);
-                                        else if (e < n) dst[e] = value(e);
-                                        if (odd && lane == 0 && n == 64) dst[63] = value(63);
-                                    }
+                                    uint8_t *to = out + ((int64_t)(row0 + at) * pitch + c) * size;
+                                    if (wide) put_single(reinterpret_cast<float *>(to), box, at, n, add);
+                                    else put_pairs(reinterpret_cast<uint16_t *>(to), box, at, n);
                                 }
                             }
                             __syncwarp();
@@ -786,11 +804,13 @@ int lce_word_tile(int64_t rows, int64_t words)
     return bn < 64 ? 64 : bn > kTileN ? kTileN : (int)bn;
 }
 
-// Splits of dx's sums: no longer than a CTA's (pair's) share of both gradients.
+// Splits of dx's sums: no longer than a CTA's (pair's) share of both gradients (301 rows,
+// 10007 words of 1000: GRADS 22 us; with the most that fill two waves 33).
 int lce_splits(int64_t rows, int64_t words, int64_t hidden)
 {
     const int64_t tile = lce_row_tile(rows), across = (hidden + kTileN - 1) / kTileN;
-    const int64_t steps = (words + BK - 1) / BK, dx = (rows + tile - 1) / tile * across, dw = (words + tile - 1) / tile * across;
+    const int64_t steps = (words + BK - 1) / BK;
+    const int64_t dx = (rows + tile - 1) / tile * across, dw = (words + tile - 1) / tile * across;
     const int64_t share = (dx * tile_cost((int)steps) + dw * tile_cost((int)((rows + BK - 1) / BK))) / lce_units(rows);
     const int64_t s = (steps + share) / (share + 1);
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;

@@ -7,6 +7,8 @@ A logit is off by e_l, so lse by the largest e_l, 2^-20 for the exponentials (2^
 their sum's additions, and its own rounding; the loss by lse's and the target's.  A gradient
 of a logit p*ca - cb is off by p*ca times (e_l + the rounding of its exponent + 2^-20), and is rounded to the
 type; fp16 holds it in units in which its smallest step is 2^-39 of the largest |dloss| + |dlse|."""
+import math
+
 import pytest
 import torch
 
@@ -516,3 +518,32 @@ def test_large_offsets(b):
     assert (dw[:-2].abs().amax() <= 4.0 + 1e-3) and (dw[7, 0] + 4.0).abs() <= 0.02
     others = dw[8:vocab - 2]
     assert others.abs().amax() <= 6.1 / 2.0e6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("hidden", [1024, 1032, 8200, 65536])
+def test_long_sums_of_one_sign(b, rows, hidden):
+    """Equal terms, whose truncation adds up: a part has 64 accumulations, each off by at most 2u of its sum, and
+    the parts' sum one rounding per part."""
+    vocab = 270
+    x = torch.full((rows, hidden), 1.1, device="cuda").bfloat16()
+    w = torch.full((vocab, hidden), 1.1, device="cuda").bfloat16()
+    targets = torch.arange(rows, device="cuda") % vocab
+    scale = torch.tensor(60.0 / hidden).item()
+    loss, lse = _forward(b, x, w, targets, "bf16", scale)
+    l = scale * hidden * float(x[0, 0]) * float(w[0, 0])
+    parts = (hidden + 1023) // 1024
+    assert ((lse.double() - (l + math.log(vocab))).abs() <= (2 * 64 + parts + 4) * U * l + 2.0 ** -20 + 4 * U * l).all()
+    assert ((loss.double() - math.log(vocab)).abs() <= 2.0 ** -19).all()   # (every logit is off by the same)
+
+
+@pytest.mark.gpu
+def test_wide_rows(b):
+    """The widest rows, and rows whose sums end inside a part."""
+    for rows, vocab, hidden in ((3, 300, 65536), (140, 90, 9000), (5, 70, 1025)):
+        x, w, targets = _inputs(rows, vocab, hidden, "bf16", "some", pad=8, seed=16)
+        loss, lse = _forward(b, x, w, targets, "bf16")
+        _check_forward(x, w, targets, 1.0, loss, lse)
+        dx, dw = _grads(b, x, w, targets, lse, None, None, "bf16")
+        _check_grads(x, w, targets, lse, None, None, "bf16", 1.0, dx, dw)
