@@ -97,35 +97,40 @@ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 template <int MODE, int CG>
 struct Share {
     static constexpr int ROWS = 128 * CG;
-    int cid, ncl, tiles;
-    int row_tiles, col_tiles;      // STATS, DLOGITS
-    int nd, nw;                    // GRADS: tiles of either kind
-    int rest, lead;                // pairs with a DX tile more; DW tiles that each of the others takes first
-    int dw_steps, dx_steps;
+    int cid, ncl;
+    int row_tiles, col_tiles;
+    int tiles, sweep;              // STATS, DLOGITS: all of them, and those of one sweep over the vocabulary
+    int own, plane, steps;         // GRADS: DX tiles that are this pair's; tiles of a split; K steps of DW
+    int nw, lead, others, ahead;   // DW tiles; those that this pair takes first, and how many pairs do; what they take in all
+    int rest;                      // its place in the round
 
     __device__ __forceinline__ void init(const VocabArgs &p, int count, int cid_, int ncl_)
     {
         cid = cid_;
         ncl = ncl_;
+        row_tiles = div_up(count, ROWS);
         if constexpr (MODE != LCE_GRADS) {
-            row_tiles = div_up(count, ROWS);
             col_tiles = div_up(p.a.words, p.bn);
             tiles = row_tiles * col_tiles;
+            sweep = p.group * col_tiles;
         } else {
             // DX tiles in turn; the pairs that have one less take DW tiles for its
             // time before the rest of those goes round
-            row_tiles = div_up(count, ROWS);
             col_tiles = div_up(p.a.hidden, p.bn);
-            dw_steps = div_up(count, BK);
-            dx_steps = div_up(p.a.words, BK);
-            nd = p.a.dx ? p.a.splits * row_tiles * col_tiles : 0;
+            plane = row_tiles * col_tiles;
+            steps = div_up(count, BK);
+            const int nd = p.a.dx ? p.a.splits * plane : 0, more = nd % ncl;   // `more` pairs have a DX tile more
             nw = p.a.dw ? div_up(p.a.words, ROWS) * col_tiles : 0;
-            rest = nd % ncl;
+            own = nd / ncl + (cid < more ? 1 : 0);
             lead = 0;
-            if (rest > 0) {
-                const int cw = tile_cost(dw_steps);
-                lead = min((tile_cost(p.split_steps) + cw / 2) / cw, div_up(nw, ncl - rest));
+            if (more > 0) {
+                const int cost = tile_cost(steps);
+                lead = min((tile_cost(p.split_steps) + cost / 2) / cost, div_up(nw, ncl - more));
             }
+            others = ncl - more;
+            ahead = lead * others;
+            rest = cid < more ? cid - more + ncl : cid - more;
+            if (cid < more) lead = 0;
         }
     }
 
@@ -134,25 +139,21 @@ struct Share {
         if constexpr (MODE != LCE_GRADS) {
             const int i = cid + j * ncl;
             if (i >= tiles) return false;
-            const int g = i / (p.group * col_tiles), r = i - g * p.group * col_tiles;
-            const int size = min(p.group, row_tiles - g * p.group);
-            const int v = r / size;
+            const int g = i / sweep, r = i - g * sweep, size = min(p.group, row_tiles - g * p.group), v = r / size;
             *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v};
             return true;
         } else {
-            const int own = nd / ncl + (cid < rest ? 1 : 0);
             if (j < own) {
-                const int i = cid + j * ncl, s = i / (row_tiles * col_tiles), r = i - s * row_tiles * col_tiles;
-                const int k0 = s * p.split_steps;
-                *t = {TILE_DX, r / col_tiles * ROWS, r % col_tiles * p.bn, k0, max(0, min(p.split_steps, dx_steps - k0)), s};
+                const int i = cid + j * ncl, s = i / plane, r = i - s * plane, m = r / col_tiles, k0 = s * p.split_steps;
+                const int nk = max(0, min(p.split_steps, div_up(p.a.words, BK) - k0));
+                *t = {TILE_DX, m * ROWS, (r - m * col_tiles) * p.bn, k0, nk, s};
                 return true;
             }
             j -= own;
-            const int mine = rest > 0 && cid >= rest ? lead : 0;
-            const int i = j < mine ? j * (ncl - rest) + cid - rest
-                                   : (rest > 0 ? lead * (ncl - rest) : 0) + (j - mine) * ncl + (cid - rest + ncl) % ncl;
+            const int i = j < lead ? j * others + rest : ahead + (j - lead) * ncl + rest;
             if (i >= nw) return false;
-            *t = {TILE_DW, i / col_tiles * ROWS, i % col_tiles * p.bn, 0, dw_steps, 0};
+            const int m = i / col_tiles;
+            *t = {TILE_DW, m * ROWS, (i - m * col_tiles) * p.bn, 0, steps, 0};
             return true;
         }
     }
@@ -575,6 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 } else {
                     const uint32_t taddr = columns + (uint32_t)(b * kTileN);
+                    const bool dx = t.kind == TILE_DX;
+                    const int rows = dx ? count : p.a.words;   // of this tile's M side
+                    const bool wide = dx || p.a.dw_f32;        // 32-bit results
+                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                    const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
+                    uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
+                                      : static_cast<uint8_t *>(p.a.dw);
+                    // rows that 16-byte words make up
+                    const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
                     if (t.nk > 0) {
                         if (!await()) break;
                         if (left <= 0) release();
@@ -591,16 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
                         }
-                        const bool dx = t.kind == TILE_DX;
-                        const int rows = dx ? count : p.a.words;   // of this tile's M side
-                        const bool wide = dx || p.a.dw_f32;        // 32-bit results
-                        const bool add = dx ? !p.a.first : p.a.accumulate != 0;
                         if ((t.nk == 0 && add) || row0 >= rows) continue;
-                        const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
-                        uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
-                                          : static_cast<uint8_t *>(p.a.dw);
-                        // rows that 16-byte words make up
-                        const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
