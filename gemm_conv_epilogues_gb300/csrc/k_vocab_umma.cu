@@ -72,8 +72,15 @@ constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 16;
 constexpr int kNarrowRows = 128;
 constexpr uint32_t kTmemCols = 512;
 
-// a tile's time in K steps, for sharing out the work: the epilogue's, where the K loop is shorter
-__host__ __device__ constexpr int tile_cost(int steps) { return (steps > 10 ? steps : 10) + 1; }
+// A tile's time in K steps, for sharing out the work: the epilogue's, where the K loop is shorter.
+// A single CTA's K step waits for memory, a pair's for the tensor cores.  (Steps of 7 rows, 88000 words of
+// 2560: 342 us, with 10 for single CTAs 396, with 2 352; of 400 rows, 32000 words of 2048: 193 us, with 5
+// for pairs 212, with 20 205.)
+constexpr int kLeastSingle = 4, kLeastPair = 10;
+__host__ __device__ constexpr int tile_cost(int cg, int steps)
+{
+    return (steps > (cg == 1 ? kLeastSingle : kLeastPair) ? steps : cg == 1 ? kLeastSingle : kLeastPair) + 1;
+}
 
 struct VocabArgs {
     LceProduct a;
@@ -124,8 +131,8 @@ struct Share {
             own = nd / ncl + (cid < more ? 1 : 0);
             lead = 0;
             if (more > 0) {
-                const int cost = tile_cost(steps);
-                lead = min((tile_cost(p.split_steps) + cost / 2) / cost, div_up(nw, ncl - more));
+                const int cost = tile_cost(CG, steps);
+                lead = min((tile_cost(CG, p.split_steps) + cost / 2) / cost, div_up(nw, ncl - more));
             }
             others = ncl - more;
             ahead = lead * others;
@@ -812,7 +819,8 @@ int lce_splits(int64_t rows, int64_t words, int64_t hidden)
     const int64_t tile = lce_row_tile(rows), across = (hidden + kTileN - 1) / kTileN;
     const int64_t steps = (words + BK - 1) / BK;
     const int64_t dx = (rows + tile - 1) / tile * across, dw = (words + tile - 1) / tile * across;
-    const int64_t share = (dx * tile_cost((int)steps) + dw * tile_cost((int)((rows + BK - 1) / BK))) / lce_units(rows);
+    const int cg = rows <= kNarrowRows ? 1 : 2;
+    const int64_t share = (dx * tile_cost(cg, (int)steps) + dw * tile_cost(cg, (int)((rows + BK - 1) / BK))) / lce_units(rows);
     const int64_t s = (steps + share) / (share + 1);
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
