@@ -32,12 +32,13 @@ constexpr int64_t kSplitBytes = (int64_t)128 << 20;  // dx's sums, where there a
 
 // ---------------------------------------------------------------- gather
 
+enum { UNIT_FIRST_ROW = 0, UNIT_ALL_ROWS = 1, UNIT_GIVEN = 2 };   // (the last: unit[0] by unit_kernel)
 struct GatherArgs {
     LceArgs a;
     int *count, *index, *target;
     float *l2, *ca, *cb;       // backward
-    float *unit;               // backward
-    int unit_given;            // fp16: unit_kernel has been there
+    float *unit;               // backward: the gradients of the logits are held times unit[0]; unit[1] is its inverse
+    int unit_from;
     uint16_t *x;
     int64_t x_pitch;
     int per_block;             // rows
@@ -88,10 +89,50 @@ __device__ __forceinline__ void zero_row(uint16_t *dst, int n, int lane, int lan
         for (int c = lane; c < n; c += lanes) dst[c] = 0;
 }
 
-// bf16's unit of the gradients of the logits (see unit_kernel).
+// The gradients of the logits are held in units of a typical |dloss|, which is often
+// that of all rows: a target's (p - 1) dloss is then rounded near one, where it is
+// off by no more than p, and not by dloss's own rounding, the same in every row (dx of 3300 rows
+// with a mean's weights: relative error 2.9e-3 without, 1.8e-3 with units).  bf16 takes the first
+// row's.  fp16, whose exponents are few, takes the largest, times 2^14:
+// a word's share of 1e-5 would otherwise lie far below its smallest.
 __device__ __forceinline__ float unit_of(float typical)
 {
     return typical > 0x1p-40f && typical < 0x1p40f ? 1.0f / typical : 1.0f;
+}
+
+// fp16's, from all rows, by a CTA of THREADS threads.
+template <int THREADS>
+__device__ __forceinline__ float unit_of_all(const LceArgs &a)
+{
+    __shared__ float2 warps[THREADS / 32];
+    float most = 0.0f, both = 0.0f;   // the largest |dloss|, and |dloss| + |dlse|, which bounds the gradients
+    for (int64_t i = threadIdx.x; i < a.rows; i += THREADS) {
+        int64_t target;
+        if (!counts(a, i, &target, false)) continue;
+        const float d = a.dloss ? fabsf(a.dloss[i]) : 1.0f;
+        most = fmaxf(most, d);
+        both = fmaxf(both, d + (a.dlse ? fabsf(a.dlse[i]) : 0.0f));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        both = fmaxf(both, __shfl_xor_sync(0xffffffffu, both, o));
+    }
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = make_float2(most, both);
+    __syncthreads();
+    for (int w = 0; w < THREADS / 32; ++w) {
+        most = fmaxf(most, warps[w].x);
+        both = fmaxf(both, warps[w].y);
+    }
+    const float size = both <= 2.0f * most ? most : both;   // (the gradients stay below 2^15, or 2^14)
+    return size > 0x1p-100f && size < 0x1p100f ? 0x1p14f / size : 1.0f;   // (a normal number, and its inverse too)
+}
+
+__global__ void __launch_bounds__(1024) unit_kernel(const __grid_constant__ LceArgs a, float *unit)
+{
+    pdl_begin();
+    const float u = unit_of_all<1024>(a);
+    if (threadIdx.x == 0) *unit = u;
 }
 
 // A CTA takes per_block rows; it counts those that count before them itself,
@@ -133,7 +174,12 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
         before += warps[w];
         earliest = min(earliest, least[w]);
     }
-    if (BACKWARD && t == 0) typical = before > 0 && a.dloss ? fabsf(a.dloss[earliest]) : 1.0f;
+    float unit = 1.0f;
+    if (BACKWARD) {
+        if (g.unit_from == UNIT_ALL_ROWS) unit = unit_of_all<kThreads>(a);
+        else if (g.unit_from == UNIT_GIVEN) unit = g.unit[0];
+        else if (t == 0) typical = before > 0 && a.dloss ? fabsf(a.dloss[earliest]) : 1.0f;
+    }
     for (int64_t base = first; base < end; base += kThreads) {
         const int64_t i = base + t;
         int64_t target = 0;
@@ -154,7 +200,8 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
             g.index[at] = (int)i;
             g.target[at] = (int)target;
             if (BACKWARD) {
-                const float d = a.dloss ? a.dloss[i] : 1.0f, unit = g.unit_given ? g.unit[0] : unit_of(typical);
+                const float d = a.dloss ? a.dloss[i] : 1.0f;
+                if (g.unit_from == UNIT_FIRST_ROW) unit = unit_of(typical);
                 g.l2[at] = a.lse[i] * kLog2e;
                 g.ca[at] = (a.dlse ? d + a.dlse[i] : d) * unit;
                 g.cb[at] = d * unit;
@@ -176,52 +223,11 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
     if (end == a.rows) {   // the last CTA
         if (t == 0) {
             *g.count = before;
-            if (BACKWARD && !g.unit_given) {
-                g.unit[0] = unit_of(typical);
-                g.unit[1] = 1.0f / g.unit[0];
-            }
+            if (BACKWARD) g.unit[1] = 1.0f / (g.unit_from == UNIT_FIRST_ROW ? unit_of(typical) : unit);
         }
         // the K steps of dw read whole sixty-fours of rows
         for (int64_t r = before + warp; r < min((int64_t)(before + 63) / 64 * 64, a.rows); r += kThreads / 32)
             zero_row(g.x + r * g.x_pitch, (int)g.x_pitch, lane, 32);
-    }
-}
-
-// The gradients of the logits are held in units of a typical |dloss|, which is often
-// that of all rows: a target's (p - 1) dloss is then rounded near one, where it is
-// off by no more than p, and not by dloss's own rounding, the same in every row (dx of 3300 rows
-// with a mean's weights: relative error 2.9e-3 without, 1.8e-3 with units).  bf16 takes the first
-// row's.  fp16, whose exponents are few, takes the largest, times 2^14:
-// a word's share of 1e-5 would otherwise lie far below its smallest.  unit[0] is
-// the factor, unit[1] its inverse.
-__global__ void __launch_bounds__(1024) unit_kernel(const __grid_constant__ LceArgs a, float *unit)
-{
-    pdl_begin();
-    __shared__ float2 warps[32];
-    float most = 0.0f, both = 0.0f;   // the largest |dloss|, and |dloss| + |dlse|, which bounds the gradients
-    for (int64_t i = threadIdx.x; i < a.rows; i += 1024) {
-        int64_t target;
-        if (!counts(a, i, &target, false)) continue;
-        const float d = a.dloss ? fabsf(a.dloss[i]) : 1.0f;
-        most = fmaxf(most, d);
-        both = fmaxf(both, d + (a.dlse ? fabsf(a.dlse[i]) : 0.0f));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-        both = fmaxf(both, __shfl_xor_sync(0xffffffffu, both, o));
-    }
-    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = make_float2(most, both);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 0; w < 32; ++w) {
-            most = fmaxf(most, warps[w].x);
-            both = fmaxf(both, warps[w].y);
-        }
-        const float size = both <= 2.0f * most ? most : both;   // (2^15 and 2^14 at most)
-        // (both are normal numbers)
-        unit[0] = size > 0x1p-100f && size < 0x1p100f ? 0x1p14f / size : 1.0f;
-        unit[1] = 1.0f / unit[0];
     }
 }
 
@@ -458,8 +464,9 @@ cudaError_t launch_gather(const LceArgs &a, const Plan &p, bool backward, cudaSt
     g.ca = at<float>(a.ws, p.ca);
     g.cb = at<float>(a.ws, p.cb);
     g.unit = at<float>(a.ws, p.unit);
-    g.unit_given = a.dtype == TF_FP16;
-    const cudaError_t e = g.unit_given ? launch_pdl(unit_kernel, dim3(1), dim3(1024), 0, st, a, g.unit) : cudaSuccess;
+    // each CTA looks through a few rows itself, one kernel through many
+    g.unit_from = a.dtype == TF_BF16 ? UNIT_FIRST_ROW : g.per_block == 1 ? UNIT_ALL_ROWS : UNIT_GIVEN;
+    const cudaError_t e = g.unit_from == UNIT_GIVEN ? launch_pdl(unit_kernel, dim3(1), dim3(1024), 0, st, a, g.unit) : cudaSuccess;
     return e != cudaSuccess ? e : launch_pdl(gather_kernel<true>, grid, dim3(kThreads), 0, st, g);
 }
 

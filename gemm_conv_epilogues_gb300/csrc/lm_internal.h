@@ -61,7 +61,7 @@ struct LceProduct {
     float2 *part;            // STATS: (maximum, sum) per slot and row
     float *at_target;        // STATS: the target's sum
     const float *l2, *ca, *cb;   // DLOGITS: lse in base 2, and what the probabilities and the target take
-    const float *unit;       // GRADS: what the gradients of the logits are held times, and its inverse
+    const float *unit;       // GRADS: unit[1] is the unit of the gradients of the logits
     void *dl;                // [rows][dl_pitch]
     float *dx;               // GRADS: [splits][rows][dx_pitch], null where not wanted
     void *dw;                // this piece's rows, null where not wanted
