@@ -308,3 +308,41 @@ def test_streams_and_graphs(b):
     torch.cuda.synchronize()
     for i in range(2):
         _check_grad(dtable[i], None, dy[i], tokens[i], 2.0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab,hidden", [(262144, 8), (262145, 8), (600001, 3), (70_000_000, 1)])
+@pytest.mark.parametrize("rows", [3, 5000, 40000])
+def test_backward_of_large_vocabularies(b, vocab, hidden, rows):
+    """Above 2^18 words the order takes two passes; words differ in either half of their number, or in both."""
+    g = torch.Generator("cuda").manual_seed(rows)
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    tokens[::3] = tokens[0] % 262144 + 262144 * torch.randint(0, max(1, vocab // 262144), (tokens[::3].numel(),), generator=g, device="cuda")
+    tokens[1::7] = vocab - 1
+    tokens[2::11] = -1
+    dy = torch.randn(rows, hidden, generator=g, device="cuda").half()
+    before = torch.randn(vocab, hidden, generator=g, device="cuda")
+    dtable = before.clone()
+    _grad(b, dy, tokens, dtable, 0.5, 1, "fp16")
+    used = torch.unique(tokens[tokens >= 0])
+    place = torch.searchsorted(used, tokens.clamp(min=0))
+    place[tokens < 0] = -1
+    _check_grad(dtable[used], before[used], dy, place, 0.5, 1)
+    dtable[used] = before[used]
+    assert torch.equal(dtable, before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [1, 0])
+def test_backward_padding_is_a_word(b, wide):
+    """The padding may be a row's number: that row has no gradient, and its rows of dy are not read."""
+    rows, vocab, hidden = 500, 7, 72
+    tokens = torch.randint(0, vocab, (rows,), device="cuda")
+    dy = torch.randn(rows, hidden, device="cuda")
+    dy[tokens == 3] = float("nan")
+    index = tokens if wide else tokens.int()
+    ws = torch.empty(b.tf_embedding_backward_workspace_size(rows, vocab, hidden), dtype=torch.uint8, device="cuda")
+    dtable = torch.full((vocab, hidden), float("nan"), device="cuda")
+    b.tf_embedding_backward(dy, hidden, index, wide, dtable, rows, vocab, hidden, 1.0, 3, 0, b.TF_FP32, ws, ws.numel())
+    assert (dtable[3] == 0).all()
+    _check_grad(dtable, None, dy, torch.where(tokens == 3, -1, tokens), 1.0, 0)
