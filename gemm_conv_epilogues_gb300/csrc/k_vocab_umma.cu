@@ -465,7 +465,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; ok && share.at(p, j, &t); ++j) {
                 const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
                 const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
-                const int left = min(width, c1) - c0;   // columns with results, up to 128
+                // rows of this tile's M side: DLOGITS also writes the zeros behind them that dw's last K step reads
+                const int rows = MODE == LCE_DLOGITS         ? (count + BK - 1) / BK * BK
+                                 : t.kind == TILE_DW ? p.a.words
+                                                     : count;
+                const int left = row0 < rows ? min(width, c1) - c0 : 0;   // columns with results, up to 128
                 int target = -1;
                 float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
                 if constexpr (MODE != LCE_GRADS) {
@@ -584,7 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     const uint32_t taddr = columns + (uint32_t)(b * kTileN);
                     const bool dx = t.kind == TILE_DX;
-                    const int rows = dx ? count : p.a.words;   // of this tile's M side
                     const bool wide = dx || p.a.dw_f32;        // 32-bit results
                     const bool add = dx ? !p.a.first : p.a.accumulate != 0;
                     const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
                         }
-                        if ((t.nk == 0 && add) || row0 >= rows) continue;
+                        if (t.nk == 0 && add) break;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
