@@ -365,7 +365,7 @@ int tf_grouped_matmul_wgrad(const void *dy, int64_t dy_stride, const void *x, in
 
 /* ---------------------------------------------------------------- embedding */
 
-/* y[i] = scale * table[tokens[i]], rounded once.
+/* y[i] = scale * table[tokens[i]], in fp32 and then rounded to dtype (scale: finite).
  *   tokens : int32 or int64 (tf_index) [rows] on the device
  *   table  : dtype (TF_FP16, TF_BF16 or TF_FP32) [vocab][hidden], contiguous
  *   y      : dtype [rows][hidden], row i at i*y_stride elements
@@ -378,8 +378,8 @@ int tf_grouped_matmul_wgrad(const void *dy, int64_t dy_stride, const void *x, in
 int tf_embedding_forward(const void *tokens, int index, const void *table, void *y, int64_t y_stride, int64_t rows,
                          int64_t vocab, int64_t hidden, float scale, int64_t padding, int dtype, tf_stream_t stream);
 
-/* Bytes of device workspace tf_embedding_backward needs (two lists of the
- * tokens, and fp32 partial sums).  It does not fall as rows grow.  Host only. */
+/* Bytes of device workspace tf_embedding_backward needs (one or two
+ * lists of the tokens, and fp32 partial sums).  It does not fall as rows grow.  Host only. */
 int64_t tf_embedding_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden);
 
 /* Gradient of the table: dtable[v] = scale * the sum of dy[i] over the rows i
@@ -409,7 +409,7 @@ int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens,
  *             row i at i*x_stride elements
  *   w       : dtype [vocab][hidden], contiguous (16-byte aligned where hidden % 8 == 0)
  *   targets : int32 or int64 (tf_index) [rows] on the device
- *   loss, lse : fp32 [rows];  scale > 0
+ *   loss, lse : fp32 [rows];  scale > 0, finite
  * Rows whose target is `ignore` (-100, say; TF_NO_INDEX: none) cost nothing and
  * get a loss and lse of 0; what x holds there, NaN included, is not read.
  * Other targets outside [0, vocab) are ignored likewise and set TF_DEVERR_INDEX.
@@ -442,11 +442,12 @@ int tf_linear_cross_entropy_forward(const void *x, int64_t x_stride, const void 
  *   dw     : dw_dtype [vocab][hidden], contiguous, or NULL; dw_dtype is dtype or
  *            TF_FP32.  With `accumulate` != 0 (TF_FP32 only) it is added to what
  *            dw holds.
- * dl is rounded to dtype, the matrix products' operand type: a relative 2^-9 (bf16) or 2^-12
- * (fp16) of each term at most, in dx and dw, also where dw is fp32.  It is held in units
- * of a typical |dloss|, in which equal weights round to nothing: bf16 takes the first counted row's (where
- * that lies between 2^-40 and 2^40), fp16 2^-14 of the largest, so that terms down to
- * 2^-28 of it keep their digits and none below 2^-39 of it counts.  Sums are fp32.
+ * dl is rounded to dtype, the matrix products' operand type: each term is off by up to 2^-8
+ * (bf16) or 2^-11 (fp16) of its value, in dx and dw, also where dw is fp32.  It is held in
+ * units of a typical |dloss|, so that equal weights add no rounding of their own: bf16 takes
+ * the first counted row's (where that lies between 2^-40 and 2^40), fp16 2^-14 of the largest,
+ * so that terms down to 2^-28 of it keep their digits and none below 2^-39 of it
+ * counts.  Sums are fp32.
  * Workspace as above. */
 int64_t tf_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden, int dtype);
 int tf_linear_cross_entropy_backward(const void *x, int64_t x_stride, const void *w, const void *targets, int index,

@@ -16,7 +16,7 @@ def b(cuda_ready):
 @pytest.mark.gpu
 @pytest.mark.parametrize("rows,vocab,hidden", [(50, 130, 64), (300, 1000, 200), (700, 2500, 328)])
 def test_tied_step(b, rows, vocab, hidden):
-    """Against 64-bit autograd of the same chain.  At most seven stored bf16 tensors (2^-9 each) lie on the
+    """Against 64-bit autograd of the same chain.  At most seven stored bf16 tensors (2^-8 each) lie on the
     longest path (y0, y, h, z, dl, dh, dy); random signs make the sum far smaller; errors are compared by norm."""
     g = torch.Generator("cuda").manual_seed(rows)
     bf = torch.bfloat16
