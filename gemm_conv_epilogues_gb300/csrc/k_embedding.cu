@@ -15,6 +15,8 @@
 //      piece is finished where it began; longer ones leave partial sums.  Other
 //      CTAs write the zeros of words that do not occur.
 //   3  the partial sums of the long words are added in order
+#include <type_traits>
+
 #include "grouped.cuh"
 #include "lm_internal.h"
 #include "ptx_sm100.cuh"
@@ -129,7 +131,8 @@ __device__ __forceinline__ uint32_t word_of(uint64_t key) { return (uint32_t)(ke
 // first takes the tokens, a second one, for more than 2^18 words, the first one's
 // keys.  A warp has a stretch of the list and counters of its own, so that places
 // follow the order of the list: below this CTA's range, smaller digits, earlier
-// warps, earlier in the warp.  (Sorting chunks and merging them took three times as long.)
+// warps, earlier in the warp.  16384 tokens take 10 us (sorting chunks and merging them took 32);
+// a million 283, for which the SMs read all tokens from L2 twice, at 8.6 TB/s.
 struct SortArgs {
     Indices tokens;
     const uint64_t *in;
@@ -142,7 +145,7 @@ struct SortArgs {
     int64_t listed_padding;
 };
 
-template <bool FIRST, bool WIDE>
+template <bool FIRST, bool WIDE, bool ONLY>
 __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_constant__ SortArgs a)
 {
     pdl_begin();
@@ -151,7 +154,10 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
     constexpr int UNROLL = 8;
     constexpr uint32_t mask = (1u << kDigitBits) - 1;
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const uint32_t range = (uint32_t)a.range, d0 = blockIdx.x * range;
+    // ONLY: the words themselves are the digits, and what is no word lies behind the last range
+    const uint32_t d0 = blockIdx.x * (uint32_t)a.range;
+    const uint32_t range = ONLY ? min((uint32_t)a.range, (uint32_t)a.vocab - d0) : (uint32_t)a.range;
+    auto place_of = [&](uint32_t word) { return (ONLY ? word : (word >> a.shift) & mask) - d0; };
     const int seg = ((a.n + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     const int lo = min(a.n, warp * seg), hi = min(a.n, lo + seg);
     for (int i = t; i < kSortWarps * a.range; i += kSortThreads) cnt[i] = 0;
@@ -159,32 +165,32 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
     __syncthreads();
     uint32_t *mine = cnt + warp * a.range;
     // 32*UNROLL entries from i on: their words (kNone: not there) and, of keys, their rows
-    auto load = [&](int i, uint32_t (&word)[UNROLL], uint32_t (&row)[UNROLL]) {
-        if constexpr (!FIRST) {
-            uint64_t v[UNROLL];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) v[u] = i + 32 * u < hi ? a.in[i + 32 * u] : ~0ull;
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                word[u] = word_of(v[u]);
-                row[u] = (uint32_t)v[u];
-            }
-        } else if constexpr (WIDE) {
-            uint64_t v[UNROLL];
+    auto load_from = [&](auto whole, int i, uint32_t (&word)[UNROLL], uint32_t (&row)[UNROLL]) {
+        auto there = [&](int u) { return decltype(whole)::value || i + 32 * u < hi; };
+        if constexpr (FIRST && !WIDE) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
-                v[u] = i + 32 * u < hi ? static_cast<const uint64_t *>(a.tokens.p)[i + 32 * u] : ~0ull;
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-                word[u] = v[u] < (uint64_t)a.vocab && (uint32_t)v[u] != a.padding ? (uint32_t)v[u] : kNone;
+                word[u] = there(u) ? static_cast<const uint32_t *>(a.tokens.p)[i + 32 * u] : kNone;
         } else {
-            uint32_t v[UNROLL];
+            const uint2 *src = FIRST ? static_cast<const uint2 *>(a.tokens.p) : reinterpret_cast<const uint2 *>(a.in);
+            uint2 v[UNROLL];
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) v[u] = there(u) ? src[i + 32 * u] : make_uint2(kNone, kNone);
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {   // a token's halves, or a key's: its row and its word
+                word[u] = !FIRST ? v[u].y : v[u].y == 0 ? v[u].x : kNone;
+                row[u] = v[u].x;
+            }
+        }
+        if (FIRST && (!ONLY || a.padding != kNone)) {
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
-                v[u] = i + 32 * u < hi ? static_cast<const uint32_t *>(a.tokens.p)[i + 32 * u] : kNone;
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) word[u] = v[u] < (uint32_t)a.vocab && v[u] != a.padding ? v[u] : kNone;
+                if ((!ONLY && word[u] >= (uint32_t)a.vocab) || word[u] == a.padding) word[u] = kNone;
         }
+    };
+    auto load = [&](int i, uint32_t (&word)[UNROLL], uint32_t (&row)[UNROLL]) {
+        if (i - lane + 32 * UNROLL <= hi) load_from(std::true_type(), i, word, row);
+        else load_from(std::false_type(), i, word, row);
     };
     // which of this lane's entries are in the range, where 32 bits hold them: few are, and only those are looked at again
     const bool marked = seg <= 32 * 32;
@@ -195,9 +201,10 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
         load(i, word, row);
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const uint32_t digit = (word[u] >> a.shift) & mask, at = digit - d0;
-            low += word[u] != kNone && digit < d0;
-            if (word[u] != kNone && at < range) {
+            const uint32_t at = place_of(word[u]);
+            const bool there = ONLY || word[u] != kNone;
+            low += there && at + d0 < d0;
+            if (there && at < range) {
                 atomicAdd(mine + at, 1u);
                 marks |= 1u << ((step + u) & 31);
             }
@@ -259,7 +266,7 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
         const unsigned active = __ballot_sync(0xffffffffu, in_range);
         if (active == 0) return;
         if (in_range) {
-            const uint32_t at = ((word >> a.shift) & mask) - d0;
+            const uint32_t at = place_of(word);
             const unsigned same = __match_any_sync(active, at);
             const uint32_t before = __popc(same & ((1u << lane) - 1u)), first = mine[at];
             a.out[first + before] = (uint64_t)word << 32 | (FIRST ? (uint32_t)i : row);
@@ -284,7 +291,7 @@ __global__ void __launch_bounds__(kSortThreads) count_sort_kernel(const __grid_c
             load(i, word, row);
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u)
-                put(i + 32 * u, word[u], row[u], word[u] != kNone && ((word[u] >> a.shift) & mask) - d0 < range);
+                put(i + 32 * u, word[u], row[u], (ONLY || word[u] != kNone) && place_of(word[u]) < range);
         }
     }
     if (blockIdx.x == gridDim.x - 1)   // the rest have no gradient
@@ -702,9 +709,9 @@ cudaError_t launch_embedding_backward(const EmbedArgs &a, cudaStream_t st)
         q.vocab = a.vocab; q.listed_padding = a.padding;
         q.padding = a.padding >= 0 && a.padding < a.vocab ? (uint32_t)a.padding : kNone;
         q.n = (int)a.rows; q.shift = pass * kDigitBits; q.range = (int)range;
-        auto kern = pass > 0          ? count_sort_kernel<false, false>
-                    : a.tokens.wide ? count_sort_kernel<true, true>
-                                    : count_sort_kernel<true, false>;
+        auto kern = pass > 0     ? count_sort_kernel<false, false, false>
+                    : passes > 1 ? (a.tokens.wide ? count_sort_kernel<true, true, false> : count_sort_kernel<true, false, false>)
+                                 : (a.tokens.wide ? count_sort_kernel<true, true, true> : count_sort_kernel<true, false, true>);
         e = raise_smem_limit(reinterpret_cast<const void *>(kern));
         if (e == cudaSuccess) e = launch_pdl(kern, grid, dim3(kSortThreads), (size_t)(kSortWarps * range * 4), st, q);
     }
