@@ -413,10 +413,11 @@ Plan plan_of(bool backward, int64_t rows, int64_t vocab, int64_t hidden)
     if (pack) p.piece = piece_of(vocab, p.w_pitch * 2, kPackBytes);
     if (!backward) {
         p.at_target = take(4 * rows);
-        // two slots per tile of 256 words, for few rows of as little as 64
-        const int64_t pieces = (vocab + p.piece - 1) / p.piece, few = rows < 256 ? rows : 256;
-        const int64_t wide = 2 * (vocab / 256 + pieces) * rows, narrow = 2 * (vocab / 64 + pieces) * few;
-        p.part = take(8 * (wide > narrow ? wide : narrow));
+        // Two slots per tile of words.  lce_word_tile makes at most units*waves/down tiles of a piece
+        // (down: row tiles), which is no more than words/256 + 1 + units/down, and rows/down is no more
+        // than a row tile: 256 rows on half of the SMs, or 128 on all.
+        const int64_t pieces = (vocab + p.piece - 1) / p.piece;
+        p.part = take(8 * 2 * ((vocab / 256 + pieces) * rows + pieces * 128 * sm_count()));
     } else {
         p.l2 = take(4 * rows);
         p.ca = take(4 * rows);

@@ -346,3 +346,19 @@ def test_backward_padding_is_a_word(b, wide):
     b.tf_embedding_backward(dy, hidden, index, wide, dtable, rows, vocab, hidden, 1.0, 3, 0, b.TF_FP32, ws, ws.numel())
     assert (dtable[3] == 0).all()
     _check_grad(dtable, None, dy, torch.where(tokens == 3, -1, tokens), 1.0, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,vocab,hidden", [(1, 5, 8), (9, 5, 8), (999, 50, 1000), (4097, 300000, 8), (5000, 3, 4096), (40000, 7, 100),
+                                               (300000, 9, 8), (70000, 500, 2048)])
+def test_workspace_is_kept_to(b, rows, vocab, hidden):
+    """Nothing is written behind the bytes that the size function asks for."""
+    for kind in ("one", "ends", "any"):
+        tokens = _tokens(kind, rows, vocab)
+        dy = torch.ones(rows, hidden, device="cuda").half()
+        dtable = torch.empty(vocab, hidden, device="cuda")
+        size = b.tf_embedding_backward_workspace_size(rows, vocab, hidden)
+        buffer = torch.full((size + (1 << 20),), 0xa5, dtype=torch.uint8, device="cuda")
+        _grad(b, dy, tokens, dtable, 1.0, 0, "fp16", ws=buffer[:size])
+        assert (buffer[size:] == 0xa5).all()
+        assert torch.equal(dtable[:, 0].double(), torch.bincount(tokens, minlength=vocab).double())

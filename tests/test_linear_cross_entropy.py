@@ -547,3 +547,24 @@ def test_wide_rows(b):
         _check_forward(x, w, targets, 1.0, loss, lse)
         dx, dw = _grads(b, x, w, targets, lse, None, None, "bf16")
         _check_grads(x, w, targets, lse, None, None, "bf16", 1.0, dx, dw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES + [(301, 10007, 8), (700, 1927, 16), (3000, 1000, 16), (3000, 257, 7), (9000, 300, 8),
+                                            (4200, 40001, 24), (5, 140001, 1003)], ids=str)
+def test_workspaces_are_kept_to(b, shape):
+    """Nothing is written behind the bytes that the size functions ask for."""
+    rows, vocab, hidden = shape
+    x, w, targets = _inputs(rows, vocab, hidden, "fp16", seed=17)
+    spaces = []
+
+    def space(size):
+        spaces.append((size, torch.full((size + (1 << 20),), 0xa5, dtype=torch.uint8, device="cuda")))
+        return spaces[-1][1][:size]
+
+    ws = space(b.tf_linear_cross_entropy_forward_workspace_size(rows, vocab, hidden, 0))
+    loss, lse = _forward(b, x, w, targets, "fp16", ws=ws)
+    ws = space(b.tf_linear_cross_entropy_backward_workspace_size(rows, vocab, hidden, 0))
+    _grads(b, x, w, targets, lse, None, None, "fp16", ws=ws)
+    for size, buffer in spaces:
+        assert (buffer[size:] == 0xa5).all()
