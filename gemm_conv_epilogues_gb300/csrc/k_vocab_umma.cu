@@ -27,7 +27,7 @@
 // MMAs run.
 // What bounds it, 4096 rows, 64000 words of 4096, bf16 (2.15 TFLOP each): STATS 1.02-1.05 ms
 // alone (2.05-2.1 PFLOP/s), DLOGITS in two pieces 1.08-1.10, GRADS 2.23-2.26; the tensor pipe is busy for
-// 95, 93 and 95.5% of the active cycles.  In a loop the power cap holds the clock down: 1.7 PFLOP/s.
+// 95, 92 and 95.5% of the active cycles.  In a loop the power cap holds the clock down: 1.7 PFLOP/s.
 // Four rows over 128000 words: 157 us, 6.7 TB/s of weights.
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
 // error word and winds down.
