@@ -317,6 +317,8 @@ constexpr int kMinPiece = 8, kMaxPiece = 1024;
 // Terms added before their sum joins the next level's: long sums of equal terms keep their digits.
 constexpr int kLevel = 64;
 constexpr int64_t kMostPieces = 32768;
+// The ring's copies under way are waited for at least this long after a wait that ran out.
+constexpr uint64_t kLeastDrainNs = 1000000000;
 
 struct SumArgs {
     const uint64_t *keys;
@@ -495,27 +497,50 @@ __global__ void __launch_bounds__(kSumThreads, RING ? 6 : 5) sum_pieces_kernel(c
                 ptx::bulk_load(&ring[(half * UNROLL + member) * kSumThreads + group * a.lanes], src, bytes, &full[group][half]);
             __syncwarp();
         };
-        // the piece's threads meet
-        auto meet = [&]() {
+        // The piece's threads meet; whether any of them says that a wait ran out.
+        auto meet = [&](bool lost) {
+            if (a.lanes == 32) {
+                const bool any = __any_sync(0xffffffffu, lost);
+                __syncwarp();
+                return any;
+            }
             __syncwarp();
-            if (a.lanes > 32) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(a.lanes) : "memory");
+            uint32_t any;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                : "=r"(any)
+                : "r"((uint32_t)lost), "r"(group + 1), "r"(a.lanes)
+                : "memory");
+            return any != 0;
         };
-        bool ok = true;   // after a wait that ran out no other is made, and the loop goes on to its end
         fetch(first, 0);
         if (first + UNROLL < limit) fetch(first + UNROLL, 1);
-        meet();
+        meet(false);
         int batch = 0;
         for (int i = first; i < limit; i += UNROLL, ++batch) {
             const int half = batch & 1;
-            if (ok && !(ok = ptx::mbar_wait(&full[group][half], (uint32_t)(batch >> 1) & 1u, a.wait_ns)))
-                atomicOr(a.err, TF_DEVERR_PRODUCER_WAIT);
+            const bool got = ptx::mbar_wait(&full[group][half], (uint32_t)(batch >> 1) & 1u, a.wait_ns);
+            if (got) {
 #pragma unroll 1
-            for (int u = 0; u < UNROLL; ++u) {
-                const uint32_t w = words[group][half][u];
-                if (w == kNone) break;   // (the last of the list, or of the word that went on)
-                add_row(w, ring[(half * UNROLL + u) * kSumThreads + threadIdx.x]);
+                for (int u = 0; u < UNROLL; ++u) {
+                    const uint32_t w = words[group][half][u];
+                    if (w == kNone) break;   // (the last of the list, or of the word that went on)
+                    add_row(w, ring[(half * UNROLL + u) * kSumThreads + threadIdx.x]);
+                }
             }
-            meet();   // the batch has been read
+            if (meet(!got)) {
+                // All of the piece's threads leave: nothing more is asked for or written, and the
+                // batches under way, this one and the next, land while the CTA still owns the ring.
+                if (member == 0) {
+                    atomicOr(a.err, TF_DEVERR_PRODUCER_WAIT);
+                    const uint64_t ns = a.wait_ns > kLeastDrainNs ? a.wait_ns : kLeastDrainNs;
+                    for (int k = batch; k <= batch + 1 && first + k * UNROLL < limit; ++k)
+                        if (!ptx::mbar_wait(&full[group][k & 1], (uint32_t)(k >> 1) & 1u, ns))
+                            atomicOr(a.err, TF_DEVERR_DRAIN_WAIT);
+                }
+                return;
+            }
+            // (the batch has been read)
             if (i + 2 * UNROLL < limit) fetch(i + 2 * UNROLL, half);
         }
     } else {

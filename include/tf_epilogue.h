@@ -502,14 +502,16 @@ int tf_unfused_affine(const void *nrm, const float *gamma, const float *beta, vo
  * tcgen05 pipeline and of the bulk-copy rings, and the cluster LayerNorm's
  * wait for its peers' partial sums) gives up after this many nanoseconds of
  * %globaltimer, records TF_DEVERR_* in a device error word and lets the
- * kernel finish cleanly.  Default 2e9 (2 s).  Host-side setting, applies to
+ * kernel finish cleanly (the embedding gradient's ring then waits for its copies
+ * under way, for a second at least).  Default 2e9 (2 s).  Host-side setting, applies to
  * later launches. */
 void tf_set_wait_limit_ns(uint64_t limit_ns);
 uint64_t tf_get_wait_limit_ns(void);
 
 /* Bits of the device error word. */
 #define TF_DEVERR_PRODUCER_WAIT 0x1u  /* conv TMA producer: a stage never freed; bulk-copy
-                                        rings (bias + GELU, LayerNorm): a stage never filled */
+                                        rings (bias + GELU, LayerNorm, embedding gradient): a stage
+                                        never filled */
 #define TF_DEVERR_MMA_WAIT 0x2u       /* MMA issuer: operands or accumulator never ready */
 #define TF_DEVERR_EPILOGUE_WAIT 0x4u  /* epilogue: accumulator never committed */
 #define TF_DEVERR_DRAIN_WAIT 0x8u     /* in-flight copies/MMAs not drained on exit */
