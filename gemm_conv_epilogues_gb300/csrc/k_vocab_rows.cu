@@ -36,7 +36,7 @@ enum { UNIT_FIRST_ROW = 0, UNIT_ALL_ROWS = 1, UNIT_GIVEN = 2 };   // (the last: 
 struct GatherArgs {
     LceArgs a;
     int *count, *index, *target;
-    float *l2, *ca, *cb;       // backward
+    float *z, *ca, *cb;        // backward
     float *unit;               // backward: the gradients of the logits are held times unit[0]; unit[1] is its inverse
     int unit_from;
     uint16_t *x;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 4) gather_kernel(const __grid_consta
             if (BACKWARD) {
                 const float d = a.dloss ? a.dloss[i] : 1.0f;
                 if (g.unit_from == UNIT_FIRST_ROW) unit = unit_of(typical);
-                g.l2[at] = a.lse[i] * kLog2e;
+                g.z[at] = a.lse[i];
                 g.ca[at] = (a.dlse ? d + a.dlse[i] : d) * unit;
                 g.cb[at] = d * unit;
             }
@@ -376,7 +376,7 @@ struct Plan {
     int64_t x_pitch, w_pitch, dl_pitch, dx_pitch;
     int64_t piece;          // words
     int splits;             // of dx
-    int64_t count, unit, index, target, l2, ca, cb, at_target, part, x, dl, dx, pack, bytes;
+    int64_t count, unit, index, target, z, ca, cb, at_target, part, x, dl, dx, pack, bytes;
 };
 
 // Words per piece where `most` bytes hold `per_word` each: as few pieces as fit, of
@@ -419,7 +419,7 @@ Plan plan_of(bool backward, int64_t rows, int64_t vocab, int64_t hidden)
         const int64_t pieces = (vocab + p.piece - 1) / p.piece;
         p.part = take(8 * 2 * ((vocab / 256 + pieces) * rows + pieces * 128 * sm_count()));
     } else {
-        p.l2 = take(4 * rows);
+        p.z = take(4 * rows);
         p.ca = take(4 * rows);
         p.cb = take(4 * rows);
         const int64_t fits = piece_of(vocab, 2 * rows, kDlBytes);
@@ -461,7 +461,7 @@ cudaError_t launch_gather(const LceArgs &a, const Plan &p, bool backward, cudaSt
     g.per_block = a.rows <= 4 * sm_count() ? 1 : a.rows <= 16384 ? 8 : (int)up((a.rows + 2047) / 2048, 8);
     const dim3 grid((unsigned)(a.rows ? (a.rows + g.per_block - 1) / g.per_block : 1));
     if (!backward) return launch_pdl(gather_kernel<false>, grid, dim3(kThreads), 0, st, g);
-    g.l2 = at<float>(a.ws, p.l2);
+    g.z = at<float>(a.ws, p.z);
     g.ca = at<float>(a.ws, p.ca);
     g.cb = at<float>(a.ws, p.cb);
     g.unit = at<float>(a.ws, p.unit);
@@ -482,7 +482,6 @@ LceProduct product_of(const LceArgs &a, const Plan &p)
     m.rows = (int)a.rows;
     m.hidden = a.hidden;
     m.dtype = a.dtype;
-    m.factor = a.scale * kLog2e;
     return m;
 }
 
@@ -514,6 +513,7 @@ cudaError_t launch_lce_forward(const LceArgs &a, cudaStream_t st)
     LceProduct m = product_of(a, p);
     m.part = at<float2>(a.ws, p.part);
     m.at_target = at<float>(a.ws, p.at_target);
+    m.factor = a.scale * kLog2e;
     for (int64_t v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += p.piece) {
         const int64_t words = a.vocab - v0 < p.piece ? a.vocab - v0 : p.piece;
         e = piece_weights(a, p, v0, words, &m, st);
@@ -535,7 +535,7 @@ cudaError_t launch_lce_backward(const LceArgs &a, cudaStream_t st)
     const Plan p = plan_of(true, a.rows, a.vocab, a.hidden);
     cudaError_t e = launch_gather(a, p, true, st);
     LceProduct m = product_of(a, p);
-    m.l2 = at<float>(a.ws, p.l2);
+    m.z = at<float>(a.ws, p.z);
     m.ca = at<float>(a.ws, p.ca);
     m.cb = at<float>(a.ws, p.cb);
     m.unit = at<float>(a.ws, p.unit);
@@ -547,14 +547,13 @@ cudaError_t launch_lce_backward(const LceArgs &a, cudaStream_t st)
     m.dw_f32 = a.dw_dtype == TF_FP32;
     m.accumulate = a.accumulate;
     m.first = 1;
+    m.factor = a.scale;
     for (int64_t v0 = 0; e == cudaSuccess && v0 < a.vocab; v0 += p.piece) {
         const int64_t words = a.vocab - v0 < p.piece ? a.vocab - v0 : p.piece;
         e = piece_weights(a, p, v0, words, &m, st);
         if (e != cudaSuccess) return e;
-        m.factor = a.scale * kLog2e;
         if (a.rows > 0) e = launch_lce_product(LCE_DLOGITS, m, st);
         if (e != cudaSuccess) return e;
-        m.factor = a.scale;
         m.dw = a.dw ? static_cast<char *>(a.dw) + v0 * a.hidden * (m.dw_f32 ? 4 : 2) : nullptr;
         e = launch_lce_product(LCE_GRADS, m, st);
         m.first = 0;

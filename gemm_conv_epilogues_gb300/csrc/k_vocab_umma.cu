@@ -471,12 +471,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                      : count;
                 const int left = row0 < rows ? min(width, c1) - c0 : 0;   // columns with results, up to 128
                 int target = -1;
-                float l2 = 0.0f, ca = 0.0f, cb = 0.0f;
+                float z = 0.0f, ca = 0.0f, cb = 0.0f;
                 if constexpr (MODE != LCE_GRADS) {
                     if (row < count) {
                         target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
                         if constexpr (MODE == LCE_DLOGITS) {
-                            l2 = __ldg(p.a.l2 + row);
+                            z = __ldg(p.a.z + row);
                             ca = __ldg(p.a.ca + row);
                             cb = __ldg(p.a.cb + row);
                         }
@@ -553,9 +553,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 const int i = 2 * u + half, c = 32 * i;
+                                // lse before log2(e), so that a sure word's exponential is one, however large its logit
+                                const float2 scale2 = make_float2(p.a.factor, p.a.factor), z2 = make_float2(-z, -z);
+                                const float2 log2e2 = make_float2(kLog2e, kLog2e);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    r[i][k] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(r[i][k]), p.a.factor, -l2)) * ca);
+                                for (int k = 0; k < 32; k += 2) {
+                                    const float2 l = make_float2(__uint_as_float(r[i][k]), __uint_as_float(r[i][k + 1]));
+                                    const float2 d = fmul2(ffma2(l, scale2, z2), log2e2);
+                                    r[i][k] = __float_as_uint(ex2_approx(d.x) * ca);
+                                    r[i][k + 1] = __float_as_uint(ex2_approx(d.y) * ca);
+                                }
                                 const int at = target - c;
                                 const bool hit = at >= 0 && at < 32 && target < left;
                                 if (__any_sync(0xffffffffu, hit)) {

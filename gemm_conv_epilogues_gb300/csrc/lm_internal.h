@@ -60,7 +60,7 @@ struct LceProduct {
     const void *x, *w;       // [rows][x_pitch], [words][w_pitch]; pitches are multiples of 8
     float2 *part;            // STATS: (maximum, sum) per slot and row
     float *at_target;        // STATS: the target's sum
-    const float *l2, *ca, *cb;   // DLOGITS: lse in base 2, and what the probabilities and the target take
+    const float *z, *ca, *cb;   // DLOGITS: lse, and what the probabilities and the target take
     const float *unit;       // GRADS: unit[1] is the unit of the gradients of the logits
     void *dl;                // [rows][dl_pitch]
     float *dx;               // GRADS: [splits][rows][dx_pitch], null where not wanted
@@ -69,7 +69,7 @@ struct LceProduct {
     int rows, words, v0, hidden;
     int slot0, splits;
     int first;               // the first piece: dx is written, not added to
-    float factor;            // scale * log2(e) for STATS and DLOGITS, scale for GRADS
+    float factor;            // scale * log2(e) for STATS, scale for DLOGITS and GRADS
     int dtype, dw_f32, accumulate;
 };
 int lce_word_tile(int64_t rows, int64_t words);   // words per tile of the logits

@@ -442,8 +442,11 @@ int tf_linear_cross_entropy_forward(const void *x, int64_t x_stride, const void 
  *   dw     : dw_dtype [vocab][hidden], contiguous, or NULL; dw_dtype is dtype or
  *            TF_FP32.  With `accumulate` != 0 (TF_FP32 only) it is added to what
  *            dw holds.
- * dl is rounded to dtype, the matrix products' operand type: each term is off by up to 2^-8
- * (bf16) or 2^-11 (fp16) of its value, in dx and dw, also where dw is fp32.  It is held in
+ * The exponential, formed in fp32, is off by up to 2^-19 + 2^-22*(|l[i][v]| + |lse[i]|) of its value; a
+ * target's term, of which dloss is taken away, by as much of exp(l - lse)*(dloss + dlse).  With
+ * scale 1, no dlse and the forward pass's lse, a target whose loss is 0 has a term of exactly 0.
+ * dl is then rounded to dtype, the matrix products' operand type: each term is off by up to 2^-8
+ * (bf16) or 2^-11 (fp16) of its value more, in dx and dw, also where dw is fp32.  It is held in
  * units of a typical |dloss|, so that equal weights add no rounding of their own: bf16 takes
  * the first counted row's (where that lies between 2^-40 and 2^40), fp16 2^-14 of the largest,
  * so that terms down to 2^-28 of it keep their digits and none below 2^-39 of it

@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from test_embedding import _check_grad, _grad, _tokens
+from test_linear_cross_entropy import _forward, _grads
+from train_reference import TYPES
 
 
 @pytest.fixture(scope="module")
@@ -45,3 +47,26 @@ def test_ring_waits_that_run_out(b, hidden):
     dtable = torch.full((vocab, hidden), float("nan"), device="cuda")
     _grad(b, dy, tokens, dtable, 1.0, 0, "bf16", ws=ws)
     assert b.tf_read_device_error() == (0, 0) and torch.equal(dtable, want)
+
+
+# ---------------------------------------------------------------- linear cross entropy
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,vocab,hidden", [(60, 900, 256), (300, 900, 1100), (130, 70, 257), (4200, 40001, 512)])
+def test_sure_targets_have_no_gradient(b, rows, vocab, hidden, dtype):
+    """Targets whose logits, of some hundred, leave every other word's exponential below the smallest number: the
+    loss is exactly 0, and so is every gradient, in one piece of the vocabulary and in several."""
+    g = torch.Generator("cuda").manual_seed(rows)
+    w = torch.randn(vocab, hidden, generator=g, device="cuda").to(TYPES[dtype])
+    targets = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    size = 400.0 / hidden
+    x = (size * (w[targets].float() + 0.1 * torch.randn(rows, hidden, generator=g, device="cuda"))).to(TYPES[dtype])
+    l = x.double() @ w.double().t()
+    hit = l.gather(1, targets[:, None])
+    assert (l.scatter(1, targets[:, None], float("-inf")) < hit - 100).all()   # e^-88 is the smallest
+    loss, lse = _forward(b, x, w, targets, dtype)
+    assert (loss == 0).all() and ((lse.double() - hit[:, 0]).abs() <= 1e-2).all()
+    dloss = torch.full((rows,), 1.0 / rows, device="cuda")
+    dx, dw = _grads(b, x, w, targets, lse, dloss, None, dtype)
+    assert (dx == 0).all() and (dw == 0).all()
