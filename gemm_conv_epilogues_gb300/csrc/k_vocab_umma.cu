@@ -22,9 +22,11 @@
 //   1     TMEM allocator and MMA issuer
 //   4-11  epilogue
 // The tensor cores truncate where fp32 additions round, so an accumulator's error grows with
-// the number of MMAs it takes.  A logit's sum is cut into parts of 1024 terms, whose
-// accumulators alternate; the epilogue's threads add them in registers while the next part's
-// MMAs run.
+// the number of MMAs it takes.  A logit's sum is cut into parts of 1024 terms, dw's into parts of
+// 4096, whose accumulators alternate; the epilogue's threads add them in registers while
+// the next part's MMAs run.  (In one accumulator the gradients of weights by a million rows of one sign
+// came out 6e-3 low, now 2e-6.)  dx's sums, of which 16 bits are kept, are cut into parts of 16384 terms, which are
+// tiles of their own that add to the fp32 sums in memory.
 // What bounds it, 4096 rows, 64000 words of 4096, bf16 (2.15 TFLOP each): STATS 1.02-1.05 ms
 // alone (2.05-2.1 PFLOP/s), DLOGITS in two pieces 1.08-1.10, GRADS 2.23-2.26; the tensor pipe is busy for
 // 95, 92 and 95.5% of the active cycles.  In a loop the power cap holds the clock down: 1.7 PFLOP/s.
@@ -59,7 +61,18 @@ constexpr int kThreads = 32 * (kFirstEpiWarp + kEpiWarps);
 constexpr int kTileN = 256;
 constexpr int kABytes = 128 * BK * 2;               // 128 rows of a K step
 constexpr int stage_bytes(int cg) { return kABytes + 256 / cg * BK * 2; }
-constexpr int kPartSteps = 16;                      // STATS, DLOGITS: K steps per part of a sum
+// Gradients whose dw sums have more than one part.  (The registers that parts take cost short
+// sums time: gradients of 7 rows over 88000 words of 2560 318 us in this kernel, 270 in the other; of 300 rows over 32000
+// words of 2048 158 and 140.)
+constexpr int LCE_LONG_GRADS = 3;
+constexpr bool of_grads(int mode) { return mode == LCE_GRADS || mode == LCE_LONG_GRADS; }
+// K steps per part of a sum in registers: 1024 terms of a logit's, 4096 of dw's.
+constexpr int kGradSteps = 64;
+// K steps per part of dx's in memory: 16384 terms come out up to 8e-5 low, a sixth of fp16's half step.  (Step of
+// 1024 rows over 128000 words of 2048: 1.465 ms, uncut 1.452; with parts of 4096 terms 1.482, and in registers 1.457;
+// of 4096 rows, 64000 words of 4096 5.06, uncut 5.05, parts of 4096 terms 5.1.)
+constexpr int kDxSteps = 256;
+constexpr int part_steps(int mode) { return mode == LCE_GRADS ? 1 << 30 : mode == LCE_LONG_GRADS ? kGradSteps : 16; }
 // Registers: the epilogue's threads hold 128 sums each while the issuing warps need few.  The
 // kernel starts with 168 per thread, and 88*128 + 208*256 = 168*384.
 constexpr int kIssueRegs = 88, kEpilogueRegs = 208;
@@ -90,11 +103,13 @@ struct VocabArgs {
     int a_box;         // rows that a load of A brings (STATS, DLOGITS)
     int group;         // STATS, DLOGITS: row tiles that share a sweep over the vocabulary
     int split_steps;   // DX: K steps per split
+    int dx_parts;      // DX: parts of a split's sum, which are added in memory
 };
 
 // A tile: rows [m0, +128*CG), columns [n0, +bn), K steps [k0, k0 + nk).
 struct Tile {
     int kind, m0, n0, k0, nk, slot;
+    bool adds;   // to what is there
 };
 enum { TILE_LOGITS = 0, TILE_DX = 1, TILE_DW = 2 };
 
@@ -116,7 +131,7 @@ struct Share {
         cid = cid_;
         ncl = ncl_;
         row_tiles = div_up(count, ROWS);
-        if constexpr (MODE != LCE_GRADS) {
+        if constexpr (!of_grads(MODE)) {
             col_tiles = div_up(p.a.words, p.bn);
             tiles = row_tiles * col_tiles;
             sweep = p.group * col_tiles;
@@ -143,24 +158,26 @@ struct Share {
 
     __device__ __forceinline__ bool at(const VocabArgs &p, int j, Tile *t) const
     {
-        if constexpr (MODE != LCE_GRADS) {
+        if constexpr (!of_grads(MODE)) {
             const int i = cid + j * ncl;
             if (i >= tiles) return false;
             const int g = i / sweep, r = i - g * sweep, size = min(p.group, row_tiles - g * p.group), v = r / size;
-            *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v};
+            *t = {TILE_LOGITS, (g * p.group + r - v * size) * ROWS, v * p.bn, 0, div_up(p.a.hidden, BK), p.a.slot0 + 2 * v, false};
             return true;
         } else {
-            if (j < own) {
-                const int i = cid + j * ncl, s = i / plane, r = i - s * plane, m = r / col_tiles, k0 = s * p.split_steps;
-                const int nk = max(0, min(p.split_steps, div_up(p.a.words, BK) - k0));
-                *t = {TILE_DX, m * ROWS, (r - m * col_tiles) * p.bn, k0, nk, s};
+            if (j < own * p.dx_parts) {
+                const int tile = j / p.dx_parts, part = j - tile * p.dx_parts, i = cid + tile * ncl;
+                const int s = i / plane, r = i - s * plane, m = r / col_tiles;
+                const int end = min((s + 1) * p.split_steps, div_up(p.a.words, BK)), k0 = s * p.split_steps + part * kDxSteps;
+                const int nk = max(0, p.dx_parts == 1 ? end - k0 : min(kDxSteps, end - k0));
+                *t = {TILE_DX, m * ROWS, (r - m * col_tiles) * p.bn, k0, nk, s, !p.a.first || part > 0};
                 return true;
             }
-            j -= own;
+            j -= own * p.dx_parts;
             const int i = j < lead ? j * others + rest : ahead + (j - lead) * ncl + rest;
             if (i >= nw) return false;
             const int m = i / col_tiles;
-            *t = {TILE_DW, m * ROWS, (i - m * col_tiles) * p.bn, 0, steps, 0};
+            *t = {TILE_DW, m * ROWS, (i - m * col_tiles) * p.bn, 0, steps, 0, p.a.accumulate != 0};
             return true;
         }
     }
@@ -249,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap map_x, const __grid_constant__ VocabArgs p)
 {
     constexpr bool PAIR = CG == 2;
-    constexpr int kStageBytes = stage_bytes(CG), kStages = kRingBytes / kStageBytes;
+    constexpr int kStageBytes = stage_bytes(CG), kStages = kRingBytes / kStageBytes, kPartSteps = part_steps(MODE);
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *empty = full + kStages;
@@ -335,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (PAIR) ptx::tma_load_2d_pair(dst, map, bar_cl, c0, c1);
                             else ptx::tma_load_2d(dst, map, bar, c0, c1);
                         };
-                        if constexpr (MODE != LCE_GRADS) {
+                        if constexpr (!of_grads(MODE)) {
                             if (leader) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(CG * (p.a_box + half) * (BK * 2)));
                             load(a_dst, &map_a, k, row);
                             load(b_dst, &map_w, k, t.n0 + crank * half);
@@ -378,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 Tile t;
                 for (int j = 0; ok && share.at(p, j, &t); ++j) {
                     if (t.nk == 0) continue;
-                    const bool a_mn = t.kind == TILE_DW, b_mn = MODE == LCE_GRADS;
+                    const bool a_mn = t.kind == TILE_DW, b_mn = of_grads(MODE);
                     const uint32_t id = idesc(128 * CG, p.bn, bf16, a_mn, b_mn);
                     const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
                     const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + kABytes, !b_mn);
@@ -387,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else ptx::umma_commit(bar);
                     };
                     for (int kb = 0; kb < t.nk; ++kb) {
-                        const bool begins = kb == 0 || (MODE != LCE_GRADS && kb % kPartSteps == 0);
-                        const bool ends = kb == t.nk - 1 || (MODE != LCE_GRADS && kb % kPartSteps == kPartSteps - 1);
+                        const bool begins = kb % kPartSteps == 0, ends = kb == t.nk - 1 || kb % kPartSteps == kPartSteps - 1;
                         if (begins) {
                             const bool got = ptx::mbar_wait<PAIR>(&tempty[b], ((taken >> b) & 1u) ^ 1u, p.wait_ns);
                             if (!__all_sync(0xffffffffu, got)) {
@@ -443,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *box = smem + kOffBox + (warp - kFirstEpiWarp) * kBoxBytes;
             const bool bf16 = p.a.dtype == TF_BF16;
             const int mid = (p.bn / 2 + 63) & ~63, c0 = h ? mid : 0, c1 = h ? p.bn : mid;   // this warp's columns of a tile
-            const float mult = p.a.factor * (MODE == LCE_GRADS ? __ldg(p.a.unit + 1) : 1.0f);
+            const float mult = p.a.factor * (of_grads(MODE) ? __ldg(p.a.unit + 1) : 1.0f);
             int b = 0;
             uint32_t seen = 0;   // parity of the results of either accumulator
             bool ok = true;
@@ -464,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             for (int j = 0; ok && share.at(p, j, &t); ++j) {
                 const int row0 = t.m0 + crank * 128 + q * 32, row = row0 + lane;
-                const int width = min(p.bn, (MODE == LCE_GRADS ? p.a.hidden : p.a.words) - t.n0);
+                const int width = min(p.bn, (of_grads(MODE) ? p.a.hidden : p.a.words) - t.n0);
                 // rows of this tile's M side: DLOGITS also writes the zeros behind them that dw's last K step reads
                 const int rows = MODE == LCE_DLOGITS         ? (count + BK - 1) / BK * BK
                                  : t.kind == TILE_DW ? p.a.words
@@ -472,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int left = row0 < rows ? min(width, c1) - c0 : 0;   // columns with results, up to 128
                 int target = -1;
                 float z = 0.0f, ca = 0.0f, cb = 0.0f;
-                if constexpr (MODE != LCE_GRADS) {
+                if constexpr (!of_grads(MODE)) {
                     if (row < count) {
                         target = __ldg(p.a.target + row) - p.a.v0 - t.n0 - c0;   // its place among this warp's columns
                         if constexpr (MODE == LCE_DLOGITS) {
@@ -501,10 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     b ^= 1;
                 };
                 const uint32_t columns = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)c0;
-                if constexpr (MODE != LCE_GRADS) {
-                    uint32_t r[4][32];   // the sums of this row's columns
+                uint32_t r[4][32];   // the sums of this row's columns
+                // adds a tile's parts
+                auto sum_parts = [&]() {
                     for (int k0 = 0; k0 < t.nk; k0 += kPartSteps) {
-                        if (!await()) break;
+                        if (!await()) return;
                         const uint32_t taddr = columns + (uint32_t)(b * kTileN);
                         if (k0 == 0) {
 #pragma unroll
@@ -529,6 +546,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         release();
                     }
+                };
+                if constexpr (!of_grads(MODE)) {
+                    sum_parts();
                     if (!ok) break;
                     if constexpr (MODE == LCE_STATS) {
                         float top = -INFINITY, sum = 0.0f;
@@ -596,37 +616,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t taddr = columns + (uint32_t)(b * kTileN);
                     const bool dx = t.kind == TILE_DX;
                     const bool wide = dx || p.a.dw_f32;        // 32-bit results
-                    const bool add = dx ? !p.a.first : p.a.accumulate != 0;
+                    const bool add = t.adds;
                     const int64_t pitch = dx ? p.a.dx_pitch : p.a.hidden;
                     uint8_t *out = dx ? reinterpret_cast<uint8_t *>(p.a.dx + (int64_t)t.slot * p.a.rows * p.a.dx_pitch)
                                       : static_cast<uint8_t *>(p.a.dw);
                     // rows that 16-byte words make up
                     const bool words = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 && pitch % (wide ? 4 : 8) == 0;
-                    if (t.nk > 0) {
+                    // several parts are added first; one is read 64 columns at a time as they leave.  (Kernels that add
+                    // parts have both halves of the loop apart, so that every sum has a register of its own.)
+                    const bool parts = MODE == LCE_LONG_GRADS && t.nk > kPartSteps;
+                    if (parts) {
+                        sum_parts();
+                        if (!ok) break;
+                    } else if (t.nk > 0) {
                         if (!await()) break;
                         if (left <= 0) release();
                     }
-#pragma unroll 1
-                    for (int u = 0; u < left; u += 64) {
-                        uint32_t r[2][32];
-                        if (t.nk > 0) {
-                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[0]);
-                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[1]);
+                    constexpr int UNROLL = MODE == LCE_LONG_GRADS ? 2 : 1;
+#pragma unroll UNROLL
+                    for (int pass = 0; pass < 2; ++pass) {
+                        const int u = 64 * pass, h0 = MODE == LCE_LONG_GRADS ? 2 * pass : 0, h1 = h0 + 1;
+                        if (u >= left) break;
+                        if (!parts && t.nk > 0) {
+                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)u, r[h0]);
+                            ptx::tmem_ld_32x32b_x32(taddr + (uint32_t)(u + 32), r[h1]);
                             ptx::tmem_ld_wait();
                             if (u + 64 >= left) release();
-                        } else {
+                        } else if (!parts) {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) r[0][k] = r[1][k] = 0u;
+                            for (int k = 0; k < 32; ++k) r[h0][k] = r[h1][k] = 0u;
                         }
                         if (t.nk == 0 && add) break;
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            r[0][k] = __float_as_uint(__uint_as_float(r[0][k]) * mult);
-                            r[1][k] = __float_as_uint(__uint_as_float(r[1][k]) * mult);
+                            r[h0][k] = __float_as_uint(__uint_as_float(r[h0][k]) * mult);
+                            r[h1][k] = __float_as_uint(__uint_as_float(r[h1][k]) * mult);
                         }
                         if (!wide) {
-                            put_half(r[0], 0);
-                            put_half(r[1], 1);
+                            put_half(r[h0], 0);
+                            put_half(r[h1], 1);
                         }
                         const int per = wide ? 4 : 8, size = wide ? 4 : 2;
 #pragma unroll
@@ -635,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (wide) {
 #pragma unroll
                                 for (int k = 0; k < 8; ++k) {
-                                    const uint32_t *v = &r[i][4 * k];
+                                    const uint32_t *v = &r[h0 + i][4 * k];
                                     box_put(box, lane, k, make_uint4(v[0], v[1], v[2], v[3]));
                                 }
                             }
@@ -733,6 +761,9 @@ cudaError_t resident(int *units)
     return cudaSuccess;
 }
 
+// K steps per split of dx's sums.
+int split_steps(const LceProduct &a) { return ((a.words + BK - 1) / BK + a.splits - 1) / a.splits; }
+
 template <int MODE, int CG>
 cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
 {
@@ -744,10 +775,11 @@ cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
     if (!p.err) return cudaErrorInitializationError;
     const int row_tiles = (a.rows + ROWS - 1) / ROWS;
     int64_t tiles;
-    if (MODE == LCE_GRADS) {
+    if (of_grads(MODE)) {
         const int nh = (a.hidden + kTileN - 1) / kTileN, step = 64 * CG;   // equal widths, in whole boxes of either CTA
         p.bn = ((a.hidden + nh - 1) / nh + step - 1) / step * step;
-        p.split_steps = ((a.words + BK - 1) / BK + a.splits - 1) / a.splits;
+        p.split_steps = split_steps(a);
+        p.dx_parts = MODE == LCE_LONG_GRADS ? 1 : (p.split_steps + kDxSteps - 1) / kDxSteps;
         const int64_t cols = (a.hidden + p.bn - 1) / p.bn;
         tiles = ((a.dx ? (int64_t)a.splits * row_tiles : 0) + (a.dw ? (a.words + ROWS - 1) / ROWS : 0)) * cols;
     } else {
@@ -768,7 +800,7 @@ cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
     CUtensorMap ma, mw, mx;
     const int rows = a.rows > 0 ? a.rows : 1;   // (dw without rows: nothing is loaded)
     bool ok;
-    if (MODE == LCE_GRADS) {
+    if (of_grads(MODE)) {
         ok = encode_rows(&ma, type, a.dl, rows, a.words, a.dl_pitch, 64, 64) &&
              encode_rows(&mw, type, a.w, a.words, a.hidden, a.w_pitch, 64, 64) &&
              encode_rows(&mx, type, a.x, rows, a.hidden, a.x_pitch, 64, 64);
@@ -839,7 +871,8 @@ cudaError_t launch_lce_product(int mode, const LceProduct &a, cudaStream_t st)
 {
     if (mode == LCE_STATS) return launch_rows<LCE_STATS>(a, st);
     if (mode == LCE_DLOGITS) return launch_rows<LCE_DLOGITS>(a, st);
-    return launch_rows<LCE_GRADS>(a, st);
+    const bool parts = a.dw && a.rows > kGradSteps * BK;
+    return parts ? launch_rows<LCE_LONG_GRADS>(a, st) : launch_rows<LCE_GRADS>(a, st);
 }
 
 }  // namespace tf

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 from test_embedding import _check_grad, _grad, _tokens
-from test_linear_cross_entropy import _forward, _grads
-from train_reference import TYPES
+from test_linear_cross_entropy import _check_grads, _forward, _grads, _inputs, _weights
+from train_reference import TYPES, U, half_step
 
 
 @pytest.fixture(scope="module")
@@ -70,3 +70,68 @@ def test_sure_targets_have_no_gradient(b, rows, vocab, hidden, dtype):
     dloss = torch.full((rows,), 1.0 / rows, device="cuda")
     dx, dw = _grads(b, x, w, targets, lse, dloss, None, dtype)
     assert (dx == 0).all() and (dw == 0).all()
+
+
+def _one_rounding(value, dtype, unit):
+    """A gradient of a logit as its type holds it in these units; that 1e-5 of its value does not change the rounding."""
+    held = torch.tensor([value * unit * s for s in (1.0, 1 - 1e-5, 1 + 1e-5)], dtype=torch.float64).to(TYPES[dtype])
+    assert held[0] == held[1] == held[2]
+    return held[0].double().item() / unit
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [5000, 70001, (1 << 20) + 777])
+def test_weight_gradient_of_many_rows_of_one_sign(b, rows, dtype):
+    """Equal logits, so that every row's gradients of them are the same numbers, whose rounding is known; x positive.
+    A part of a sum has 4096 terms, 256 accumulations, each truncated by at most 2u; the parts' sum rounds by u each."""
+    vocab, hidden = 200, 24
+    g = torch.Generator("cuda").manual_seed(rows)
+    x = (1 + torch.rand(rows, hidden, generator=g, device="cuda")).to(TYPES[dtype])
+    w = torch.zeros(vocab, hidden, dtype=TYPES[dtype], device="cuda")
+    targets = torch.full((rows,), 3, device="cuda")
+    loss, lse = _forward(b, x, w, targets, dtype)
+    unit = 1.0 if dtype == "bf16" else 2.0 ** 14
+    d = torch.full((vocab, 1), _one_rounding(1 / vocab, dtype, unit), dtype=torch.float64, device="cuda")
+    d[3] = _one_rounding(1 / vocab - 1, dtype, unit)
+    want = d * x.double().sum(0)
+    _, dw = _grads(b, x, w, targets, lse, None, None, dtype, want=("dw",), dw_dtype="fp32")
+    parts = (rows + 4095) // 4096
+    assert ((dw.double() - want).abs() <= (2 * 256 + parts + 4) * U * want.abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [4, 200])
+def test_input_gradient_of_many_words_of_one_sign(b, rows, dtype):
+    """Equal logits of four million words; positive weights, and dlse alone.  A part of a sum has 16384 terms, 1024
+    accumulations, each truncated by at most 2u; up to 64 parts, splits and pieces are added to one result."""
+    vocab, hidden = (1 << 22) - 333, 64
+    g = torch.Generator("cuda").manual_seed(rows)
+    w = torch.rand(vocab, hidden, generator=g, device="cuda").add_(1).to(TYPES[dtype])
+    x = torch.zeros(rows, hidden, dtype=TYPES[dtype], device="cuda")
+    targets = torch.arange(rows, device="cuda")
+    loss, lse = _forward(b, x, w, targets, dtype)
+    total = torch.zeros(hidden, dtype=torch.float64, device="cuda")
+    for part in w.split(1 << 19):
+        total += part.double().sum(0)
+    d = _one_rounding(1 / vocab, dtype, 1.0 if dtype == "bf16" else 2.0 ** 14)
+    zero, one = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")
+    dx, _ = _grads(b, x, w, targets, lse, zero, one, dtype, want=("dx",))
+    off = half_step(dtype) + (2 * 1024 + 64) * U
+    assert ((dx.double() - d * total).abs() <= off * d * total).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(4097, 1500, 328), (9001, 9001, 72), (100, 140001, 200), (140, 70001, 1002), (9000, 300, 65)], ids=str)
+def test_gradients_in_several_parts(b, shape):
+    """More than 4096 rows, words of a split, or both; tiles of every width, some of them empty."""
+    x, w, targets = _inputs(*shape, "bf16", "some", pad=8, seed=18)
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    dloss, dlse = _weights(targets)
+    before = torch.randn(shape[1], shape[2], device="cuda")
+    dw = before.clone()
+    dx, _ = _grads(b, x, w, targets, lse, dloss, dlse, "bf16", dw=dw, dw_dtype="fp32", accumulate=1)
+    _check_grads(x, w, targets, lse, dloss, dlse, "bf16", 1.0, dx, dw, "fp32", before)
+    _, dw = _grads(b, x, w, targets, lse, dloss, dlse, "bf16")
+    _check_grads(x, w, targets, lse, dloss, dlse, "bf16", 1.0, None, dw)
