@@ -95,7 +95,7 @@ int check_lce(const void *w, const void *targets, int index, int64_t rows, int64
               int dtype)
 {
     if (rows < 0 || vocab <= 0 || hidden <= 0 || !w || (rows > 0 && !targets) || bad_dtype(dtype) || bad_index(index) ||
-        !finite(scale) || !(scale > 0.0f))
+        !finite(scale * kLog2e) || !(scale > 0.0f))
         return TF_ERR_INVALID_ARG;
     if (dtype == TF_FP32 || rows > kLceMaxRows || vocab > kLceMaxVocab || hidden > kLceMaxHidden ||
         !aligned_to(w, hidden % 8 == 0 ? 16 : 2) || !aligned_to(targets, index_size(index)))

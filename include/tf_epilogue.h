@@ -409,7 +409,7 @@ int tf_embedding_backward(const void *dy, int64_t dy_stride, const void *tokens,
  *             row i at i*x_stride elements
  *   w       : dtype [vocab][hidden], contiguous (16-byte aligned where hidden % 8 == 0)
  *   targets : int32 or int64 (tf_index) [rows] on the device
- *   loss, lse : fp32 [rows];  scale > 0, finite
+ *   loss, lse : fp32 [rows];  scale > 0, scale*log2(e) finite in fp32
  * Rows whose target is `ignore` (-100, say; TF_NO_INDEX: none) cost nothing and
  * get a loss and lse of 0; what x holds there, NaN included, is not read.
  * Other targets outside [0, vocab) are ignored likewise and set TF_DEVERR_INDEX.

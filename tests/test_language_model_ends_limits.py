@@ -17,6 +17,25 @@ def b(cuda_ready):
     assert binding.tf_read_device_error() == (0, 0)
 
 
+# ---------------------------------------------------------------- refusals (no GPU)
+
+def test_scale_whose_exponents_overflow(native_lib):
+    """The exponents take scale*log2(e): where that is infinite, a largest logit's 0*infinity would make every loss NaN."""
+    from gemm_conv_epilogues_gb300 import binding as b
+    p = 1 << 20
+    n0 = b.tf_launch_count()
+
+    def calls(scale):   # no rows: where the scale is accepted there is nothing to do
+        return [b.tf_linear_cross_entropy_forward(None, 64, p, None, 1, None, None, 0, 100, 64, scale, -100, 1, None, 0, 0,
+                                                  check=False),
+                b.tf_linear_cross_entropy_backward(None, 64, p, None, 1, None, None, None, p, 64, None, 0, 100, 64, scale, -100, 0,
+                                                   1, 1, None, 0, 0, check=False)]
+
+    assert calls(3.0e38) == [b.TF_ERR_INVALID_ARG] * 2
+    assert calls(2.35e38) == [b.TF_OK] * 2   # 2.35e38*log2(e) is 3.39e38, and the largest number 3.40e38
+    assert b.tf_launch_count() == n0
+
+
 # ---------------------------------------------------------------- embedding
 
 @pytest.mark.gpu
