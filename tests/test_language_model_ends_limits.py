@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from test_embedding import _check_grad, _grad, _tokens
-from test_linear_cross_entropy import _check_grads, _forward, _grads, _inputs, _weights
+from test_linear_cross_entropy import IGNORE, _check_grads, _forward, _grads, _inputs, _weights
 from train_reference import TYPES, U, half_step
 
 
@@ -66,6 +66,42 @@ def test_ring_waits_that_run_out(b, hidden):
     dtable = torch.full((vocab, hidden), float("nan"), device="cuda")
     _grad(b, dy, tokens, dtable, 1.0, 0, "bf16", ws=ws)
     assert b.tf_read_device_error() == (0, 0) and torch.equal(dtable, want)
+
+
+def _other_words(tokens, padding, vocab):
+    """The tokens whose rows have a gradient; -1 in the others' places."""
+    return torch.where((tokens == padding) | (tokens < 0) | (tokens >= vocab), -1, tokens)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("wide", [1, 0])
+@pytest.mark.parametrize("vocab", [150001, 262144, 262145, 600001])
+@pytest.mark.parametrize("rows", [900, 40000, 140000])
+def test_orders_of_either_token_type(b, vocab, rows, wide):
+    """One pass and two, tokens that a warp keeps marks of and those that it reads again, a padding that is a word, and
+    tokens outside the vocabulary, far outside too."""
+    g = torch.Generator("cuda").manual_seed(rows)
+    padding = vocab // 3
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    tokens[::5] = tokens[0]          # a frequent word
+    tokens[1::5] = tokens[1] % 262144 + 262144 * (vocab // 262144 - 1 if vocab > 262144 else 0)
+    tokens[2::9] = padding
+    dy = torch.randn(rows, 8, generator=g, device="cuda").half()
+    for outside in (False, True):
+        if outside:
+            tokens[3::11] = vocab
+            tokens[4::11] = (1 << 40) + 5 if wide else (1 << 31) - 1
+            tokens[5::11] = -7
+        keep = _other_words(tokens, padding, vocab)
+        dy[keep < 0] = float("nan")
+        before = torch.randn(vocab, 8, generator=g, device="cuda")
+        for accumulate in (0, 1):
+            dtable = before.clone()
+            ws = torch.full((b.tf_embedding_backward_workspace_size(rows, vocab, 8),), 0xff, dtype=torch.uint8, device="cuda")
+            b.tf_embedding_backward(dy, 8, tokens if wide else tokens.int(), wide, dtable, rows, vocab, 8, 1.5, padding,
+                                    accumulate, b.TF_FP16, ws, ws.numel())
+            assert b.tf_read_device_error() == ((b.TF_ERR_TIMEOUT, b.TF_DEVERR_INDEX) if outside else (0, 0))
+            _check_grad(dtable, before, dy, keep, 1.5, accumulate)
 
 
 # ---------------------------------------------------------------- linear cross entropy
@@ -142,7 +178,8 @@ def test_input_gradient_of_many_words_of_one_sign(b, rows, dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", [(4097, 1500, 328), (9001, 9001, 72), (100, 140001, 200), (140, 70001, 1002), (9000, 300, 65)], ids=str)
+@pytest.mark.parametrize("shape", [(4097, 1500, 328), (9001, 9001, 72), (100, 140001, 200), (140, 70001, 1002), (9000, 300, 65)],
+                         ids=str)
 def test_gradients_in_several_parts(b, shape):
     """More than 4096 rows, words of a split, or both; tiles of every width, some of them empty."""
     x, w, targets = _inputs(*shape, "bf16", "some", pad=8, seed=18)
@@ -154,3 +191,65 @@ def test_gradients_in_several_parts(b, shape):
     _check_grads(x, w, targets, lse, dloss, dlse, "bf16", 1.0, dx, dw, "fp32", before)
     _, dw = _grads(b, x, w, targets, lse, dloss, dlse, "bf16")
     _check_grads(x, w, targets, lse, dloss, dlse, "bf16", 1.0, None, dw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("shape", [(3, 500, 64), (33, 700, 200), (600, 1111, 77)], ids=str)
+def test_dlse_without_dloss(b, shape, dtype):
+    x, w, targets = _inputs(*shape, dtype, "some", seed=19)
+    loss, lse = _forward(b, x, w, targets, dtype)
+    dlse = 0.5 * torch.randn(shape[0], device="cuda")
+    dlse[targets == IGNORE] = float("nan")
+    dx, dw = _grads(b, x, w, targets, lse, None, dlse, dtype, dw_dtype="fp32")
+    _check_grads(x, w, targets, lse, None, dlse, dtype, 1.0, dx, dw, "fp32")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(4000, 40001, 40), (4200, 40001, 72), (5, 140001, 1003)], ids=str)
+def test_accumulates_over_pieces(b, shape):
+    """Each piece of the vocabulary (of gradients of logits, or of copied weights) adds to its own rows of dw, once."""
+    x, w, targets = _inputs(*shape, "bf16", "some", seed=20)
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    dloss, dlse = _weights(targets)
+    before = torch.randn(shape[1], shape[2], device="cuda")
+    dw = before.clone()
+    dx, _ = _grads(b, x, w, targets, lse, dloss, dlse, "bf16", dw=dw, dw_dtype="fp32", accumulate=1)
+    _check_grads(x, w, targets, lse, dloss, dlse, "bf16", 1.0, dx, dw, "fp32", before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("shape", [(40, 333, 64), (300, 500, 264), (5000, 300, 72), (40, 333, 65)], ids=str)
+def test_accumulates_at_odd_addresses(b, shape, offset):
+    """A dw inside a 16-byte word, whose values are added one by one; nothing beside it is touched."""
+    rows, vocab, hidden = shape
+    x, w, targets = _inputs(*shape, "bf16", "some", seed=21)
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    before = torch.randn(vocab, hidden, device="cuda")
+    flat = torch.full((vocab * hidden + offset + 8,), 7.0, device="cuda")
+    dw = flat[offset:offset + vocab * hidden].view(vocab, hidden)
+    dw.copy_(before)
+    _grads(b, x, w, targets, lse, None, None, "bf16", dw=dw, dw_dtype="fp32", accumulate=1)
+    _check_grads(x, w, targets, lse, None, None, "bf16", 1.0, None, dw, "fp32", before)
+    assert (flat[:offset] == 7.0).all() and (flat[offset + vocab * hidden:] == 7.0).all()
+
+
+@pytest.mark.gpu
+def test_input_gradient_of_weights_past_2_31(b):
+    """Only the last two words, past 2^31 elements, have weights: dx is their two gradients of logits times those."""
+    vocab, hidden, rows = 2_100_000, 1040, 3
+    w = torch.zeros(vocab, hidden, dtype=torch.bfloat16, device="cuda")
+    w[-1, :4], w[-2, :4] = 1.0, -0.5
+    x = torch.zeros(rows, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:, :4] = torch.tensor([[2.0], [4.0], [0.0]], device="cuda")
+    targets = torch.tensor([vocab - 1, 7, vocab - 2], device="cuda")
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    dx, _ = _grads(b, x, w, targets, lse, None, None, "bf16", want=("dx",))
+    l = torch.stack([4 * x[:, 0].double(), -2 * x[:, 0].double()], 1)
+    d = torch.exp(l - torch.log(vocab - 2 + l.exp().sum(1, keepdim=True)))
+    d -= torch.tensor([[1.0, 0], [0, 0], [0, 1.0]], device="cuda")
+    ref = (d * torch.tensor([1.0, -0.5], device="cuda")).sum(1)
+    # one rounding of each gradient of a logit and of the result; the exponentials' own 2^-17 of their value
+    off = 2.0 ** -8 * ((d.abs() * torch.tensor([1.0, 0.5], device="cuda")).sum(1) * (1 + 2.0 ** -8) + ref.abs()) + 2.0 ** -17
+    assert ((dx[:, :4].double() - ref[:, None]).abs() <= off[:, None]).all() and (dx[:, 4:] == 0).all()
