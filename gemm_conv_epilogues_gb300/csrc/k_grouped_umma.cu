@@ -100,15 +100,6 @@ struct UmmaArgs {
     int64_t dy_stride;
 };
 
-// Arrives once on the mbarrier at this offset in both CTAs of the pair.
-__device__ __forceinline__ void commit_both(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     ptx::smem_u32(bar)),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
@@ -666,10 +657,10 @@ __global__ void __launch_bounds__(threads_of(MODE), 1)
 #pragma unroll
                             for (int k = 0; k < BK / UMMA_K; ++k) mma(d_tmem, as + k * a_step, bs + k * b_step, id, 1u);
                         }
-                        if constexpr (PAIR) commit_both(&empty[stage]);
+                        if constexpr (PAIR) ptx::umma_commit_both(&empty[stage]);
                         else ptx::umma_commit(&empty[stage]);
                         if (kb == nkb - 1) {
-                            if constexpr (PAIR) commit_both(&tfull[c]);
+                            if constexpr (PAIR) ptx::umma_commit_both(&tfull[c]);
                             else ptx::umma_commit(&tfull[c]);
                         }
                     }

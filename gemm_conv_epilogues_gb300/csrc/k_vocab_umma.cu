@@ -183,15 +183,6 @@ struct Share {
     }
 };
 
-// Arrives once on the mbarrier at this offset in both CTAs of the pair.
-__device__ __forceinline__ void commit_both(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                     ptx::smem_u32(bar)),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
 // The box: row `lane`'s piece i of 16 bytes on the way in, row 4i + lane/8's piece
 // lane%8 on the way out; the pieces are swizzled so that neither side meets a bank twice.
 __device__ __forceinline__ void box_put(uint8_t *box, int lane, int i, uint4 v)
@@ -400,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t a_step = a_mn ? desc_step(false) : desc_step(true), b_step = desc_step(!b_mn);
                     const uint32_t a_low = desc_low(base, !a_mn), b_low = desc_low(base + kABytes, !b_mn);
                     auto commit = [&](uint64_t *bar) {
-                        if constexpr (PAIR) commit_both(bar);
+                        if constexpr (PAIR) ptx::umma_commit_both(bar);
                         else ptx::umma_commit(bar);
                     };
                     for (int kb = 0; kb < t.nk; ++kb) {
@@ -788,7 +779,6 @@ cudaError_t launch_mode(const LceProduct &a, cudaStream_t st)
         // rows whose tiles of x stay in L2 while the vocabulary goes past
         const int64_t fit = ((int64_t)32 << 20) / ((int64_t)ROWS * a.x_pitch * 2);
         p.group = fit < 1 ? 1 : fit > row_tiles ? row_tiles : (int)fit;
-        if (p.group < 1) p.group = 1;
         tiles = (int64_t)row_tiles * ((a.words + p.bn - 1) / p.bn);
     }
     if (tiles == 0) return cudaSuccess;

@@ -353,6 +353,15 @@ __device__ __forceinline__ void umma_commit_pair(uint32_t bar_cluster)
                  : "memory");
 }
 
+// The same on the mbarrier at this offset in both CTAs of the pair.
+__device__ __forceinline__ void umma_commit_both(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+                     smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
 // Arrives once on the mbarrier when every tcgen05 operation this thread has
 // issued so far has completed.
 __device__ __forceinline__ void umma_commit(uint64_t *bar)
