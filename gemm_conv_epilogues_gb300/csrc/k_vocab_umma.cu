@@ -28,8 +28,9 @@
 // came out 6e-3 low, now 2e-6.)  dx's sums, of which 16 bits are kept, are cut into parts of 16384 terms, which are
 // tiles of their own that add to the fp32 sums in memory.
 // What bounds it, 4096 rows, 64000 words of 4096, bf16 (2.15 TFLOP each): STATS 1.02-1.05 ms
-// alone (2.05-2.1 PFLOP/s), DLOGITS in two pieces 1.08-1.10, GRADS 2.23-2.26; the tensor pipe is busy for
-// 95, 92 and 95.5% of the active cycles.  In a loop the power cap holds the clock down: 1.7 PFLOP/s.
+// alone (2.05-2.1 PFLOP/s), DLOGITS in two pieces 1.08-1.10, GRADS 2.23-2.26.  In a loop the power cap holds the
+// clock down: 1.7 PFLOP/s.  With 4096 rows and 16384 words of 2048 the tensor pipe is busy for 95, 92 and 96% of the
+// active cycles, with 1024 rows and 128000 words of 2048 for 97, 94 and 92%.
 // Four rows over 128000 words: 157 us, 6.7 TB/s of weights.
 // Every wait is bounded (ptx::mbar_wait); a role that times out sets the device
 // error word and winds down.
@@ -68,9 +69,9 @@ constexpr int LCE_LONG_GRADS = 3;
 constexpr bool of_grads(int mode) { return mode == LCE_GRADS || mode == LCE_LONG_GRADS; }
 // K steps per part of a sum in registers: 1024 terms of a logit's, 4096 of dw's.
 constexpr int kGradSteps = 64;
-// K steps per part of dx's in memory: 16384 terms come out up to 8e-5 low, a sixth of fp16's half step.  (Step of
-// 1024 rows over 128000 words of 2048: 1.465 ms, uncut 1.452; with parts of 4096 terms 1.482, and in registers 1.457;
-// of 4096 rows, 64000 words of 4096 5.06, uncut 5.05, parts of 4096 terms 5.1.)
+// K steps per part of dx's in memory: 16384 terms of one sign come out 8e-5 low, a sixth of fp16's half step.
+// (Step of 1024 rows over 128000 words of 2048: 1.46 ms, uncut 1.45, with parts of 4096 terms 1.48; of 4096 rows, 64000
+// words of 4096: 5.00, uncut 4.96, with parts of 4096 terms 5.06.)
 constexpr int kDxSteps = 256;
 constexpr int part_steps(int mode) { return mode == LCE_GRADS ? 1 << 30 : mode == LCE_LONG_GRADS ? kGradSteps : 16; }
 // Registers: the epilogue's threads hold 128 sums each while the issuing warps need few.  The
@@ -670,6 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     if (row0 + at >= rows || col >= pitch) continue;
                                     uint4 *to = reinterpret_cast<uint4 *>(dst + (int64_t)(4 * k) * pitch * size);
                                     uint4 v = box_get(box, at, piece);
+                                    // dx's are added by the L2, for which no thread waits (dx alone, 64 rows, 128000 words
+                                    // of 4096: 418 us, with loads 437); a sum's parts come from one thread, so in order
+                                    if (add && dx) {
+                                        asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to),
+                                                     "f"(__uint_as_float(v.x)), "f"(__uint_as_float(v.y)),
+                                                     "f"(__uint_as_float(v.z)), "f"(__uint_as_float(v.w))
+                                                     : "memory");
+                                        continue;
+                                    }
                                     if (add) {
                                         const uint4 o = *to;
                                         v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));

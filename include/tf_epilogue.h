@@ -442,16 +442,18 @@ int tf_linear_cross_entropy_forward(const void *x, int64_t x_stride, const void 
  *   dw     : dw_dtype [vocab][hidden], contiguous, or NULL; dw_dtype is dtype or
  *            TF_FP32.  With `accumulate` != 0 (TF_FP32 only) it is added to what
  *            dw holds.
- * The exponential, formed in fp32, is off by up to 2^-19 + 2^-22*(|l[i][v]| + |lse[i]|) of its value; a
- * target's term, of which dloss is taken away, by as much of exp(l - lse)*(dloss + dlse).  With
- * scale 1, no dlse and the forward pass's lse, a target whose loss is 0 has a term of exactly 0.
- * dl is then rounded to dtype, the matrix products' operand type: each term is off by up to 2^-8
- * (bf16) or 2^-11 (fp16) of its value more, in dx and dw, also where dw is fp32.  It is held in
- * units of a typical |dloss|, so that equal weights add no rounding of their own: bf16 takes
- * the first counted row's (where that lies between 2^-40 and 2^40), fp16 2^-14 of the largest,
- * so that terms down to 2^-28 of it keep their digits and none below 2^-39 of it
- * counts.  Sums are fp32, dw's in parts of 4096 terms and dx's of 16384: where the terms have one sign, a
- * part comes out low by up to 2e-5 or 8e-5 of its value.
+ * The exponential, formed in fp32 from the forward pass's sums, is off by up to
+ * 2^-19 + 2^-22*(|l[i][v]| + |lse[i]|) of its value; a target's term, of which dloss is taken
+ * away, by as much of exp(l - lse)*(dloss + dlse).  With scale 1, no dlse and the forward
+ * pass's lse, a target whose loss is 0 has a term of exactly 0.
+ * dl is then rounded to dtype, the matrix products' operand type: each term is off by up to
+ * 2^-8 (bf16) or 2^-11 (fp16) of its value more, in dx and dw, also where dw is fp32.  It is held
+ * in units of a typical |dloss|, so that equal weights add no rounding of their own: bf16 takes
+ * the first counted row's (where that lies between 2^-40 and 2^40: a row 2^127 times as
+ * large and larger becomes infinite), fp16 2^-14 of the largest, so that terms down to
+ * 2^-28 of it keep their digits and none below 2^-39 of it counts.
+ * Sums are fp32, dw's in parts of 4096 terms and dx's of 16384: where the terms have one sign,
+ * a part comes out low by up to 3e-5 or 1.2e-4 of its value.
  * Workspace as above. */
 int64_t tf_linear_cross_entropy_backward_workspace_size(int64_t rows, int64_t vocab, int64_t hidden, int dtype);
 int tf_linear_cross_entropy_backward(const void *x, int64_t x_stride, const void *w, const void *targets, int index,
