@@ -41,9 +41,9 @@ def test_scale_whose_exponents_overflow(native_lib):
 @pytest.mark.gpu
 @pytest.mark.parametrize("hidden", [256, 512, 1024, 4096])
 def test_ring_waits_that_run_out(b, hidden):
-    """A limit of nothing: copies that are not there at the first looks are given up, and the error word says so; copies
-    under way have landed before the kernel ends (no drain runs out), and later calls are not touched by it.
-    One, two and four pieces to a CTA, and rows of several slices."""
+    """A limit of nothing: a copy that has not come when a wait's looks are over (each waits some microseconds itself, so
+    that all may come) is given up, and the error word says so; copies under way have landed before the kernel ends (no drain
+    runs out), and later calls are not touched by it.  One, two and four pieces to a CTA, and rows of several slices."""
     rows, vocab = 60000, 5000
     tokens = _tokens("zipf", rows, vocab)
     dy = torch.randn(rows, hidden, device="cuda").bfloat16()
