@@ -253,3 +253,49 @@ def test_input_gradient_of_weights_past_2_31(b):
     # one rounding of each gradient of a logit and of the result; the exponentials' own 2^-17 of their value
     off = 2.0 ** -8 * ((d.abs() * torch.tensor([1.0, 0.5], device="cuda")).sum(1) * (1 + 2.0 ** -8) + ref.abs()) + 2.0 ** -17
     assert ((dx[:, :4].double() - ref[:, None]).abs() <= off[:, None]).all() and (dx[:, 4:] == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("mask", ["all", "most", "last"])
+def test_masks_of_many_rows(b, mask, dtype):
+    """More rows than one part of dw's sums, of which none count, or fewer than a part."""
+    rows, vocab, hidden = 5000, 700, 136
+    x, w, targets = _inputs(rows, vocab, hidden, dtype, mask, seed=22)
+    if mask == "all":
+        targets[:] = IGNORE
+        x[:] = float("nan")
+    loss, lse = _forward(b, x, w, targets, dtype)
+    dloss, dlse = _weights(targets)
+    dx, dw = _grads(b, x, w, targets, lse, dloss, dlse, dtype)
+    _check_grads(x, w, targets, lse, dloss, dlse, dtype, 1.0, dx, dw)
+    before = torch.randn(vocab, hidden, device="cuda")
+    dw = before.clone()
+    _grads(b, x, w, targets, lse, dloss, dlse, dtype, dw=dw, dw_dtype="fp32", accumulate=1, want=("dw",))
+    _check_grads(x, w, targets, lse, dloss, dlse, dtype, 1.0, None, dw, "fp32", before)
+    if mask == "all":
+        assert torch.equal(dw, before)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(5000, 3000, 200), (64, 140001, 136), (300, 140001, 72), (4200, 40001, 72)], ids=str)
+def test_equal_bits_of_parts(b, shape):
+    """Sums whose parts are added in registers or in memory, over splits and pieces: the same bits again, also from a
+    graph, over a workspace that holds other numbers."""
+    x, w, targets = _inputs(*shape, "bf16", "some", seed=23)
+    loss, lse = _forward(b, x, w, targets, "bf16")
+    dloss, dlse = _weights(targets)
+    ws = torch.full((b.tf_linear_cross_entropy_backward_workspace_size(*shape, 1),), 0xff, dtype=torch.uint8, device="cuda")
+    first = _grads(b, x, w, targets, lse, dloss, dlse, "bf16", ws=ws)
+    for fill in (0x3f, 0xc1):
+        ws.fill_(fill)
+        again = _grads(b, x, w, targets, lse, dloss, dlse, "bf16", ws=ws)
+        assert all(torch.equal(p, q) for p, q in zip(first, again))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = _grads(b, x, w, targets, lse, dloss, dlse, "bf16", ws=ws)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(float("nan"))
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(first, outs))
